@@ -268,6 +268,148 @@ int moe_decode_layer_profiled(const moe_dims* dims, const moe_layer_weights* w, 
                               const moe_route_out* route_out, void* ws, size_t ws_bytes,
                               void* stream, void* const* events, int32_t n_events);
 
+/* ---------------------------------------------------------------- around the layer
+ *
+ * The operators next to the layer in a transformer block: the residual add
+ * and RMS norm that make its input, routing rules other than the softmax
+ * top-8 of moe_route, and projections of packed int4 weights with low-rank
+ * adapters. They follow the conventions at the top of this file. */
+
+/* Element types of moe_add_rmsnorm. */
+#define MOE_BF16 0
+#define MOE_F16 1
+#define MOE_F32 2
+/* 8-bit outputs of moe_add_rmsnorm: none, signed integers -127..127, or
+ * e4m3 floating point (OCP: no infinities, largest value 448). */
+#define MOE_OUT8_NONE 0
+#define MOE_OUT8_INT8 1
+#define MOE_OUT8_E4M3 2
+
+/* Row length H (1..16384), element type of the rows (x, residual, h, y) and
+ * of the weight (the rows' type or MOE_F32), 8-bit output and the number of
+ * consecutive values that share one of its scales (group: 0 = the whole row,
+ * or 32, 64, 128 or 256, dividing H), eps > 0, and a constant added to every
+ * weight (1 for weights stored as their distance from one, else 0). */
+typedef struct {
+  int32_t H, dtype, weight_dtype, out8, group;
+  float eps, weight_offset;
+} moe_norm;
+
+/* Residual add and RMS norm of T rows, per row:
+ *   h = x + residual, rounded to the rows' type (h = x without a residual)
+ *   r = 1 / sqrt(mean(h^2) + eps)
+ *   v = h * r * (weight + weight_offset)
+ *   y = v, rounded to the rows' type
+ *   s = max |v| over a group / 127 (int8) or / 448 (e4m3)
+ *   q = v / s, rounded to the nearest 8-bit value (ties to even), limited to
+ *       +-127 / +-448; 0 where s = 0
+ * with sums and v in fp32 (q is formed from v, not from y). x [T][H] with row
+ * stride ldx; residual, h_out, y [T][H] and q [T][H] (one byte a value) with
+ * row strides ld_residual, ld_h, ld_y, ld_q, all in elements, from H to 2^20
+ * (those of null pointers are not looked at); scales
+ * [T][H / group] (one per row for group 0) contiguous. residual, h_out, y may
+ * each be null; q and scales are both given with an 8-bit output and both
+ * null without; h_out, y or q has to be given. h_out may be x or residual
+ * and y may be x, residual or h_out, with the same row stride (each row is
+ * read whole before it is written; y over h_out leaves y); any other overlap
+ * of an output with another argument is not allowed. Pointers need their
+ * element's alignment only; 16-byte aligned rows are faster. A NaN or
+ * infinity in a row makes its y NaN or 0 as the formulas do in fp32 and the
+ * scales of the groups it reaches NaN or infinite (q: 0, or e4m3's NaN). The
+ * sum of squares has fp32's range: rows of values beyond about 1e19 / sqrt(H)
+ * overflow to r = 0. T = 0 is a no-op. */
+int moe_add_rmsnorm(const moe_norm* norm, const void* x, int64_t ldx, const void* residual,
+                    int64_t ld_residual, const void* weight, void* h_out, int64_t ld_h, void* y,
+                    int64_t ld_y, void* q, int64_t ld_q, float* scales, int32_t T, void* stream);
+
+/* Scores of a gate. */
+#define MOE_SCORE_SOFTMAX 0 /* softmax over the E logits            */
+#define MOE_SCORE_SIGMOID 1 /* 1 / (1 + exp(-logit)) of each logit  */
+/* How a group of experts is ranked. */
+#define MOE_GROUP_MAX 0  /* by its largest key                  */
+#define MOE_GROUP_TOP2 1 /* by the sum of its two largest keys  */
+
+/* A routing rule. For one token, over E logits:
+ *   score_e = softmax or sigmoid of the logits
+ *   key_e   = score_e + balance_bias_e (null: 0)
+ *   the n_groups groups of E / n_groups consecutive experts are ranked as
+ *   group_score says, and the topk_groups best (ties: the lower group) keep
+ *   their experts;
+ *   the top_k largest keys among those are selected, larger first, ties to
+ *   the lower expert;
+ *   weight_j = score_j, divided by the sum over the selected experts if
+ *   renorm (0 if that sum is 0), times scale.
+ * Ranks are those of the scores and keys evaluated in 64 bits. An expert
+ * whose logit is -inf or NaN, or whose key is -inf or NaN, is masked: it
+ * ranks after every other, has weight 0, and does not count towards its
+ * group's rank (a group of masked experts ranks last). A logit of +inf takes
+ * the softmax's mass (shared equally among several). Where masking leaves
+ * fewer than top_k experts, the lowest masked ones fill the remaining slots,
+ * with weight 0. Supported: E 1..256, top_k 1..16 and <= E, block_m 32 or 16,
+ * n_groups 1..64 dividing E, topk_groups 1..n_groups with at least top_k
+ * experts in them, scale finite. balance_bias is a device pointer. */
+typedef struct {
+  int32_t E, top_k, block_m, score, n_groups, topk_groups, group_score, renorm;
+  float scale;
+  const float* balance_bias; /* [E] fp32, or NULL */
+} moe_gate;
+
+/* moe_max_blocks and the workspace of moe_route_gated for a gate. */
+int64_t moe_gate_max_blocks(const moe_gate* gate, int32_t T);
+int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes);
+
+/* moe_route with a gate: from fp32 logits [T][E] (device) every field of
+ * `out` (k = gate->top_k, E = gate->E, block_m = gate->block_m). Results do
+ * not depend on the workspace's contents. T = 0 is a no-op. */
+int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const moe_route_out* out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* moe_prefill_layer and moe_decode_layer with a gate in the place of the
+ * softmax top-8: the same arguments, workspaces (moe_workspace_bytes) and
+ * results, with topk_idx and topk_w from the gate. gate->E, top_k and block_m
+ * have to be the dims' (MOE_EINVAL otherwise). */
+int moe_prefill_layer_gated(const moe_dims* dims, const moe_gate* gate, const moe_layer_weights* w,
+                            const uint16_t* x, uint16_t* y, int32_t T, int32_t chunk_T,
+                            float* logits_out, const moe_route_out* route_out, void* ws,
+                            size_t ws_bytes, void* stream);
+int moe_decode_layer_gated(const moe_dims* dims, const moe_gate* gate, const moe_layer_weights* w,
+                           const uint16_t* x, uint16_t* y, int32_t T, float* logits_out,
+                           const moe_route_out* route_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Low-rank adapters of one projection [N][K]: n adapters with space for R
+ * ranks each (R % 8 == 0, 8..128). Adapter a adds
+ * scales[a] * B_a (A_a x) with the first ranks[a] rows of A_a and columns of
+ * B_a (ranks[a] is limited to 0..R); what lies behind them is not used. A, B
+ * 16-byte aligned, ranks and scales 4-byte aligned; all device pointers. */
+typedef struct {
+  int32_t n, R;
+  const uint16_t* A;    /* [n][R][K] bf16                */
+  const uint16_t* B;    /* [n][N][R] bf16                */
+  const int32_t* ranks; /* [n], or NULL: R for each      */
+  const float* scales;  /* [n], or NULL: 1 for each      */
+} moe_adapters;
+
+/* Workspace of moe_project for up to T tokens (R: the adapters' R, 0 without
+ * adapters). */
+int moe_project_workspace_bytes(int32_t N, int32_t K, int32_t R, int32_t T, size_t* bytes);
+
+/* A projection by packed int4 weights beside the adapters of many requests:
+ *   y[t] = W x[t] + scales[a] * B_a (A_a x[t]),  a = adapter_of[t]
+ * for x [T][K] and y [T][N] bf16 with row strides ldx >= K, ldy >= N
+ * (elements, multiples of 8, at most 2^20). blob: a pack_int4_g64 blob (device) of one
+ * matrix [N][K] (count 1, not paired); N % 64 == 0, K % 128 == 0, K <= 16384,
+ * N <= 65536. adapter_of [T] (device, int32) names each token's adapter, in
+ * any order; -1, and any other value outside 0..n-1, means none. ad and
+ * adapter_of are both given or both null. An adapter's NaN or infinity
+ * reaches its own tokens only. gemm is a MOE_GEMM_* value: how W enters the
+ * matrix cores, as in moe_dims (EXACT: used exactly, WIDE: rounded once to
+ * bf16, AUTO: by the number of tokens). fp32 accumulation; A_a x is kept to
+ * at least 16 significant bits between the two products; y is rounded once.
+ * x and y must not overlap. ws 16-byte aligned. T = 0 is a no-op. */
+int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64_t ldx, uint16_t* y,
+                int64_t ldy, int32_t T, const moe_adapters* ad, const int32_t* adapter_of,
+                int32_t gemm, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of an error code. */
 const char* moe_strerror(int code);
 

@@ -23,12 +23,17 @@ MOE_ESCRATCH = -7
 NOALLOC_SCRATCH_BYTES = 320 * 1024
 MODE_PREFILL, MODE_DECODE, MODE_ROUTE = 0, 1, 2
 GEMM_AUTO, GEMM_EXACT, GEMM_WIDE = 0, 1, 2
+BF16, F16, F32 = 0, 1, 2
+OUT8_NONE, OUT8_INT8, OUT8_E4M3 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 HEADER_BYTES = 256
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class MoeDims(ctypes.Structure):
@@ -45,6 +50,21 @@ class MoeLayerWeights(ctypes.Structure):
 class MoeRouteOut(ctypes.Structure):
     _fields_ = [("topk_idx", _vp), ("topk_w", _vp), ("hist", _vp), ("offsets", _vp),
                 ("perm", _vp), ("inv_perm", _vp), ("block_map", _vp), ("num_blocks", _vp)]
+
+
+class MoeNorm(ctypes.Structure):
+    _fields_ = [("H", _i32), ("dtype", _i32), ("weight_dtype", _i32), ("out8", _i32), ("group", _i32),
+                ("eps", _f32), ("weight_offset", _f32)]
+
+
+class MoeGate(ctypes.Structure):
+    _fields_ = [("E", _i32), ("top_k", _i32), ("block_m", _i32), ("score", _i32), ("n_groups", _i32),
+                ("topk_groups", _i32), ("group_score", _i32), ("renorm", _i32), ("scale", _f32),
+                ("balance_bias", _vp)]
+
+
+class MoeAdapters(ctypes.Structure):
+    _fields_ = [("n", _i32), ("R", _i32), ("A", _vp), ("B", _vp), ("ranks", _vp), ("scales", _vp)]
 
 
 class MoeError(RuntimeError):
@@ -97,6 +117,17 @@ def lib():
                                                P(MoeRouteOut), _vp]
         L.moe_ceiling_read.argtypes = [_vp, _sz, _vp, _vp]
         L.moe_ceiling_mfma.argtypes = [_i32, _i32, _vp, _vp, P(ctypes.c_double), _vp]
+        L.moe_add_rmsnorm.argtypes = [P(MoeNorm), _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
+                                      _i64, _vp, _i32, _vp]
+        L.moe_gate_max_blocks.argtypes = [P(MoeGate), _i32]
+        L.moe_gate_max_blocks.restype = _i64
+        L.moe_gate_workspace_bytes.argtypes = [P(MoeGate), _i32, P(_sz)]
+        L.moe_route_gated.argtypes = [P(MoeGate), _vp, _i32, P(MoeRouteOut), _vp, _sz, _vp]
+        L.moe_prefill_layer_gated.argtypes = [P(MoeDims), P(MoeGate)] + L.moe_prefill_layer.argtypes[1:]
+        L.moe_decode_layer_gated.argtypes = [P(MoeDims), P(MoeGate)] + L.moe_decode_layer.argtypes[1:]
+        L.moe_project_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, P(_sz)]
+        L.moe_project.argtypes = [_vp, _i32, _i32, _vp, _i64, _vp, _i64, _i32, P(MoeAdapters), _vp, _i32,
+                                  _vp, _sz, _vp]
         L.moe_strerror.argtypes = [ctypes.c_int]
         L.moe_strerror.restype = ctypes.c_char_p
         L.moe_test_dequant.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]
@@ -105,7 +136,9 @@ def lib():
                      "moe_prefill_layer_profiled", "moe_decode_layer_profiled",
                      "moe_prefill_layer_host_routed", "moe_unfused_weight_bytes",
                      "moe_prefill_layer_unfused", "moe_ceiling_read", "moe_ceiling_mfma",
-                     "moe_decode_layer_noalloc"):
+                     "moe_decode_layer_noalloc", "moe_add_rmsnorm", "moe_gate_workspace_bytes",
+                     "moe_route_gated", "moe_prefill_layer_gated", "moe_decode_layer_gated",
+                     "moe_project_workspace_bytes", "moe_project"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -144,7 +177,9 @@ def _stream(stream, device=None):
 
 # ------------------------------------------------------------------ packing (host)
 
-def moe_max_blocks(d: MoeDims, T: int) -> int:
+def moe_max_blocks(d: MoeDims | MoeGate, T: int) -> int:
+    if isinstance(d, MoeGate):
+        return moe_gate_max_blocks(d, T)
     v = lib().moe_max_blocks(ctypes.byref(d), T)
     if v < 0:
         raise MoeError(int(v), "moe_max_blocks")
@@ -245,9 +280,9 @@ class DeviceWeights:
 
 
 class RouteBuffers:
-    """Device buffers for moe_route_out sized for T tokens."""
+    """Device buffers for moe_route_out sized for T tokens (of a layer's dims or a gate)."""
 
-    def __init__(self, d: MoeDims, T: int, device="cuda"):
+    def __init__(self, d: MoeDims | MoeGate, T: int, device="cuda"):
         import torch
         k = d.top_k
         mb = moe_max_blocks(d, T)
@@ -400,3 +435,205 @@ def ceiling_clock_mhz(clocks) -> float:
 def moe_test_dequant(blob, count, N, K, paired, expert, out, stream=None):
     _check(lib().moe_test_dequant(_ptr(blob), count, N, K, int(paired), expert, _ptr(out),
                                   _stream(stream)), "moe_test_dequant")
+
+
+# ------------------------------------------------------------------ around the layer
+#
+# These wrappers also check what the C entry points cannot see: the tensors'
+# sizes, types and devices (ValueError). The work goes to the current stream
+# of the tensors' device unless `stream` says otherwise.
+
+def _type_code(dtype):
+    import torch
+    codes = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+    if isinstance(dtype, int) and dtype in codes.values():
+        return dtype
+    if dtype not in codes:
+        raise ValueError(f"rows of {dtype} are not supported (bfloat16, float16 or float32)")
+    return codes[dtype]
+
+
+def _torch_type(code):
+    import torch
+    return (torch.bfloat16, torch.float16, torch.float32)[code]
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
+
+
+class _Rows:
+    """The checks of a [T, width] tensor whose rows are contiguous: its address and row stride."""
+
+    @staticmethod
+    def of(t, T, width, dtypes, name):
+        if t.dtype not in dtypes or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width:
+            raise ValueError(f"{name}: [{T}, {width}] of {dtypes[0]} is needed, got {list(t.shape)} of {t.dtype}")
+        s0, s1 = t.stride()
+        if width > 1 and s1 != 1:
+            raise ValueError(f"{name}: the values of a row have to be contiguous")
+        if T <= 1:
+            s0 = max(s0, width)  # the stride of a single row says nothing
+        return t.data_ptr(), s0
+
+
+def _flat(t, n, dtype, name):
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous values of {dtype} are needed, got {list(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
+def _call(device, stream, f):
+    """f(stream handle) with `device` current."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors on a GPU are needed, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return f(_stream(stream, device))
+    return f(_stream(stream, device))
+
+
+def norm(H, dtype=BF16, weight_dtype=None, eps=1e-6, weight_offset=0.0, out8=OUT8_NONE, group=0) -> MoeNorm:
+    """What moe_add_rmsnorm does to rows of H values (dtype: a torch type or BF16 / F16 / F32)."""
+    code = _type_code(dtype)
+    return MoeNorm(H, code, code if weight_dtype is None else _type_code(weight_dtype), out8, group, eps,
+                   weight_offset)
+
+
+def moe_add_rmsnorm(n: MoeNorm, x, weight, T: int, residual=None, h_out=None, y=None, q=None, scales=None,
+                    stream=None):
+    """h = x + residual, y = h / rms(h) * weight for T rows, and q, scales: y in 8 bits."""
+    import torch
+    _on(x.device, weight, residual, h_out, y, q, scales)
+    rows, H = (_torch_type(n.dtype),), n.H
+    a = [_Rows.of(x, T, H, rows, "x")]
+    for t, name in ((residual, "residual"), (h_out, "h_out"), (y, "y")):
+        a.append((None, 0) if t is None else _Rows.of(t, T, H, rows, name))
+    if q is not None:
+        bytes8 = (torch.int8, torch.uint8) if n.out8 == OUT8_INT8 else (torch.float8_e4m3fn, torch.uint8)
+        a.append(_Rows.of(q, T, H, bytes8, "q"))
+    else:
+        a.append((None, 0))
+    sp = None if scales is None else _flat(scales, T * (H // n.group if n.group else 1), torch.float32, "scales")
+    w = _flat(weight, H, _torch_type(n.weight_dtype), "weight")
+    _check(_call(x.device, stream, lambda s: lib().moe_add_rmsnorm(
+        ctypes.byref(n), *a[0], *a[1], w, *a[2], *a[3], *a[4], sp, T, s)), "moe_add_rmsnorm")
+
+
+def gate(E=256, top_k=8, block_m=32, score=SCORE_SOFTMAX, n_groups=1, topk_groups=1, group_score=GROUP_MAX,
+         renorm=True, scale=1.0, balance_bias=None) -> MoeGate:
+    """A routing rule (balance_bias: an fp32 device tensor [E] that the gate keeps alive)."""
+    import torch
+    bias = None if balance_bias is None else _flat(balance_bias, E, torch.float32, "balance_bias")
+    g = MoeGate(E, top_k, block_m, score, n_groups, topk_groups, group_score, int(renorm), scale, bias)
+    g.bias_tensor = balance_bias
+    return g
+
+
+def moe_gate_max_blocks(g: MoeGate, T: int) -> int:
+    v = lib().moe_gate_max_blocks(ctypes.byref(g), T)
+    if v < 0:
+        raise MoeError(int(v), "moe_gate_max_blocks")
+    return int(v)
+
+
+def gate_workspace(g: MoeGate, T: int, device="cuda"):
+    """Workspace of moe_route_gated for up to T tokens."""
+    import torch
+    n = _sz(0)
+    _check(lib().moe_gate_workspace_bytes(ctypes.byref(g), T, ctypes.byref(n)), "moe_gate_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _check_route_out(g, T, out):
+    _need(out.topk_idx.numel() >= T * g.top_k and out.hist.numel() >= g.E and
+          out.block_map.shape[0] >= moe_max_blocks(g, T), "route_out: buffers of this gate and T are needed")
+
+
+def moe_route_gated(g: MoeGate, logits, T: int, out: RouteBuffers, ws, stream=None):
+    import torch
+    _on(logits.device, out.topk_idx, ws, g.bias_tensor)
+    lp = _flat(logits, T * g.E, torch.float32, "logits")
+    _check_route_out(g, T, out)
+    _check(_call(logits.device, stream, lambda s: lib().moe_route_gated(
+        ctypes.byref(g), lp, T, ctypes.byref(out.struct), ws.data_ptr(), ws.numel(), s)), "moe_route_gated")
+
+
+def moe_prefill_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, chunk_T: int = 0,
+                            logits_out=None, route_out: RouteBuffers | None = None, ws=None, stream=None):
+    """moe_prefill_layer routed by a gate."""
+    ro = ctypes.byref(route_out.struct) if route_out is not None else None
+    _check(lib().moe_prefill_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
+                                         _ptr(y), T, chunk_T, _ptr(logits_out), ro, _ptr(ws),
+                                         0 if ws is None else ws.numel(), _stream(stream)),
+           "moe_prefill_layer_gated")
+
+
+def moe_decode_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, logits_out=None,
+                           route_out: RouteBuffers | None = None, ws=None, stream=None):
+    """moe_decode_layer routed by a gate."""
+    ro = ctypes.byref(route_out.struct) if route_out is not None else None
+    _check(lib().moe_decode_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
+                                        _ptr(y), T, _ptr(logits_out), ro, _ptr(ws),
+                                        0 if ws is None else ws.numel(), _stream(stream)),
+           "moe_decode_layer_gated")
+
+
+class Adapters:
+    """Low-rank adapters of one projection: A [n, R, K] and B [n, N, R] bf16, ranks [n] int32 (None: R
+    each), scales [n] fp32 (None: 1 each), all on one GPU."""
+
+    def __init__(self, A, B, ranks=None, scales=None):
+        import torch
+        bf16 = (torch.bfloat16, torch.int16)
+        _need(A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0] and A.shape[1] == B.shape[2] and
+              A.dtype in bf16 and B.dtype in bf16 and A.is_contiguous() and B.is_contiguous(),
+              "adapters: contiguous A [n, R, K] and B [n, N, R] of bfloat16 are needed")
+        _on(A.device, B, ranks, scales)
+        self.n, self.R, self.K = A.shape
+        self.N = B.shape[1]
+        self.t = (A, B, ranks, scales)
+        self.device = A.device
+        self.struct = MoeAdapters(self.n, self.R, A.data_ptr(), B.data_ptr(),
+                                  None if ranks is None else _flat(ranks, self.n, torch.int32, "ranks"),
+                                  None if scales is None else _flat(scales, self.n, torch.float32, "scales"))
+
+
+def project_workspace(N, K, T, adapters: Adapters | None = None, device=None):
+    """Workspace of moe_project for up to T tokens."""
+    import torch
+    n = _sz(0)
+    _check(lib().moe_project_workspace_bytes(N, K, adapters.R if adapters else 0, T, ctypes.byref(n)),
+           "moe_project_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=device or (adapters.device if adapters else "cuda"))
+
+
+def moe_project(blob, N: int, K: int, x, y, T: int, adapters: Adapters | None = None, adapter_of=None,
+                gemm: int = GEMM_AUTO, ws=None, stream=None):
+    """y[t] = W x[t] + scale B_a (A_a x[t]) for a packed int4 matrix [N, K] (pack_int4_g64 of one unpaired
+    matrix) and the adapter a = adapter_of[t] of each token (-1: none)."""
+    import torch
+    bf16 = (torch.bfloat16, torch.int16)
+    _need(blob.dtype == torch.uint8 and blob.numel() >= moe_packed_bytes(1, N, K, False) > 0,
+          "blob: a pack_int4_g64 blob of one [N, K] matrix is needed")
+    xp, ldx = _Rows.of(x, T, K, bf16, "x")
+    yp, ldy = _Rows.of(y, T, N, bf16, "y")
+    _on(x.device, blob, y, adapter_of, ws)
+    ap = op = None
+    if adapters is not None:
+        _need(adapters.N == N and adapters.K == K, "adapters: another projection's")
+        _on(x.device, adapters.t[0])
+        ap = ctypes.byref(adapters.struct)
+    if adapter_of is not None:
+        op = _flat(adapter_of, T, torch.int32, "adapter_of")
+    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(_call(x.device, stream, lambda s: lib().moe_project(
+        blob.data_ptr(), N, K, xp, ldx, yp, ldy, T, ap, op, gemm, wp, wn, s)), "moe_project")

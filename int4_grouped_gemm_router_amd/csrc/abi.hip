@@ -2,6 +2,7 @@
 // chunk loop, and the launches on the caller's stream (include/moe_int4.h).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/moe_int4.h"
@@ -148,6 +149,63 @@ bool weights_aligned(const moe_layer_weights* w) {
          al16(w->experts_down) && al16(w->shared_gate_up) && al16(w->shared_down);
 }
 
+// Row strides of the operators around the layer (elements): in-tile offsets
+// of a few hundred rows stay 32-bit in the kernels.
+constexpr int64_t kMaxRowStride = int64_t(1) << 20;
+
+bool project_dims_ok(int N, int K) {
+  return N > 0 && N % 64 == 0 && N <= 65536 && K > 0 && K % 128 == 0 && K <= 16384;
+}
+bool rank_space_ok(int R) { return R >= 8 && R <= kMaxRank && R % 8 == 0; }
+
+bool gate_ok(const moe_gate* g) {
+  return g->E >= 1 && g->E <= 256 && g->top_k >= 1 && g->top_k <= kMaxGateK && g->top_k <= g->E &&
+         (g->block_m == 32 || g->block_m == 16) && g->n_groups >= 1 && g->n_groups <= kMaxGateGroups &&
+         g->E % g->n_groups == 0 && g->topk_groups >= 1 && g->topk_groups <= g->n_groups &&
+         g->topk_groups * (g->E / g->n_groups) >= g->top_k;
+}
+
+// MOE_OK, or why the gate is refused.
+int check_gate(const moe_gate* g) {
+  if (!g || (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) ||
+      (g->group_score != MOE_GROUP_MAX && g->group_score != MOE_GROUP_TOP2) ||
+      (g->renorm != 0 && g->renorm != 1) || !std::isfinite(g->scale) || !al4(g->balance_bias))
+    return MOE_EINVAL;
+  return gate_ok(g) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+GateArgs gate_args(const moe_gate* g) {
+  GateArgs a{};
+  a.balance = g->balance_bias;
+  a.E = g->E;
+  a.k = g->top_k;
+  a.sigmoid = g->score == MOE_SCORE_SIGMOID;
+  a.n_groups = g->n_groups;
+  a.topk_groups = g->topk_groups;
+  a.group_top2 = g->group_score == MOE_GROUP_TOP2;
+  a.renorm = g->renorm;
+  a.scale = g->scale;
+  return a;
+}
+
+// A gate for the layer: the layer's own dims, routed by the gate.
+int check_layer_gate(const moe_dims* dims, const moe_gate* g) {
+  if (!dims) return MOE_EINVAL;
+  const int rc = check_gate(g);
+  if (rc != MOE_OK) return rc;
+  if (!dims_ok(dims)) return MOE_EUNSUPPORTED;
+  return g->E == dims->E && g->top_k == dims->top_k && g->block_m == dims->block_m ? MOE_OK : MOE_EINVAL;
+}
+
+// The part of the dims that moe_route's metadata goes by, for a gate.
+moe_dims gate_dims(const moe_gate* g) {
+  moe_dims d{};
+  d.E = g->E;
+  d.top_k = g->top_k;
+  d.block_m = g->block_m;
+  return d;
+}
+
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 // Optional timing hook: records events[i] before the i-th kernel launch and
@@ -168,10 +226,10 @@ constexpr int kDecodeLaunches = 3;
 int prefill_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_t* x, uint16_t* y,
                  int32_t T, int32_t chunk_T, float* logits_out, const moe_route_out* route_out,
                  void* ws, size_t ws_bytes, void* stream, Recorder rec, bool host_routed = false,
-                 uint8_t* unfused_w = nullptr);
+                 uint8_t* unfused_w = nullptr, const moe_gate* gate = nullptr);
 int decode_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_t* x, uint16_t* y,
                 int32_t T, float* logits_out, const moe_route_out* route_out, void* ws,
-                size_t ws_bytes, void* stream, hipEvent_t* ev);
+                size_t ws_bytes, void* stream, hipEvent_t* ev, const moe_gate* gate = nullptr);
 int decode_args(const moe_dims* dims, const moe_layer_weights* w, const uint16_t* x, uint16_t* y,
                 int32_t T, float* logits_out, const moe_route_out* route_out);
 
@@ -299,7 +357,7 @@ namespace {
 int prefill_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_t* x, uint16_t* y,
                  int32_t T, int32_t chunk_T, float* logits_out, const moe_route_out* route_out,
                  void* ws, size_t ws_bytes, void* stream, Recorder rec, bool host_routed,
-                 uint8_t* unfused_w) {
+                 uint8_t* unfused_w, const moe_gate* gate) {
   if (!dims || T < 0) return MOE_EINVAL;
   if (!dims_ok(dims) || too_many_pairs(dims, T)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -344,7 +402,20 @@ int prefill_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_
     ta.E = E;
     ta.k = k;
     if (rec.mark(s) != hipSuccess) return MOE_EHIP;
-    if (launch_topk(ta, s) != hipSuccess) return MOE_EHIP;
+    if (gate) {
+      GateArgs ga = gate_args(gate);
+      ga.partial = ta.partial;
+      ga.splits = ta.splits;
+      ga.rbias = ta.rbias;
+      ga.logits_out = ta.logits_out;
+      ga.topk_idx = ta.topk_idx;
+      ga.topk_w = ta.topk_w;
+      ga.chunk_hist = ta.chunk_hist;
+      ga.T = Tn;
+      if (launch_gate_topk(ga, s) != hipSuccess) return MOE_EHIP;
+    } else if (launch_topk(ta, s) != hipSuccess) {
+      return MOE_EHIP;
+    }
 
     ScatterArgs sa{};
     sa.topk_idx = topk_idx;
@@ -501,7 +572,7 @@ int decode_args(const moe_dims* dims, const moe_layer_weights* w, const uint16_t
 
 int decode_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_t* x, uint16_t* y,
                 int32_t T, float* logits_out, const moe_route_out* route_out, void* ws,
-                size_t ws_bytes, void* stream, hipEvent_t* ev) {
+                size_t ws_bytes, void* stream, hipEvent_t* ev, const moe_gate* gate) {
   const int rc = decode_args(dims, w, x, y, T, logits_out, route_out);
   if (rc != MOE_OK || T == 0) return rc;
   if (!ws || !al16(ws)) return MOE_EINVAL;
@@ -540,6 +611,10 @@ int decode_impl(const moe_dims* dims, const moe_layer_weights* w, const uint16_t
   a.E = dims->E;
   a.k = dims->top_k;
   a.block_m = dims->block_m;
+  if (gate) {
+    const GateArgs ga = gate_args(gate);
+    return hip_status(launch_decode(a, static_cast<hipStream_t>(stream), ev, &ga));
+  }
   return hip_status(launch_decode(a, static_cast<hipStream_t>(stream), ev));
 }
 
@@ -586,6 +661,188 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_weights* w, c
   if (!ws) return MOE_EHIP;
   return decode_impl(dims, w, x, y, T, logits_out, route_out, ws, MOE_NOALLOC_SCRATCH_BYTES, stream,
                      nullptr);
+}
+
+int64_t moe_gate_max_blocks(const moe_gate* gate, int32_t T) {
+  const int rc = check_gate(gate);
+  if (rc != MOE_OK) return rc;
+  if (T < 0) return MOE_EINVAL;
+  const moe_dims d = gate_dims(gate);
+  return max_blocks(&d, T);
+}
+
+int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes) {
+  if (!bytes || T < 0) return MOE_EINVAL;
+  const int rc = check_gate(gate);
+  if (rc != MOE_OK) return rc;
+  const moe_dims d = gate_dims(gate);
+  if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
+  int32_t* ch;
+  *bytes = route_ws(&d, std::max(T, 1), nullptr, &ch);
+  return MOE_OK;
+}
+
+int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const moe_route_out* out,
+                    void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0) return MOE_EINVAL;
+  const int rc = check_gate(gate);
+  if (rc != MOE_OK) return rc;
+  const moe_dims d = gate_dims(gate);
+  if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !route_out_ok(out) || !ws || !al4(logits) || !al16(ws)) return MOE_EINVAL;
+  int32_t* chunk_hist;
+  if (ws_bytes < route_ws(&d, T, ws, &chunk_hist)) return MOE_EWORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (launch_fill_zero(chunk_hist, n_chunks(&d, T) * d.E, s) != hipSuccess) return MOE_EHIP;
+  GateArgs ga = gate_args(gate);
+  ga.partial = logits;
+  ga.splits = 1;
+  ga.topk_idx = out->topk_idx;
+  ga.topk_w = out->topk_w;
+  ga.chunk_hist = chunk_hist;
+  ga.T = T;
+  if (launch_gate_topk(ga, s) != hipSuccess) return MOE_EHIP;
+  ScatterArgs sa{};
+  sa.topk_idx = out->topk_idx;
+  sa.chunk_hist = chunk_hist;
+  sa.hist = out->hist;
+  sa.offsets = out->offsets;
+  sa.perm = out->perm;
+  sa.inv_perm = out->inv_perm;
+  sa.block_map = out->block_map;
+  sa.num_blocks = out->num_blocks;
+  sa.T = T;
+  sa.E = d.E;
+  sa.k = d.top_k;
+  sa.block_m = d.block_m;
+  return hip_status(launch_scan_scatter(sa, s));
+}
+
+int moe_prefill_layer_gated(const moe_dims* dims, const moe_gate* gate, const moe_layer_weights* w,
+                            const uint16_t* x, uint16_t* y, int32_t T, int32_t chunk_T,
+                            float* logits_out, const moe_route_out* route_out, void* ws,
+                            size_t ws_bytes, void* stream) {
+  const int rc = check_layer_gate(dims, gate);
+  if (rc != MOE_OK) return rc;
+  return prefill_impl(dims, w, x, y, T, chunk_T, logits_out, route_out, ws, ws_bytes, stream,
+                      Recorder{}, false, nullptr, gate);
+}
+
+int moe_decode_layer_gated(const moe_dims* dims, const moe_gate* gate, const moe_layer_weights* w,
+                           const uint16_t* x, uint16_t* y, int32_t T, float* logits_out,
+                           const moe_route_out* route_out, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_layer_gate(dims, gate);
+  if (rc != MOE_OK) return rc;
+  return decode_impl(dims, w, x, y, T, logits_out, route_out, ws, ws_bytes, stream, nullptr, gate);
+}
+
+int moe_add_rmsnorm(const moe_norm* n, const void* x, int64_t ldx, const void* residual,
+                    int64_t ld_residual, const void* weight, void* h_out, int64_t ld_h, void* y,
+                    int64_t ld_y, void* q, int64_t ld_q, float* scales, int32_t T, void* stream) {
+  if (!n || T < 0 || n->dtype < MOE_BF16 || n->dtype > MOE_F32 ||
+      (n->weight_dtype != n->dtype && n->weight_dtype != MOE_F32) || n->out8 < MOE_OUT8_NONE ||
+      n->out8 > MOE_OUT8_E4M3 || !std::isfinite(n->eps) || n->eps <= 0.f ||
+      !std::isfinite(n->weight_offset))
+    return MOE_EINVAL;
+  if (n->H < 1 || n->H > kNormMaxH) return MOE_EUNSUPPORTED;
+  if (n->group != 0 && ((n->group != 32 && n->group != 64 && n->group != 128 && n->group != 256) ||
+                        n->H % n->group))
+    return MOE_EUNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || (!h_out && !y && !q) || (q != nullptr) != (n->out8 != MOE_OUT8_NONE) ||
+      (scales != nullptr) != (q != nullptr))
+    return MOE_EINVAL;
+  const int eb = n->dtype == MOE_F32 ? 4 : 2, wb = n->weight_dtype == MOE_F32 ? 4 : 2;
+  const void* rows[] = {x, residual, h_out, y};
+  const int64_t lds[] = {ldx, ld_residual, ld_h, ld_y};
+  uint64_t bits = reinterpret_cast<uintptr_t>(weight) & 15;
+  if (bits % wb || !al4(scales) || (q && ld_q < n->H)) return MOE_EINVAL;
+  for (int i = 0; i < 4; ++i) {
+    if (!rows[i]) continue;
+    if (lds[i] < n->H || lds[i] > kMaxRowStride || reinterpret_cast<uintptr_t>(rows[i]) % eb) return MOE_EINVAL;
+    bits |= (reinterpret_cast<uintptr_t>(rows[i]) | (uint64_t)lds[i] * eb) & 15;
+  }
+  if (q) {
+    if (ld_q > kMaxRowStride) return MOE_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(q) | (uint64_t)ld_q) & 7) bits |= 1;
+  }
+  // an output may replace a row that has been read only where both have one stride
+  if ((h_out && ((h_out == x && ld_h != ldx) || (h_out == residual && ld_h != ld_residual))) ||
+      (y && ((y == x && ld_y != ldx) || (y == residual && ld_y != ld_residual) || (y == h_out && ld_y != ld_h))))
+    return MOE_EINVAL;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.h_out = h_out;
+  a.y = y;
+  a.q = q;
+  a.scales = scales;
+  a.ldx = ldx;
+  a.ld_residual = ld_residual;
+  a.ld_h = ld_h;
+  a.ld_y = ld_y;
+  a.ld_q = ld_q;
+  a.T = T;
+  a.H = n->H;
+  a.dtype = n->dtype;
+  a.weight_f32 = n->weight_dtype == MOE_F32;
+  a.out8 = n->out8;
+  a.group = n->group;
+  a.aligned = bits == 0;
+  a.eps = n->eps;
+  a.weight_offset = n->weight_offset;
+  return hip_status(launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_project_workspace_bytes(int32_t N, int32_t K, int32_t R, int32_t T, size_t* bytes) {
+  if (!bytes || T < 0 || R < 0) return MOE_EINVAL;
+  if (!project_dims_ok(N, K) || (R && !rank_space_ok(R))) return MOE_EUNSUPPORTED;
+  *bytes = project_ws_bytes(N, K, R, std::max(T, 1));
+  return MOE_OK;
+}
+
+int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64_t ldx, uint16_t* y,
+                int64_t ldy, int32_t T, const moe_adapters* ad, const int32_t* adapter_of,
+                int32_t gemm, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || gemm < MOE_GEMM_AUTO || gemm > MOE_GEMM_WIDE || (ad != nullptr) != (adapter_of != nullptr))
+    return MOE_EINVAL;
+  if (!project_dims_ok(N, K)) return MOE_EUNSUPPORTED;
+  if (ad) {
+    if (ad->n < 1 || !ad->A || !ad->B || !al16(ad->A) || !al16(ad->B) || !al4(ad->ranks) ||
+        !al4(ad->scales) || !al4(adapter_of))
+      return MOE_EINVAL;
+    if (!rank_space_ok(ad->R)) return MOE_EUNSUPPORTED;
+  }
+  if (T == 0) return MOE_OK;
+  const int R = ad ? ad->R : 0;
+  const size_t need = project_ws_bytes(N, K, R, T);
+  if (!blob || !x || !y || !al16(blob) || !al16(x) || !al16(y) || ldx < K || ldy < N || ldx % 8 ||
+      ldy % 8 || ldx > kMaxRowStride || ldy > kMaxRowStride || (need && !ws) || !al16(ws))
+    return MOE_EINVAL;
+  if (ws_bytes < need) return MOE_EWORKSPACE;
+  ProjectArgs a{};
+  a.blob = static_cast<const uint8_t*>(blob) + kHeaderBytes;
+  a.x = x;
+  a.y = y;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.N = N;
+  a.K = K;
+  a.T = T;
+  a.gemm = gemm;
+  a.R = R;
+  if (ad) {
+    a.adapter_of = adapter_of;
+    a.A = ad->A;
+    a.B = ad->B;
+    a.ranks = ad->ranks;
+    a.scales = ad->scales;
+    a.n = ad->n;
+  }
+  a.ws = ws;
+  return hip_status(launch_project(a, static_cast<hipStream_t>(stream)));
 }
 
 const char* moe_strerror(int code) {

@@ -15,7 +15,9 @@
 //                   unique selected experts, then computes gate/up + SwiGLU
 //                   for (unique expert or shared expert) x (64-column wave
 //                   tile); a token set that picks one expert twice shares its
-//                   read; block 0 also writes the routing metadata
+//                   read; block 0 also writes the routing metadata (with a
+//                   routing rule other than the softmax top-k, a launch of
+//                   its own selects the experts first and they are read here)
 //   decode_down     per token and 16-column tile (32 from two tokens on) of
 //                   the output: the
 //                   down projection of the token's (token, slot) pairs, then
@@ -59,11 +61,18 @@ __device__ inline void load_route_logits(const DecodeArgs& a, float (&lv)[4]) {
 }
 
 // Requires kDecThreads threads; every thread must call it, with the logits
-// from load_route_logits().
+// from load_route_logits(), or, with GIVEN, with this thread's selected
+// expert and its weight in lv[0] and lv[1] (threads < T k).
+template <bool GIVEN>
 __device__ void decode_route(const DecodeArgs& a, const float (&lv)[4], DecodeRoute& r) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = a.E, P = a.T * kK;
-  if (wave < a.T) {
+  if constexpr (GIVEN) {
+    if (tid < P) {
+      r.sel_e[tid] = __float_as_int(lv[0]);
+      r.sel_w[tid] = lv[1];
+    }
+  } else if (wave < a.T) {
     const int t = wave;
     uint32_t key[4];
     float val[4];
@@ -248,7 +257,9 @@ __global__ __launch_bounds__(256) void decode_router_kernel(DecodeArgs a) {
 // logits are loaded first; the activations are staged in LDS while the
 // logits are in flight; after the routing each wave issues all of its
 // groups' weight loads at once.
-template <int GPW, int NH>
+// GIVEN: topk_idx and topk_w hold the routing already (a gate's), and it is
+// read instead of recomputed.
+template <int GPW, int NH, bool GIVEN>
 __global__ __launch_bounds__(kDecThreads) void decode_gateup_kernel(DecodeArgs a) {
   __shared__ DecodeRoute r;
   __shared__ float red[kDecWaves][kDecodeMaxT][NH][kWaveCols / 2];
@@ -283,18 +294,25 @@ __global__ __launch_bounds__(kDecThreads) void decode_gateup_kernel(DecodeArgs a
     for (int i = 0; i < kXPer; ++i)
       xv[i] = reinterpret_cast<const u32x4*>(a.x)[min(tid + i * kDecThreads, n16 - 1)];
     float lv[4];
-    load_route_logits(a, lv);
+    if constexpr (GIVEN) {
+      lv[0] = __int_as_float(a.topk_idx[min(tid, P - 1)]);
+      lv[1] = a.topk_w[min(tid, P - 1)];
+    } else {
+      load_route_logits(a, lv);
+    }
     // the activations go to LDS while the logits are still in flight
 #pragma unroll
     for (int i = 0; i < kXPer; ++i)
       if (tid + i * kDecThreads < n16) xs_l[tid + i * kDecThreads] = xv[i];
-    decode_route(a, lv, r);  // its barriers also publish xs_l
+    decode_route<GIVEN>(a, lv, r);  // its barriers also publish xs_l
   }
 
   if (blockIdx.x == 0) {
     if (tid < P) {
-      a.topk_idx[tid] = r.sel_e[tid];
-      a.topk_w[tid] = r.sel_w[tid];
+      if constexpr (!GIVEN) {
+        a.topk_idx[tid] = r.sel_e[tid];
+        a.topk_w[tid] = r.sel_w[tid];
+      }
       if (a.perm) {
         a.perm[r.pos_of_pair[tid]] = tid;
         a.inv_perm[tid] = r.pos_of_pair[tid];
@@ -540,30 +558,31 @@ __global__ __launch_bounds__(kDecThreads) void decode_down_kernel(DecodeArgs a) 
 namespace {
 
 // Smallest groups-per-wave instantiation that covers G groups with 8 waves.
-template <int NH>
+template <int NH, bool GIVEN>
 hipError_t launch_gateup_nh(int G, dim3 grid, hipStream_t s, const DecodeArgs& a) {
   if (G <= kDecWaves)
-    hipLaunchKernelGGL((decode_gateup_kernel<1, NH>), grid, dim3(kDecThreads), 0, s, a);
+    hipLaunchKernelGGL((decode_gateup_kernel<1, NH, GIVEN>), grid, dim3(kDecThreads), 0, s, a);
   else if (G <= 2 * kDecWaves)
-    hipLaunchKernelGGL((decode_gateup_kernel<2, NH>), grid, dim3(kDecThreads), 0, s, a);
+    hipLaunchKernelGGL((decode_gateup_kernel<2, NH, GIVEN>), grid, dim3(kDecThreads), 0, s, a);
   else if (G <= 4 * kDecWaves)
-    hipLaunchKernelGGL((decode_gateup_kernel<4, NH>), grid, dim3(kDecThreads), 0, s, a);
+    hipLaunchKernelGGL((decode_gateup_kernel<4, NH, GIVEN>), grid, dim3(kDecThreads), 0, s, a);
   else if (G <= 8 * kDecWaves)
-    hipLaunchKernelGGL((decode_gateup_kernel<8, NH>), grid, dim3(kDecThreads), 0, s, a);
+    hipLaunchKernelGGL((decode_gateup_kernel<8, NH, GIVEN>), grid, dim3(kDecThreads), 0, s, a);
   else
     return hipErrorInvalidValue;
   return hipSuccess;
 }
 
 // Half-tile blocks at one token, whole wave tiles from two tokens on.
+template <bool GIVEN>
 hipError_t launch_gateup(int G, int slots, int n_wt, int T, hipStream_t s, const DecodeArgs& a) {
-  if (T == 1) return launch_gateup_nh<1>(G, dim3((slots * n_wt * 2 + 15) / 16 * 16), s, a);
-  return launch_gateup_nh<2>(G, dim3(slots * n_wt), s, a);
+  if (T == 1) return launch_gateup_nh<1, GIVEN>(G, dim3((slots * n_wt * 2 + 15) / 16 * 16), s, a);
+  return launch_gateup_nh<2, GIVEN>(G, dim3(slots * n_wt), s, a);
 }
 
 }  // namespace
 
-hipError_t launch_decode(const DecodeArgs& a, hipStream_t s, hipEvent_t* ev) {
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t s, hipEvent_t* ev, const GateArgs* gate) {
   const PackGeom gu = pack_geom(a.I, a.H, 1);
   const PackGeom dn = pack_geom(a.H, a.I, 0);
   if (gu.G > kMaxGroups || dn.G > kMaxGroups || a.T > kDecodeMaxT || a.k != kK)
@@ -573,7 +592,21 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t s, hipEvent_t* ev) {
   if (ev && (e = hipEventRecord(ev[0], s)) != hipSuccess) return e;
   hipLaunchKernelGGL(decode_router_kernel, dim3(a.E), dim3(256), 0, s, a);
   if (ev && (e = hipEventRecord(ev[1], s)) != hipSuccess) return e;
-  if ((e = launch_gateup(gu.G, slots, gu.n_wt, a.T, s, a)) != hipSuccess) return e;
+  if (gate) {
+    GateArgs ga = *gate;
+    ga.partial = a.logits;
+    ga.splits = 1;
+    ga.rbias = nullptr;  // the router kernel added it
+    ga.logits_out = nullptr;
+    ga.topk_idx = a.topk_idx;
+    ga.topk_w = a.topk_w;
+    ga.chunk_hist = nullptr;
+    ga.T = a.T;
+    if ((e = launch_gate_topk(ga, s)) != hipSuccess) return e;
+  }
+  e = gate ? launch_gateup<true>(gu.G, slots, gu.n_wt, a.T, s, a)
+           : launch_gateup<false>(gu.G, slots, gu.n_wt, a.T, s, a);
+  if (e != hipSuccess) return e;
   if (ev && (e = hipEventRecord(ev[2], s)) != hipSuccess) return e;
   if (a.T == 1)
     hipLaunchKernelGGL(decode_down_kernel<1>, dim3(a.T * dn.n_wt * 4), dim3(kDecThreads), 0, s, a);  // (a multiple of 16)

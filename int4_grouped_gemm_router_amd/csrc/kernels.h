@@ -115,8 +115,61 @@ struct DecodeArgs {
   int T, H, I, E, k, block_m;
 };
 
+// ---- around the layer
+
+constexpr int kNormBf16 = 0, kNormF16 = 1, kNormF32 = 2;  // MOE_BF16, MOE_F16, MOE_F32
+constexpr int kOut8None = 0, kOut8Int8 = 1, kOut8E4m3 = 2;
+constexpr int kNormMaxH = 16384;
+
+struct NormArgs {
+  const void *x, *residual, *weight;  // residual: or null
+  void *h_out, *y, *q;                // each or null
+  float* scales;
+  int64_t ldx, ld_residual, ld_h, ld_y, ld_q;
+  int T, H, dtype, weight_f32, out8, group;
+  int aligned;  // 1: every row starts on 16 bytes (q: 8)
+  float eps, weight_offset;
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
+
+constexpr int kMaxGateK = 16;       // experts per token of a gate
+constexpr int kMaxGateGroups = 64;
+
+struct GateArgs {
+  const float* partial;   // [splits][T][E]
+  int splits;
+  const float* rbias;     // [E] or null: added to the logits
+  float* logits_out;      // [T][E] or null
+  const float* balance;   // [E] or null: added to the scores for selection
+  int32_t* topk_idx;      // [T][k]
+  float* topk_w;          // [T][k]
+  int32_t* chunk_hist;    // [chunks][E] (zeroed beforehand) or null
+  int T, E, k, sigmoid, n_groups, topk_groups, group_top2, renorm;
+  float scale;
+};
+hipError_t launch_gate_topk(const GateArgs& a, hipStream_t s);
+
+constexpr int kMaxRank = 128;
+
+struct ProjectArgs {
+  const uint8_t* blob;       // one matrix [N][K] (past the header)
+  const uint16_t* x;         // [T], row stride ldx
+  uint16_t* y;               // [T], row stride ldy
+  const int32_t* adapter_of; // [T] or null: no adapters
+  const uint16_t *A, *B;     // [n][R][K], [n][N][R]
+  const int32_t* ranks;      // [n] or null
+  const float* scales;       // [n] or null
+  void* ws;                  // project_ws_bytes
+  int64_t ldx, ldy;
+  int N, K, T, n, R, gemm;
+};
+size_t project_ws_bytes(int N, int K, int R, int T);
+hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
+
 // ev (optional): four events recorded before each of the three launches and after the last.
-// Requires k == 8.
-hipError_t launch_decode(const DecodeArgs& a, hipStream_t s, hipEvent_t* ev = nullptr);
+// gate (optional): a routing rule in the place of the softmax top-k (its sizes
+// are a's; no events then). Requires k == 8.
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t s, hipEvent_t* ev = nullptr,
+                         const GateArgs* gate = nullptr);
 
 }  // namespace moe
