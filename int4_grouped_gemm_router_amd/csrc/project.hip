@@ -3,16 +3,36 @@
 //
 //   z[t] = scales[a] * A_a x[t],  y[t] = W x[t] + B_a z[t],  a = adapter_of[t]
 //
-// Two launches: the adapters' first product into the workspace, then the
-// projection, whose epilogue adds the second product.
+// Two launches: the adapters' first product z into the workspace (fp32 sums,
+// kept as two bf16 halves: 16 significant bits), then the projection, in
+// whose epilogue B_a z is a few more matrix-core operations per tile.
+//
+// Tokens are never sorted by adapter: a 16-token tile walks over the distinct
+// adapters of its tokens (one in a prompt, up to 16 in a batch of single
+// tokens, where every adapter's bytes have to be read anyway), and a token
+// takes the results of its own adapter by selection, so that another
+// adapter's NaN or infinity never reaches it.
+//
+// The projection has two kernels:
+//   project_split_kernel  exact codes; a block's eight waves split K and join
+//                         through LDS: few rows, where the weights' bytes and
+//                         the latency of one pass count
+//   project_tile_kernel   256 x 256 tiles; each weight is expanded once per
+//                         tile to bf16 and shared through LDS by its 256
+//                         rows: many rows, where the matrix cores count
 #include "kernels.h"
+#include "wide_expand.h"
 
 namespace moe {
 
 namespace {
 
+constexpr int kPWaves = 8;
+constexpr int kPThreads = 64 * kPWaves;
+
+// The adapter of token t, or -1.
 __device__ inline int adapter_at(const ProjectArgs& a, int t) {
-  const int i = a.adapter_of[t];
+  const int i = t < a.T ? a.adapter_of[t] : -1;
   return i >= 0 && i < a.n ? i : -1;
 }
 
@@ -20,81 +40,433 @@ __device__ inline int rank_of(const ProjectArgs& a, int i) {
   return a.ranks ? min(max(a.ranks[i], 0), a.R) : a.R;
 }
 
+// z's two halves [T][R]: the bf16 value nearest to z, and that of the rest.
+__device__ inline uint16_t* z_hi(const ProjectArgs& a) { return static_cast<uint16_t*>(a.ws); }
+__device__ inline uint16_t* z_lo(const ProjectArgs& a) { return z_hi(a) + (int64_t)a.T * a.R; }
+
+// Eight consecutive ranks from r0 of row `row` of a [rows][R] array, zero
+// from rank `have` (<= R) on.
+__device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int r0, int have) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  const int left = have - r0;
+  if (left > 0) {
+    v = *reinterpret_cast<const u32x4*>(base + row * R + r0);
+    if (left < 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = left >= 2 * j + 2 ? v[j] : (left == 2 * j + 1 ? v[j] & 0xFFFFu : 0u);
+    }
+  }
+  return v;
+}
+
 }  // namespace
 
-// z [T][R] fp32. Grid: T blocks of four waves; wave w takes ranks w, w + 4, ...
-__global__ __launch_bounds__(256) void adapter_down_kernel(ProjectArgs a) {
-  const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i = adapter_at(a, t);
-  const int rank = i >= 0 ? rank_of(a, i) : 0;
-  const float scale = i >= 0 && a.scales ? a.scales[i] : 1.f;
-  const uint16_t* x = a.x + (int64_t)t * a.ldx;
-  for (int r = wave; r < a.R; r += 4) {
-    float v = 0.f;
-    if (r < rank) {
-      const uint16_t* A = a.A + ((int64_t)i * a.R + r) * a.K;
-      for (int c = 2 * lane; c < a.K; c += 128) {
-        const uint32_t xv = *reinterpret_cast<const uint32_t*>(x + c);
-        const uint32_t av = *reinterpret_cast<const uint32_t*>(A + c);
-        v = __builtin_fmaf(bf16lo(xv), bf16lo(av), v);
-        v = __builtin_fmaf(bf16hi(xv), bf16hi(av), v);
+// The adapters' first product. Block: one tile of 16 tokens, 16 ranks, and
+// every `entries`-th distinct adapter of the tile; the eight waves split K.
+// Grid: token tiles x rank tiles x entries (entries fastest).
+__global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, int entries) {
+  __shared__ float red[kPWaves][16][17];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, kb = lane >> 4;
+  const int n_rt = (a.R + 15) / 16;
+  const int entry = blockIdx.x % entries, rt = blockIdx.x / entries % n_rt;
+  const int t0 = blockIdx.x / entries / n_rt * 16;
+  const int mine = adapter_at(a, t0 + c16);
+  const uint16_t* x = a.x + (int64_t)min(t0 + c16, a.T - 1) * a.ldx + 8 * kb;
+  const int chunks = a.K / 128;
+  uint64_t rem = __ballot(mine >= 0) & 0xFFFFull;
+  for (int j = 0; rem; ++j) {
+    const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
+    const uint64_t same = __ballot(mine == ad) & 0xFFFFull;
+    rem &= ~same;
+    if (j % entries != entry) continue;
+    const int rank = rank_of(a, ad);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    if (16 * rt < rank) {
+      const uint16_t* A = a.A + ((int64_t)ad * a.R + min(16 * rt + c16, a.R - 1)) * a.K + 8 * kb;
+      for (int c = wave; c < chunks; c += kPWaves) {
+        u32x4 xv[4], av[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          xv[s] = *reinterpret_cast<const u32x4*>(x + 128 * c + 32 * s);
+          av[s] = *reinterpret_cast<const u32x4*>(A + 128 * c + 32 * s);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) acc = mfma16(xv[s], av[s], acc);
       }
-      v = wave_sum(v) * scale;
     }
-    if (lane == 0) static_cast<float*>(a.ws)[(int64_t)t * a.R + r] = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][4 * kb + i][c16] = acc[i];
+    __syncthreads();
+    if (tid < 256) {
+      const int row = tid >> 4, r = 16 * rt + (tid & 15);
+      if ((same >> row & 1) && r < a.R) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPWaves; ++w) v += red[w][row][tid & 15];
+        if (a.scales) v *= a.scales[ad];
+        if (r >= rank) v = 0.f;
+        const uint16_t hi = f2bf(v);
+        const int64_t at = (int64_t)(t0 + row) * a.R + r;
+        z_hi(a)[at] = hi;
+        z_lo(a)[at] = f2bf(v - bf16f(hi));
+      }
+    }
+    __syncthreads();
   }
 }
 
-// Grid: (N / 64, ceil(T / 16)); block: one wave, 16 tokens by 64 columns.
-// Exact codes: acc += s * x.(128 + q) + (b - 128 s) * sum(x) per group.
-__global__ __launch_bounds__(64) void project_kernel(ProjectArgs a) {
-  const int lane = threadIdx.x, c16 = lane & 15, kb = lane >> 4;
-  const int wt = blockIdx.x, t0 = blockIdx.y * 16;
+// Few rows: a block owns 16 MS tokens and 16 CT columns; wave w takes the
+// 64-input groups w, w + 8, ... with its operands straight from memory (the
+// next group's loads in flight while one is multiplied), and the eight
+// partial tiles are added in LDS in a fixed order. With the codes expanded to
+// the exact bf16 values 128 + q, per group and column
+//   acc += s * x.(128 + q) + (b - 128 s) * sum(x)
+// which is x . (q s + b) with the weights used exactly. The distinct adapters
+// of the tokens are dealt out over the waves too: their B_a z goes to a tile
+// of its own in LDS, added last, so a token's result does not depend on the
+// others.
+template <int MS, int CT>
+struct SplitLds {
+  static constexpr int kStride = 16 * CT + 4;  // floats; the pad spreads the rows over the banks
+  float red[kPWaves + 1][16 * MS][kStride];    // the waves' tiles, then the adapters'
+};
+
+template <int MS, int CT>
+__global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a) {
+  __shared__ SplitLds<MS, CT> L;
+  constexpr int kSub = 4 / CT;  // blocks per 64-column wave tile
+  constexpr int NW = CT == 4 ? 2 : 1;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, kb = lane >> 4;
   const PackGeom geom = pack_geom(a.N, a.K, 0);
   const int G = geom.G;
+  const int row_tiles = (a.T + 16 * MS - 1) / (16 * MS);
+  // XCD x (blocks go to XCD b % 8 in turn) takes a contiguous range of units,
+  // row tiles fastest, so the row tiles of one column tile share its weights
+  // in that XCD's L2
+  const int units = row_tiles * geom.n_wt * kSub;
+  const int xcd = blockIdx.x & 7;
+  const int u0 = (int)((int64_t)units * xcd / 8), u1 = (int)((int64_t)units * (xcd + 1) / 8);
+  const int u = u0 + (blockIdx.x >> 3);
+  if (u >= u1) return;
+  const int t0 = u % row_tiles * (16 * MS), cb = u / row_tiles;
+  const int wt = cb / kSub, ct0 = CT * (cb % kSub);
   const ExpandConsts xk = expand_consts();
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  const uint16_t* x = a.x + (int64_t)min(t0 + c16, a.T - 1) * a.ldx + 8 * kb;
-  const uint8_t* nib = a.blob + geom.nib_off + (int64_t)wt * G * kNibBytes + lane * 16;
+
+  const uint16_t* x[MS];
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms) x[ms] = a.x + (int64_t)min(t0 + 16 * ms + c16, a.T - 1) * a.ldx + 8 * kb;
+  const uint8_t* nib = a.blob + geom.nib_off + (int64_t)wt * G * kNibBytes + lane * 16 + (ct0 >> 1) * 1024 + (ct0 & 1) * 8;
   const uint8_t* sbp = a.blob + geom.sb_off + (int64_t)wt * G * kSbBytes + c16 * 16;
-  f32x4 acc[4];
+
+  u32x4 xa[2][MS][2], w[2][NW], sb[2];
+  auto load = [&](int g, int s) {
+    g = min(g, G - 1);
+    if constexpr (CT == 1) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(nib + (int64_t)g * kNibBytes);
+      w[s][0] = u32x4{v.x, v.y, 0u, 0u};
+    } else {
 #pragma unroll
-  for (int ct = 0; ct < 4; ++ct) acc[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int g = 0; g < G; ++g) {
-    const u32x4 a0 = *reinterpret_cast<const u32x4*>(x + g * kGroup);
-    const u32x4 a1 = *reinterpret_cast<const u32x4*>(x + g * kGroup + 32);
-    const u32x4 w0 = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes);
-    const u32x4 w1 = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes + 1024);
-    const u32x4 sbv = *reinterpret_cast<const u32x4*>(sbp + (int64_t)g * kSbBytes);
-    const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    const float sc[4] = {bf16lo(sbv.x), bf16hi(sbv.x), bf16lo(sbv.y), bf16hi(sbv.y)};
-    const float bi[4] = {bf16lo(sbv.z), bf16hi(sbv.z), bf16lo(sbv.w), bf16hi(sbv.w)};
-    f32x4 xs = mfma16(a0, ones, f32x4{0.f, 0.f, 0.f, 0.f});
-    xs = mfma16(a1, ones, xs);
+      for (int h = 0; h < NW; ++h) w[s][h] = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes + 1024 * h);
+    }
+    sb[s] = *reinterpret_cast<const u32x4*>(sbp + (int64_t)g * kSbBytes);
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      f32x4 p = mfma16(a0, expand_codes(words[2 * ct], xk), f32x4{0.f, 0.f, 0.f, 0.f});
-      p = mfma16(a1, expand_codes(words[2 * ct + 1], xk), p);
-      const float bp = bi[ct] - 128.0f * sc[ct];
+    for (int ms = 0; ms < MS; ++ms) {
+      xa[s][ms][0] = *reinterpret_cast<const u32x4*>(x[ms] + g * kGroup);
+      xa[s][ms][1] = *reinterpret_cast<const u32x4*>(x[ms] + g * kGroup + 32);
+    }
+  };
+  load(wave, 0);
+  load(wave + kPWaves, 1);
+
+  // ---- B_a z of the tokens with an adapter
+  uint64_t with = 0;  // rows of the block with an adapter
+  if (a.adapter_of) {
+    const int mine = lane < 16 * MS ? adapter_at(a, t0 + lane) : -1;
+    with = __ballot(mine >= 0);
+    uint64_t rem = with;
+    for (int j = 0; rem; ++j) {
+      const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
+      const uint64_t same = __ballot(mine == ad);
+      rem &= ~same;
+      if (j % kPWaves != wave) continue;
+      const int rank = rank_of(a, ad);
+      f32x4 d[MS][CT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[ct][i] = __builtin_fmaf(bp, xs[i], __builtin_fmaf(sc[ct], p[i], acc[ct][i]));
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) d[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < rank; s += 32) {
+        u32x4 bv[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          bv[ct] = rank_chunk(a.B, (int64_t)ad * a.N + 64 * wt + 16 * (ct0 + ct) + c16, a.R, s + 8 * kb, rank);
+#pragma unroll
+        for (int ms = 0; ms < MS; ++ms) {
+          if (same >> (16 * ms) & 0xFFFFull) {
+            const int64_t t = min(t0 + 16 * ms + c16, a.T - 1);
+            const u32x4 zh = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
+            const u32x4 zl = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) d[ms][ct] = mfma16(zl, bv[ct], mfma16(zh, bv[ct], d[ms][ct]));
+          }
+        }
+      }
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * ms + 4 * kb + i;
+          if (same >> row & 1) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) L.red[kPWaves][row][16 * ct + c16] = d[ms][ct][i];
+          }
+        }
+    }
+  }
+
+  // ---- W x
+  f32x4 acc[MS][CT];
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](int s) {
+    const uint32_t words[8] = {w[s][0].x, w[s][0].y, w[s][0].z, w[s][0].w, w[s][NW - 1].x, w[s][NW - 1].y,
+                               w[s][NW - 1].z, w[s][NW - 1].w};
+    f32x4 xs[MS];
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms)
+      xs[ms] = mfma16(xa[s][ms][1], ones, mfma16(xa[s][ms][0], ones, f32x4{0.f, 0.f, 0.f, 0.f}));
+    // this block's scales and biases: pairs of columns tiles per word
+    const uint32_t sw0 = CT == 4 || ct0 < 2 ? sb[s].x : sb[s].y, bw0 = CT == 4 || ct0 < 2 ? sb[s].z : sb[s].w;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const uint32_t sw = ct < 2 ? sw0 : sb[s].y, bw = ct < 2 ? bw0 : sb[s].w;
+      const bool hi = CT == 1 ? (ct0 & 1) : (ct & 1);
+      const float sc = hi ? bf16hi(sw) : bf16lo(sw), bi = hi ? bf16hi(bw) : bf16lo(bw);
+      const float bp = bi - 128.0f * sc;
+      const u32x4 b0 = expand_codes(words[2 * ct], xk), b1 = expand_codes(words[2 * ct + 1], xk);
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms) {
+        f32x4 p = mfma16(xa[s][ms][0], b0, f32x4{0.f, 0.f, 0.f, 0.f});
+        p = mfma16(xa[s][ms][1], b1, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[ms][ct][i] = __builtin_fmaf(bp, xs[ms][i], __builtin_fmaf(sc, p[i], acc[ms][ct][i]));
+      }
+    }
+  };
+  for (int g = wave; g < G; g += 2 * kPWaves) {
+    step(0);
+    load(g + 2 * kPWaves, 0);
+    if (g + kPWaves < G) step(1);
+    load(g + 3 * kPWaves, 1);
+  }
+
+  // ---- join
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) L.red[wave][16 * ms + 4 * kb + i][16 * ct + c16] = acc[ms][ct][i];
+  __syncthreads();
+  constexpr int kPairs = 8 * CT;  // column pairs per row
+  for (int p = tid; p < 16 * MS * kPairs; p += kPThreads) {
+    const int row = p / kPairs, c = 2 * (p % kPairs);
+    if (t0 + row >= a.T) break;
+    float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPWaves; ++q) {
+      const f32x2 v = *reinterpret_cast<const f32x2*>(&L.red[q][row][c]);
+      v0 += v.x;
+      v1 += v.y;
+    }
+    if (with >> row & 1) {
+      const f32x2 v = *reinterpret_cast<const f32x2*>(&L.red[kPWaves][row][c]);
+      v0 += v.x;
+      v1 += v.y;
+    }
+    *reinterpret_cast<uint32_t*>(a.y + (int64_t)(t0 + row) * a.ldy + 64 * wt + 16 * ct0 + c) = pack_bf16x2(v0, v1);
+  }
+}
+
+// Many rows: a block of eight waves owns 32 RS tokens x 256 columns; wave w
+// owns token half w / 4 (16 RS tokens) and the 64 columns of wave tile w % 4.
+// Per 64-input group the activation rows arrive through registers and the
+// weights' codes are expanded once (each wave half a wave tile) to bf16
+// w = q s + b; both go to a two-stage LDS buffer in operand order, and the
+// matrix cores form w . x (the weights as the first operand, so that a lane
+// ends up with four consecutive columns of one token and stores them
+// directly). Waves w and w + 4 share a SIMD: one expands the next group
+// before its matrix-core operations and the other after them, so that one's
+// expansion runs under the other's products.
+template <int RS>
+struct TileLds {
+  u32x4 x[2][2 * RS][2][64];  // [stage][16-token subtile][k half][lane]
+  u32x4 w[2][4][8][64];       // [stage][wave tile][2 ct + k half][lane]
+};
+
+template <int RS>
+__global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs a) {
+  __shared__ TileLds<RS> L;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, kb = lane >> 4;
+  const int wr = wave >> 2, wc = wave & 3;
+  const PackGeom geom = pack_geom(a.N, a.K, 0);
+  const int G = geom.G;
+  const int row_tiles = (a.T + 32 * RS - 1) / (32 * RS), col_tiles = (geom.n_wt + 3) / 4;
+  const int units = row_tiles * col_tiles;
+  const int xcd = blockIdx.x & 7;
+  const int u0 = (int)((int64_t)units * xcd / 8), u1 = (int)((int64_t)units * (xcd + 1) / 8);
+  const int u = u0 + (blockIdx.x >> 3);
+  if (u >= u1) return;
+  const int t0 = u % row_tiles * (32 * RS), wt0 = u / row_tiles * 4;
+
+  // activations: wave w stages the fragments 2 RS/4... of subtiles
+  constexpr int kFrags = 4 * RS / kPWaves;  // per wave: (subtile, k half) pairs
+  const uint16_t* xs[kFrags];
+#pragma unroll
+  for (int f = 0; f < kFrags; ++f) {
+    const int q = wave * kFrags + f;
+    xs[f] = a.x + (int64_t)min(t0 + 16 * (q >> 1) + c16, a.T - 1) * a.ldx + 32 * (q & 1) + 8 * kb;
+  }
+  // weights: wave w expands half w & 1 (column tiles 2 (w & 1), + 1) of wave tile w >> 1
+  const int ewt = min(wt0 + (wave >> 1), geom.n_wt - 1), eh = wave & 1;
+  const uint8_t* nib = a.blob + geom.nib_off + (int64_t)ewt * G * kNibBytes + 1024 * eh + lane * 16;
+  const uint8_t* sbp = a.blob + geom.sb_off + (int64_t)ewt * G * kSbBytes + c16 * 16;
+  const WideExpand xk = wide_expand_consts();
+
+  u32x4 ax[kFrags], cw[2], sbv[2];
+  auto load_x = [&](int g) {
+    g = min(g, G - 1);
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) ax[f] = *reinterpret_cast<const u32x4*>(xs[f] + g * kGroup);
+  };
+  auto store_x = [&](int st) {
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      const int q = wave * kFrags + f;
+      L.x[st][q >> 1][q & 1][lane] = ax[f];
+    }
+  };
+  auto load_w = [&](int g, int s) {
+    g = min(g, G - 1);
+    cw[s] = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes);
+    sbv[s] = *reinterpret_cast<const u32x4*>(sbp + (int64_t)g * kSbBytes);
+  };
+  auto expand = [&](int s, int st) {
+    const uint32_t sp = eh ? sbv[s].y : sbv[s].x, bp = eh ? sbv[s].w : sbv[s].z;
+    const ColAffine c0 = col_affine(bf16lo(sp), bf16lo(bp)), c1 = col_affine(bf16hi(sp), bf16hi(bp));
+    u32x4* o = &L.w[st][wave >> 1][4 * eh][lane];
+    o[0] = expand_bf16(cw[s].x, c0, xk);
+    o[64] = expand_bf16(cw[s].y, c0, xk);
+    o[128] = expand_bf16(cw[s].z, c1, xk);
+    o[192] = expand_bf16(cw[s].w, c1, xk);
+  };
+
+  f32x4 acc[RS][4];
+#pragma unroll
+  for (int ms = 0; ms < RS; ++ms)
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  load_x(0);
+  load_w(0, 0);
+  load_w(1, 1);
+  store_x(0);
+  expand(0, 0);
+  lds_barrier();
+  // one group: stage S holds it; the codes of group g + 1 are in slot 1 - S
+  auto step = [&](int g, auto S_) {
+    constexpr int S = decltype(S_)::value;
+    load_x(g + 1);
+    load_w(g + 2, S);
+    if (wr == 0) expand(1 - S, 1 - S);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4 bw[4];
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct + ks][lane];
+#pragma unroll
+      for (int ms = 0; ms < RS; ++ms) {
+        const u32x4 av = L.x[S][wr * RS + ms][ks][lane];
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ct], av, acc[ms][ct]);
+      }
+    }
+    if (wr == 1) expand(1 - S, 1 - S);
+    store_x(1 - S);
+    // the next group is in LDS, and every wave is done with this one's stage
+    lds_barrier();
+  };
+  for (int g = 0; g < G; g += 2) {  // G is even
+    step(g, std::integral_constant<int, 0>{});
+    step(g + 1, std::integral_constant<int, 1>{});
+  }
+
+  // ---- B_a z, then y; lane: token c16 of each subtile, columns 4 kb .. 4 kb + 3 of each column tile
+  const int wt = wt0 + wc;
+  if (wt >= geom.n_wt) return;
+  const int tw = t0 + wr * 16 * RS;
+  if (a.adapter_of) {
+    int mine[RS];
+#pragma unroll
+    for (int ms = 0; ms < RS; ++ms) mine[ms] = adapter_at(a, tw + 16 * ms + c16);
+    for (int s = 0; s < a.R; s += 32) {
+      u32x4 zh[RS], zl[RS];
+#pragma unroll
+      for (int ms = 0; ms < RS; ++ms) {
+        const int64_t t = min(tw + 16 * ms + c16, a.T - 1);
+        zh[ms] = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
+        zl[ms] = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
+      }
+      int held = -1;
+      u32x4 bv[4];
+#pragma unroll
+      for (int ms = 0; ms < RS; ++ms) {
+        uint64_t rem = __ballot(mine[ms] >= 0);
+        while (rem) {
+          const int ad = __builtin_amdgcn_readlane(mine[ms], __builtin_ctzll(rem));
+          const bool is = mine[ms] == ad;
+          const uint64_t same = __ballot(is);
+          rem &= ~same;
+          if (ad != held) {
+            held = ad;
+            const int rank = rank_of(a, ad);
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct)
+              bv[ct] = rank_chunk(a.B, (int64_t)ad * a.N + 64 * wt + 16 * ct + c16, a.R, s + 8 * kb, rank);
+          }
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct) {
+            const f32x4 d = mfma16(bv[ct], zl[ms], mfma16(bv[ct], zh[ms], f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[ms][ct][i] = is ? acc[ms][ct][i] + d[i] : acc[ms][ct][i];
+          }
+        }
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 4 * kb + i;
-    if (t >= a.T) continue;
-    const int ad = a.adapter_of ? adapter_at(a, t) : -1;
-    const int rank = ad >= 0 ? rank_of(a, ad) : 0;
+  for (int ms = 0; ms < RS; ++ms) {
+    const int t = tw + 16 * ms + c16;
+    if (t < a.T) {
+      uint16_t* y = a.y + (int64_t)t * a.ldy + 64 * wt + 4 * kb;
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      const int n = 64 * wt + 16 * ct + c16;
-      float v = acc[ct][i];
-      if (ad >= 0) {
-        const uint16_t* B = a.B + ((int64_t)ad * a.N + n) * a.R;
-        for (int r = 0; r < rank; ++r) v = __builtin_fmaf(static_cast<float*>(a.ws)[(int64_t)t * a.R + r], bf16f(B[r]), v);
+      for (int ct = 0; ct < 4; ++ct) {
+        u32x2 o;
+        o.x = pack_bf16x2(acc[ms][ct][0], acc[ms][ct][1]);
+        o.y = pack_bf16x2(acc[ms][ct][2], acc[ms][ct][3]);
+        *reinterpret_cast<u32x2*>(y + 16 * ct) = o;
       }
-      a.y[(int64_t)t * a.ldy + n] = f2bf(v);
     }
   }
 }
@@ -103,10 +475,42 @@ size_t project_ws_bytes(int /*N*/, int /*K*/, int R, int T) {
   return ((size_t)T * R * 4 + 255) / 256 * 256;
 }
 
-hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
-  if (a.adapter_of) hipLaunchKernelGGL(adapter_down_kernel, dim3(a.T), dim3(256), 0, s, a);
-  hipLaunchKernelGGL(project_kernel, dim3(a.N / 64, (a.T + 15) / 16), dim3(64), 0, s, a);
+namespace {
+
+template <int MS, int CT>
+hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
+  const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * (a.N / 64) * (4 / CT);
+  const int64_t blocks = (units + 7) / 8 * 8;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((project_split_kernel<MS, CT>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
+}
+
+template <int RS>
+hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
+  const int64_t units = (int64_t)((a.T + 32 * RS - 1) / (32 * RS)) * ((a.N + 255) / 256);
+  const int64_t blocks = (units + 7) / 8 * 8;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(project_tile_kernel<RS>, dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
+  if (a.adapter_of) {
+    const int64_t tiles = (int64_t)((a.T + 15) / 16) * ((a.R + 15) / 16);
+    int entries = min(min(16, a.n), a.T);
+    while (entries > 1 && tiles * entries > 1024) entries = (entries + 1) / 2;
+    if (tiles * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * entries)), dim3(kPThreads), 0, s, a, entries);
+  }
+  const bool tile = a.gemm == 2 || (a.gemm == 0 && a.T >= 1024);
+  if (tile) return (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 128 ? launch_tile<8>(a, s) : launch_tile<4>(a, s);
+  if (a.T <= 16) return launch_split<1, 1>(a, s);
+  if (a.T <= 32) return launch_split<2, 1>(a, s);
+  if (a.T <= 64) return launch_split<2, 2>(a, s);
+  return launch_split<2, 4>(a, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,48 @@
+// int4 codes -> bf16 weights w = q s + b with one rounding, as the wide GEMMs
+// and the tiled projection feed the matrix cores.
+#pragma once
+
+#include "device.h"
+
+namespace moe {
+
+struct WideExpand {
+  uint32_t mask_lo, magic;  // 0x000F000F, fp16 1024 | 1024
+};
+
+// Hidden from the optimiser so that (w & mask) | magic is selected as one
+// bitwise three-input op with register operands.
+__device__ inline WideExpand wide_expand_consts() {
+  WideExpand k;
+  asm volatile("v_mov_b32 %0, 0x000F000F" : "=v"(k.mask_lo));
+  asm volatile("v_mov_b32 %0, 0x64006400" : "=v"(k.magic));
+  return k;
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// Per column and group: the scale s and the offset b - 1024 s (exact in fp32
+// for the bf16 inputs' exponent spans).
+struct ColAffine {
+  float s, c;
+};
+
+__device__ inline ColAffine col_affine(float s, float b) {
+  return ColAffine{s, __builtin_fmaf(-1024.0f, s, b)};
+}
+
+// One packed word (eight codes of one column, k = 8 consecutive inputs, code
+// o at nibble (o & 1) * 4 + (o >> 1)) -> the eight bf16 weights in k order:
+// ((w >> 4d) & 0x000F000F) | 0x64006400 is the fp16 pair (1024 + q_2d,
+// 1024 + q_2d+1), and (1024 + q) s + (b - 1024 s) = q s + b with one rounding.
+__device__ inline u32x4 expand_bf16(uint32_t w, const ColAffine& c, const WideExpand& k) {
+  u32x4 r;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const f16x2 h = __builtin_bit_cast(f16x2, ((w >> (4 * d)) & k.mask_lo) | k.magic);
+    r[d] = pack_bf16x2(__builtin_fmaf((float)h.x, c.s, c.c), __builtin_fmaf((float)h.y, c.s, c.c));
+  }
+  return r;
+}
+
+}  // namespace moe
