@@ -71,16 +71,6 @@ struct WideLds {
 // epilogue transposes through LDS with differently typed accesses).
 __device__ inline void wide_fence() { asm volatile("" ::: "memory"); }
 
-// Buffer resources: 32-bit offsets from a uniform base, and reads past
-// `bytes` return zero instead of touching memory.
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ inline rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-__device__ inline u32x4 bload(rsrc_t r, uint32_t voff, uint32_t soff) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
-}
-
 }  // namespace
 
 // Grid: 8 * n_tiles * ceil(max_slots / 8) blocks of 512 threads. Block b

@@ -328,39 +328,47 @@ __global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs 
   const int u0 = (int)((int64_t)units * xcd / 8), u1 = (int)((int64_t)units * (xcd + 1) / 8);
   const int u = u0 + (blockIdx.x >> 3);
   if (u >= u1) return;
-  const int t0 = u % row_tiles * (32 * RS), wt0 = u / row_tiles * 4;
+  const int ct0 = u % col_tiles, t0 = u / col_tiles * (32 * RS), wt0 = 4 * ct0;
+  // the groups are taken in turn from a start that depends on the column
+  // tile: rows a multiple of 4 KB apart put one group of every row into one
+  // L2 channel, and blocks that all read the same group wait for it
+  int gx = 2 * ct0 % G, gw = gx;  // next group to load: activations, codes
 
-  // activations: wave w stages the fragments 2 RS/4... of subtiles
-  constexpr int kFrags = 4 * RS / kPWaves;  // per wave: (subtile, k half) pairs
-  const uint16_t* xs[kFrags];
+  // activations: wave w stages both k halves of RS / 4 subtiles
+  constexpr int kXRows = RS / 4;
+  const int rows = min(32 * RS, a.T - t0);
+  const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
+  uint32_t xoff[kXRows];
 #pragma unroll
-  for (int f = 0; f < kFrags; ++f) {
-    const int q = wave * kFrags + f;
-    xs[f] = a.x + (int64_t)min(t0 + 16 * (q >> 1) + c16, a.T - 1) * a.ldx + 32 * (q & 1) + 8 * kb;
-  }
+  for (int f = 0; f < kXRows; ++f)
+    xoff[f] = (uint32_t)min(16 * (wave * kXRows + f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
   // weights: wave w expands half w & 1 (column tiles 2 (w & 1), + 1) of wave tile w >> 1
   const int ewt = min(wt0 + (wave >> 1), geom.n_wt - 1), eh = wave & 1;
-  const uint8_t* nib = a.blob + geom.nib_off + (int64_t)ewt * G * kNibBytes + 1024 * eh + lane * 16;
-  const uint8_t* sbp = a.blob + geom.sb_off + (int64_t)ewt * G * kSbBytes + c16 * 16;
+  const rsrc_t wres = make_rsrc(a.blob, (uint32_t)geom.expert_bytes);
+  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)ewt * G * kNibBytes + 1024 * eh);
+  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)ewt * G * kSbBytes);
   const WideExpand xk = wide_expand_consts();
 
-  u32x4 ax[kFrags], cw[2], sbv[2];
-  auto load_x = [&](int g) {
-    g = min(g, G - 1);
+  u32x4 ax[kXRows][2], cw[2], sbv[2];
+  auto load_x = [&]() {
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f) ax[f] = *reinterpret_cast<const u32x4*>(xs[f] + g * kGroup);
+    for (int f = 0; f < kXRows; ++f) {
+      ax[f][0] = bload(xres, xoff[f], (uint32_t)gx * (2 * kGroup));
+      ax[f][1] = bload(xres, xoff[f] + 64, (uint32_t)gx * (2 * kGroup));
+    }
+    gx = gx + 1 < G ? gx + 1 : 0;
   };
   auto store_x = [&](int st) {
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f) {
-      const int q = wave * kFrags + f;
-      L.x[st][q >> 1][q & 1][lane] = ax[f];
+    for (int f = 0; f < kXRows; ++f) {
+      L.x[st][wave * kXRows + f][0][lane] = ax[f][0];
+      L.x[st][wave * kXRows + f][1][lane] = ax[f][1];
     }
   };
-  auto load_w = [&](int g, int s) {
-    g = min(g, G - 1);
-    cw[s] = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes);
-    sbv[s] = *reinterpret_cast<const u32x4*>(sbp + (int64_t)g * kSbBytes);
+  auto load_w = [&](int s) {
+    cw[s] = bload(wres, lane * 16, nbase + (uint32_t)gw * kNibBytes);
+    sbv[s] = bload(wres, c16 * 16, sbase + (uint32_t)gw * kSbBytes);
+    gw = gw + 1 < G ? gw + 1 : 0;
   };
   auto expand = [&](int s, int st) {
     const uint32_t sp = eh ? sbv[s].y : sbv[s].x, bp = eh ? sbv[s].w : sbv[s].z;
@@ -378,38 +386,48 @@ __global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs 
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  load_x(0);
-  load_w(0, 0);
-  load_w(1, 1);
+  load_x();
+  load_w(0);
+  load_w(1);
   store_x(0);
   expand(0, 0);
   lds_barrier();
   // one group: stage S holds it; the codes of group g + 1 are in slot 1 - S
-  auto step = [&](int g, auto S_) {
+  auto step = [&](auto S_) {
     constexpr int S = decltype(S_)::value;
-    load_x(g + 1);
-    load_w(g + 2, S);
+    load_x();
+    load_w(S);
     if (wr == 0) expand(1 - S, 1 - S);
+    // operands stream from LDS: a k half's four weight fragments together,
+    // the activation fragments one ahead of their products (the scheduling
+    // fences keep that order; without them the compiler gathers the reads
+    // and spills)
+    u32x4 bw[4], av[2];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      u32x4 bw[4];
+    for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct][lane];
+    av[0] = L.x[S][wr * RS][0][lane];
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct + ks][lane];
+    for (int f = 0; f < 2 * RS; ++f) {
+      const int ks = f / RS, ms = f % RS;
+      if (f + 1 < 2 * RS) av[(f + 1) & 1] = L.x[S][wr * RS + (f + 1) % RS][(f + 1) / RS][lane];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int ms = 0; ms < RS; ++ms) {
-        const u32x4 av = L.x[S][wr * RS + ms][ks][lane];
+      for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ct], av[f & 1], acc[ms][ct]);
+      if (f == RS - 1) {
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ct], av, acc[ms][ct]);
+        for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct + 1][lane];
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (wr == 1) expand(1 - S, 1 - S);
     store_x(1 - S);
     // the next group is in LDS, and every wave is done with this one's stage
     lds_barrier();
   };
+  // (the loads past the last group wrap around and are not used)
   for (int g = 0; g < G; g += 2) {  // G is even
-    step(g, std::integral_constant<int, 0>{});
-    step(g + 1, std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
   }
 
   // ---- B_a z, then y; lane: token c16 of each subtile, columns 4 kb .. 4 kb + 3 of each column tile
@@ -421,17 +439,17 @@ __global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs 
 #pragma unroll
     for (int ms = 0; ms < RS; ++ms) mine[ms] = adapter_at(a, tw + 16 * ms + c16);
     for (int s = 0; s < a.R; s += 32) {
-      u32x4 zh[RS], zl[RS];
-#pragma unroll
-      for (int ms = 0; ms < RS; ++ms) {
-        const int64_t t = min(tw + 16 * ms + c16, a.T - 1);
-        zh[ms] = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
-        zl[ms] = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
-      }
       int held = -1;
-      u32x4 bv[4];
+      u32x4 bv[4], zh[2], zl[2];
+      auto load_z = [&](int ms) {
+        const int64_t t = min(tw + 16 * ms + c16, a.T - 1);
+        zh[ms & 1] = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
+        zl[ms & 1] = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
+      };
+      load_z(0);
 #pragma unroll
       for (int ms = 0; ms < RS; ++ms) {
+        if (ms + 1 < RS) load_z(ms + 1);
         uint64_t rem = __ballot(mine[ms] >= 0);
         while (rem) {
           const int ad = __builtin_amdgcn_readlane(mine[ms], __builtin_ctzll(rem));
@@ -447,7 +465,7 @@ __global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs 
           }
 #pragma unroll
           for (int ct = 0; ct < 4; ++ct) {
-            const f32x4 d = mfma16(bv[ct], zl[ms], mfma16(bv[ct], zh[ms], f32x4{0.f, 0.f, 0.f, 0.f}));
+            const f32x4 d = mfma16(bv[ct], zl[ms & 1], mfma16(bv[ct], zh[ms & 1], f32x4{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[ms][ct][i] = is ? acc[ms][ct][i] + d[i] : acc[ms][ct][i];
           }

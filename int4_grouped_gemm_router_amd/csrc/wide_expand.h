@@ -1,5 +1,5 @@
-// int4 codes -> bf16 weights w = q s + b with one rounding, as the wide GEMMs
-// and the tiled projection feed the matrix cores.
+// What the wide GEMMs and the tiled projection share: int4 codes -> bf16
+// weights w = q s + b with one rounding, and buffer loads.
 #pragma once
 
 #include "device.h"
@@ -43,6 +43,16 @@ __device__ inline u32x4 expand_bf16(uint32_t w, const ColAffine& c, const WideEx
     r[d] = pack_bf16x2(__builtin_fmaf((float)h.x, c.s, c.c), __builtin_fmaf((float)h.y, c.s, c.c));
   }
   return r;
+}
+
+// Buffer resources: 32-bit offsets from a uniform base, and reads past
+// `bytes` return zero instead of touching memory.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ inline rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+__device__ inline u32x4 bload(rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
 }
 
 }  // namespace moe
