@@ -20,6 +20,9 @@
 //   project_tile_kernel   256 x 256 tiles; each weight is expanded once per
 //                         tile to bf16 and shared through LDS by its 256
 //                         rows: many rows, where the matrix cores count
+#include <cstdlib>
+#include <type_traits>
+
 #include "kernels.h"
 #include "wide_expand.h"
 
@@ -297,92 +300,106 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
   }
 }
 
-// Many rows: a block of eight waves owns 32 RS tokens x 256 columns; wave w
-// owns token half w / 4 (16 RS tokens) and the 64 columns of wave tile w % 4.
-// Per 64-input group the activation rows arrive through registers and the
-// weights' codes are expanded once (each wave half a wave tile) to bf16
-// w = q s + b; both go to a two-stage LDS buffer in operand order, and the
-// matrix cores form w . x (the weights as the first operand, so that a lane
-// ends up with four consecutive columns of one token and stores them
-// directly). Waves w and w + 4 share a SIMD: one expands the next group
-// before its matrix-core operations and the other after them, so that one's
-// expansion runs under the other's products.
-template <int RS>
+// Many rows: a block owns 16 MS tokens x 64 CW columns, its waves are CW
+// column waves times KS parts of K. A wave owns all of the block's tokens and
+// one wave tile (64 columns) over its part's groups: it expands each weight
+// of its columns once, in registers, to bf16 w = q s + b (two vector
+// instructions a weight, shared by 16 MS tokens), and the activation rows,
+// which the CW column waves share, arrive through registers in a three-stage
+// LDS ring in operand order. The weights are the first operand of the matrix
+// cores, so that a lane ends up with four consecutive columns of one token
+// and stores them directly.
+//
+// Per group a wave has two halves of 4 MS products; the next half's four
+// operands are expanded between the products of this one. The ring is three
+// deep so that a group's first operands can be read before the barrier that
+// ends the previous one.
+template <int MS, int CW, int KS>
 struct TileLds {
-  u32x4 x[2][2 * RS][2][64];  // [stage][16-token subtile][k half][lane]
-  u32x4 w[2][4][8][64];       // [stage][wave tile][2 ct + k half][lane]
+  static constexpr int kStage = MS * 2 * 64;  // 16-byte words: [16-token subtile][k half][lane]
+  union {
+    u32x4 x[KS][3][kStage];
+    f32x4 part[KS > 1 ? CW * KS : 1][KS > 1 ? MS * 2 : 1][64];  // the join: half a wave's tile each
+  };
 };
 
-template <int RS>
-__global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs a) {
-  __shared__ TileLds<RS> L;
+template <int MS, int CW, int KS>
+__global__ __launch_bounds__(64 * CW * KS, 2) void project_tile_kernel(ProjectArgs a) {
+  typedef TileLds<MS, CW, KS> Lds;
+  __shared__ Lds L;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kb = lane >> 4;
-  const int wr = wave >> 2, wc = wave & 3;
+  const int wc = wave % CW, kp = wave / CW;
   const PackGeom geom = pack_geom(a.N, a.K, 0);
   const int G = geom.G;
-  const int row_tiles = (a.T + 32 * RS - 1) / (32 * RS), col_tiles = (geom.n_wt + 3) / 4;
+  const int row_tiles = (a.T + 16 * MS - 1) / (16 * MS), col_tiles = (geom.n_wt + CW - 1) / CW;
   const int units = row_tiles * col_tiles;
+  // XCD x takes a contiguous range of units, column tiles fastest: the rows
+  // of few row tiles stay in its L2
   const int xcd = blockIdx.x & 7;
   const int u0 = (int)((int64_t)units * xcd / 8), u1 = (int)((int64_t)units * (xcd + 1) / 8);
   const int u = u0 + (blockIdx.x >> 3);
   if (u >= u1) return;
-  const int ct0 = u % col_tiles, t0 = u / col_tiles * (32 * RS), wt0 = 4 * ct0;
-  // the groups are taken in turn from a start that depends on the column
-  // tile: rows a multiple of 4 KB apart put one group of every row into one
-  // L2 channel, and blocks that all read the same group wait for it
-  int gx = 2 * ct0 % G, gw = gx;  // next group to load: activations, codes
+  const int ctile = u % col_tiles, t0 = u / col_tiles * (16 * MS);
+  const int wt_raw = ctile * CW + wc, wt = min(wt_raw, geom.n_wt - 1);
+  // this part's groups [g0, g0 + ng), taken in turn from a start that depends
+  // on the column tile: rows a multiple of 4 KB apart have one group of every
+  // row in the same L2 channel, and blocks in step would all wait for it
+  const int per = (G + KS - 1) / KS;
+  const int g0 = min(kp * per, G), ng = min(per, G - g0);
+  const int steps = (per + 1) / 2 * 2;  // every part runs as many (the barriers), its own ng with products
+  int gx = ng > 0 ? 2 * ctile % ng : 0, gw = gx;
 
-  // activations: wave w stages both k halves of RS / 4 subtiles
-  constexpr int kXRows = RS / 4;
-  const int rows = min(32 * RS, a.T - t0);
+  // activations: wave wc of the part stages subtiles wc, wc + CW, ...
+  constexpr int kXRows = MS / CW;
+  static_assert(kXRows * CW == MS, "subtiles split evenly over the column waves");
+  const int rows = min(16 * MS, a.T - t0);
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
   uint32_t xoff[kXRows];
 #pragma unroll
   for (int f = 0; f < kXRows; ++f)
-    xoff[f] = (uint32_t)min(16 * (wave * kXRows + f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
-  // weights: wave w expands half w & 1 (column tiles 2 (w & 1), + 1) of wave tile w >> 1
-  const int ewt = min(wt0 + (wave >> 1), geom.n_wt - 1), eh = wave & 1;
+    xoff[f] = (uint32_t)min(16 * (wc + CW * f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
   const rsrc_t wres = make_rsrc(a.blob, (uint32_t)geom.expert_bytes);
-  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)ewt * G * kNibBytes + 1024 * eh);
-  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)ewt * G * kSbBytes);
+  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)wt * G * kNibBytes);
+  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)wt * G * kSbBytes);
   const WideExpand xk = wide_expand_consts();
 
-  u32x4 ax[kXRows][2], cw[2], sbv[2];
+  u32x4 ax[kXRows][2], cw[2][2], sbv[2];
   auto load_x = [&]() {
+    const uint32_t at = (uint32_t)min(g0 + gx, G - 1) * (2 * kGroup);
 #pragma unroll
     for (int f = 0; f < kXRows; ++f) {
-      ax[f][0] = bload(xres, xoff[f], (uint32_t)gx * (2 * kGroup));
-      ax[f][1] = bload(xres, xoff[f] + 64, (uint32_t)gx * (2 * kGroup));
+      ax[f][0] = bload(xres, xoff[f], at);
+      ax[f][1] = bload(xres, xoff[f] + 64, at);
     }
-    gx = gx + 1 < G ? gx + 1 : 0;
+    gx = gx + 1 < ng ? gx + 1 : 0;
   };
   auto store_x = [&](int st) {
+    u32x4* o = &L.x[kp][st][lane];
 #pragma unroll
     for (int f = 0; f < kXRows; ++f) {
-      L.x[st][wave * kXRows + f][0][lane] = ax[f][0];
-      L.x[st][wave * kXRows + f][1][lane] = ax[f][1];
+      o[(wc + CW * f) * 128] = ax[f][0];
+      o[(wc + CW * f) * 128 + 64] = ax[f][1];
     }
   };
   auto load_w = [&](int s) {
-    cw[s] = bload(wres, lane * 16, nbase + (uint32_t)gw * kNibBytes);
-    sbv[s] = bload(wres, c16 * 16, sbase + (uint32_t)gw * kSbBytes);
-    gw = gw + 1 < G ? gw + 1 : 0;
+    const uint32_t g = (uint32_t)min(g0 + gw, G - 1);
+    cw[s][0] = bload(wres, lane * 16, nbase + g * kNibBytes);
+    cw[s][1] = bload(wres, lane * 16, nbase + g * kNibBytes + 1024);
+    sbv[s] = bload(wres, c16 * 16, sbase + g * kSbBytes);
+    gw = gw + 1 < ng ? gw + 1 : 0;
   };
-  auto expand = [&](int s, int st) {
-    const uint32_t sp = eh ? sbv[s].y : sbv[s].x, bp = eh ? sbv[s].w : sbv[s].z;
-    const ColAffine c0 = col_affine(bf16lo(sp), bf16lo(bp)), c1 = col_affine(bf16hi(sp), bf16hi(bp));
-    u32x4* o = &L.w[st][wave >> 1][4 * eh][lane];
-    o[0] = expand_bf16(cw[s].x, c0, xk);
-    o[64] = expand_bf16(cw[s].y, c0, xk);
-    o[128] = expand_bf16(cw[s].z, c1, xk);
-    o[192] = expand_bf16(cw[s].w, c1, xk);
+  u32x4 bw[2][4];  // the k halves' operands
+  auto expand1 = [&](int s, int ks, int ct) {  // column tile ct's
+    const uint32_t sp = ct < 2 ? sbv[s].x : sbv[s].y, bp = ct < 2 ? sbv[s].z : sbv[s].w;
+    const ColAffine c = ct & 1 ? col_affine(bf16hi(sp), bf16hi(bp)) : col_affine(bf16lo(sp), bf16lo(bp));
+    bw[ks][ct] = expand_bf16(cw[s][ct >> 1][2 * (ct & 1) + ks], c, xk);
   };
 
-  f32x4 acc[RS][4];
+  f32x4 acc[MS][4];
 #pragma unroll
-  for (int ms = 0; ms < RS; ++ms)
+  for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -390,50 +407,76 @@ __global__ __launch_bounds__(kPThreads, 1) void project_tile_kernel(ProjectArgs 
   load_w(0);
   load_w(1);
   store_x(0);
-  expand(0, 0);
+  load_x();
+#pragma unroll
+  for (int ct = 0; ct < 4; ++ct) expand1(0, 0, ct);
+  store_x(1);
   lds_barrier();
-  // one group: stage S holds it; the codes of group g + 1 are in slot 1 - S
-  auto step = [&](auto S_) {
+  int st = 0;  // ring stage of this step's group
+  u32x4 av[2];
+  av[0] = L.x[kp][0][lane];
+  // one group: its codes are in slot S (k half 0 already expanded), the next group's in slot 1 - S
+  auto step = [&](int i, auto S_) {
     constexpr int S = decltype(S_)::value;
-    load_x();
-    load_w(S);
-    if (wr == 0) expand(1 - S, 1 - S);
-    // operands stream from LDS: a k half's four weight fragments together,
-    // the activation fragments one ahead of their products (the scheduling
-    // fences keep that order; without them the compiler gathers the reads
-    // and spills)
-    u32x4 bw[4], av[2];
+    const u32x4* xs = &L.x[kp][st][lane];
+    const int st1 = st + 1 < 3 ? st + 1 : 0, st2 = st1 + 1 < 3 ? st1 + 1 : 0;
+    const u32x4* xn = &L.x[kp][st1][lane];
+    load_x();  // group i + 2, to LDS at the end of this step
+    if (KS == 1 || i < ng) {
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct][lane];
-    av[0] = L.x[S][wr * RS][0][lane];
+      for (int f = 0; f < 2 * MS; ++f) {
+        const int ks = f / MS, ms = f % MS;
+        av[(f + 1) & 1] = f + 1 < 2 * MS ? xs[((f + 1) % MS) * 128 + (f + 1) / MS * 64] : xn[0];
+        // the next half's operands, spread over this half's products
+        if (ms * 4 % MS == 0) {
+          if (ks == 0)
+            expand1(S, 1, ms * 4 / MS);
+          else
+            expand1(1 - S, 0, ms * 4 / MS);
+        }
+        if (f == MS) load_w(S);  // group i + 2: slot S is expanded
 #pragma unroll
-    for (int f = 0; f < 2 * RS; ++f) {
-      const int ks = f / RS, ms = f % RS;
-      if (f + 1 < 2 * RS) av[(f + 1) & 1] = L.x[S][wr * RS + (f + 1) % RS][(f + 1) / RS][lane];
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ct], av[f & 1], acc[ms][ct]);
-      if (f == RS - 1) {
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct) bw[ct] = L.w[S][wc][2 * ct + 1][lane];
+        for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ks][ct], av[f & 1], acc[ms][ct]);
+        // (without these fences the compiler gathers the reads and spills)
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if (wr == 1) expand(1 - S, 1 - S);
-    store_x(1 - S);
-    // the next group is in LDS, and every wave is done with this one's stage
+    store_x(st2);
+    st = st1;
+    // group i + 2 is in LDS, and every wave is done with group i's stage
     lds_barrier();
   };
-  // (the loads past the last group wrap around and are not used)
-  for (int g = 0; g < G; g += 2) {  // G is even
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
+  for (int i = 0; i < steps; i += 2) {
+    step(i, std::integral_constant<int, 0>{});
+    step(i + 1, std::integral_constant<int, 1>{});
   }
 
+  // ---- join the parts of K: in each round a wave gives the half of its
+  // subtiles that its partner keeps and adds what it gets
+  int mine0 = 0;  // first subtile this wave ends up with
+#pragma unroll
+  for (int n = KS, m = MS; n > 1; n /= 2, m /= 2) {
+    const bool up = kp & (n / 2);  // keeps the upper half
+#pragma unroll
+    for (int ms = 0; ms < m / 2; ++ms)
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) {
+        L.part[wave][ms * 4 + ct][lane] = up ? acc[ms][ct] : acc[m / 2 + ms][ct];
+        acc[ms][ct] = up ? acc[m / 2 + ms][ct] : acc[ms][ct];
+      }
+    lds_barrier();
+#pragma unroll
+    for (int ms = 0; ms < m / 2; ++ms)
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) acc[ms][ct] += L.part[wave ^ (n / 2 * CW)][ms * 4 + ct][lane];
+    mine0 += up ? m / 2 : 0;
+    if (n > 2) lds_barrier();
+  }
+  constexpr int RS = MS / KS;  // subtiles left
+
   // ---- B_a z, then y; lane: token c16 of each subtile, columns 4 kb .. 4 kb + 3 of each column tile
-  const int wt = wt0 + wc;
-  if (wt >= geom.n_wt) return;
-  const int tw = t0 + wr * 16 * RS;
+  if (wt_raw >= geom.n_wt) return;
+  const int tw = t0 + 16 * mine0;
   if (a.adapter_of) {
     int mine[RS];
 #pragma unroll
@@ -504,12 +547,12 @@ hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int RS>
+template <int MS, int CW, int KS>
 hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
-  const int64_t units = (int64_t)((a.T + 32 * RS - 1) / (32 * RS)) * ((a.N + 255) / 256);
+  const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * ((a.N / 64 + CW - 1) / CW);
   const int64_t blocks = (units + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(project_tile_kernel<RS>, dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
+  hipLaunchKernelGGL((project_tile_kernel<MS, CW, KS>), dim3((unsigned)blocks), dim3(64 * CW * KS), 0, s, a);
   return hipGetLastError();
 }
 
@@ -524,7 +567,17 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * entries)), dim3(kPThreads), 0, s, a, entries);
   }
   const bool tile = a.gemm == 2 || (a.gemm == 0 && a.T >= 1024);
-  if (tile) return (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256) >= 128 ? launch_tile<8>(a, s) : launch_tile<4>(a, s);
+  if (tile) {
+    static const char* v = getenv("PJV");
+    const int k = v ? atoi(v) : 0;
+    if (k == 1) return launch_tile<8, 4, 2>(a, s);
+    if (k == 2) return launch_tile<8, 2, 2>(a, s);
+    if (k == 3) return launch_tile<4, 2, 4>(a, s);
+    if (k == 4) return launch_tile<4, 4, 1>(a, s);
+    if (k == 5) return launch_tile<8, 8, 1>(a, s);
+    if (k == 6) return launch_tile<4, 4, 2>(a, s);
+    return launch_tile<8, 4, 1>(a, s);
+  }
   if (a.T <= 16) return launch_split<1, 1>(a, s);
   if (a.T <= 32) return launch_split<2, 1>(a, s);
   if (a.T <= 64) return launch_split<2, 2>(a, s);
