@@ -300,40 +300,38 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
   }
 }
 
-// Many rows: a block owns 16 MS tokens x 64 CW columns, its waves are CW
-// column waves times KS parts of K. A wave owns all of the block's tokens and
-// one wave tile (64 columns) over its part's groups: it expands each weight
-// of its columns once, in registers, to bf16 w = q s + b (two vector
-// instructions a weight, shared by 16 MS tokens), and the activation rows,
-// which the CW column waves share, arrive through registers in a three-stage
-// LDS ring in operand order. The weights are the first operand of the matrix
-// cores, so that a lane ends up with four consecutive columns of one token
-// and stores them directly.
+// Many rows: a block of eight waves owns 32 RS tokens x 256 columns; wave w
+// owns token half w / 4 (RS 16-token subtiles) and the 64 columns of wave
+// tile w % 4. Per 64-input group each weight is expanded once, by one of the
+// eight waves (half a wave tile each), to bf16 w = q s + b, and goes to LDS in
+// operand order beside the activation rows; each is read by the waves that
+// share it. The weights are the first operand of the matrix cores, so that a
+// lane ends up with four consecutive columns of one token and stores them
+// directly.
 //
-// Per group a wave has two halves of 4 MS products; the next half's four
-// operands are expanded between the products of this one. The ring is three
-// deep so that a group's first operands can be read before the barrier that
-// ends the previous one.
-template <int MS, int CW, int KS>
+// The matrix cores take 16 cycles a product; the same SIMD issues about two
+// vector instructions under each (two waves a SIMD), so the expansion, about
+// 2.4 instructions a weight, is spread evenly over the products, one pair of
+// weights per four of them. The unit of the pipeline is half a group (k half,
+// 32 inputs): in half h the products of h run while h + 2 is written to LDS,
+// and the first operands of h + 1 are read before the barrier that ends h
+// (h + 1 was complete at the barrier before).
+template <int RS>
 struct TileLds {
-  static constexpr int kStage = MS * 2 * 64;  // 16-byte words: [16-token subtile][k half][lane]
-  union {
-    u32x4 x[KS][3][kStage];
-    f32x4 part[KS > 1 ? CW * KS : 1][KS > 1 ? MS * 2 : 1][64];  // the join: half a wave's tile each
-  };
+  u32x4 x[2][2][2 * RS][64];  // [group % 2][k half][16-token subtile][lane]
+  u32x4 w[2][2][4][4][64];    // [group % 2][k half][wave tile][column tile][lane]
 };
 
-template <int MS, int CW, int KS>
-__global__ __launch_bounds__(64 * CW * KS, 2) void project_tile_kernel(ProjectArgs a) {
-  typedef TileLds<MS, CW, KS> Lds;
-  __shared__ Lds L;
+template <int RS>
+__global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs a) {
+  __shared__ TileLds<RS> L;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kb = lane >> 4;
-  const int wc = wave % CW, kp = wave / CW;
+  const int wr = wave >> 2, wc = wave & 3;
   const PackGeom geom = pack_geom(a.N, a.K, 0);
   const int G = geom.G;
-  const int row_tiles = (a.T + 16 * MS - 1) / (16 * MS), col_tiles = (geom.n_wt + CW - 1) / CW;
+  const int row_tiles = (a.T + 32 * RS - 1) / (32 * RS), col_tiles = (geom.n_wt + 3) / 4;
   const int units = row_tiles * col_tiles;
   // XCD x takes a contiguous range of units, column tiles fastest: the rows
   // of few row tiles stay in its L2
@@ -341,142 +339,135 @@ __global__ __launch_bounds__(64 * CW * KS, 2) void project_tile_kernel(ProjectAr
   const int u0 = (int)((int64_t)units * xcd / 8), u1 = (int)((int64_t)units * (xcd + 1) / 8);
   const int u = u0 + (blockIdx.x >> 3);
   if (u >= u1) return;
-  const int ctile = u % col_tiles, t0 = u / col_tiles * (16 * MS);
-  const int wt_raw = ctile * CW + wc, wt = min(wt_raw, geom.n_wt - 1);
-  // this part's groups [g0, g0 + ng), taken in turn from a start that depends
-  // on the column tile: rows a multiple of 4 KB apart have one group of every
-  // row in the same L2 channel, and blocks in step would all wait for it
-  const int per = (G + KS - 1) / KS;
-  const int g0 = min(kp * per, G), ng = min(per, G - g0);
-  const int steps = (per + 1) / 2 * 2;  // every part runs as many (the barriers), its own ng with products
-  int gx = ng > 0 ? 2 * ctile % ng : 0, gw = gx;
+  const int ctile = u % col_tiles, t0 = u / col_tiles * (32 * RS);
+  // the groups are taken in turn from a start that depends on the column
+  // tile: rows a multiple of 4 KB apart have one group of every row in the
+  // same L2 channel, and blocks in step would all wait for it
+  int gx = 2 * ctile % G, gw = gx;  // next group to load: activations, codes
 
-  // activations: wave wc of the part stages subtiles wc, wc + CW, ...
-  constexpr int kXRows = MS / CW;
-  static_assert(kXRows * CW == MS, "subtiles split evenly over the column waves");
-  const int rows = min(16 * MS, a.T - t0);
+  // activations: wave w stages subtiles w * RS / 4, ...
+  constexpr int kXRows = RS / 4;
+  const int rows = min(32 * RS, a.T - t0);
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
   uint32_t xoff[kXRows];
 #pragma unroll
   for (int f = 0; f < kXRows; ++f)
-    xoff[f] = (uint32_t)min(16 * (wc + CW * f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
+    xoff[f] = (uint32_t)min(16 * (wave * kXRows + f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
+  // weights: wave w expands column tiles 2 eh, 2 eh + 1 of wave tile ew
+  const int ew = wave >> 1, eh = wave & 1;
+  const int ewt = min(4 * ctile + ew, geom.n_wt - 1);
   const rsrc_t wres = make_rsrc(a.blob, (uint32_t)geom.expert_bytes);
-  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)wt * G * kNibBytes);
-  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)wt * G * kSbBytes);
+  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)ewt * G * kNibBytes + 1024 * eh);
+  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)ewt * G * kSbBytes);
   const WideExpand xk = wide_expand_consts();
 
-  u32x4 ax[kXRows][2], cw[2][2], sbv[2];
-  auto load_x = [&]() {
-    const uint32_t at = (uint32_t)min(g0 + gx, G - 1) * (2 * kGroup);
+  // (loads past the last group wrap around and are not used)
+  u32x4 ax[kXRows][2], cw[2], sbv[2];
+  auto load_x = [&](int ks) {
 #pragma unroll
-    for (int f = 0; f < kXRows; ++f) {
-      ax[f][0] = bload(xres, xoff[f], at);
-      ax[f][1] = bload(xres, xoff[f] + 64, at);
-    }
-    gx = gx + 1 < ng ? gx + 1 : 0;
+    for (int f = 0; f < kXRows; ++f) ax[f][ks] = bload(xres, xoff[f] + 64 * ks, (uint32_t)gx * (2 * kGroup));
+    if (ks) gx = gx + 1 < G ? gx + 1 : 0;
   };
-  auto store_x = [&](int st) {
-    u32x4* o = &L.x[kp][st][lane];
+  auto store_x = [&](int st, int ks) {
 #pragma unroll
-    for (int f = 0; f < kXRows; ++f) {
-      o[(wc + CW * f) * 128] = ax[f][0];
-      o[(wc + CW * f) * 128 + 64] = ax[f][1];
-    }
+    for (int f = 0; f < kXRows; ++f) L.x[st][ks][wave * kXRows + f][lane] = ax[f][ks];
   };
   auto load_w = [&](int s) {
-    const uint32_t g = (uint32_t)min(g0 + gw, G - 1);
-    cw[s][0] = bload(wres, lane * 16, nbase + g * kNibBytes);
-    cw[s][1] = bload(wres, lane * 16, nbase + g * kNibBytes + 1024);
-    sbv[s] = bload(wres, c16 * 16, sbase + g * kSbBytes);
-    gw = gw + 1 < ng ? gw + 1 : 0;
+    cw[s] = bload(wres, lane * 16, nbase + (uint32_t)gw * kNibBytes);
+    sbv[s] = bload(wres, c16 * 16, sbase + (uint32_t)gw * kSbBytes);
+    gw = gw + 1 < G ? gw + 1 : 0;
   };
-  u32x4 bw[2][4];  // the k halves' operands
-  auto expand1 = [&](int s, int ks, int ct) {  // column tile ct's
-    const uint32_t sp = ct < 2 ? sbv[s].x : sbv[s].y, bp = ct < 2 ? sbv[s].z : sbv[s].w;
-    const ColAffine c = ct & 1 ? col_affine(bf16hi(sp), bf16hi(bp)) : col_affine(bf16lo(sp), bf16lo(bp));
-    bw[ks][ct] = expand_bf16(cw[s][ct >> 1][2 * (ct & 1) + ks], c, xk);
+  ColAffine ca[2];
+  auto affine = [&](int s) {
+    const uint32_t sp = eh ? sbv[s].y : sbv[s].x, bp = eh ? sbv[s].w : sbv[s].z;
+    ca[0] = col_affine(bf16lo(sp), bf16lo(bp));
+    ca[1] = col_affine(bf16hi(sp), bf16hi(bp));
+  };
+  u32x4 ex;
+  // the p-th of a k half's eight pairs of weights: column tile p / 4, pair p % 4
+  auto expand_pair = [&](int s, int ks, int p) {
+    ex[p & 3] = expand_bf16x2(cw[s][2 * (p >> 2) + ks], p & 3, ca[p >> 2], xk);
+    if ((p & 3) == 3) L.w[s][ks][ew][2 * eh + (p >> 2)][lane] = ex;
   };
 
-  f32x4 acc[MS][4];
+  f32x4 acc[RS][4];
 #pragma unroll
-  for (int ms = 0; ms < MS; ++ms)
+  for (int ms = 0; ms < RS; ++ms)
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  load_x();
+  // group 0 into LDS, group 1 in flight
+  load_x(0);
+  load_x(1);
   load_w(0);
   load_w(1);
-  store_x(0);
-  load_x();
+  store_x(0, 0);
+  store_x(0, 1);
+  load_x(0);
+  load_x(1);
+  affine(0);
 #pragma unroll
-  for (int ct = 0; ct < 4; ++ct) expand1(0, 0, ct);
-  store_x(1);
+  for (int p = 0; p < 16; ++p) expand_pair(0, p >> 3, p & 7);
+  load_w(0);  // group 2
   lds_barrier();
-  int st = 0;  // ring stage of this step's group
-  u32x4 av[2];
-  av[0] = L.x[kp][0][lane];
-  // one group: its codes are in slot S (k half 0 already expanded), the next group's in slot 1 - S
-  auto step = [&](int i, auto S_) {
-    constexpr int S = decltype(S_)::value;
-    const u32x4* xs = &L.x[kp][st][lane];
-    const int st1 = st + 1 < 3 ? st + 1 : 0, st2 = st1 + 1 < 3 ? st1 + 1 : 0;
-    const u32x4* xn = &L.x[kp][st1][lane];
-    load_x();  // group i + 2, to LDS at the end of this step
-    if (KS == 1 || i < ng) {
+  // activation operands are read kAhead subtiles ahead of their products (LDS
+  // answers in about the time of eight products), the weights' half a half
+  constexpr int kAhead = 3, kRing = 4;
+  static_assert(RS % kRing == 0 && kAhead < kRing, "ring slots are the same in every half");
+  u32x4 av[kRing], bw[2][4];
 #pragma unroll
-      for (int f = 0; f < 2 * MS; ++f) {
-        const int ks = f / MS, ms = f % MS;
-        av[(f + 1) & 1] = f + 1 < 2 * MS ? xs[((f + 1) % MS) * 128 + (f + 1) / MS * 64] : xn[0];
-        // the next half's operands, spread over this half's products
-        if (ms * 4 % MS == 0) {
-          if (ks == 0)
-            expand1(S, 1, ms * 4 / MS);
-          else
-            expand1(1 - S, 0, ms * 4 / MS);
+  for (int ct = 0; ct < 4; ++ct) bw[0][ct] = L.w[0][0][wc][ct][lane];
+#pragma unroll
+  for (int f = 0; f < kAhead; ++f) av[f] = L.x[0][0][wr * RS + f][lane];
+  // half ks of group i in stage S = i % 2; group i + 1's half ks is written meanwhile, from code slot 1 - S
+  auto half = [&](auto S_, auto ks_) {
+    constexpr int S = decltype(S_)::value, ks = decltype(ks_)::value;
+    constexpr int Sn = ks ? 1 - S : S, kn = 1 - ks;  // the half after this one
+    if constexpr (ks == 0) affine(1 - S);
+    store_x(1 - S, ks);  // the next group's
+    load_x(ks);          // and the one after it
+#pragma unroll
+    for (int ms = 0; ms < RS; ++ms) {
+      const int fa = ms + kAhead;
+      av[fa % kRing] = fa < RS ? L.x[S][ks][wr * RS + fa][lane] : L.x[Sn][kn][wr * RS + fa - RS][lane];
+      if (ms >= RS / 2) {
+#pragma unroll
+        for (int q = 0; q < 8 / RS; ++q) {
+          const int ct = (ms - RS / 2) * (8 / RS) + q;
+          bw[kn][ct] = L.w[Sn][kn][wc][ct][lane];
         }
-        if (f == MS) load_w(S);  // group i + 2: slot S is expanded
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ks][ct], av[f & 1], acc[ms][ct]);
-        // (without these fences the compiler gathers the reads and spills)
-        __builtin_amdgcn_sched_barrier(0);
       }
+      // the eight pairs over the first three quarters of the subtiles
+#pragma unroll
+      for (int p = ms * 32 / (3 * RS); p < min(8, (ms + 1) * 32 / (3 * RS)); ++p) expand_pair(1 - S, ks, p);
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = mfma16(bw[ks][ct], av[ms % kRing], acc[ms][ct]);
+      // (without these fences the compiler gathers the reads and spills)
+      __builtin_amdgcn_sched_barrier(0);
     }
-    store_x(st2);
-    st = st1;
-    // group i + 2 is in LDS, and every wave is done with group i's stage
-    lds_barrier();
+    if constexpr (ks == 1) load_w(1 - S);  // group i + 3: slot 1 - S is expanded
+    // What this half wrote has to be in LDS, and its reads done, before any
+    // wave goes on; the last quarter's reads, of the next half's operands,
+    // may be under way (LDS answers in order, and they come last).
+    static_assert(RS == 8 || RS == 4, "reads after the last write: two subtiles' two, or one's three");
+    if constexpr (RS == 8)
+      asm volatile("s_waitcnt lgkmcnt(4)\n\ts_barrier" ::: "memory");
+    else
+      asm volatile("s_waitcnt lgkmcnt(3)\n\ts_barrier" ::: "memory");
   };
-  for (int i = 0; i < steps; i += 2) {
-    step(i, std::integral_constant<int, 0>{});
-    step(i + 1, std::integral_constant<int, 1>{});
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  for (int g = 0; g < G; g += 2) {  // G is even
+    half(I0{}, I0{});
+    half(I0{}, I1{});
+    half(I1{}, I0{});
+    half(I1{}, I1{});
   }
-
-  // ---- join the parts of K: in each round a wave gives the half of its
-  // subtiles that its partner keeps and adds what it gets
-  int mine0 = 0;  // first subtile this wave ends up with
-#pragma unroll
-  for (int n = KS, m = MS; n > 1; n /= 2, m /= 2) {
-    const bool up = kp & (n / 2);  // keeps the upper half
-#pragma unroll
-    for (int ms = 0; ms < m / 2; ++ms)
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        L.part[wave][ms * 4 + ct][lane] = up ? acc[ms][ct] : acc[m / 2 + ms][ct];
-        acc[ms][ct] = up ? acc[m / 2 + ms][ct] : acc[ms][ct];
-      }
-    lds_barrier();
-#pragma unroll
-    for (int ms = 0; ms < m / 2; ++ms)
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) acc[ms][ct] += L.part[wave ^ (n / 2 * CW)][ms * 4 + ct][lane];
-    mine0 += up ? m / 2 : 0;
-    if (n > 2) lds_barrier();
-  }
-  constexpr int RS = MS / KS;  // subtiles left
 
   // ---- B_a z, then y; lane: token c16 of each subtile, columns 4 kb .. 4 kb + 3 of each column tile
-  if (wt_raw >= geom.n_wt) return;
-  const int tw = t0 + 16 * mine0;
+  const int wt = 4 * ctile + wc;
+  if (wt >= geom.n_wt) return;
+  const int tw = t0 + 16 * RS * wr;
   if (a.adapter_of) {
     int mine[RS];
 #pragma unroll
@@ -547,12 +538,12 @@ hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MS, int CW, int KS>
+template <int RS>
 hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
-  const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * ((a.N / 64 + CW - 1) / CW);
+  const int64_t units = (int64_t)((a.T + 32 * RS - 1) / (32 * RS)) * ((a.N + 255) / 256);
   const int64_t blocks = (units + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((project_tile_kernel<MS, CW, KS>), dim3((unsigned)blocks), dim3(64 * CW * KS), 0, s, a);
+  hipLaunchKernelGGL(project_tile_kernel<RS>, dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -570,13 +561,8 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   if (tile) {
     static const char* v = getenv("PJV");
     const int k = v ? atoi(v) : 0;
-    if (k == 1) return launch_tile<8, 4, 2>(a, s);
-    if (k == 2) return launch_tile<8, 2, 2>(a, s);
-    if (k == 3) return launch_tile<4, 2, 4>(a, s);
-    if (k == 4) return launch_tile<4, 4, 1>(a, s);
-    if (k == 5) return launch_tile<8, 8, 1>(a, s);
-    if (k == 6) return launch_tile<4, 4, 2>(a, s);
-    return launch_tile<8, 4, 1>(a, s);
+    if (k == 1) return launch_tile<4>(a, s);
+    return launch_tile<8>(a, s);
   }
   if (a.T <= 16) return launch_split<1, 1>(a, s);
   if (a.T <= 32) return launch_split<2, 1>(a, s);

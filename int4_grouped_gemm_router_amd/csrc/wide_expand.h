@@ -34,14 +34,17 @@ __device__ inline ColAffine col_affine(float s, float b) {
 // One packed word (eight codes of one column, k = 8 consecutive inputs, code
 // o at nibble (o & 1) * 4 + (o >> 1)) -> the eight bf16 weights in k order:
 // ((w >> 4d) & 0x000F000F) | 0x64006400 is the fp16 pair (1024 + q_2d,
-// 1024 + q_2d+1), and (1024 + q) s + (b - 1024 s) = q s + b with one rounding.
+// 1024 + q_2d+1), and (1024 + q) s + (b - 1024 s) = q s + b with one rounding;
+// expand_bf16x2 forms the d-th pair.
+__device__ inline uint32_t expand_bf16x2(uint32_t w, int d, const ColAffine& c, const WideExpand& k) {
+  const f16x2 h = __builtin_bit_cast(f16x2, ((w >> (4 * d)) & k.mask_lo) | k.magic);
+  return pack_bf16x2(__builtin_fmaf((float)h.x, c.s, c.c), __builtin_fmaf((float)h.y, c.s, c.c));
+}
+
 __device__ inline u32x4 expand_bf16(uint32_t w, const ColAffine& c, const WideExpand& k) {
   u32x4 r;
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const f16x2 h = __builtin_bit_cast(f16x2, ((w >> (4 * d)) & k.mask_lo) | k.magic);
-    r[d] = pack_bf16x2(__builtin_fmaf((float)h.x, c.s, c.c), __builtin_fmaf((float)h.y, c.s, c.c));
-  }
+  for (int d = 0; d < 4; ++d) r[d] = expand_bf16x2(w, d, c, k);
   return r;
 }
 
