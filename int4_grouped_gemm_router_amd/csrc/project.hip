@@ -362,15 +362,12 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
   const WideExpand xk = wide_expand_consts();
 
   // (loads past the last group wrap around and are not used)
-  u32x4 ax[kXRows][2], cw[2], sbv[2];
-  auto load_x = [&](int ks) {
+  u32x4 cw[2], sbv[2];
+  auto load_x = [&](int st, int ks) {
 #pragma unroll
-    for (int f = 0; f < kXRows; ++f) ax[f][ks] = bload(xres, xoff[f] + 64 * ks, (uint32_t)gx * (2 * kGroup));
+    for (int f = 0; f < kXRows; ++f)
+      bload_lds(xres, &L.x[st][ks][wave * kXRows + f][0], xoff[f] + 64 * ks, (uint32_t)gx * (2 * kGroup));
     if (ks) gx = gx + 1 < G ? gx + 1 : 0;
-  };
-  auto store_x = [&](int st, int ks) {
-#pragma unroll
-    for (int f = 0; f < kXRows; ++f) L.x[st][ks][wave * kXRows + f][lane] = ax[f][ks];
   };
   auto load_w = [&](int s) {
     cw[s] = bload(wres, lane * 16, nbase + (uint32_t)gw * kNibBytes);
@@ -397,18 +394,16 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
     for (int ct = 0; ct < 4; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // group 0 into LDS, group 1 in flight
-  load_x(0);
-  load_x(1);
+  load_x(0, 0);
+  load_x(0, 1);
   load_w(0);
   load_w(1);
-  store_x(0, 0);
-  store_x(0, 1);
-  load_x(0);
-  load_x(1);
+  load_x(1, 0);
   affine(0);
 #pragma unroll
   for (int p = 0; p < 16; ++p) expand_pair(0, p >> 3, p & 7);
   load_w(0);  // group 2
+  __builtin_amdgcn_s_waitcnt(0);  // (a wait the compiler sees: the loop starts with nothing outstanding)
   lds_barrier();
   // activation operands are read kAhead subtiles ahead of their products (LDS
   // answers in about the time of eight products), the weights' half a half
@@ -424,8 +419,7 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
     constexpr int S = decltype(S_)::value, ks = decltype(ks_)::value;
     constexpr int Sn = ks ? 1 - S : S, kn = 1 - ks;  // the half after this one
     if constexpr (ks == 0) affine(1 - S);
-    store_x(1 - S, ks);  // the next group's
-    load_x(ks);          // and the one after it
+    load_x(ks ? S : 1 - S, kn);  // three halves on, into the stage that the last half read
 #pragma unroll
     for (int ms = 0; ms < RS; ++ms) {
       const int fa = ms + kAhead;
@@ -446,14 +440,16 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (ks == 1) load_w(1 - S);  // group i + 3: slot 1 - S is expanded
-    // What this half wrote has to be in LDS, and its reads done, before any
-    // wave goes on; the last quarter's reads, of the next half's operands,
-    // may be under way (LDS answers in order, and they come last).
-    static_assert(RS == 8 || RS == 4, "reads after the last write: two subtiles' two, or one's three");
+    // Before any wave goes on: the activations of two halves on are in LDS
+    // (what was issued after them may be under way: this half's copies, and
+    // two loads of codes), what this half wrote too, and its reads are done
+    // (LDS answers in order; the last quarter's reads, of the next half's
+    // operands, may be under way).
+    static_assert(RS == 8 || RS == 4, "copies per half; reads after the last write");
     if constexpr (RS == 8)
-      asm volatile("s_waitcnt lgkmcnt(4)\n\ts_barrier" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(4) lgkmcnt(4)\n\ts_barrier" ::: "memory");
     else
-      asm volatile("s_waitcnt lgkmcnt(3)\n\ts_barrier" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(3) lgkmcnt(3)\n\ts_barrier" ::: "memory");
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
@@ -465,6 +461,8 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
   }
 
   // ---- B_a z, then y; lane: token c16 of each subtile, columns 4 kb .. 4 kb + 3 of each column tile
+  // (the last half's copies into LDS and reads of it end here, in every wave)
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const int wt = 4 * ctile + wc;
   if (wt >= geom.n_wt) return;
   const int tw = t0 + 16 * RS * wr;
@@ -507,19 +505,30 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
       }
     }
   }
+  // through LDS, so that eight lanes store a row's 128 bytes (the stages are
+  // read no more: the last half's reads wrapped around and are not used)
+  constexpr int kRow = 144;  // bytes; 128 and a pad that spreads the rows over the banks
+  uint8_t* tr = reinterpret_cast<uint8_t*>(&L) + wave * (2 * 16 * kRow);
 #pragma unroll
   for (int ms = 0; ms < RS; ++ms) {
-    const int t = tw + 16 * ms + c16;
-    if (t < a.T) {
-      uint16_t* y = a.y + (int64_t)t * a.ldy + 64 * wt + 4 * kb;
+    uint8_t* tb = tr + (ms & 1) * (16 * kRow);
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        u32x2 o;
-        o.x = pack_bf16x2(acc[ms][ct][0], acc[ms][ct][1]);
-        o.y = pack_bf16x2(acc[ms][ct][2], acc[ms][ct][3]);
-        *reinterpret_cast<u32x2*>(y + 16 * ct) = o;
-      }
+    for (int ct = 0; ct < 4; ++ct) {
+      u32x2 o;
+      o.x = pack_bf16x2(acc[ms][ct][0], acc[ms][ct][1]);
+      o.y = pack_bf16x2(acc[ms][ct][2], acc[ms][ct][3]);
+      *reinterpret_cast<u32x2*>(tb + c16 * kRow + 32 * ct + 8 * kb) = o;
     }
+    // (a wave's LDS accesses execute in order)
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = 8 * q + (lane >> 3), t = tw + 16 * ms + r;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(tb + r * kRow + 16 * (lane & 7));
+      if (t < a.T)
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(a.y + (int64_t)t * a.ldy + 64 * wt + 8 * (lane & 7)));
+    }
+    asm volatile("" ::: "memory");
   }
 }
 

@@ -57,5 +57,18 @@ __device__ inline rsrc_t make_rsrc(const void* base, uint32_t bytes) {
 __device__ inline u32x4 bload(rsrc_t r, uint32_t voff, uint32_t soff) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
 }
+__device__ inline u32x2 bload2(rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)voff, (int)soff, 0));
+}
+__device__ inline uint32_t bload1(rsrc_t r, uint32_t voff, uint32_t soff) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, (int)soff, 0);
+}
+
+// 64 x 16 bytes straight to LDS: lane l's 16 bytes at `voff` go to dst + 16 l
+// (dst the same in every lane). Counted by vmcnt; the compiler does not wait
+// for it.
+__device__ inline void bload_lds(rsrc_t r, void* dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, (int)voff, (int)soff, 0, 0);
+}
 
 }  // namespace moe
