@@ -66,9 +66,14 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 }  // namespace
 
 // The adapters' first product. Block: one tile of 16 tokens, 16 ranks, and
-// every `entries`-th distinct adapter of the tile; the eight waves split K.
-// Grid: token tiles x rank tiles x entries (entries fastest).
+// every `entries`-th distinct adapter of the tile; the eight waves split K in
+// chunks of 128. Grid: token tiles x rank tiles x entries (entries fastest).
+// What counts is latency (a prompt of 4096 tokens reads 64 KB of activations
+// and 64 KB of one adapter a block): the first kHeld chunks of activations
+// are under way before the adapters are known and serve every entry, and an
+// entry's first kHeld chunks of A are under way before its rank is known.
 __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, int entries) {
+  constexpr int kHeld = 2;
   __shared__ float red[kPWaves][16][17];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -79,26 +84,40 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
   const int mine = adapter_at(a, t0 + c16);
   const uint16_t* x = a.x + (int64_t)min(t0 + c16, a.T - 1) * a.ldx + 8 * kb;
   const int chunks = a.K / 128;
+  auto load = [&](const uint16_t* p, int c, u32x4 (&v)[4]) {
+    c = min(c, chunks - 1);  // (a chunk past the last is not used)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = *reinterpret_cast<const u32x4*>(p + 128 * c + 32 * s);
+  };
+  u32x4 xv[kHeld][4];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) load(x, wave + kPWaves * h, xv[h]);
+  __builtin_amdgcn_sched_barrier(0);
   uint64_t rem = __ballot(mine >= 0) & 0xFFFFull;
   for (int j = 0; rem; ++j) {
     const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
     const uint64_t same = __ballot(mine == ad) & 0xFFFFull;
     rem &= ~same;
     if (j % entries != entry) continue;
+    const uint16_t* A = a.A + ((int64_t)ad * a.R + min(16 * rt + c16, a.R - 1)) * a.K + 8 * kb;
+    u32x4 av[kHeld][4];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) load(A, wave + kPWaves * h, av[h]);
     const int rank = rank_of(a, ad);
+    const float scale = a.scales ? a.scales[ad] : 1.f;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    if (16 * rt < rank) {
-      const uint16_t* A = a.A + ((int64_t)ad * a.R + min(16 * rt + c16, a.R - 1)) * a.K + 8 * kb;
-      for (int c = wave; c < chunks; c += kPWaves) {
-        u32x4 xv[4], av[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          xv[s] = *reinterpret_cast<const u32x4*>(x + 128 * c + 32 * s);
-          av[s] = *reinterpret_cast<const u32x4*>(A + 128 * c + 32 * s);
-        }
+    for (int h = 0; h < kHeld; ++h)
+      if (wave + kPWaves * h < chunks) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) acc = mfma16(xv[s], av[s], acc);
+        for (int s = 0; s < 4; ++s) acc = mfma16(xv[h][s], av[h][s], acc);
       }
+    for (int c = wave + kPWaves * kHeld; c < chunks; c += kPWaves) {
+      u32x4 xc[4], ac[4];
+      load(x, c, xc);
+      load(A, c, ac);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc = mfma16(xc[s], ac[s], acc);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][4 * kb + i][c16] = acc[i];
@@ -109,7 +128,7 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kPWaves; ++w) v += red[w][row][tid & 15];
-        if (a.scales) v *= a.scales[ad];
+        v *= scale;
         if (r >= rank) v = 0.f;
         const uint16_t hi = f2bf(v);
         const int64_t at = (int64_t)(t0 + row) * a.R + r;
@@ -562,7 +581,7 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   if (a.adapter_of) {
     const int64_t tiles = (int64_t)((a.T + 15) / 16) * ((a.R + 15) / 16);
     int entries = min(min(16, a.n), a.T);
-    while (entries > 1 && tiles * entries > 1024) entries = (entries + 1) / 2;
+    while (entries > 1 && tiles * entries > 512) entries = (entries + 1) / 2;
     if (tiles * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * entries)), dim3(kPThreads), 0, s, a, entries);
   }
