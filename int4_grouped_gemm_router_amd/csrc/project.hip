@@ -47,6 +47,31 @@ __device__ inline int rank_of(const ProjectArgs& a, int i) {
 __device__ inline uint16_t* z_hi(const ProjectArgs& a) { return static_cast<uint16_t*>(a.ws); }
 __device__ inline uint16_t* z_lo(const ProjectArgs& a) { return z_hi(a) + (int64_t)a.T * a.R; }
 
+// A fragment (16 rows x 32 inputs, 16 bytes a lane) is copied from rows in
+// memory to LDS by a wave: lane l copies chunk frag_chunk(l) (8 inputs) of row
+// frag_row(l) to slot l. Four lanes cover a row's 64 bytes: sixteen lanes in a
+// row that each read another row cost the address unit a cycle each, four
+// times as long. Lane (c16, kb) of the matrix cores finds row c16, chunk kb in
+// frag_slot(c16, kb); the chunks are swizzled so that the sixteen rows of one
+// chunk lie in different LDS banks.
+__device__ inline int frag_row(int l) { return l >> 2; }
+__device__ inline int frag_chunk(int l) { return (l & 3) ^ (l >> 4); }
+__device__ inline int frag_slot(int c16, int kb) { return 4 * c16 + (kb ^ (c16 >> 2)); }
+
+// Waits until all but the newest N vector memory operations are done.
+template <int N>
+__device__ inline void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// The first `left` of eight ranks, the others zero.
+__device__ inline u32x4 rank_mask(u32x4 v, int left) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = left >= 2 * j + 2 ? v[j] : (left == 2 * j + 1 ? v[j] & 0xFFFFu : 0u);
+  return v;
+}
+
 // Eight consecutive ranks from r0 of row `row` of a [rows][R] array, zero
 // from rank `have` (<= R) on.
 __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int r0, int have) {
@@ -54,11 +79,7 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
   const int left = have - r0;
   if (left > 0) {
     v = *reinterpret_cast<const u32x4*>(base + row * R + r0);
-    if (left < 8) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = left >= 2 * j + 2 ? v[j] : (left == 2 * j + 1 ? v[j] & 0xFFFFu : 0u);
-    }
+    if (left < 8) v = rank_mask(v, left);
   }
   return v;
 }
@@ -141,24 +162,31 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 }
 
 // Few rows: a block owns 16 MS tokens and 16 CT columns; wave w takes the
-// 64-input groups w, w + 8, ... with its operands straight from memory (the
-// next group's loads in flight while one is multiplied), and the eight
-// partial tiles are added in LDS in a fixed order. With the codes expanded to
-// the exact bf16 values 128 + q, per group and column
+// 64-input groups w, w + 8, ... on its own: D groups ahead, the codes go to
+// registers and the activations to the wave's own ring in LDS (no barrier:
+// the wave waits for its copies), and the eight partial tiles are added in
+// LDS in a fixed order. With the codes expanded to the exact bf16 values
+// 128 + q, per group and column
 //   acc += s * x.(128 + q) + (b - 128 s) * sum(x)
 // which is x . (q s + b) with the weights used exactly. The distinct adapters
-// of the tokens are dealt out over the waves too: their B_a z goes to a tile
-// of its own in LDS, added last, so a token's result does not depend on the
-// others.
-template <int MS, int CT>
+// of the tokens are dealt out over the waves too; their operands are loaded
+// ahead of the groups (NE adapters a wave, the first 32 ranks), and their
+// B_a z goes to a tile of its own, added last, so a token's result does not
+// depend on the others.
+template <int MS, int CT, int D>
 struct SplitLds {
   static constexpr int kStride = 16 * CT + 4;  // floats; the pad spreads the rows over the banks
-  float red[kPWaves + 1][16 * MS][kStride];    // the waves' tiles, then the adapters'
+  static constexpr int kPlanes = MS * CT >= 16 ? 4 : 8;  // partial tiles held at once
+  union {
+    u32x4 x[kPWaves][D][MS][2][64];           // [wave][slot][16-token subtile][k half][frag_slot]
+    float red[kPlanes + 1][16 * MS][kStride]; // the waves' tiles, then the adapters'
+  };
 };
 
-template <int MS, int CT>
-__global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a) {
-  __shared__ SplitLds<MS, CT> L;
+template <int MS, int CT, int D, int NE>
+__global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs a) {
+  typedef SplitLds<MS, CT, D> Lds;
+  __shared__ Lds L;
   constexpr int kSub = 4 / CT;  // blocks per 64-column wave tile
   constexpr int NW = CT == 4 ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -180,76 +208,92 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
   const ExpandConsts xk = expand_consts();
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 
-  const uint16_t* x[MS];
-#pragma unroll
-  for (int ms = 0; ms < MS; ++ms) x[ms] = a.x + (int64_t)min(t0 + 16 * ms + c16, a.T - 1) * a.ldx + 8 * kb;
-  const uint8_t* nib = a.blob + geom.nib_off + (int64_t)wt * G * kNibBytes + lane * 16 + (ct0 >> 1) * 1024 + (ct0 & 1) * 8;
-  const uint8_t* sbp = a.blob + geom.sb_off + (int64_t)wt * G * kSbBytes + c16 * 16;
+  int mine = -1;  // lane r: the adapter of row r
+  if (a.adapter_of && lane < 16 * MS) mine = adapter_at(a, t0 + lane);
 
-  u32x4 xa[2][MS][2], w[2][NW], sb[2];
-  auto load = [&](int g, int s) {
-    g = min(g, G - 1);
+  const int rows = min(16 * MS, a.T - t0);
+  const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
+  uint32_t xoff[MS];
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+    xoff[ms] = (uint32_t)min(16 * ms + frag_row(lane), rows - 1) * (uint32_t)(a.ldx * 2) + 16 * frag_chunk(lane);
+  const int xl = frag_slot(c16, kb);
+  const rsrc_t wres = make_rsrc(a.blob, (uint32_t)geom.expert_bytes);
+  const uint32_t nbase = (uint32_t)(geom.nib_off + (int64_t)wt * G * kNibBytes + (ct0 >> 1) * 1024 + (ct0 & 1) * 8);
+  const uint32_t sbase = (uint32_t)(geom.sb_off + (int64_t)wt * G * kSbBytes);
+
+  // this wave's groups: wave, wave + 8, ... (loads past the last repeat it
+  // and are not used)
+  const int ng = wave < G ? (G - wave + kPWaves - 1) / kPWaves : 0;
+  int next = wave;
+  u32x4 w[D][NW], sb[D];
+  auto load = [&](int s) {
+    const uint32_t g = (uint32_t)min(next, G - 1);
+    next += kPWaves;
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      bload_lds(xres, &L.x[wave][s][ms][0][0], xoff[ms], g * (2 * kGroup));
+      bload_lds(xres, &L.x[wave][s][ms][1][0], xoff[ms] + 64, g * (2 * kGroup));
+    }
     if constexpr (CT == 1) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(nib + (int64_t)g * kNibBytes);
+      const u32x2 v = bload2(wres, lane * 16, nbase + g * kNibBytes);
       w[s][0] = u32x4{v.x, v.y, 0u, 0u};
     } else {
 #pragma unroll
-      for (int h = 0; h < NW; ++h) w[s][h] = *reinterpret_cast<const u32x4*>(nib + (int64_t)g * kNibBytes + 1024 * h);
+      for (int h = 0; h < NW; ++h) w[s][h] = bload(wres, lane * 16, nbase + g * kNibBytes + 1024 * h);
     }
-    sb[s] = *reinterpret_cast<const u32x4*>(sbp + (int64_t)g * kSbBytes);
+    sb[s] = bload(wres, c16 * 16, sbase + g * kSbBytes);
+  };
+#pragma unroll
+  for (int s = 0; s < D; ++s) load(s);
+
+  // ---- the wave's adapters: the distinct ones of the rows, in row order,
+  // every eighth; the first NE's operands are loaded here
+  struct Entry {
+    int ad;
+    uint64_t same;  // its rows
+  };
+  const uint64_t with = __ballot(mine >= 0);  // rows with an adapter
+  auto entry = [&](uint64_t& rem) {
+    Entry e;
+    e.ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
+    e.same = __ballot(mine == e.ad);
+    rem &= ~e.same;
+    return e;
+  };
+  struct Operands {
+    u32x4 b[CT], zh[MS], zl[MS];
+  };
+  auto load_operands = [&](const Entry& e, int s, Operands& o) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+      o.b[ct] = rank_chunk(a.B, (int64_t)e.ad * a.N + 64 * wt + 16 * (ct0 + ct) + c16, a.R, s + 8 * kb, a.R);
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
-      xa[s][ms][0] = *reinterpret_cast<const u32x4*>(x[ms] + g * kGroup);
-      xa[s][ms][1] = *reinterpret_cast<const u32x4*>(x[ms] + g * kGroup + 32);
+      const int64_t t = min(t0 + 16 * ms + c16, a.T - 1);
+      o.zh[ms] = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
+      o.zl[ms] = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
     }
   };
-  load(wave, 0);
-  load(wave + kPWaves, 1);
-
-  // ---- B_a z of the tokens with an adapter
-  uint64_t with = 0;  // rows of the block with an adapter
-  if (a.adapter_of) {
-    const int mine = lane < 16 * MS ? adapter_at(a, t0 + lane) : -1;
-    with = __ballot(mine >= 0);
+  Entry first[NE];
+  Operands ops[NE];
+  int rank_first[NE];
+  uint64_t left = 0;  // rows whose adapters come after the first NE of every wave
+  if (with) {
     uint64_t rem = with;
-    for (int j = 0; rem; ++j) {
-      const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
-      const uint64_t same = __ballot(mine == ad);
-      rem &= ~same;
-      if (j % kPWaves != wave) continue;
-      const int rank = rank_of(a, ad);
-      f32x4 d[MS][CT];
 #pragma unroll
-      for (int ms = 0; ms < MS; ++ms)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) d[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < rank; s += 32) {
-        u32x4 bv[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          bv[ct] = rank_chunk(a.B, (int64_t)ad * a.N + 64 * wt + 16 * (ct0 + ct) + c16, a.R, s + 8 * kb, rank);
-#pragma unroll
-        for (int ms = 0; ms < MS; ++ms) {
-          if (same >> (16 * ms) & 0xFFFFull) {
-            const int64_t t = min(t0 + 16 * ms + c16, a.T - 1);
-            const u32x4 zh = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
-            const u32x4 zl = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) d[ms][ct] = mfma16(zl, bv[ct], mfma16(zh, bv[ct], d[ms][ct]));
-          }
-        }
+    for (int k = 0; k < NE; ++k) {
+      first[k].same = 0;
+      for (int j = 0; j < kPWaves && rem; ++j) {
+        const Entry e = entry(rem);
+        if (j == wave) first[k] = e;
       }
-#pragma unroll
-      for (int ms = 0; ms < MS; ++ms)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 16 * ms + 4 * kb + i;
-          if (same >> row & 1) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) L.red[kPWaves][row][16 * ct + c16] = d[ms][ct][i];
-          }
-        }
+      if (first[k].same) {
+        rank_first[k] = rank_of(a, first[k].ad);
+        load_operands(first[k], 0, ops[k]);
+      }
     }
+    left = rem;
   }
 
   // ---- W x
@@ -259,13 +303,19 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) acc[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto step = [&](int s) {
+    u32x4 xa[MS][2];
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      xa[ms][0] = L.x[wave][s][ms][0][xl];
+      xa[ms][1] = L.x[wave][s][ms][1][xl];
+    }
     const uint32_t words[8] = {w[s][0].x, w[s][0].y, w[s][0].z, w[s][0].w, w[s][NW - 1].x, w[s][NW - 1].y,
                                w[s][NW - 1].z, w[s][NW - 1].w};
     f32x4 xs[MS];
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms)
-      xs[ms] = mfma16(xa[s][ms][1], ones, mfma16(xa[s][ms][0], ones, f32x4{0.f, 0.f, 0.f, 0.f}));
-    // this block's scales and biases: pairs of columns tiles per word
+      xs[ms] = mfma16(xa[ms][1], ones, mfma16(xa[ms][0], ones, f32x4{0.f, 0.f, 0.f, 0.f}));
+    // this block's scales and biases: pairs of column tiles per word
     const uint32_t sw0 = CT == 4 || ct0 < 2 ? sb[s].x : sb[s].y, bw0 = CT == 4 || ct0 < 2 ? sb[s].z : sb[s].w;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -276,28 +326,97 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
       const u32x4 b0 = expand_codes(words[2 * ct], xk), b1 = expand_codes(words[2 * ct + 1], xk);
 #pragma unroll
       for (int ms = 0; ms < MS; ++ms) {
-        f32x4 p = mfma16(xa[s][ms][0], b0, f32x4{0.f, 0.f, 0.f, 0.f});
-        p = mfma16(xa[s][ms][1], b1, p);
+        f32x4 p = mfma16(xa[ms][0], b0, f32x4{0.f, 0.f, 0.f, 0.f});
+        p = mfma16(xa[ms][1], b1, p);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           acc[ms][ct][i] = __builtin_fmaf(bp, xs[ms][i], __builtin_fmaf(sc, p[i], acc[ms][ct][i]));
       }
     }
   };
-  for (int g = wave; g < G; g += 2 * kPWaves) {
-    step(0);
-    load(g + 2 * kPWaves, 0);
-    if (g + kPWaves < G) step(1);
-    load(g + 3 * kPWaves, 1);
+  for (int i = 0; i < ng; i += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      // a slot's copies are in LDS when its codes, loaded after them, are
+      // in registers: wait for all but the newer slots' loads
+      constexpr int kLoads = 2 * MS + NW + 1;
+      wait_loads<kLoads*(D - 1)>();
+      if (i + s < ng) step(s);
+      // (the slot's reads are done before its next copies are issued)
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      load(s);
+    }
   }
 
   // ---- join
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every copy has landed, every ring is read
+  constexpr int kPlanes = Lds::kPlanes;
+  auto put = [&](int plane) {
 #pragma unroll
-  for (int ms = 0; ms < MS; ++ms)
+    for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) L.red[wave][16 * ms + 4 * kb + i][16 * ct + c16] = acc[ms][ct][i];
+        for (int ct = 0; ct < CT; ++ct) L.red[plane][16 * ms + 4 * kb + i][16 * ct + c16] = acc[ms][ct][i];
+  };
+  if (kPlanes == kPWaves) {
+    put(wave);
+  } else {
+    if (wave >= kPlanes) put(wave - kPlanes);
+    lds_barrier();
+    if (wave < kPlanes) {
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) acc[ms][ct][i] += L.red[wave][16 * ms + 4 * kb + i][16 * ct + c16];
+      put(wave);
+    }
+  }
+  if (with) {
+    auto finish = [&](const Entry& e, int rank, const Operands& o0) {
+      f32x4 d[MS][CT];
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) d[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+      auto add = [&](const Operands& o, int s) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const u32x4 b = rank_mask(o.b[ct], rank - s - 8 * kb);
+#pragma unroll
+          for (int ms = 0; ms < MS; ++ms) d[ms][ct] = mfma16(o.zl[ms], b, mfma16(o.zh[ms], b, d[ms][ct]));
+        }
+      };
+      add(o0, 0);
+      for (int s = 32; s < rank; s += 32) {
+        Operands o;
+        load_operands(e, s, o);
+        add(o, s);
+      }
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * ms + 4 * kb + i;
+          if (e.same >> row & 1) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) L.red[kPlanes][row][16 * ct + c16] = d[ms][ct][i];
+          }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < NE; ++k)
+      if (first[k].same) finish(first[k], rank_first[k], ops[k]);
+    for (int j = 0; left; ++j) {
+      const Entry e = entry(left);
+      if (j % kPWaves != wave) continue;
+      Operands o;
+      load_operands(e, 0, o);
+      finish(e, rank_of(a, e.ad), o);
+    }
+  }
   __syncthreads();
   constexpr int kPairs = 8 * CT;  // column pairs per row
   for (int p = tid; p < 16 * MS * kPairs; p += kPThreads) {
@@ -305,13 +424,13 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
     if (t0 + row >= a.T) break;
     float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-    for (int q = 0; q < kPWaves; ++q) {
+    for (int q = 0; q < kPlanes; ++q) {
       const f32x2 v = *reinterpret_cast<const f32x2*>(&L.red[q][row][c]);
       v0 += v.x;
       v1 += v.y;
     }
     if (with >> row & 1) {
-      const f32x2 v = *reinterpret_cast<const f32x2*>(&L.red[kPWaves][row][c]);
+      const f32x2 v = *reinterpret_cast<const f32x2*>(&L.red[kPlanes][row][c]);
       v0 += v.x;
       v1 += v.y;
     }
@@ -337,7 +456,7 @@ __global__ __launch_bounds__(kPThreads) void project_split_kernel(ProjectArgs a)
 // (h + 1 was complete at the barrier before).
 template <int RS>
 struct TileLds {
-  u32x4 x[2][2][2 * RS][64];  // [group % 2][k half][16-token subtile][lane]
+  u32x4 x[2][2][2 * RS][64];  // [group % 2][k half][16-token subtile][frag_slot]
   u32x4 w[2][2][4][4][64];    // [group % 2][k half][wave tile][column tile][lane]
 };
 
@@ -362,7 +481,7 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
   // the groups are taken in turn from a start that depends on the column
   // tile: rows a multiple of 4 KB apart have one group of every row in the
   // same L2 channel, and blocks in step would all wait for it
-  int gx = 2 * ctile % G, gw = gx;  // next group to load: activations, codes
+  int gx = ctile * G / col_tiles, gw = gx;  // next group to load: activations, codes
 
   // activations: wave w stages subtiles w * RS / 4, ...
   constexpr int kXRows = RS / 4;
@@ -371,7 +490,9 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
   uint32_t xoff[kXRows];
 #pragma unroll
   for (int f = 0; f < kXRows; ++f)
-    xoff[f] = (uint32_t)min(16 * (wave * kXRows + f) + c16, rows - 1) * (uint32_t)(a.ldx * 2) + 16 * kb;
+    xoff[f] = (uint32_t)min(16 * (wave * kXRows + f) + frag_row(lane), rows - 1) * (uint32_t)(a.ldx * 2) +
+              16 * frag_chunk(lane);
+  const int xl = frag_slot(c16, kb);  // where this lane's operand is in a fragment
   // weights: wave w expands column tiles 2 eh, 2 eh + 1 of wave tile ew
   const int ew = wave >> 1, eh = wave & 1;
   const int ewt = min(4 * ctile + ew, geom.n_wt - 1);
@@ -432,7 +553,7 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
 #pragma unroll
   for (int ct = 0; ct < 4; ++ct) bw[0][ct] = L.w[0][0][wc][ct][lane];
 #pragma unroll
-  for (int f = 0; f < kAhead; ++f) av[f] = L.x[0][0][wr * RS + f][lane];
+  for (int f = 0; f < kAhead; ++f) av[f] = L.x[0][0][wr * RS + f][xl];
   // half ks of group i in stage S = i % 2; group i + 1's half ks is written meanwhile, from code slot 1 - S
   auto half = [&](auto S_, auto ks_) {
     constexpr int S = decltype(S_)::value, ks = decltype(ks_)::value;
@@ -442,7 +563,7 @@ __global__ __launch_bounds__(kPThreads, 2) void project_tile_kernel(ProjectArgs 
 #pragma unroll
     for (int ms = 0; ms < RS; ++ms) {
       const int fa = ms + kAhead;
-      av[fa % kRing] = fa < RS ? L.x[S][ks][wr * RS + fa][lane] : L.x[Sn][kn][wr * RS + fa - RS][lane];
+      av[fa % kRing] = fa < RS ? L.x[S][ks][wr * RS + fa][xl] : L.x[Sn][kn][wr * RS + fa - RS][xl];
       if (ms >= RS / 2) {
 #pragma unroll
         for (int q = 0; q < 8 / RS; ++q) {
@@ -557,12 +678,12 @@ size_t project_ws_bytes(int /*N*/, int /*K*/, int R, int T) {
 
 namespace {
 
-template <int MS, int CT>
+template <int MS, int CT, int D, int NE>
 hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * (a.N / 64) * (4 / CT);
   const int64_t blocks = (units + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((project_split_kernel<MS, CT>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
+  hipLaunchKernelGGL((project_split_kernel<MS, CT, D, NE>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -592,10 +713,22 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
     if (k == 1) return launch_tile<4>(a, s);
     return launch_tile<8>(a, s);
   }
-  if (a.T <= 16) return launch_split<1, 1>(a, s);
-  if (a.T <= 32) return launch_split<2, 1>(a, s);
-  if (a.T <= 64) return launch_split<2, 2>(a, s);
-  return launch_split<2, 4>(a, s);
+  static const char* v = getenv("PJS");
+  const int k = v ? atoi(v) : 0;
+  if (k == 1) return launch_split<1, 1, 4, 2>(a, s);
+  if (k == 2) return launch_split<2, 1, 4, 4>(a, s);
+  if (k == 3) return launch_split<2, 2, 4, 4>(a, s);
+  if (k == 4) return launch_split<2, 2, 2, 4>(a, s);
+  if (k == 5) return launch_split<2, 4, 4, 1>(a, s);
+  if (k == 6) return launch_split<2, 4, 2, 1>(a, s);
+  if (k == 7) return launch_split<4, 2, 2, 1>(a, s);
+  if (k == 8) return launch_split<4, 4, 2, 1>(a, s);
+  if (k == 9) return launch_split<1, 2, 4, 2>(a, s);
+  if (k == 10) return launch_split<1, 4, 4, 2>(a, s);
+  if (a.T <= 16) return launch_split<1, 1, 4, 2>(a, s);
+  if (a.T <= 32) return launch_split<2, 1, 4, 4>(a, s);
+  if (a.T <= 64) return launch_split<2, 2, 4, 4>(a, s);
+  return launch_split<4, 4, 2, 1>(a, s);
 }
 
 }  // namespace moe
