@@ -20,7 +20,6 @@
 //   project_tile_kernel   256 x 256 tiles; each weight is expanded once per
 //                         tile to bf16 and shared through LDS by its 256
 //                         rows: many rows, where the matrix cores count
-#include <cstdlib>
 #include <type_traits>
 
 #include "kernels.h"
@@ -88,14 +87,20 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 
 // The adapters' first product. Block: one tile of 16 tokens, 16 ranks, and
 // every `entries`-th distinct adapter of the tile; the eight waves split K in
-// chunks of 128. Grid: token tiles x rank tiles x entries (entries fastest).
-// What counts is latency (a prompt of 4096 tokens reads 64 KB of activations
-// and 64 KB of one adapter a block): the first kHeld chunks of activations
-// are under way before the adapters are known and serve every entry, and an
-// entry's first kHeld chunks of A are under way before its rank is known.
+// chunks of 128 inputs, kHeld of them at a time in the wave's own part of LDS
+// (no barrier: the wave waits for its copies). Grid: token tiles x rank tiles
+// x entries (entries fastest). What counts is latency: the activations are
+// under way before the adapters are known and serve every entry while they
+// are held, and an entry's part of A is under way before its rank is known.
+struct DownLds {
+  static constexpr int kHeld = 2;
+  u32x4 x[kPWaves][kHeld][4][64], a[kPWaves][kHeld][4][64];  // [wave][chunk][32 inputs][frag_slot]
+  float red[kPWaves][16][17];
+};
+
 __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, int entries) {
-  constexpr int kHeld = 2;
-  __shared__ float red[kPWaves][16][17];
+  __shared__ DownLds L;
+  constexpr int kHeld = DownLds::kHeld;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kb = lane >> 4;
@@ -103,52 +108,59 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
   const int entry = blockIdx.x % entries, rt = blockIdx.x / entries % n_rt;
   const int t0 = blockIdx.x / entries / n_rt * 16;
   const int mine = adapter_at(a, t0 + c16);
-  const uint16_t* x = a.x + (int64_t)min(t0 + c16, a.T - 1) * a.ldx + 8 * kb;
-  const int chunks = a.K / 128;
-  auto load = [&](const uint16_t* p, int c, u32x4 (&v)[4]) {
-    c = min(c, chunks - 1);  // (a chunk past the last is not used)
+  const int chunks = a.K / 128, batches = (chunks + kPWaves * kHeld - 1) / (kPWaves * kHeld);
+  const int slot = frag_slot(c16, kb);
+  // wave w's chunks of a batch: w, w + 8 (chunks past the last repeat it and are not used)
+  auto chunk = [&](int batch, int h) { return batch * kPWaves * kHeld + kPWaves * h + wave; };
+  auto copy = [&](rsrc_t r, uint32_t off, int batch, u32x4 (&dst)[kHeld][4][64]) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = *reinterpret_cast<const u32x4*>(p + 128 * c + 32 * s);
+    for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        bload_lds(r, &dst[h][s][0], off + 64 * s, (uint32_t)min(chunk(batch, h), chunks - 1) * 256);
   };
-  u32x4 xv[kHeld][4];
-#pragma unroll
-  for (int h = 0; h < kHeld; ++h) load(x, wave + kPWaves * h, xv[h]);
-  __builtin_amdgcn_sched_barrier(0);
+  const int rows = min(16, a.T - t0), ranks = min(16, a.R - 16 * rt);
+  const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
+  const uint32_t xoff = (uint32_t)min(frag_row(lane), rows - 1) * (uint32_t)(a.ldx * 2) + 16 * frag_chunk(lane);
+  const uint32_t aoff = (uint32_t)min(frag_row(lane), ranks - 1) * (uint32_t)(a.K * 2) + 16 * frag_chunk(lane);
+  int held = 0;
+  copy(xres, xoff, 0, L.x[wave]);
   uint64_t rem = __ballot(mine >= 0) & 0xFFFFull;
   for (int j = 0; rem; ++j) {
     const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
     const uint64_t same = __ballot(mine == ad) & 0xFFFFull;
     rem &= ~same;
     if (j % entries != entry) continue;
-    const uint16_t* A = a.A + ((int64_t)ad * a.R + min(16 * rt + c16, a.R - 1)) * a.K + 8 * kb;
-    u32x4 av[kHeld][4];
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) load(A, wave + kPWaves * h, av[h]);
-    const int rank = rank_of(a, ad);
-    const float scale = a.scales ? a.scales[ad] : 1.f;
+    const rsrc_t ares = make_rsrc(a.A + ((int64_t)ad * a.R + 16 * rt) * a.K, (uint32_t)ranks * (uint32_t)a.K * 2);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if (wave + kPWaves * h < chunks) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) acc = mfma16(xv[h][s], av[h][s], acc);
+    int rank = 0;
+    float scale = 1.f;
+    for (int b = 0; b < batches; ++b) {
+      if (held != b) copy(xres, xoff, b, L.x[wave]);
+      held = b;
+      copy(ares, aoff, b, L.a[wave]);
+      if (b == 0) {
+        rank = rank_of(a, ad);
+        if (a.scales) scale = a.scales[ad];
       }
-    for (int c = wave + kPWaves * kHeld; c < chunks; c += kPWaves) {
-      u32x4 xc[4], ac[4];
-      load(x, c, xc);
-      load(A, c, ac);
+      wait_loads<0>();
 #pragma unroll
-      for (int s = 0; s < 4; ++s) acc = mfma16(xc[s], ac[s], acc);
+      for (int h = 0; h < kHeld; ++h)
+        if (chunk(b, h) < chunks) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) acc = mfma16(L.x[wave][h][s][slot], L.a[wave][h][s][slot], acc);
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next copies
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][4 * kb + i][c16] = acc[i];
+    for (int i = 0; i < 4; ++i) L.red[wave][4 * kb + i][c16] = acc[i];
     __syncthreads();
     if (tid < 256) {
       const int row = tid >> 4, r = 16 * rt + (tid & 15);
       if ((same >> row & 1) && r < a.R) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kPWaves; ++w) v += red[w][row][tid & 15];
+        for (int w = 0; w < kPWaves; ++w) v += L.red[w][row][tid & 15];
         v *= scale;
         if (r >= rank) v = 0.f;
         const uint16_t hi = f2bf(v);
@@ -159,6 +171,7 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
     }
     __syncthreads();
   }
+  wait_loads<0>();  // no copy outlives its block
 }
 
 // Few rows: a block owns 16 MS tokens and 16 CT columns; wave w takes the
@@ -702,33 +715,41 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   if (a.adapter_of) {
     const int64_t tiles = (int64_t)((a.T + 15) / 16) * ((a.R + 15) / 16);
     int entries = min(min(16, a.n), a.T);
-    while (entries > 1 && tiles * entries > 512) entries = (entries + 1) / 2;
+    while (entries > 1 && tiles * entries > 256) entries = (entries + 1) / 2;
     if (tiles * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * entries)), dim3(kPThreads), 0, s, a, entries);
   }
-  const bool tile = a.gemm == 2 || (a.gemm == 0 && a.T >= 1024);
-  if (tile) {
-    static const char* v = getenv("PJV");
-    const int k = v ? atoi(v) : 0;
-    if (k == 1) return launch_tile<4>(a, s);
-    return launch_tile<8>(a, s);
+  // The kernel and tile that take least, from what each measured at K = 2048
+  // (all of them grow with K alike): a start and a time per round of 256
+  // units, one for each compute unit, in tenths of a microsecond. Small tiles
+  // start fastest and lose when there are many: 64 tokens by 4096 columns
+  // take 15.2 us in 16 x 16 tiles and 5.3 in 32 x 32, 500 by 2048 31 and 10.3
+  // (64 x 64), 1024 by 4096 40 in 64 x 64 and 33 in 128 x 256, 4096 by 4096
+  // 77 in 128 x 256 and 62 in 256 x 256.
+  struct Tiling {
+    int rows, cols, start, round;
+    hipError_t (*launch)(const ProjectArgs&, hipStream_t);
+  };
+  static const Tiling tilings[] = {
+      {16, 16, 22, 20, launch_split<1, 1, 4, 2>},   {16, 32, 24, 20, launch_split<1, 2, 4, 2>},
+      {16, 64, 15, 36, launch_split<1, 4, 4, 2>},   {32, 32, 12, 39, launch_split<2, 2, 2, 4>},
+      {32, 64, 6, 57, launch_split<2, 4, 2, 1>},    {64, 64, 0, 100, launch_split<4, 4, 2, 1>},
+      {128, 256, 0, 330, launch_tile<4>},           {256, 256, 0, 600, launch_tile<8>},
+  };
+  constexpr int kSplits = 6, kAll = 8;
+  const int first = a.gemm == 2 ? kSplits : 0, last = a.gemm == 1 ? kSplits : kAll;
+  const Tiling* best = nullptr;
+  int64_t least = 0;
+  for (int i = first; i < last; ++i) {
+    const Tiling& t = tilings[i];
+    const int64_t units = (int64_t)((a.T + t.rows - 1) / t.rows) * ((a.N + t.cols - 1) / t.cols);
+    const int64_t cost = t.start + (units + 255) / 256 * t.round;
+    if (!best || cost < least) {
+      best = &t;
+      least = cost;
+    }
   }
-  static const char* v = getenv("PJS");
-  const int k = v ? atoi(v) : 0;
-  if (k == 1) return launch_split<1, 1, 4, 2>(a, s);
-  if (k == 2) return launch_split<2, 1, 4, 4>(a, s);
-  if (k == 3) return launch_split<2, 2, 4, 4>(a, s);
-  if (k == 4) return launch_split<2, 2, 2, 4>(a, s);
-  if (k == 5) return launch_split<2, 4, 4, 1>(a, s);
-  if (k == 6) return launch_split<2, 4, 2, 1>(a, s);
-  if (k == 7) return launch_split<4, 2, 2, 1>(a, s);
-  if (k == 8) return launch_split<4, 4, 2, 1>(a, s);
-  if (k == 9) return launch_split<1, 2, 4, 2>(a, s);
-  if (k == 10) return launch_split<1, 4, 4, 2>(a, s);
-  if (a.T <= 16) return launch_split<1, 1, 4, 2>(a, s);
-  if (a.T <= 32) return launch_split<2, 1, 4, 4>(a, s);
-  if (a.T <= 64) return launch_split<2, 2, 4, 4>(a, s);
-  return launch_split<4, 4, 2, 1>(a, s);
+  return best->launch(a, s);
 }
 
 }  // namespace moe
