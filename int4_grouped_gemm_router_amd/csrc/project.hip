@@ -85,11 +85,11 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 
 }  // namespace
 
-// The adapters' first product. Block: one tile of 16 tokens, 16 ranks, and
-// every `entries`-th distinct adapter of the tile; the eight waves split K in
-// chunks of 128 inputs, kHeld of them at a time in the wave's own part of LDS
-// (no barrier: the wave waits for its copies). Grid: token tiles x rank tiles
-// x entries (entries fastest). What counts is latency: the activations are
+// The adapters' first product. Block: one tile of 16 tokens, every
+// `entries`-th distinct adapter of the tile and every `parts`-th 16 ranks of
+// it; the eight waves split K in chunks of 128 inputs, kHeld of them at a time
+// in the wave's own part of LDS (no barrier: the wave waits for its copies).
+// Grid: token tiles x parts x entries (entries fastest). What counts is latency: the activations are
 // under way before the adapters are known and serve every entry while they
 // are held, and an entry's part of A is under way before its rank is known.
 struct DownLds {
@@ -98,15 +98,15 @@ struct DownLds {
   float red[kPWaves][16][17];
 };
 
-__global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, int entries) {
+__global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, int entries, int parts) {
   __shared__ DownLds L;
   constexpr int kHeld = DownLds::kHeld;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kb = lane >> 4;
   const int n_rt = (a.R + 15) / 16;
-  const int entry = blockIdx.x % entries, rt = blockIdx.x / entries % n_rt;
-  const int t0 = blockIdx.x / entries / n_rt * 16;
+  const int entry = blockIdx.x % entries, part = blockIdx.x / entries % parts;
+  const int t0 = blockIdx.x / entries / parts * 16;
   const int mine = adapter_at(a, t0 + c16);
   const int chunks = a.K / 128, batches = (chunks + kPWaves * kHeld - 1) / (kPWaves * kHeld);
   const int slot = frag_slot(c16, kb);
@@ -119,10 +119,9 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
       for (int s = 0; s < 4; ++s)
         bload_lds(r, &dst[h][s][0], off + 64 * s, (uint32_t)min(chunk(batch, h), chunks - 1) * 256);
   };
-  const int rows = min(16, a.T - t0), ranks = min(16, a.R - 16 * rt);
+  const int rows = min(16, a.T - t0);
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
   const uint32_t xoff = (uint32_t)min(frag_row(lane), rows - 1) * (uint32_t)(a.ldx * 2) + 16 * frag_chunk(lane);
-  const uint32_t aoff = (uint32_t)min(frag_row(lane), ranks - 1) * (uint32_t)(a.K * 2) + 16 * frag_chunk(lane);
   int held = 0;
   copy(xres, xoff, 0, L.x[wave]);
   uint64_t rem = __ballot(mine >= 0) & 0xFFFFull;
@@ -131,45 +130,49 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
     const uint64_t same = __ballot(mine == ad) & 0xFFFFull;
     rem &= ~same;
     if (j % entries != entry) continue;
-    const rsrc_t ares = make_rsrc(a.A + ((int64_t)ad * a.R + 16 * rt) * a.K, (uint32_t)ranks * (uint32_t)a.K * 2);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int rank = 0;
-    float scale = 1.f;
-    for (int b = 0; b < batches; ++b) {
-      if (held != b) copy(xres, xoff, b, L.x[wave]);
-      held = b;
-      copy(ares, aoff, b, L.a[wave]);
-      if (b == 0) {
-        rank = rank_of(a, ad);
-        if (a.scales) scale = a.scales[ad];
-      }
-      wait_loads<0>();
-#pragma unroll
-      for (int h = 0; h < kHeld; ++h)
-        if (chunk(b, h) < chunks) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) acc = mfma16(L.x[wave][h][s][slot], L.a[wave][h][s][slot], acc);
+    for (int rt = part; rt < n_rt; rt += parts) {
+      const int ranks = min(16, a.R - 16 * rt);
+      const rsrc_t ares = make_rsrc(a.A + ((int64_t)ad * a.R + 16 * rt) * a.K, (uint32_t)ranks * (uint32_t)a.K * 2);
+      const uint32_t aoff = (uint32_t)min(frag_row(lane), ranks - 1) * (uint32_t)(a.K * 2) + 16 * frag_chunk(lane);
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      int rank = 0;
+      float scale = 1.f;
+      for (int b = 0; b < batches; ++b) {
+        if (held != b) copy(xres, xoff, b, L.x[wave]);
+        held = b;
+        copy(ares, aoff, b, L.a[wave]);
+        if (b == 0) {
+          rank = rank_of(a, ad);
+          if (a.scales) scale = a.scales[ad];
         }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next copies
-    }
+        wait_loads<0>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) L.red[wave][4 * kb + i][c16] = acc[i];
-    __syncthreads();
-    if (tid < 256) {
-      const int row = tid >> 4, r = 16 * rt + (tid & 15);
-      if ((same >> row & 1) && r < a.R) {
-        float v = 0.f;
+        for (int h = 0; h < kHeld; ++h)
+          if (chunk(b, h) < chunks) {
 #pragma unroll
-        for (int w = 0; w < kPWaves; ++w) v += L.red[w][row][tid & 15];
-        v *= scale;
-        if (r >= rank) v = 0.f;
-        const uint16_t hi = f2bf(v);
-        const int64_t at = (int64_t)(t0 + row) * a.R + r;
-        z_hi(a)[at] = hi;
-        z_lo(a)[at] = f2bf(v - bf16f(hi));
+            for (int s = 0; s < 4; ++s) acc = mfma16(L.x[wave][h][s][slot], L.a[wave][h][s][slot], acc);
+          }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next copies
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) L.red[wave][4 * kb + i][c16] = acc[i];
+      __syncthreads();
+      if (tid < 256) {
+        const int row = tid >> 4, r = 16 * rt + (tid & 15);
+        if ((same >> row & 1) && r < a.R) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < kPWaves; ++w) v += L.red[w][row][tid & 15];
+          v *= scale;
+          if (r >= rank) v = 0.f;
+          const uint16_t hi = f2bf(v);
+          const int64_t at = (int64_t)(t0 + row) * a.R + r;
+          z_hi(a)[at] = hi;
+          z_lo(a)[at] = f2bf(v - bf16f(hi));
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   wait_loads<0>();  // no copy outlives its block
 }
@@ -713,11 +716,15 @@ hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
 
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   if (a.adapter_of) {
-    const int64_t tiles = (int64_t)((a.T + 15) / 16) * ((a.R + 15) / 16);
-    int entries = min(min(16, a.n), a.T);
-    while (entries > 1 && tiles * entries > 256) entries = (entries + 1) / 2;
-    if (tiles * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * entries)), dim3(kPThreads), 0, s, a, entries);
+    // blocks for each rank tile and for several adapters of a token tile while
+    // there are compute units for them
+    const int64_t tiles = (a.T + 15) / 16;
+    int parts = (a.R + 15) / 16, entries = min(min(16, a.n), a.T);
+    while (parts > 1 && tiles * parts > 256) parts = (parts + 1) / 2;
+    while (entries > 1 && tiles * parts * entries > 256) entries = (entries + 1) / 2;
+    if (tiles * parts * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * parts * entries)), dim3(kPThreads), 0, s, a, entries,
+                       parts);
   }
   // The kernel and tile that take least, from what each measured at K = 2048
   // (all of them grow with K alike): a start and a time per round of 256
