@@ -188,6 +188,11 @@ GateArgs gate_args(const moe_gate* g) {
   return a;
 }
 
+// (never 0, so that a caller's buffer has an address)
+size_t gate_ws_bytes(const moe_gate* g, int T) {
+  return std::max<size_t>((gate_counts_bytes(g->E, T) + 255) / 256 * 256, 256);
+}
+
 // A gate for the layer: the layer's own dims, routed by the gate.
 int check_layer_gate(const moe_dims* dims, const moe_gate* g) {
   if (!dims) return MOE_EINVAL;
@@ -677,8 +682,7 @@ int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes) {
   if (rc != MOE_OK) return rc;
   const moe_dims d = gate_dims(gate);
   if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
-  int32_t* ch;
-  *bytes = route_ws(&d, std::max(T, 1), nullptr, &ch);
+  *bytes = gate_ws_bytes(gate, T);
   return MOE_OK;
 }
 
@@ -691,32 +695,28 @@ int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const 
   if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!logits || !route_out_ok(out) || !ws || !al4(logits) || !al16(ws)) return MOE_EINVAL;
-  int32_t* chunk_hist;
-  if (ws_bytes < route_ws(&d, T, ws, &chunk_hist)) return MOE_EWORKSPACE;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (launch_fill_zero(chunk_hist, n_chunks(&d, T) * d.E, s) != hipSuccess) return MOE_EHIP;
+  if (ws_bytes < gate_ws_bytes(gate, T)) return MOE_EWORKSPACE;
   GateArgs ga = gate_args(gate);
   ga.partial = logits;
   ga.splits = 1;
   ga.topk_idx = out->topk_idx;
   ga.topk_w = out->topk_w;
-  ga.chunk_hist = chunk_hist;
+  ga.counts = static_cast<uint16_t*>(ws);
   ga.T = T;
-  if (launch_gate_topk(ga, s) != hipSuccess) return MOE_EHIP;
-  ScatterArgs sa{};
-  sa.topk_idx = out->topk_idx;
-  sa.chunk_hist = chunk_hist;
-  sa.hist = out->hist;
-  sa.offsets = out->offsets;
-  sa.perm = out->perm;
-  sa.inv_perm = out->inv_perm;
-  sa.block_map = out->block_map;
-  sa.num_blocks = out->num_blocks;
-  sa.T = T;
-  sa.E = d.E;
-  sa.k = d.top_k;
-  sa.block_m = d.block_m;
-  return hip_status(launch_scan_scatter(sa, s));
+  GateScatter sc{};
+  sc.topk_idx = out->topk_idx;
+  sc.counts = ga.counts;
+  sc.hist = out->hist;
+  sc.offsets = out->offsets;
+  sc.perm = out->perm;
+  sc.inv_perm = out->inv_perm;
+  sc.block_map = out->block_map;
+  sc.num_blocks = out->num_blocks;
+  sc.T = T;
+  sc.E = d.E;
+  sc.k = d.top_k;
+  sc.block_m = d.block_m;
+  return hip_status(launch_gate_route(ga, sc, static_cast<hipStream_t>(stream)));
 }
 
 int moe_prefill_layer_gated(const moe_dims* dims, const moe_gate* gate, const moe_layer_weights* w,
