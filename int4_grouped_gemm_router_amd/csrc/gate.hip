@@ -14,7 +14,7 @@
 // one in a hundred) is decided again in 64 bits.
 //
 // Kernels:
-//   gate_topk     one wave per token, four consecutive experts a lane; for
+//   gate_topk     sixteen lanes per token, four tokens a wave; for
 //                 moe_route_gated also the expert counts of each 32 tokens
 //   gate_scatter  per 128 tokens: totals and bases per expert from those
 //                 counts, a stable scatter, and a share of the block map
@@ -28,7 +28,8 @@ namespace {
 
 constexpr int kGateWaves = 16;
 constexpr int kGateThreads = 64 * kGateWaves;
-constexpr int kCountTokens = 32;                  // tokens per row of counts
+constexpr int kTopkWaves = 8;                     // of a gate_topk block
+constexpr int kCountTokens = 4 * kTopkWaves;      // tokens per row of counts
 constexpr int kScatterTokens = 4 * kCountTokens;  // tokens per scatter block
 constexpr int kGateSmallT = 64;
 
@@ -63,11 +64,42 @@ __device__ inline double wave_sum_f64(double v) {
   return v;
 }
 
-__device__ inline float wave_max_f32(float v) {  // v no NaN
-  const uint32_t k = wave_max_u32(logit_key(v));
-  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+// Reductions over the 16 lanes of a row, returned to each of them: lane ^ 1,
+// lane ^ 2, mirror within 8, mirror within 16.
+template <class F>
+__device__ inline float row_reduce(float v, F f) {
+  v = f(v, __uint_as_float(dpp<0xB1>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(dpp<0x4E>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(dpp<0x141>(__float_as_uint(v))));
+  return f(v, __uint_as_float(dpp<0x140>(__float_as_uint(v))));
 }
-__device__ inline float wave_min_f32(float v) { return -wave_max_f32(-v); }
+__device__ inline float row_max(float v) {
+  return row_reduce(v, [](float x, float y) { return fmaxf(x, y); });
+}
+__device__ inline float row_min(float v) {
+  return row_reduce(v, [](float x, float y) { return fminf(x, y); });
+}
+__device__ inline float row_sum(float v) {
+  return row_reduce(v, [](float x, float y) { return x + y; });
+}
+__device__ inline uint32_t row_max_u32(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  return max(v, dpp<0x140>(v));
+}
+template <int CTRL>
+__device__ inline double dpp_f64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = dpp<CTRL>((uint32_t)u), hi = dpp<CTRL>((uint32_t)(u >> 32));
+  return __longlong_as_double((long long)(hi << 32 | lo));
+}
+__device__ inline double row_sum_f64(double v) {
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x141>(v);
+  return v + dpp_f64<0x140>(v);
+}
 
 // Group of expert e: e / size as the high half of e * ceil(2^32 / size), exact
 // for e < 256 (size 1 has no such factor).
@@ -176,193 +208,242 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
   w = (float)(v * (double)a.scale);
 }
 
-// One token's selection (lane j < k: the expert of rank j and its weight).
-// gl: 256 floats of LDS of this wave's own. bmax: the largest |bias|.
-__device__ void gate_select(const GateArgs& a, const float (&l)[4], const float (&b)[4], float bmax, float* gl,
-                            int& sel, float& w) {
-  const int lane = threadIdx.x & 63, E = a.E, k = a.k;
-  const float mx = wave_max_f32(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+// The sum over the router's K splits plus the router's bias: logits of token
+// t, N consecutive experts from e on (those from E on are not read).
+template <int N>
+__device__ inline void load_logits(const GateArgs& a, int64_t t, int e, float (&v)[N]) {
+  const int E = a.E;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  if (N == 4 && a.vectors) {
+    if (e < E)
+      for (int sp = 0; sp < a.splits; ++sp) {
+        const f32x4 p = *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)sp * a.T + t) * E + e);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += p[i];
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e + i < E)
+        for (int sp = 0; sp < a.splits; ++sp) v[i] += a.partial[((int64_t)sp * a.T + t) * E + e + i];
+  }
+  if (a.rbias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e + i < E) v[i] += a.rbias[e + i];
+  }
+}
+
+// A wave's own LDS, per token: the keys for the groups (one word of padding
+// per sixteen spreads the groups over the banks), the groups' rank keys and
+// whether they are kept; then the logits.
+struct SelectLds {
+  float v[4][256 + 16];
+  float group[4][kMaxGateGroups];
+  uint8_t kept[4][kMaxGateGroups];
+};
+__device__ inline int key_at(int e) { return e + (e >> 4); }
+
+// Four tokens' selections, t0 + lane / 16 each: lane c = lane % 16 < k gets
+// the expert of rank c and its weight. Lane c holds the experts
+// 64 j + 4 c + u (j < NJ, u < 4) of its token. KD: at least min(k, 15) + 1.
+template <int NJ, int KD>
+__device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ], float bmax, SelectLds& L, int& sel,
+                            float& w) {
+  constexpr int NS = 4 * NJ;
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int E = a.E, k = a.k;
+  const int64_t t = min(t0 + q, a.T - 1);
+  float l[NS];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    float v[4];
+    load_logits(a, t, 64 * j + 4 * c, v);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = 64 * j + 4 * c + u;
+      if (a.logits_out && e < E && t0 + q < a.T) a.logits_out[t * E + e] = v[u];
+      l[4 * j + u] = e < E && v[u] == v[u] ? v[u] : -INFINITY;
+    }
+  }
+  float mx = l[0];
+#pragma unroll
+  for (int i = 1; i < NS; ++i) mx = fmaxf(mx, l[i]);
+  mx = row_max(mx);
   // fp32 scores with the hardware exponential and reciprocal. Errors: the
   // exponent's product and the difference to the maximum round by 2^-24 of
   // their size, which moves e^-d by at most 2^-24 d e^-d < 2^-25 absolute;
   // the exponential, the reciprocal and the sum of up to 256 terms add a few
   // 2^-24 of the value, and adding the bias 2^-24 of the key. All together
-  // stay below 2^-20 of (largest score + largest bias), the bound `err`.
-  float s[4], top = 1.0f;
+  // stay below 2^-20 of the range, largest score + largest bias.
+  float s[NS], top = 1.0f, z = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float d = a.sigmoid ? -l[i] : (l[i] == mx ? 0.f : l[i] - mx);
-    const float p = __expf(d);
+  for (int i = 0; i < NS; ++i) {
+    const float p = __expf(a.sigmoid ? -l[i] : (l[i] == mx ? 0.f : l[i] - mx));
     s[i] = l[i] == -INFINITY ? 0.f : (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + p) : p);
+    z += s[i];
   }
   if (!a.sigmoid) {
-    const float z = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+    z = row_sum(z);
     top = z > 0.f ? 1.0f / z : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] *= top;
+    for (int i = 0; i < NS; ++i) s[i] *= top;
   }
-  const float err = 0x1p-20f * (top + bmax);
-  float hv[4];     // keys, larger first after the sort
-  uint32_t hk[4], he[4];
+  const float range = top + bmax;
+  const float err = 0x1p-20f * range;
+  bool near = !(range < 1e30f);  // a decision the fp32 keys cannot settle
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hv[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-    if (!(hv[i] == hv[i])) hv[i] = -INFINITY;
-    he[i] = 4 * lane + i;
-    hk[i] = (int)he[i] < E ? logit_key(hv[i]) : 0u;
+  for (int i = 0; i < NS; ++i) {
+    s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
+    if (!(s[i] == s[i])) s[i] = -INFINITY;
   }
-  bool near = false;  // a decision the fp32 keys cannot settle
+  uint32_t in = ~0u;  // bit i: expert i's group is kept
   if (a.n_groups > 1) {
-    // 2^lg lanes per group, each over every 2^lg-th expert of it
-    const int size = a.group_size, lg = a.group_lanes_log2, g = lane >> lg, p = lane & ((1 << lg) - 1);
+    // group g: 2^lg lanes (up to sixteen groups), or lane g % 16
+    const int size = a.group_size, lg = a.group_lanes_log2, p = c & ((1 << lg) - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((int)he[i] < E) gl[he[i]] = hv[i];
+    for (int i = 0; i < NS; ++i) L.v[q][key_at(64 * (i >> 2) + 4 * c + (i & 3))] = s[i];
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    float m1 = -INFINITY, m2 = -INFINITY;
-    if (g < a.n_groups)
+    float lo = INFINITY, hi = -INFINITY;
+    for (int g = c >> lg; g < a.n_groups; g += 16) {
+      float m1 = -INFINITY, m2 = -INFINITY;
       for (int i = p; i < size; i += 1 << lg) {
-        const float v = gl[g * size + i];
+        const float v = L.v[q][key_at(g * size + i)];
         m2 = fmaxf(m2, fminf(m1, v));
         m1 = fmaxf(m1, v);
       }
-    for (int o = 1; o < 1 << lg; o <<= 1) {
-      const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
-      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-      m1 = fmaxf(m1, o1);
+      for (int o = 1; o < 1 << lg; o <<= 1) {
+        const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
+        m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+        m1 = fmaxf(m1, o1);
+      }
+      if (p == 0) L.group[q][g] = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    const float gs = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
-    int rank = 0;
-    for (int q = 0; q < a.n_groups; ++q) {
-      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gs), q << lg));
-      rank += v > gs || (v == gs && q < g);
+    for (int g = c; g < a.n_groups; g += 16) {
+      const float mine = L.group[q][g];
+      int rank = 0;
+      for (int o = 0; o < a.n_groups; ++o) {
+        const float v = L.group[q][o];
+        rank += v > mine || (v == mine && o < g);
+      }
+      const bool kept = rank < a.topk_groups;
+      L.kept[q][g] = kept;
+      if (kept)
+        lo = fminf(lo, mine);
+      else
+        hi = fmaxf(hi, mine);
     }
-    const bool in = g < a.n_groups && rank < a.topk_groups, out = g < a.n_groups && rank >= a.topk_groups;
-    if (a.topk_groups < a.n_groups) {
-      const float lo = wave_min_f32(in ? gs : INFINITY), hi = wave_max_f32(out ? gs : -INFINITY);
-      near = hi > -INFINITY && !(lo - hi > 4.0f * err);
-    }
-    const uint64_t kept = __ballot(in);
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    lo = row_min(lo);
+    hi = row_max(hi);
+    near |= hi > -INFINITY && !(lo - hi > 4.0f * err);
+    in = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if ((int)he[i] < E && !(kept >> (group_of(a, (int)he[i]) << lg) & 1)) hk[i] = 0u;
+    for (int i = 0; i < NS; ++i) {
+      const int e = 64 * (i >> 2) + 4 * c + (i & 3);
+      in |= (e < E && L.kept[q][group_of(a, min(e, E - 1))] ? 1u : 0u) << i;
+    }
   }
-  // the lane's four in order: larger key first, equal keys by expert
-  auto order = [&](int x, int y) {
-    const bool sw = hk[y] > hk[x] || (hk[y] == hk[x] && he[y] < he[x]);
-    const uint32_t k0 = hk[x], e0 = he[x];
-    const float v0 = hv[x];
-    hk[x] = sw ? hk[y] : k0;
-    he[x] = sw ? he[y] : e0;
-    hv[x] = sw ? hv[y] : v0;
-    hk[y] = sw ? k0 : hk[y];
-    he[y] = sw ? e0 : he[y];
-    hv[y] = sw ? v0 : hv[y];
-  };
-  float sl[4] = {l[0], l[1], l[2], l[3]};
-  order(0, 1);
-  order(2, 3);
-  order(0, 2);
-  order(1, 3);
-  order(1, 2);
-  sel = 0;
-  float sel_k = -INFINITY;
-  uint32_t last = 0;  // the order key of rank k, 0: none
+  // keys as 24-bit fixed point over the range (0: masked or out of the
+  // running), then the lane's slot and the lane: all keys of a token differ
+  const float scale = 16777000.0f / (range + bmax);
+  uint32_t key[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const uint32_t v = s[i] == -INFINITY || !(in >> i & 1) ? 0u : 1u + (uint32_t)(fmaxf(s[i] + bmax, 0.f) * scale);
+    key[i] = v << 8 | (uint32_t)(i << 4) | (uint32_t)c;
+  }
+  // the lane's keys in descending order
+#pragma unroll
+  for (int n = 2; n <= NS; n *= 2)
+#pragma unroll
+    for (int j = n / 2; j > 0; j /= 2)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int o = i ^ j;
+        if (o > i) {
+          const uint32_t x = max(key[i], key[o]), y = min(key[i], key[o]);
+          key[i] = (i & n) == 0 ? x : y;
+          key[o] = (i & n) == 0 ? y : x;
+        }
+      }
+  // k + 1 rounds: the row's largest head; its lane drops it
+  constexpr int ND = NS < KD ? NS : KD;
+  uint32_t mine = 0, next = 0;  // the keys of rank c and c + 1
   for (int r = 0; r <= k; ++r) {
-    const uint32_t m = wave_max_u32(hk[0]);
-    if (r == k) {
-      last = m;
-      break;
-    }
-    const bool at_max = hk[0] == m;
-    uint64_t cand = __ballot(at_max);
-    // (equal keys: lanes hold consecutive experts, so the lowest lane has the lowest)
-    const int win = __builtin_ctzll(cand);
-    const int we = __builtin_amdgcn_readlane((int)he[0], win);
-    const float wv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hv[0]), win));
-    if (lane == r) {
-      sel = we;
-      sel_k = wv;
-    }
-    if (lane == win) {
-      hk[0] = hk[1];
-      hk[1] = hk[2];
-      hk[2] = hk[3];
-      hk[3] = 0u;
-      he[0] = he[1];
-      he[1] = he[2];
-      he[2] = he[3];
-      hv[0] = hv[1];
-      hv[1] = hv[2];
-      hv[2] = hv[3];
-    }
+    const uint32_t m = row_max_u32(key[0]);
+    mine = c == r ? m : mine;
+    next = c == r - 1 ? m : next;
+    const bool own = key[0] == m;
+#pragma unroll
+    for (int i = 0; i + 1 < ND; ++i) key[i] = own ? key[i + 1] : key[i];
+    if constexpr (ND == NS) key[NS - 1] = own ? 0u : key[NS - 1];
   }
-  const float last_v = last ? __uint_as_float(last & 0x80000000u ? last & 0x7FFFFFFFu : ~last) : -INFINITY;
-  const float next_v = lane + 1 < k ? __shfl_down(sel_k, 1) : last_v;
-  near |= lane < k && next_v > -INFINITY && !(sel_k - next_v > 2.0f * err);
+  // twice the bound in steps of the fixed point (2^-20 of the range is 8 to
+  // 16 of 2^24 steps over range + bias), and the steps the keys were cut by
+  constexpr uint32_t kNear = 36;
+  const uint32_t vm = mine >> 8, vn = next >> 8;
+  if (c < k) near |= vm == 0 || (vn > 0 && vm - vn <= kNear);
+  sel = 64 * (int)(mine >> 6 & 3) + 4 * (int)(mine & 15) + (int)(mine >> 4 & 3);
   // the weights in 64 bits from the selected logits; where the fp32 sum over
   // the experts is used (softmax, not renormalised) it errs by a few 2^-24
-  const int src = sel >> 2, sub = sel & 3;
-  const float c0 = __shfl(sl[0], src), c1 = __shfl(sl[1], src), c2 = __shfl(sl[2], src), c3 = __shfl(sl[3], src);
-  const float lsel = sub == 0 ? c0 : sub == 1 ? c1 : sub == 2 ? c2 : c3;
-  if (__ballot(near)) {
-    gate_select_exact(a, l, b, mx, sel, w);
-    return;
-  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    *reinterpret_cast<f32x4*>(&L.v[q][64 * j + 4 * c]) = f32x4{l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
   double v = 0.0;
-  if (lane < k && sel_k > -INFINITY) {
-    const double e = exp(a.sigmoid ? -(double)lsel : (lsel == mx ? 0.0 : (double)lsel - (double)mx));
+  if (c < k) {
+    const float x = L.v[q][sel];
+    const double e = exp(a.sigmoid ? -(double)x : (x == mx ? 0.0 : (double)x - (double)mx));
     v = a.sigmoid ? 1.0 / (1.0 + e) : e;
   }
   if (a.renorm) {
-    double z = v;
-    for (int o = 1; o < 16; o <<= 1) z += __shfl_xor(z, o);  // k <= 16: the first row of lanes
-    v = z > 0.0 ? v / z : 0.0;
+    const double sum = row_sum_f64(v);
+    v = sum > 0.0 ? v / sum : 0.0;
   } else if (!a.sigmoid) {
     v *= (double)top;
   }
   w = (float)(v * (double)a.scale);
-}
-
-// The lane's four logits of token t (masked: -inf) and, once, its biases.
-__device__ inline void load_logits(const GateArgs& a, int64_t t, float (&l)[4]) {
-  const int lane = threadIdx.x & 63, e = 4 * lane, E = a.E;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (a.vectors) {
-    if (e < E)
-      for (int sp = 0; sp < a.splits; ++sp) {
-        const f32x4 p = *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)sp * a.T + t) * E + e);
+  // in doubt: those tokens again, one at a time
+  uint64_t doubt = __ballot(near && t0 + q < a.T);
+  while (doubt) {
+    const int row = __builtin_ctzll(doubt) >> 4;
+    doubt &= ~(0xFFFFull << (16 * row));
+    float l4[4], b4[4], top4;
+    load_logits(a, t0 + row, 4 * lane, l4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += p[i];
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e + i < E)
-        for (int sp = 0; sp < a.splits; ++sp) v[i] += a.partial[((int64_t)sp * a.T + t) * E + e + i];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (e + i < E) {
-      if (a.rbias) v[i] += a.rbias[e + i];
-      if (a.logits_out) a.logits_out[t * E + e + i] = v[i];
-      l[i] = v[i] == v[i] ? v[i] : -INFINITY;
-    } else {
-      l[i] = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (!(e < E && l4[i] == l4[i])) l4[i] = -INFINITY;
+      b4[i] = a.balance && e < E ? a.balance[e] : 0.f;
+    }
+    top4 = __shfl(mx, 16 * row);
+    int se;
+    float we;
+    gate_select_exact(a, l4, b4, top4, se, we);
+    se = __shfl(se, c);
+    we = __shfl(we, c);
+    if (q == row) {
+      sel = se;
+      w = we;
     }
   }
 }
 
-__device__ inline float load_biases(const GateArgs& a, float (&b)[4]) {
-  const int e = 4 * (threadIdx.x & 63);
+// The lane's biases and the largest magnitude among all.
+template <int NJ>
+__device__ inline float load_biases(const GateArgs& a, float (&b)[4 * NJ]) {
+  const int c = threadIdx.x & 15;
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    b[i] = a.balance && e + i < a.E ? a.balance[e + i] : 0.f;
-    m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);  // (a NaN bias is the largest, and leaves every token near)
+  for (int i = 0; i < 4 * NJ; ++i) {
+    const int e = 64 * (i >> 2) + 4 * c + (i & 3);
+    b[i] = a.balance && e < a.E ? a.balance[e] : 0.f;
+    m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);  // (a NaN bias is the largest, and leaves every token in doubt)
   }
-  return a.balance ? __uint_as_float(wave_max_u32(m)) : 0.f;
+  return a.balance ? __uint_as_float(row_max_u32(m)) : 0.f;
 }
 
 // Exclusive prefix sum of v over the first 256 threads of the block (total in
@@ -454,30 +535,26 @@ __device__ inline void write_map(const GateScatter& a, PlaceLds& L, int tot, int
 
 }  // namespace
 
-// Grid: ceil(T / 32). Block: 16 waves, two tokens each. COUNTS: the block
+// Grid: ceil(T / 32). Block: 8 waves, four tokens each. COUNTS: the block
 // writes its row of expert counts [ceil(T / 32)][E rounded up to 8] uint16;
 // otherwise counts are added to chunk_hist (when given).
-template <bool COUNTS>
-__global__ __launch_bounds__(kGateThreads) void gate_topk_kernel(GateArgs a) {
-  __shared__ float gl[kGateWaves][256];
+template <int NJ, int KD, bool COUNTS>
+__global__ __launch_bounds__(64 * kTopkWaves) void gate_topk_kernel(GateArgs a) {
+  __shared__ SelectLds L[kTopkWaves];
   __shared__ int cnt[COUNTS ? 256 : 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15;
   if constexpr (COUNTS) {
     if (tid < 256) cnt[tid] = 0;
     __syncthreads();
   }
-  float b[4];
-  const float bmax = load_biases(a, b);
-#pragma unroll 1
-  for (int q = 0; q < kCountTokens / kGateWaves; ++q) {
-    const int t = blockIdx.x * kCountTokens + q * kGateWaves + wave;
-    if (t >= a.T) break;
-    float l[4], w;
+  const int t0 = blockIdx.x * kCountTokens + 4 * wave, t = t0 + (lane >> 4);
+  if (t0 < a.T) {
+    float b[4 * NJ], w;
+    const float bmax = load_biases<NJ>(a, b);
     int sel;
-    load_logits(a, t, l);
-    gate_select(a, l, b, bmax, gl[wave], sel, w);
-    if (lane < a.k) {
-      const int64_t pair = (int64_t)t * a.k + lane;
+    gate_select<NJ, KD>(a, t0, b, bmax, L[wave], sel, w);
+    if (t < a.T && c < a.k) {
+      const int64_t pair = (int64_t)t * a.k + c;
       a.topk_idx[pair] = sel;
       a.topk_w[pair] = w;
       if constexpr (COUNTS)
@@ -551,24 +628,26 @@ __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter 
   place_pairs(a, L, pe, p0, n);
 }
 
-// One block: up to kGateSmallT tokens, four a wave.
+// One block of 16 waves: up to kGateSmallT = 64 tokens, four a wave.
+template <int NJ, int KD>
 __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, GateScatter sc) {
-  __shared__ PlaceLds L;
+  __shared__ union {
+    SelectLds select[kGateWaves];
+    PlaceLds place;
+  } L;
   __shared__ int32_t pe[kGateSmallT * kMaxGateK];
   __shared__ int cnt[256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15;
   if (tid < 256) cnt[tid] = 0;
   __syncthreads();
-  float b[4];
-  const float bmax = load_biases(a, b);
-#pragma unroll 1
-  for (int t = wave; t < a.T; t += kGateWaves) {
-    float l[4], w;
+  const int t0 = 4 * wave, t = t0 + (lane >> 4);
+  if (t0 < a.T) {
+    float b[4 * NJ], w;
+    const float bmax = load_biases<NJ>(a, b);
     int sel;
-    load_logits(a, t, l);
-    gate_select(a, l, b, bmax, reinterpret_cast<float*>(L.at[wave]), sel, w);
-    if (lane < a.k) {
-      const int pair = t * a.k + lane;
+    gate_select<NJ, KD>(a, t0, b, bmax, L.select[wave], sel, w);
+    if (t < a.T && c < a.k) {
+      const int pair = t * a.k + c;
       a.topk_idx[pair] = sel;
       a.topk_w[pair] = w;
       pe[pair] = sel;
@@ -578,10 +657,10 @@ __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, Ga
   __syncthreads();
   const int tot = tid < a.E ? cnt[tid] : 0;
   int pairs;
-  const int off = scan256(tot, L.scratch, pairs);
-  if (tid < a.E) L.base[tid] = off;
-  write_map(sc, L, tot, off, pairs, 0, 1);
-  place_pairs(sc, L, pe, 0, pairs);
+  const int off = scan256(tot, L.place.scratch, pairs);
+  if (tid < a.E) L.place.base[tid] = off;
+  write_map(sc, L.place, tot, off, pairs, 0, 1);
+  place_pairs(sc, L.place, pe, 0, pairs);
 }
 
 size_t gate_counts_bytes(int E, int T) {
@@ -596,28 +675,46 @@ GateArgs prepared(const GateArgs& in) {
   a.group_size = a.E / a.n_groups;
   a.group_magic = a.group_size > 1 ? (uint32_t)((0x100000000ull + a.group_size - 1) / a.group_size) : 0u;
   a.group_lanes_log2 = 0;
-  while ((2 << a.group_lanes_log2) * a.n_groups <= 64) ++a.group_lanes_log2;
+  while ((2 << a.group_lanes_log2) * a.n_groups <= 16) ++a.group_lanes_log2;
   a.vectors = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.partial) & 15) == 0;
   return a;
+}
+
+enum class GateLaunch { kTopk, kCounts, kSmall };
+
+// Lanes hold four experts for E <= 64, eight for E <= 128, else sixteen; up
+// to eight experts per token need nine heads of each.
+template <GateLaunch L, int NJ, int KD>
+void launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
+  const dim3 grid((a.T + kCountTokens - 1) / kCountTokens), block(64 * kTopkWaves);
+  if constexpr (L == GateLaunch::kSmall)
+    hipLaunchKernelGGL((gate_small_kernel<NJ, KD>), dim3(1), dim3(kGateThreads), 0, s, a, *sc);
+  else
+    hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, L == GateLaunch::kCounts>), grid, block, 0, s, a);
+}
+template <GateLaunch L>
+hipError_t launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
+  if (a.E <= 64)
+    launch_gate<L, 1, 16>(a, sc, s);
+  else if (a.E <= 128)
+    launch_gate<L, 2, 16>(a, sc, s);
+  else if (a.k <= 8)
+    launch_gate<L, 4, 9>(a, sc, s);
+  else
+    launch_gate<L, 4, 16>(a, sc, s);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gate_topk(const GateArgs& in, hipStream_t s) {
-  const GateArgs a = prepared(in);
-  const dim3 grid((a.T + kCountTokens - 1) / kCountTokens);
-  hipLaunchKernelGGL(gate_topk_kernel<false>, grid, dim3(kGateThreads), 0, s, a);
-  return hipGetLastError();
+  return launch_gate<GateLaunch::kTopk>(prepared(in), nullptr, s);
 }
 
 hipError_t launch_gate_route(const GateArgs& in, const GateScatter& sc, hipStream_t s) {
   const GateArgs a = prepared(in);
-  if (a.T <= kGateSmallT) {
-    hipLaunchKernelGGL(gate_small_kernel, dim3(1), dim3(kGateThreads), 0, s, a, sc);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(gate_topk_kernel<true>, dim3((a.T + kCountTokens - 1) / kCountTokens), dim3(kGateThreads), 0, s, a);
-  const hipError_t e = hipGetLastError();
+  if (a.T <= kGateSmallT) return launch_gate<GateLaunch::kSmall>(a, &sc, s);
+  const hipError_t e = launch_gate<GateLaunch::kCounts>(a, nullptr, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gate_scatter_kernel, dim3((a.T + kScatterTokens - 1) / kScatterTokens), dim3(kGateThreads), 0, s, sc);
   return hipGetLastError();
