@@ -189,8 +189,8 @@ GateArgs gate_args(const moe_gate* g) {
 }
 
 // (never 0, so that a caller's buffer has an address)
-size_t gate_ws_bytes(const moe_gate* g, int T) {
-  return std::max<size_t>((gate_counts_bytes(g->E, T) + 255) / 256 * 256, 256);
+size_t gate_ws_bytes(int T) {
+  return std::max<size_t>((gate_counts_bytes(T) + 255) / 256 * 256, 256);
 }
 
 // A gate for the layer: the layer's own dims, routed by the gate.
@@ -682,7 +682,7 @@ int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes) {
   if (rc != MOE_OK) return rc;
   const moe_dims d = gate_dims(gate);
   if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
-  *bytes = gate_ws_bytes(gate, T);
+  *bytes = gate_ws_bytes(T);
   return MOE_OK;
 }
 
@@ -695,13 +695,13 @@ int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const 
   if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!logits || !route_out_ok(out) || !ws || !al4(logits) || !al16(ws)) return MOE_EINVAL;
-  if (ws_bytes < gate_ws_bytes(gate, T)) return MOE_EWORKSPACE;
+  if (ws_bytes < gate_ws_bytes(T)) return MOE_EWORKSPACE;
   GateArgs ga = gate_args(gate);
   ga.partial = logits;
   ga.splits = 1;
   ga.topk_idx = out->topk_idx;
   ga.topk_w = out->topk_w;
-  ga.counts = static_cast<uint16_t*>(ws);
+  ga.counts = static_cast<uint8_t*>(ws);
   ga.T = T;
   GateScatter sc{};
   sc.topk_idx = out->topk_idx;

@@ -15,7 +15,7 @@
 //
 // Kernels:
 //   gate_topk     sixteen lanes per token, four tokens a wave; for
-//                 moe_route_gated also the expert counts of each 32 tokens
+//                 moe_route_gated also the expert counts of each block
 //   gate_scatter  per 128 tokens: totals and bases per expert from those
 //                 counts, a stable scatter, and a share of the block map
 //   gate_small    both in one block, for up to kGateSmallT tokens
@@ -28,9 +28,7 @@ namespace {
 
 constexpr int kGateWaves = 16;
 constexpr int kGateThreads = 64 * kGateWaves;
-constexpr int kTopkWaves = 8;                     // of a gate_topk block
-constexpr int kCountTokens = 4 * kTopkWaves;      // tokens per row of counts
-constexpr int kScatterTokens = 4 * kCountTokens;  // tokens per scatter block
+constexpr int kScatterTokens = 128;  // tokens per scatter block
 constexpr int kGateSmallT = 64;
 
 // Order-preserving 64-bit image of a key (never 0, so 0 can mark an expert
@@ -47,16 +45,17 @@ __device__ inline double key_value(uint64_t o) {
   return __longlong_as_double((long long)(o >> 63 ? o & 0x7FFFFFFFFFFFFFFFull : ~o));
 }
 
-// Largest key over the wave, ties to the lower index, returned to every lane.
+// Largest key over the wave and its index, returned to every lane; ties to the
+// lowest lane, whose index has to be the lowest too. (Two 32-bit maxima over
+// the lanes; shuffles of the 64-bit keys took seven times as long, which a
+// late wave in doubt adds to the whole launch.)
 __device__ inline void wave_best(uint64_t& k, int& i) {
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t ok = __shfl_xor((unsigned long long)k, o);
-    const int oi = __shfl_xor(i, o);
-    if (ok > k || (ok == k && oi < i)) {
-      k = ok;
-      i = oi;
-    }
-  }
+  const uint32_t hi = (uint32_t)(k >> 32), lo = (uint32_t)k;
+  const uint32_t mh = wave_max_u32(hi), ml = wave_max_u32(hi == mh ? lo : 0u);
+  const uint64_t best = (uint64_t)mh << 32 | ml;
+  const int win = __builtin_ctzll(__ballot(k == best));
+  i = __builtin_amdgcn_readlane(i, win);
+  k = best;
 }
 
 __device__ inline double wave_sum_f64(double v) {
@@ -108,9 +107,10 @@ __device__ inline int group_of(const GateArgs& a, int e) {
 }
 
 // One token's selection in 64 bits: lane j < k gets the expert of rank j and
-// its weight. l: the lane's logits (-inf: masked), b: their biases.
-__device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const float (&b)[4], float mx, int& sel,
-                                  float& w) {
+// its weight. l: the lane's logits (-inf: masked), b: their biases; kept: per
+// group whether it is kept, or null where that is to be decided too.
+__device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const float (&b)[4], float mx,
+                                  const uint8_t* kept_groups, int& sel, float& w) {
   const int lane = threadIdx.x & 63, E = a.E, k = a.k;
   double score[4];
   uint64_t key[4];
@@ -138,7 +138,13 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
       if (key[i] == kMaskedKey) score[i] = 0.0;
     }
   }
-  if (a.n_groups > 1) {
+  if (a.n_groups > 1 && kept_groups) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (e < E && !kept_groups[group_of(a, e)]) key[i] = 0;
+    }
+  } else if (a.n_groups > 1) {
     uint64_t mine = 0;  // lane g: the rank key of group g
     for (int g = 0; g < a.n_groups; ++g) {
       auto best_but = [&](int skip, int& at) {
@@ -209,29 +215,26 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
 }
 
 // The sum over the router's K splits plus the router's bias: logits of token
-// t, N consecutive experts from e on (those from E on are not read).
-template <int N>
-__device__ inline void load_logits(const GateArgs& a, int64_t t, int e, float (&v)[N]) {
+// t, four consecutive experts from e on (the last four, or the last one
+// repeated, where e is past the end: no branch separates the loads).
+__device__ inline void load_logits(const GateArgs& a, int64_t t, int e, float (&v)[4]) {
   const int E = a.E;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  if (N == 4 && a.vectors) {
-    if (e < E)
-      for (int sp = 0; sp < a.splits; ++sp) {
-        const f32x4 p = *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)sp * a.T + t) * E + e);
+  for (int i = 0; i < 4; ++i) v[i] = 0.f;
+  if (a.vectors) {
+    for (int sp = 0; sp < a.splits; ++sp) {
+      const f32x4 p = *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)sp * a.T + t) * E + min(e, E - 4));
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += p[i];
-      }
+      for (int i = 0; i < 4; ++i) v[i] += p[i];
+    }
   } else {
+    for (int sp = 0; sp < a.splits; ++sp)
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (e + i < E)
-        for (int sp = 0; sp < a.splits; ++sp) v[i] += a.partial[((int64_t)sp * a.T + t) * E + e + i];
+      for (int i = 0; i < 4; ++i) v[i] += a.partial[((int64_t)sp * a.T + t) * E + min(e + i, E - 1)];
   }
   if (a.rbias) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (e + i < E) v[i] += a.rbias[e + i];
+    for (int i = 0; i < 4; ++i) v[i] += a.rbias[min(e + i, E - 1)];
   }
 }
 
@@ -263,36 +266,51 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = 64 * j + 4 * c + u;
-      if (a.logits_out && e < E && t0 + q < a.T) a.logits_out[t * E + e] = v[u];
-      l[4 * j + u] = e < E && v[u] == v[u] ? v[u] : -INFINITY;
+      l[4 * j + u] = (e < E) & (v[u] == v[u]) ? v[u] : -INFINITY;
+    }
+    if (a.logits_out && t0 + q < a.T) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (64 * j + 4 * c + u < E) a.logits_out[t * E + 64 * j + 4 * c + u] = v[u];
     }
   }
   float mx = l[0];
 #pragma unroll
   for (int i = 1; i < NS; ++i) mx = fmaxf(mx, l[i]);
   mx = row_max(mx);
-  // fp32 scores with the hardware exponential and reciprocal. Errors: the
-  // exponent's product and the difference to the maximum round by 2^-24 of
-  // their size, which moves e^-d by at most 2^-24 d e^-d < 2^-25 absolute;
-  // the exponential, the reciprocal and the sum of up to 256 terms add a few
-  // 2^-24 of the value, and adding the bias 2^-24 of the key. All together
-  // stay below 2^-20 of the range, largest score + largest bias.
-  float s[NS], top = 1.0f, z = 0.f;
+  // fp32 scores with the hardware exponential and reciprocal. Errors, with
+  // u = 2^-24: the exponent's product and the difference to the maximum round
+  // by u of their size, which moves e^-d by at most u d e^-d < u / 2; the
+  // exponential, the reciprocal and the quotient add 2 u of the value each,
+  // the softmax's sum, added in pairs, 8 u, and the bias's addition u of the
+  // key. Of the range, largest score + largest bias, that is below 16 u with
+  // a softmax and below 8 u with a sigmoid, whose derivative is at most 1/4.
+  float s[NS], top = 1.0f;
+  if (a.sigmoid) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const float p = __expf(a.sigmoid ? -l[i] : (l[i] == mx ? 0.f : l[i] - mx));
-    s[i] = l[i] == -INFINITY ? 0.f : (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + p) : p);
-    z += s[i];
-  }
-  if (!a.sigmoid) {
-    z = row_sum(z);
-    top = z > 0.f ? 1.0f / z : 0.f;
+    for (int i = 0; i < NS; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));  // (-inf: 1 / inf)
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float p = __expf(l[i] == mx ? 0.f : l[i] - mx);
+      s[i] = l[i] == -INFINITY ? 0.f : p;
+    }
+    float z[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) z[i] = s[i];
+#pragma unroll
+    for (int n = NS / 2; n > 0; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] += z[i + n];
+    const float sum = row_sum(z[0]);
+    top = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) s[i] *= top;
   }
   const float range = top + bmax;
-  const float err = 0x1p-20f * range;
-  bool near = !(range < 1e30f);  // a decision the fp32 keys cannot settle
+  const float err = (a.sigmoid ? 0x1p-21f : 0x1p-20f) * range;
+  // a decision the fp32 keys cannot settle, and whether it is one of groups
+  bool near = !(range < 1e30f), near_groups = near;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
@@ -338,12 +356,14 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     lo = row_min(lo);
     hi = row_max(hi);
-    near |= hi > -INFINITY && !(lo - hi > 4.0f * err);
+    near_groups |= hi > -INFINITY && !(lo - hi > 4.0f * err);
+    near |= near_groups;
     in = 0u;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int e = 64 * (i >> 2) + 4 * c + (i & 3);
-      in |= (e < E && L.kept[q][group_of(a, min(e, E - 1))] ? 1u : 0u) << i;
+      const uint32_t kept = L.kept[q][group_of(a, min(e, E - 1))];
+      in |= (e < E ? kept : 0u) << i;
     }
   }
   // keys as 24-bit fixed point over the range (0: masked or out of the
@@ -352,7 +372,8 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
   uint32_t key[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const uint32_t v = s[i] == -INFINITY || !(in >> i & 1) ? 0u : 1u + (uint32_t)(fmaxf(s[i] + bmax, 0.f) * scale);
+    const bool out = (s[i] == -INFINITY) | !(in >> i & 1);
+    const uint32_t v = out ? 0u : 1u + (uint32_t)(fmaxf(s[i] + bmax, 0.f) * scale);
     key[i] = v << 8 | (uint32_t)(i << 4) | (uint32_t)c;
   }
   // the lane's keys in descending order
@@ -381,11 +402,11 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
     for (int i = 0; i + 1 < ND; ++i) key[i] = own ? key[i + 1] : key[i];
     if constexpr (ND == NS) key[NS - 1] = own ? 0u : key[NS - 1];
   }
-  // twice the bound in steps of the fixed point (2^-20 of the range is 8 to
-  // 16 of 2^24 steps over range + bias), and the steps the keys were cut by
-  constexpr uint32_t kNear = 36;
+  // twice the bound in steps of the fixed point (16 u of the range is at most
+  // 16 of the 2^24 steps over range + bias), and what the steps cut off
+  const uint32_t close = (a.sigmoid ? 16 : 32) + 4;
   const uint32_t vm = mine >> 8, vn = next >> 8;
-  if (c < k) near |= vm == 0 || (vn > 0 && vm - vn <= kNear);
+  if (c < k) near |= vm == 0 || (vn > 0 && vm - vn <= close);
   sel = 64 * (int)(mine >> 6 & 3) + 4 * (int)(mine & 15) + (int)(mine >> 4 & 3);
   // the weights in 64 bits from the selected logits; where the fp32 sum over
   // the experts is used (softmax, not renormalised) it errs by a few 2^-24
@@ -408,6 +429,7 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
   w = (float)(v * (double)a.scale);
   // in doubt: those tokens again, one at a time
   uint64_t doubt = __ballot(near && t0 + q < a.T);
+  const uint64_t doubt_groups = __ballot(near_groups);
   while (doubt) {
     const int row = __builtin_ctzll(doubt) >> 4;
     doubt &= ~(0xFFFFull << (16 * row));
@@ -422,7 +444,7 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
     top4 = __shfl(mx, 16 * row);
     int se;
     float we;
-    gate_select_exact(a, l4, b4, top4, se, we);
+    gate_select_exact(a, l4, b4, top4, doubt_groups >> (16 * row) & 0xFFFF ? nullptr : L.kept[row], se, we);
     se = __shfl(se, c);
     we = __shfl(we, c);
     if (q == row) {
@@ -436,14 +458,15 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
 template <int NJ>
 __device__ inline float load_biases(const GateArgs& a, float (&b)[4 * NJ]) {
   const int c = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) b[i] = 0.f;
+  if (!a.balance) return 0.f;
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) {
-    const int e = 64 * (i >> 2) + 4 * c + (i & 3);
-    b[i] = a.balance && e < a.E ? a.balance[e] : 0.f;
-    m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);  // (a NaN bias is the largest, and leaves every token in doubt)
-  }
-  return a.balance ? __uint_as_float(row_max_u32(m)) : 0.f;
+  for (int i = 0; i < 4 * NJ; ++i) b[i] = a.balance[min(64 * (i >> 2) + 4 * c + (i & 3), a.E - 1)];
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+  return __uint_as_float(row_max_u32(m));  // (a NaN bias is the largest, and leaves every token in doubt)
 }
 
 // Exclusive prefix sum of v over the first 256 threads of the block (total in
@@ -484,11 +507,13 @@ __device__ inline void place_pairs(const GateScatter& a, PlaceLds& L, const int3
   for (int i = f + lane; i < end; i += 64) atomicAdd(&L.at[wave][pe[i]], 1);
   __syncthreads();
   if (tid < a.E) {
-    int run = L.base[tid];
+    int c[kGateWaves], run = L.base[tid];
+#pragma unroll
+    for (int w = 0; w < kGateWaves; ++w) c[w] = L.at[w][tid];
+#pragma unroll
     for (int w = 0; w < kGateWaves; ++w) {
-      const int c = L.at[w][tid];
       L.at[w][tid] = run;
-      run += c;
+      run += c[w];
     }
   }
   __syncthreads();
@@ -535,19 +560,19 @@ __device__ inline void write_map(const GateScatter& a, PlaceLds& L, int tot, int
 
 }  // namespace
 
-// Grid: ceil(T / 32). Block: 8 waves, four tokens each. COUNTS: the block
-// writes its row of expert counts [ceil(T / 32)][E rounded up to 8] uint16;
+// Grid: ceil(T / (4 W)). Block: W waves, four tokens each. COUNTS: the block
+// writes its row of expert counts [grid][256] bytes (at most 64 each);
 // otherwise counts are added to chunk_hist (when given).
-template <int NJ, int KD, bool COUNTS>
-__global__ __launch_bounds__(64 * kTopkWaves) void gate_topk_kernel(GateArgs a) {
-  __shared__ SelectLds L[kTopkWaves];
+template <int NJ, int KD, int W, bool COUNTS>
+__global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
+  __shared__ SelectLds L[W];
   __shared__ int cnt[COUNTS ? 256 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15;
   if constexpr (COUNTS) {
     if (tid < 256) cnt[tid] = 0;
     __syncthreads();
   }
-  const int t0 = blockIdx.x * kCountTokens + 4 * wave, t = t0 + (lane >> 4);
+  const int t0 = (blockIdx.x * W + wave) * 4, t = t0 + (lane >> 4);
   if (t0 < a.T) {
     float b[4 * NJ], w;
     const float bmax = load_biases<NJ>(a, b);
@@ -565,55 +590,47 @@ __global__ __launch_bounds__(64 * kTopkWaves) void gate_topk_kernel(GateArgs a) 
   }
   if constexpr (COUNTS) {
     __syncthreads();
-    const int Ep = round_up(a.E, 8);
-    if (tid < Ep) a.counts[(int64_t)blockIdx.x * Ep + tid] = (uint16_t)cnt[tid];
+    if (tid < 256) a.counts[(int64_t)blockIdx.x * 256 + tid] = (uint8_t)cnt[tid];
   }
 }
 
 // Grid: ceil(T / 128). Block: 16 waves. Every block sums all rows of counts
-// (512 rows of 512 bytes for 16384 tokens: 16-byte loads, 32 row groups).
+// (256 rows of 256 bytes for 4096 and for 16384 tokens), a wave a row at a
+// time, a lane four experts.
 __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter a) {
   __shared__ PlaceLds L;
   __shared__ int32_t pe[kScatterTokens * kMaxGateK];
   __shared__ int part[2][kGateWaves][256];  // [total, before][wave]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = a.E, Ep = round_up(E, 8), cols = Ep / 8;
+  const int E = a.E;
   const int p0 = blockIdx.x * kScatterTokens * a.k, n = min(kScatterTokens * a.k, a.T * a.k - p0);
-  for (int i = tid; i < n; i += kGateThreads) pe[i] = a.topk_idx[p0 + i];
-  const int rows = (a.T + kCountTokens - 1) / kCountTokens, mine = blockIdx.x * (kScatterTokens / kCountTokens);
+  const int rows = (a.T + a.count_tokens - 1) / a.count_tokens, mine = blockIdx.x * (kScatterTokens / a.count_tokens);
   {
-    const int c = lane & 31, rg = 2 * wave + (lane >> 5);
-    int tot[8] = {0, 0, 0, 0, 0, 0, 0, 0}, bef[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int r0 = 0; r0 < rows; r0 += 32 * 4) {
-      u32x4 v[4];
+    int tot[4] = {0, 0, 0, 0}, bef[4] = {0, 0, 0, 0};
+    constexpr int kRows = 8;  // loads under way
+    for (int r0 = wave; r0 < rows; r0 += kRows * kGateWaves) {
+      uint32_t v[kRows];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = min(r0 + 32 * j + rg, rows - 1);
-        v[j] = *reinterpret_cast<const u32x4*>(a.counts + (int64_t)r * Ep + 8 * min(c, cols - 1));
-      }
+      for (int j = 0; j < kRows; ++j)
+        v[j] = *reinterpret_cast<const uint32_t*>(a.counts + (int64_t)min(r0 + kGateWaves * j, rows - 1) * 256 + 4 * lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = r0 + 32 * j + rg;
+      for (int j = 0; j < kRows; ++j) {
+        const int r = r0 + kGateWaves * j;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const int lo = r < rows ? (int)(v[j][h] & 0xFFFFu) : 0, hi = r < rows ? (int)(v[j][h] >> 16) : 0;
-          tot[2 * h] += lo;
-          tot[2 * h + 1] += hi;
-          bef[2 * h] += r < mine ? lo : 0;
-          bef[2 * h + 1] += r < mine ? hi : 0;
+          const int x = r < rows ? (int)(v[j] >> (8 * h) & 0xFFu) : 0;
+          tot[h] += x;
+          bef[h] += r < mine ? x : 0;
         }
       }
     }
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      tot[h] += __shfl_xor(tot[h], 32);
-      bef[h] += __shfl_xor(bef[h], 32);
-      if (lane < 32) {
-        part[0][wave][8 * c + h] = c < cols ? tot[h] : 0;
-        part[1][wave][8 * c + h] = c < cols ? bef[h] : 0;
-      }
+    for (int h = 0; h < 4; ++h) {
+      part[0][wave][4 * lane + h] = tot[h];
+      part[1][wave][4 * lane + h] = bef[h];
     }
   }
+  for (int i = tid; i < n; i += kGateThreads) pe[i] = a.topk_idx[p0 + i];
   __syncthreads();
   int tot = 0, bef = 0;
   if (tid < E)
@@ -663,8 +680,14 @@ __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, Ga
   place_pairs(sc, L.place, pe, 0, pairs);
 }
 
-size_t gate_counts_bytes(int E, int T) {
-  return T <= kGateSmallT ? 0 : (size_t)((T + kCountTokens - 1) / kCountTokens) * round_up(E, 8) * 2;
+// Selection blocks of 4 waves (16 tokens) up to 4096 tokens: they spread few
+// tokens over the chip (512 tokens: 10.2 us in blocks of 32, 13.9 in blocks of
+// 64). Blocks of 16 waves beyond: a quarter of the rows of counts, which every
+// scatter block sums (16384 tokens: 12.8 us with 512 rows, 9.7 with 256).
+static int count_tokens(int T) { return T <= 4096 ? 16 : 64; }
+
+size_t gate_counts_bytes(int T) {
+  return T <= kGateSmallT ? 0 : (size_t)((T + count_tokens(T) - 1) / count_tokens(T)) * 256;
 }
 
 namespace {
@@ -686,11 +709,12 @@ enum class GateLaunch { kTopk, kCounts, kSmall };
 // to eight experts per token need nine heads of each.
 template <GateLaunch L, int NJ, int KD>
 void launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
-  const dim3 grid((a.T + kCountTokens - 1) / kCountTokens), block(64 * kTopkWaves);
   if constexpr (L == GateLaunch::kSmall)
     hipLaunchKernelGGL((gate_small_kernel<NJ, KD>), dim3(1), dim3(kGateThreads), 0, s, a, *sc);
+  else if (L == GateLaunch::kCounts && count_tokens(a.T) == 64)
+    hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 16, true>), dim3((a.T + 63) / 64), dim3(1024), 0, s, a);
   else
-    hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, L == GateLaunch::kCounts>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 4, L == GateLaunch::kCounts>), dim3((a.T + 15) / 16), dim3(256), 0, s, a);
 }
 template <GateLaunch L>
 hipError_t launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
@@ -711,8 +735,10 @@ hipError_t launch_gate_topk(const GateArgs& in, hipStream_t s) {
   return launch_gate<GateLaunch::kTopk>(prepared(in), nullptr, s);
 }
 
-hipError_t launch_gate_route(const GateArgs& in, const GateScatter& sc, hipStream_t s) {
+hipError_t launch_gate_route(const GateArgs& in, const GateScatter& scatter, hipStream_t s) {
   const GateArgs a = prepared(in);
+  GateScatter sc = scatter;
+  sc.count_tokens = count_tokens(a.T);
   if (a.T <= kGateSmallT) return launch_gate<GateLaunch::kSmall>(a, &sc, s);
   const hipError_t e = launch_gate<GateLaunch::kCounts>(a, nullptr, s);
   if (e != hipSuccess) return e;

@@ -144,7 +144,7 @@ struct GateArgs {
   int32_t* topk_idx;      // [T][k]
   float* topk_w;          // [T][k]
   int32_t* chunk_hist;    // [chunks][E] (zeroed beforehand) or null
-  uint16_t* counts;       // gate_counts_bytes (launch_gate_route)
+  uint8_t* counts;        // gate_counts_bytes (launch_gate_route)
   int T, E, k, sigmoid, n_groups, topk_groups, group_top2, renorm;
   float scale;
   // set by the launchers
@@ -156,12 +156,13 @@ hipError_t launch_gate_topk(const GateArgs& a, hipStream_t s);
 
 struct GateScatter {
   const int32_t* topk_idx;
-  const uint16_t* counts;
+  const uint8_t* counts;
   int32_t *hist, *offsets, *perm, *inv_perm, *block_map, *num_blocks;
   int T, E, k, block_m;
+  int count_tokens;  // per row of counts; set by the launcher
 };
 // Everything moe_route gives, in one launch for few tokens, two otherwise.
-size_t gate_counts_bytes(int E, int T);
+size_t gate_counts_bytes(int T);
 hipError_t launch_gate_route(const GateArgs& a, const GateScatter& sc, hipStream_t s);
 
 constexpr int kMaxRank = 128;
