@@ -756,16 +756,11 @@ int moe_add_rmsnorm(const moe_norm* n, const void* x, int64_t ldx, const void* r
   const int eb = n->dtype == MOE_F32 ? 4 : 2, wb = n->weight_dtype == MOE_F32 ? 4 : 2;
   const void* rows[] = {x, residual, h_out, y};
   const int64_t lds[] = {ldx, ld_residual, ld_h, ld_y};
-  uint64_t bits = reinterpret_cast<uintptr_t>(weight) & 15;
-  if (bits % wb || !al4(scales) || (q && ld_q < n->H)) return MOE_EINVAL;
+  if (reinterpret_cast<uintptr_t>(weight) % wb || !al4(scales) || (q && (ld_q < n->H || ld_q > kMaxRowStride)))
+    return MOE_EINVAL;
   for (int i = 0; i < 4; ++i) {
     if (!rows[i]) continue;
     if (lds[i] < n->H || lds[i] > kMaxRowStride || reinterpret_cast<uintptr_t>(rows[i]) % eb) return MOE_EINVAL;
-    bits |= (reinterpret_cast<uintptr_t>(rows[i]) | (uint64_t)lds[i] * eb) & 15;
-  }
-  if (q) {
-    if (ld_q > kMaxRowStride) return MOE_EINVAL;
-    if ((reinterpret_cast<uintptr_t>(q) | (uint64_t)ld_q) & 7) bits |= 1;
   }
   // an output may replace a row that has been read only where both have one stride
   if ((h_out && ((h_out == x && ld_h != ldx) || (h_out == residual && ld_h != ld_residual))) ||
@@ -790,7 +785,6 @@ int moe_add_rmsnorm(const moe_norm* n, const void* x, int64_t ldx, const void* r
   a.weight_f32 = n->weight_dtype == MOE_F32;
   a.out8 = n->out8;
   a.group = n->group;
-  a.aligned = bits == 0;
   a.eps = n->eps;
   a.weight_offset = n->weight_offset;
   return hip_status(launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));

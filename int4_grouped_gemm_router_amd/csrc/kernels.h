@@ -127,7 +127,6 @@ struct NormArgs {
   float* scales;
   int64_t ldx, ld_residual, ld_h, ld_y, ld_q;
   int T, H, dtype, weight_f32, out8, group;
-  int aligned;  // 1: every row starts on 16 bytes (q: 8)
   float eps, weight_offset;
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
