@@ -7,9 +7,8 @@
 // threads (up to 16384 values), so x and residual are read once and every
 // output is written once; the sum of squares and v are fp32. The memory
 // traffic bounds it, and for a few rows the latency of one load, one
-// reduction and one store. Rows of up to 2048 values belong to one wave or a
-// quarter of one: no barrier, and a lane's four loads of each input under way
-// at once. Threads keep their weights over the rows they take in turn.
+// reduction and one store. Threads keep their weights over the rows they take
+// in turn.
 #include <type_traits>
 
 #include "kernels.h"
@@ -288,26 +287,20 @@ void launch_shape(const NormArgs& a, hipStream_t s) {
   }
 }
 
-// Rows of up to 2048 values: a wave each once there are enough rows to fill the
-// chip with waves, else the four waves of a block each, which wait for a
-// quarter of the loads (2048 values: one row 3.1 us against 3.9, 512 rows with
-// int8 4.9 against 6.3; 4096 rows 13.0 by waves against 18.5 by blocks).
-constexpr int kNormFewRows = 1024;
-
+// One load of each input per thread where the threads of a block or of a wave
+// allow it, more blocks rather than longer rows per thread: rows of 2048
+// values by 256 threads take 2.4 us for one row, 4.8 for 1024, 51.5 for 16384
+// (5.2 TB/s), by one wave with four loads a lane 3.9, 6.3 and 54.7.
 template <class R>
 void launch_rows(const NormArgs& a, hipStream_t s) {
-  if (a.T <= kNormFewRows && a.H > 512 && a.H <= 2048)
-    launch_shape<R, 256, 1>(a, s);
-  else if (a.H <= 128)
+  if (a.H <= 128)
     launch_shape<R, 16, 1>(a, s);
-  else if (a.H <= 256)
-    launch_shape<R, 16, 2>(a, s);
   else if (a.H <= 512)
     launch_shape<R, 64, 1>(a, s);
   else if (a.H <= 1024)
     launch_shape<R, 64, 2>(a, s);
   else if (a.H <= 2048)
-    launch_shape<R, 64, 4>(a, s);
+    launch_shape<R, 256, 1>(a, s);
   else if (a.H <= 4096)
     launch_shape<R, 256, 2>(a, s);
   else if (a.H <= 8192)
