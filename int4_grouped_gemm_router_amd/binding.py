@@ -453,9 +453,20 @@ def _type_code(dtype):
     return codes[dtype]
 
 
-def _torch_type(code):
-    import torch
-    return (torch.bfloat16, torch.float16, torch.float32)[code]
+_types = None  # per type code the torch types whose bits a tensor of it may hold; at BITS8 + out8 those of 8 bits
+BITS8 = 3
+
+
+def _types_of(code):
+    global _types
+    if _types is None:
+        import torch
+        _types = ((torch.bfloat16,), (torch.float16,), (torch.float32,), (), (torch.int8, torch.uint8),
+                  (torch.float8_e4m3fn, torch.uint8), (torch.bfloat16, torch.int16))
+    return _types[code]
+
+
+_BF16_BITS = BITS8 + 3
 
 
 def _need(ok, what):
@@ -463,42 +474,47 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _on(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: one device is needed")
+def _rows(t, T, width, dtypes, dev, name):
+    """Address and row stride of a [>= T, width] tensor whose rows are contiguous, on GPU `dev`."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype not in dtypes or len(shape) != 2 or shape[0] < T or shape[1] != width:
+        raise ValueError(f"{name}: [{T}, {width}] of {dtypes[0]} is needed, got {list(shape)} of {t.dtype}")
+    if stride[1] != 1 and width > 1:
+        raise ValueError(f"{name}: the values of a row have to be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
+    # the stride of a single row says nothing
+    return t.data_ptr(), (stride[0] if T > 1 else max(stride[0], width))
 
 
-class _Rows:
-    """The checks of a [T, width] tensor whose rows are contiguous: its address and row stride."""
-
-    @staticmethod
-    def of(t, T, width, dtypes, name):
-        if t.dtype not in dtypes or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width:
-            raise ValueError(f"{name}: [{T}, {width}] of {dtypes[0]} is needed, got {list(t.shape)} of {t.dtype}")
-        s0, s1 = t.stride()
-        if width > 1 and s1 != 1:
-            raise ValueError(f"{name}: the values of a row have to be contiguous")
-        if T <= 1:
-            s0 = max(s0, width)  # the stride of a single row says nothing
-        return t.data_ptr(), s0
-
-
-def _flat(t, n, dtype, name):
+def _flat(t, n, dtype, name, dev=None):
+    """Address of at least n contiguous values."""
     if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous values of {dtype} are needed, got {list(t.shape)} of {t.dtype}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
     return t.data_ptr()
 
 
-def _call(device, stream, f):
-    """f(stream handle) with `device` current."""
+def _gpu(t):
+    """Index of the GPU that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"tensors on a GPU are needed, got {t.device}")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """The C entry point with a stream as its last argument, GPU `dev` being current."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"tensors on a GPU are needed, got {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return f(_stream(stream, device))
-    return f(_stream(stream, device))
+    f = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, _stream(stream))
+    if code != MOE_OK:
+        raise MoeError(code, name)
 
 
 def norm(H, dtype=BF16, weight_dtype=None, eps=1e-6, weight_offset=0.0, out8=OUT8_NONE, group=0) -> MoeNorm:
@@ -511,28 +527,28 @@ def norm(H, dtype=BF16, weight_dtype=None, eps=1e-6, weight_offset=0.0, out8=OUT
 def moe_add_rmsnorm(n: MoeNorm, x, weight, T: int, residual=None, h_out=None, y=None, q=None, scales=None,
                     stream=None):
     """h = x + residual, y = h / rms(h) * weight for T rows, and q, scales: y in 8 bits."""
-    import torch
-    _on(x.device, weight, residual, h_out, y, q, scales)
-    rows, H = (_torch_type(n.dtype),), n.H
-    a = [_Rows.of(x, T, H, rows, "x")]
-    for t, name in ((residual, "residual"), (h_out, "h_out"), (y, "y")):
-        a.append((None, 0) if t is None else _Rows.of(t, T, H, rows, name))
+    H, types, dev = n.H, _types_of(n.dtype), x.get_device()
+    xp, ldx = _rows(x, T, H, types, dev, "x")
+    rp = hp = yp = qp = sp = None
+    ldr = ldh = ldy = ldq = 0
+    if residual is not None:
+        rp, ldr = _rows(residual, T, H, types, dev, "residual")
+    if h_out is not None:
+        hp, ldh = _rows(h_out, T, H, types, dev, "h_out")
+    if y is not None:
+        yp, ldy = _rows(y, T, H, types, dev, "y")
     if q is not None:
-        bytes8 = (torch.int8, torch.uint8) if n.out8 == OUT8_INT8 else (torch.float8_e4m3fn, torch.uint8)
-        a.append(_Rows.of(q, T, H, bytes8, "q"))
-    else:
-        a.append((None, 0))
-    sp = None if scales is None else _flat(scales, T * (H // n.group if n.group else 1), torch.float32, "scales")
-    w = _flat(weight, H, _torch_type(n.weight_dtype), "weight")
-    _check(_call(x.device, stream, lambda s: lib().moe_add_rmsnorm(
-        ctypes.byref(n), *a[0], *a[1], w, *a[2], *a[3], *a[4], sp, T, s)), "moe_add_rmsnorm")
+        qp, ldq = _rows(q, T, H, _types_of(BITS8 + (n.out8 or OUT8_INT8)), dev, "q")
+    if scales is not None:
+        sp = _flat(scales, T * (H // n.group if n.group else 1), _types_of(F32)[0], "scales", dev)
+    wp = _flat(weight, H, _types_of(n.weight_dtype)[0], "weight", dev)
+    _call("moe_add_rmsnorm", _gpu(x), stream, ctypes.byref(n), xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, qp, ldq, sp, T)
 
 
 def gate(E=256, top_k=8, block_m=32, score=SCORE_SOFTMAX, n_groups=1, topk_groups=1, group_score=GROUP_MAX,
          renorm=True, scale=1.0, balance_bias=None) -> MoeGate:
     """A routing rule (balance_bias: an fp32 device tensor [E] that the gate keeps alive)."""
-    import torch
-    bias = None if balance_bias is None else _flat(balance_bias, E, torch.float32, "balance_bias")
+    bias = None if balance_bias is None else _flat(balance_bias, E, _types_of(F32)[0], "balance_bias")
     g = MoeGate(E, top_k, block_m, score, n_groups, topk_groups, group_score, int(renorm), scale, bias)
     g.bias_tensor = balance_bias
     return g
@@ -553,18 +569,17 @@ def gate_workspace(g: MoeGate, T: int, device="cuda"):
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
-def _check_route_out(g, T, out):
-    _need(out.topk_idx.numel() >= T * g.top_k and out.hist.numel() >= g.E and
-          out.block_map.shape[0] >= moe_max_blocks(g, T), "route_out: buffers of this gate and T are needed")
-
-
 def moe_route_gated(g: MoeGate, logits, T: int, out: RouteBuffers, ws, stream=None):
-    import torch
-    _on(logits.device, out.topk_idx, ws, g.bias_tensor)
-    lp = _flat(logits, T * g.E, torch.float32, "logits")
-    _check_route_out(g, T, out)
-    _check(_call(logits.device, stream, lambda s: lib().moe_route_gated(
-        ctypes.byref(g), lp, T, ctypes.byref(out.struct), ws.data_ptr(), ws.numel(), s)), "moe_route_gated")
+    """moe_route with a gate: the routing metadata of T tokens from fp32 logits."""
+    dev = _gpu(logits)
+    lp = _flat(logits, T * g.E, _types_of(F32)[0], "logits", dev)
+    if (out.topk_idx.numel() < T * g.top_k or out.hist.numel() < g.E or
+            out.block_map.shape[0] < (T * g.top_k + g.block_m - 1) // g.block_m + g.E):
+        raise ValueError("route_out: buffers of this gate and T are needed")
+    bias = getattr(g, "bias_tensor", None)
+    if out.topk_idx.get_device() != dev or ws.get_device() != dev or (bias is not None and bias.get_device() != dev):
+        raise ValueError("logits, route_out, workspace and balance_bias: one GPU is needed")
+    _call("moe_route_gated", dev, stream, ctypes.byref(g), lp, T, ctypes.byref(out.struct), ws.data_ptr(), ws.numel())
 
 
 def moe_prefill_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, chunk_T: int = 0,
@@ -589,15 +604,15 @@ def moe_decode_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: in
 
 class Adapters:
     """Low-rank adapters of one projection: A [n, R, K] and B [n, N, R] bf16, ranks [n] int32 (None: R
-    each), scales [n] fp32 (None: 1 each), all on one GPU."""
+    each), scales [n] fp32 (None: 1 each), all on one device."""
 
     def __init__(self, A, B, ranks=None, scales=None):
         import torch
-        bf16 = (torch.bfloat16, torch.int16)
+        bf16 = _types_of(_BF16_BITS)
         _need(A.dim() == 3 and B.dim() == 3 and A.shape[0] == B.shape[0] and A.shape[1] == B.shape[2] and
               A.dtype in bf16 and B.dtype in bf16 and A.is_contiguous() and B.is_contiguous(),
               "adapters: contiguous A [n, R, K] and B [n, N, R] of bfloat16 are needed")
-        _on(A.device, B, ranks, scales)
+        _need(all(t is None or t.device == A.device for t in (B, ranks, scales)), "adapters: one device is needed")
         self.n, self.R, self.K = A.shape
         self.N = B.shape[1]
         self.t = (A, B, ranks, scales)
@@ -621,19 +636,21 @@ def moe_project(blob, N: int, K: int, x, y, T: int, adapters: Adapters | None = 
     """y[t] = W x[t] + scale B_a (A_a x[t]) for a packed int4 matrix [N, K] (pack_int4_g64 of one unpaired
     matrix) and the adapter a = adapter_of[t] of each token (-1: none)."""
     import torch
-    bf16 = (torch.bfloat16, torch.int16)
-    _need(blob.dtype == torch.uint8 and blob.numel() >= moe_packed_bytes(1, N, K, False) > 0,
-          "blob: a pack_int4_g64 blob of one [N, K] matrix is needed")
-    xp, ldx = _Rows.of(x, T, K, bf16, "x")
-    yp, ldy = _Rows.of(y, T, N, bf16, "y")
-    _on(x.device, blob, y, adapter_of, ws)
-    ap = op = None
+    dev, types = x.get_device(), _types_of(_BF16_BITS)
+    # (the bytes moe_packed_bytes gives: a header, the codes, scales and biases, to 256 bytes)
+    if N % 64 == 0 and K % 64 == 0:
+        _flat(blob, HEADER_BYTES + (N * K // 2 + N * K // 16 + 255) // 256 * 256, torch.uint8, "blob", dev)
+    xp, ldx = _rows(x, T, K, types, dev, "x")
+    yp, ldy = _rows(y, T, N, types, dev, "y")
+    ap = op = wp = None
+    wn = 0
     if adapters is not None:
-        _need(adapters.N == N and adapters.K == K, "adapters: another projection's")
-        _on(x.device, adapters.t[0])
+        if adapters.N != N or adapters.K != K or adapters.t[0].get_device() != dev:
+            raise ValueError("adapters: another projection's, or on another device")
         ap = ctypes.byref(adapters.struct)
     if adapter_of is not None:
-        op = _flat(adapter_of, T, torch.int32, "adapter_of")
-    wp, wn = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-    _check(_call(x.device, stream, lambda s: lib().moe_project(
-        blob.data_ptr(), N, K, xp, ldx, yp, ldy, T, ap, op, gemm, wp, wn, s)), "moe_project")
+        op = _flat(adapter_of, T, torch.int32, "adapter_of", dev)
+    if ws is not None:
+        wn = ws.numel()
+        wp = _flat(ws, 0, torch.uint8, "ws", dev)
+    _call("moe_project", _gpu(x), stream, blob.data_ptr(), N, K, xp, ldx, yp, ldy, T, ap, op, gemm, wp, wn)
