@@ -252,17 +252,23 @@ __device__ inline int key_at(int e) { return e + (e >> 4); }
 // the expert of rank c and its weight. Lane c holds the experts
 // 64 j + 4 c + u (j < NJ, u < 4) of its token. KD: at least min(k, 15) + 1.
 template <int NJ, int KD>
-__device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ], float bmax, SelectLds& L, int& sel,
-                            float& w) {
+__device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, float& w) {
   constexpr int NS = 4 * NJ;
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int E = a.E, k = a.k;
   const int64_t t = min(t0 + q, a.T - 1);
-  float l[NS];
+  float l[NS], b[NS], lv[NJ][4];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) load_logits(a, t, 64 * j + 4 * c, lv[j]);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) b[i] = 0.f;
+  if (a.balance) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) b[i] = a.balance[min(64 * (i >> 2) + 4 * c + (i & 3), E - 1)];
+  }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    float v[4];
-    load_logits(a, t, 64 * j + 4 * c, v);
+    const float(&v)[4] = lv[j];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = 64 * j + 4 * c + u;
@@ -307,6 +313,13 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
 #pragma unroll
     for (int i = 0; i < NS; ++i) s[i] *= top;
   }
+  float bmax = 0.f;  // the largest |bias| (a NaN is the largest of all, and leaves every token in doubt)
+  if (a.balance) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+    bmax = __uint_as_float(row_max_u32(m));
+  }
   const float range = top + bmax;
   const float err = (a.sigmoid ? 0x1p-21f : 0x1p-20f) * range;
   // a decision the fp32 keys cannot settle, and whether it is one of groups
@@ -326,25 +339,44 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
     float lo = INFINITY, hi = -INFINITY;
     for (int g = c >> lg; g < a.n_groups; g += 16) {
       float m1 = -INFINITY, m2 = -INFINITY;
-      for (int i = p; i < size; i += 1 << lg) {
-        const float v = L.v[q][key_at(g * size + i)];
-        m2 = fmaxf(m2, fminf(m1, v));
-        m1 = fmaxf(m1, v);
+      constexpr int kReads = 8;  // under way at once
+      for (int i0 = p; i0 < size; i0 += kReads << lg) {
+        float v[kReads];
+#pragma unroll
+        for (int j = 0; j < kReads; ++j) v[j] = L.v[q][key_at(g * size + min(i0 + (j << lg), size - 1))];
+#pragma unroll
+        for (int j = 0; j < kReads; ++j) {
+          const float x = i0 + (j << lg) < size ? v[j] : -INFINITY;
+          m2 = fmaxf(m2, fminf(m1, x));
+          m1 = fmaxf(m1, x);
+        }
       }
-      for (int o = 1; o < 1 << lg; o <<= 1) {
-        const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
-        m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-        m1 = fmaxf(m1, o1);
-      }
+      // over the group's lanes (all that hold a part agree after each step)
+      auto join = [&](uint32_t o1, uint32_t o2) {
+        const float x1 = __uint_as_float(o1), x2 = __uint_as_float(o2);
+        m2 = fmaxf(fmaxf(m2, x2), fminf(m1, x1));
+        m1 = fmaxf(m1, x1);
+      };
+      const auto u = [](float f) { return __float_as_uint(f); };
+      if (lg >= 1) join(dpp<0xB1>(u(m1)), dpp<0xB1>(u(m2)));
+      if (lg >= 2) join(dpp<0x4E>(u(m1)), dpp<0x4E>(u(m2)));
+      if (lg >= 3) join(dpp<0x141>(u(m1)), dpp<0x141>(u(m2)));
+      if (lg >= 4) join(dpp<0x140>(u(m1)), dpp<0x140>(u(m2)));
       if (p == 0) L.group[q][g] = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     for (int g = c; g < a.n_groups; g += 16) {
       const float mine = L.group[q][g];
       int rank = 0;
-      for (int o = 0; o < a.n_groups; ++o) {
-        const float v = L.group[q][o];
-        rank += v > mine || (v == mine && o < g);
+      for (int o0 = 0; o0 < a.n_groups; o0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = L.group[q][min(o0 + j, a.n_groups - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int o = o0 + j;
+          rank += (o < a.n_groups) & ((v[j] > mine) | ((v[j] == mine) & (o < g)));
+        }
       }
       const bool kept = rank < a.topk_groups;
       L.kept[q][g] = kept;
@@ -454,21 +486,6 @@ __device__ void gate_select(const GateArgs& a, int t0, const float (&b)[4 * NJ],
   }
 }
 
-// The lane's biases and the largest magnitude among all.
-template <int NJ>
-__device__ inline float load_biases(const GateArgs& a, float (&b)[4 * NJ]) {
-  const int c = threadIdx.x & 15;
-#pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) b[i] = 0.f;
-  if (!a.balance) return 0.f;
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) b[i] = a.balance[min(64 * (i >> 2) + 4 * c + (i & 3), a.E - 1)];
-#pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);
-  return __uint_as_float(row_max_u32(m));  // (a NaN bias is the largest, and leaves every token in doubt)
-}
-
 // Exclusive prefix sum of v over the first 256 threads of the block (total in
 // every thread); every thread calls it.
 __device__ inline int scan256(int v, int* scratch /* 4 ints */, int& total) {
@@ -574,10 +591,9 @@ __global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
   }
   const int t0 = (blockIdx.x * W + wave) * 4, t = t0 + (lane >> 4);
   if (t0 < a.T) {
-    float b[4 * NJ], w;
-    const float bmax = load_biases<NJ>(a, b);
     int sel;
-    gate_select<NJ, KD>(a, t0, b, bmax, L[wave], sel, w);
+    float w;
+    gate_select<NJ, KD>(a, t0, L[wave], sel, w);
     if (t < a.T && c < a.k) {
       const int64_t pair = (int64_t)t * a.k + c;
       a.topk_idx[pair] = sel;
@@ -659,10 +675,9 @@ __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, Ga
   __syncthreads();
   const int t0 = 4 * wave, t = t0 + (lane >> 4);
   if (t0 < a.T) {
-    float b[4 * NJ], w;
-    const float bmax = load_biases<NJ>(a, b);
     int sel;
-    gate_select<NJ, KD>(a, t0, b, bmax, L.select[wave], sel, w);
+    float w;
+    gate_select<NJ, KD>(a, t0, L.select[wave], sel, w);
     if (t < a.T && c < a.k) {
       const int pair = t * a.k + c;
       a.topk_idx[pair] = sel;
