@@ -158,7 +158,7 @@ struct GateScatter {
   const uint8_t* counts;
   int32_t *hist, *offsets, *perm, *inv_perm, *block_map, *num_blocks;
   int T, E, k, block_m;
-  int count_tokens;  // per row of counts; set by the launcher
+  int count_tokens, pieces;  // tokens per row of counts, pieces per block; set by the launcher
 };
 // Everything moe_route gives, in one launch for few tokens, two otherwise.
 size_t gate_counts_bytes(int T);

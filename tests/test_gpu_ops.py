@@ -268,6 +268,14 @@ def test_gate_odd_sizes(T, E, k):
         _check_gate(l, _run_gate(l, block_m=16, **kw), block_m=16, **kw)
 
 
+@pytest.mark.parametrize("T,E,k", [(65537, 24, 3), (70001, 200, 1), (140000, 8, 2)])
+def test_gate_many_tokens(T, E, k):
+    # several pieces of tokens for each block of the scatter
+    rng = np.random.default_rng(T)
+    l = _logits(rng, T, E, "plain")
+    _check_gate(l, _run_gate(l, top_k=k, score="softmax"), top_k=k, score="softmax")
+
+
 def test_gate_keys_closer_than_fp32():
     # score + bias differ by less than an fp32 exponential errs: the bias of expert e makes its key the
     # same as its neighbour's up to the bias's own rounding, so only 64 bits tell them apart
