@@ -396,15 +396,16 @@ int moe_project_workspace_bytes(int32_t N, int32_t K, int32_t R, int32_t T, size
 /* A projection by packed int4 weights beside the adapters of many requests:
  *   y[t] = W x[t] + scales[a] * B_a (A_a x[t]),  a = adapter_of[t]
  * for x [T][K] and y [T][N] bf16 with row strides ldx >= K, ldy >= N
- * (elements, multiples of 8, at most 2^20). blob: a pack_int4_g64 blob (device) of one
- * matrix [N][K] (count 1, not paired); N % 64 == 0, K % 128 == 0, K <= 16384,
- * N <= 65536. adapter_of [T] (device, int32) names each token's adapter, in
- * any order; -1, and any other value outside 0..n-1, means none. ad and
- * adapter_of are both given or both null. An adapter's NaN or infinity
+ * (elements, multiples of 8, at most 2^20). blob: a pack_int4_g64 blob
+ * (device) of one matrix [N][K] (count 1, not paired); N % 64 == 0, K % 128 == 0, K <= 16384,
+ * N <= 65536, T <= 2^30. adapter_of [T] (device, int32) names each token's
+ * adapter, in any order; -1, and any other value outside 0..n-1, means none.
+ * ad and adapter_of are both given or both null. An adapter's NaN or infinity
  * reaches its own tokens only. gemm is a MOE_GEMM_* value: how W enters the
  * matrix cores, as in moe_dims (EXACT: used exactly, WIDE: rounded once to
- * bf16, AUTO: by the number of tokens). fp32 accumulation; A_a x is kept to
- * at least 16 significant bits between the two products; y is rounded once.
+ * bf16, AUTO: whichever takes less time for T and N). fp32 accumulation; A_a x
+ * is kept to at least 16 significant bits between the two products; y is
+ * rounded once.
  * x and y must not overlap. ws 16-byte aligned. T = 0 is a no-op. */
 int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64_t ldx, uint16_t* y,
                 int64_t ldy, int32_t T, const moe_adapters* ad, const int32_t* adapter_of,

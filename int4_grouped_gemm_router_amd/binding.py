@@ -463,6 +463,8 @@ def _types_of(code):
         import torch
         _types = ((torch.bfloat16,), (torch.float16,), (torch.float32,), (), (torch.int8, torch.uint8),
                   (torch.float8_e4m3fn, torch.uint8), (torch.bfloat16, torch.int16))
+    if not 0 <= code < len(_types) or not _types[code]:
+        raise ValueError(f"element type {code} is not known")
     return _types[code]
 
 
@@ -554,6 +556,12 @@ def gate(E=256, top_k=8, block_m=32, score=SCORE_SOFTMAX, n_groups=1, topk_group
     return g
 
 
+def _bias_on(g, dev):
+    bias = getattr(g, "bias_tensor", None)
+    if bias is not None and bias.get_device() != dev:
+        raise ValueError(f"balance_bias: on {bias.device}, other tensors on device {dev}: one GPU is needed")
+
+
 def moe_gate_max_blocks(g: MoeGate, T: int) -> int:
     v = lib().moe_gate_max_blocks(ctypes.byref(g), T)
     if v < 0:
@@ -576,15 +584,17 @@ def moe_route_gated(g: MoeGate, logits, T: int, out: RouteBuffers, ws, stream=No
     if (out.topk_idx.numel() < T * g.top_k or out.hist.numel() < g.E or
             out.block_map.shape[0] < (T * g.top_k + g.block_m - 1) // g.block_m + g.E):
         raise ValueError("route_out: buffers of this gate and T are needed")
-    bias = getattr(g, "bias_tensor", None)
-    if out.topk_idx.get_device() != dev or ws.get_device() != dev or (bias is not None and bias.get_device() != dev):
-        raise ValueError("logits, route_out, workspace and balance_bias: one GPU is needed")
-    _call("moe_route_gated", dev, stream, ctypes.byref(g), lp, T, ctypes.byref(out.struct), ws.data_ptr(), ws.numel())
+    if out.topk_idx.get_device() != dev:
+        raise ValueError("logits and route_out: one GPU is needed")
+    _bias_on(g, dev)
+    wp = _flat(ws, 0, _types_of(BITS8 + OUT8_INT8)[1], "ws", dev)
+    _call("moe_route_gated", dev, stream, ctypes.byref(g), lp, T, ctypes.byref(out.struct), wp, ws.numel())
 
 
 def moe_prefill_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, chunk_T: int = 0,
                             logits_out=None, route_out: RouteBuffers | None = None, ws=None, stream=None):
     """moe_prefill_layer routed by a gate."""
+    _bias_on(g, _gpu(x))
     ro = ctypes.byref(route_out.struct) if route_out is not None else None
     _check(lib().moe_prefill_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
                                          _ptr(y), T, chunk_T, _ptr(logits_out), ro, _ptr(ws),
@@ -595,6 +605,7 @@ def moe_prefill_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: i
 def moe_decode_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, logits_out=None,
                            route_out: RouteBuffers | None = None, ws=None, stream=None):
     """moe_decode_layer routed by a gate."""
+    _bias_on(g, _gpu(x))
     ro = ctypes.byref(route_out.struct) if route_out is not None else None
     _check(lib().moe_decode_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
                                         _ptr(y), T, _ptr(logits_out), ro, _ptr(ws),

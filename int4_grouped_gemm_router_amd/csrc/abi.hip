@@ -156,6 +156,8 @@ constexpr int64_t kMaxRowStride = int64_t(1) << 20;
 bool project_dims_ok(int N, int K) {
   return N > 0 && N % 64 == 0 && N <= 65536 && K > 0 && K % 128 == 0 && K <= 16384;
 }
+// (token indices and their tiles stay 32-bit)
+constexpr int32_t kMaxProjectT = 1 << 30;
 bool rank_space_ok(int R) { return R >= 8 && R <= kMaxRank && R % 8 == 0; }
 
 bool gate_ok(const moe_gate* g) {
@@ -792,7 +794,7 @@ int moe_add_rmsnorm(const moe_norm* n, const void* x, int64_t ldx, const void* r
 
 int moe_project_workspace_bytes(int32_t N, int32_t K, int32_t R, int32_t T, size_t* bytes) {
   if (!bytes || T < 0 || R < 0) return MOE_EINVAL;
-  if (!project_dims_ok(N, K) || (R && !rank_space_ok(R))) return MOE_EUNSUPPORTED;
+  if (!project_dims_ok(N, K) || T > kMaxProjectT || (R && !rank_space_ok(R))) return MOE_EUNSUPPORTED;
   *bytes = project_ws_bytes(N, K, R, std::max(T, 1));
   return MOE_OK;
 }
@@ -802,7 +804,7 @@ int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64
                 int32_t gemm, void* ws, size_t ws_bytes, void* stream) {
   if (T < 0 || gemm < MOE_GEMM_AUTO || gemm > MOE_GEMM_WIDE || (ad != nullptr) != (adapter_of != nullptr))
     return MOE_EINVAL;
-  if (!project_dims_ok(N, K)) return MOE_EUNSUPPORTED;
+  if (!project_dims_ok(N, K) || T > kMaxProjectT) return MOE_EUNSUPPORTED;
   if (ad) {
     if (ad->n < 1 || !ad->A || !ad->B || !al16(ad->A) || !al16(ad->B) || !al4(ad->ranks) ||
         !al4(ad->scales) || !al4(adapter_of))

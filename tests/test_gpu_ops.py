@@ -357,6 +357,25 @@ def test_gated_layer(T, chunk):
         assert rel <= 5e-3, f"{name}: {rel}"     # the layer's own bar
 
 
+def test_gate_binding_checks_tensors():
+    _, w, _ = synth.generate("tiny_t32", with_x=False)
+    dw, T = B.DeviceWeights.from_logical(w), 2
+    x = torch.zeros((T, w.H), dtype=torch.int16, device="cuda")
+    g = B.gate(w.E, 8, balance_bias=torch.zeros(w.E))          # a bias in host memory
+    for f, mode in ((B.moe_prefill_layer_gated, B.MODE_PREFILL), (B.moe_decode_layer_gated, B.MODE_DECODE)):
+        with pytest.raises(ValueError):
+            f(dw.dims, g, dw, x, torch.empty_like(x), T, ws=B.workspace(dw.dims, T, mode))
+    logits, ok = torch.zeros((T, w.E), device="cuda"), B.gate(w.E, 8)
+    out, ws = B.RouteBuffers(ok, T), B.gate_workspace(ok, T)
+    with pytest.raises(ValueError):
+        B.moe_route_gated(g, logits, T, out, ws)
+    for bad in (ws[:1].expand(ws.numel()), ws.cpu(), ws.view(torch.int32)):
+        with pytest.raises(ValueError):
+            B.moe_route_gated(ok, logits, T, out, bad)
+    with pytest.raises(ValueError):
+        B.moe_route_gated(ok, logits.cpu(), T, out, ws)
+
+
 def test_gated_layer_with_the_softmax_rule_is_the_layer():
     _, w, _ = synth.generate("tiny_t32", with_x=False)
     dw = B.DeviceWeights.from_logical(w)

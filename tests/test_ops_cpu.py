@@ -159,6 +159,17 @@ def test_project_refusals():
     assert L.moe_project_workspace_bytes(100, 256, 8, 4, by(n)) == B.MOE_EUNSUPPORTED
     assert L.moe_project_workspace_bytes(128, 256, 8, -1, by(n)) == B.MOE_EINVAL
     assert L.moe_project_workspace_bytes(128, 256, 8, 4, None) == B.MOE_EINVAL
+    assert L.moe_project_workspace_bytes(128, 256, 8, (1 << 30) + 1, by(n)) == B.MOE_EUNSUPPORTED
+    assert _project(T=(1 << 30) + 1) == B.MOE_EUNSUPPORTED
+    assert _project(T=0x7FFFFFFF) == B.MOE_EUNSUPPORTED
+
+
+def test_unknown_types_are_refused_by_the_binding():
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16)
+    for n in (B.MoeNorm(64, 3, 3, 0, 0, 1e-6, 0.0), B.MoeNorm(64, -1, 0, 0, 0, 1e-6, 0.0), B.norm(64, out8=7)):
+        with pytest.raises(ValueError):
+            B.moe_add_rmsnorm(n, x, w, 2, y=torch.empty_like(x), q=torch.zeros(2, 64, dtype=torch.int8),
+                              scales=torch.zeros(2))
 
 
 def test_project_binding_checks_tensors():
