@@ -47,21 +47,21 @@ __device__ inline double key_value(uint64_t o) {
 }
 
 // Largest key over the wave and its index, returned to every lane; ties to the
-// lowest lane, whose index has to be the lowest too. (Two 32-bit maxima over
-// the lanes; shuffles of the 64-bit keys took seven times as long, which a
-// late wave in doubt adds to the whole launch.)
+// lowest lane, whose index has to be the lowest too. (A 32-bit maximum over
+// the lanes, and a second one where the upper halves tie; shuffles of the
+// 64-bit keys took seven times as long, which a late wave in doubt adds to
+// the whole launch.)
 __device__ inline void wave_best(uint64_t& k, int& i) {
   const uint32_t hi = (uint32_t)(k >> 32), lo = (uint32_t)k;
-  const uint32_t mh = wave_max_u32(hi), ml = wave_max_u32(hi == mh ? lo : 0u);
-  const uint64_t best = (uint64_t)mh << 32 | ml;
-  const int win = __builtin_ctzll(__ballot(k == best));
+  const uint32_t mh = wave_max_u32(hi);
+  uint64_t at = __ballot(hi == mh);
+  if (at & (at - 1)) {
+    const uint32_t ml = wave_max_u32(hi == mh ? lo : 0u);
+    at = __ballot(hi == mh && lo == ml);
+  }
+  const int win = __builtin_ctzll(at);
   i = __builtin_amdgcn_readlane(i, win);
-  k = best;
-}
-
-__device__ inline double wave_sum_f64(double v) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  k = (uint64_t)mh << 32 | (uint32_t)__builtin_amdgcn_readlane(lo, win);
 }
 
 // Reductions over the 16 lanes of a row, returned to each of them: lane ^ 1,
@@ -100,6 +100,16 @@ __device__ inline double row_sum_f64(double v) {
   v += dpp_f64<0x141>(v);
   return v + dpp_f64<0x140>(v);
 }
+__device__ inline double readlane_f64(double v, int lane) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)u, lane);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+  return __longlong_as_double((long long)(hi << 32 | lo));
+}
+__device__ inline double wave_sum_f64(double v) {
+  v = row_sum_f64(v);
+  return (readlane_f64(v, 0) + readlane_f64(v, 16)) + (readlane_f64(v, 32) + readlane_f64(v, 48));
+}
 
 // Group of expert e: e / size as the high half of e * ceil(2^32 / size), exact
 // for e < 256 (size 1 has no such factor).
@@ -107,45 +117,34 @@ __device__ inline int group_of(const GateArgs& a, int e) {
   return a.group_size == 1 ? e : (int)__umulhi((uint32_t)e, a.group_magic);
 }
 
-// One token's selection in 64 bits: lane j < k gets the expert of rank j and
-// its weight. l: the lane's logits (-inf: masked), b: their biases; kept: per
-// group whether it is kept, or null where that is to be decided too.
-__device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const float (&b)[4], float mx,
-                                  const uint8_t* kept_groups, int& sel, float& w) {
+// One token's selection in 64 bits: lane j < k gets the expert of rank j, with
+// kMaskedSel added where it is masked. l: the lane's logits (-inf: masked), b:
+// their biases; kept: bit g: group g is kept (decided here if !groups_known).
+constexpr int kMaskedSel = 256;
+__device__ int gate_select_exact(const GateArgs& a, const float (&l)[4], const float (&b)[4], float mx,
+                                 bool groups_known, uint64_t kept) {
   const int lane = threadIdx.x & 63, E = a.E, k = a.k;
   double score[4];
   uint64_t key[4];
-  double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (l[i] == -INFINITY)
-      score[i] = 0.0;
-    else if (a.sigmoid)
-      score[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-    else
-      score[i] = l[i] == mx ? 1.0 : exp((double)l[i] - (double)mx);
-    sum += score[i];
+    const double e = exp(a.sigmoid ? -(double)l[i] : (l[i] == mx ? 0.0 : (double)l[i] - (double)mx));
+    score[i] = l[i] == -INFINITY ? 0.0 : e;
   }
-  if (!a.sigmoid) {
-    sum = wave_sum_f64(sum);
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) score[i] = 1.0 / (1.0 + score[i]);
+  } else {
+    const double sum = wave_sum_f64((score[0] + score[1]) + (score[2] + score[3]));
 #pragma unroll
     for (int i = 0; i < 4; ++i) score[i] = sum > 0.0 ? score[i] / sum : 0.0;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     key[i] = 0;
-    if (4 * lane + i < E) {
-      key[i] = l[i] == -INFINITY ? kMaskedKey : key_order(score[i] + (double)b[i]);
-      if (key[i] == kMaskedKey) score[i] = 0.0;
-    }
+    if (4 * lane + i < E) key[i] = l[i] == -INFINITY ? kMaskedKey : key_order(score[i] + (double)b[i]);
   }
-  if (a.n_groups > 1 && kept_groups) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = 4 * lane + i;
-      if (e < E && !kept_groups[group_of(a, e)]) key[i] = 0;
-    }
-  } else if (a.n_groups > 1) {
+  if (a.n_groups > 1 && !groups_known) {
     uint64_t mine = 0;  // lane g: the rank key of group g
     for (int g = 0; g < a.n_groups; ++g) {
       auto best_but = [&](int skip, int& at) {
@@ -170,7 +169,7 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
       }
       if (lane == g) mine = best;
     }
-    uint64_t kept = 0;
+    kept = 0;
     for (int r = 0; r < a.topk_groups; ++r) {
       uint64_t best = mine;
       int at = lane;
@@ -178,14 +177,15 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
       kept |= 1ull << at;
       if (lane == at) mine = 0;
     }
+  }
+  if (a.n_groups > 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = 4 * lane + i;
       if (e < E && !(kept >> group_of(a, e) & 1)) key[i] = 0;
     }
   }
-  double sel_score = 0.0;
-  sel = 0;
+  int sel = 0;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0;
     int at = E;
@@ -196,58 +196,61 @@ __device__ void gate_select_exact(const GateArgs& a, const float (&l)[4], const 
         at = 4 * lane + i;
       }
     wave_best(best, at);
-    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (at == 4 * lane + i) {
-        s = score[i];
-        key[i] = 0;
-      }
-    s = __shfl(s, at >> 2);
-    if (lane == r) {
-      sel = at;
-      sel_score = s;
-    }
+      if (at == 4 * lane + i) key[i] = 0;
+    if (lane == r) sel = best == kMaskedKey ? at + kMaskedSel : at;
   }
-  const double z = wave_sum_f64(lane < k ? sel_score : 0.0);
-  double v = sel_score;
-  if (a.renorm) v = z > 0.0 ? v / z : 0.0;
-  w = (float)(v * (double)a.scale);
+  return sel;
 }
 
-// The sum over the router's K splits plus the router's bias: logits of token
-// t, four consecutive experts from e on (the last four, or the last one
-// repeated, where e is past the end: no branch separates the loads).
-__device__ inline void load_logits(const GateArgs& a, int64_t t, int e, float (&v)[4]) {
+// v[j][u] += row[64 j + e + u], four consecutive values each, all NJ loads
+// under way at once (the last four, or the last one repeated, where they are
+// past the end: no branch separates the loads).
+template <int NJ>
+__device__ inline void add_row(const GateArgs& a, const float* row, int e, float (&v)[NJ][4]) {
   const int E = a.E;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = 0.f;
+  f32x4 p[NJ];
   if (a.vectors) {
-    for (int sp = 0; sp < a.splits; ++sp) {
-      const f32x4 p = *reinterpret_cast<const f32x4*>(a.partial + ((int64_t)sp * a.T + t) * E + min(e, E - 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += p[i];
-    }
+    for (int j = 0; j < NJ; ++j) p[j] = *reinterpret_cast<const f32x4*>(row + min(64 * j + e, E - 4));
   } else {
-    for (int sp = 0; sp < a.splits; ++sp)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += a.partial[((int64_t)sp * a.T + t) * E + min(e + i, E - 1)];
-  }
-  if (a.rbias) {
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += a.rbias[min(e + i, E - 1)];
+      for (int u = 0; u < 4; ++u) p[j][u] = row[min(64 * j + e + u, E - 1)];
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[j][u] += p[j][u];
 }
 
 // A wave's own LDS, per token: the keys for the groups (one word of padding
-// per sixteen spreads the groups over the banks), the groups' rank keys and
-// whether they are kept; then the logits.
+// per sixteen spreads the groups over the banks), or the two largest of every
+// four consecutive keys; the groups' rank keys; then the logits.
 struct SelectLds {
   float v[4][256 + 16];
   float group[4][kMaxGateGroups];
-  uint8_t kept[4][kMaxGateGroups];
 };
 __device__ inline int key_at(int e) { return e + (e >> 4); }
+
+// The two largest of values that are joined one or two at a time.
+struct Top2 {
+  float m1 = -INFINITY, m2 = -INFINITY;
+  __device__ void add(float x) {
+    m2 = fmaxf(m2, fminf(m1, x));
+    m1 = fmaxf(m1, x);
+  }
+  __device__ void add(float x1, float x2) {  // x1 >= x2
+    m2 = fmaxf(fmaxf(m2, x2), fminf(m1, x1));
+    m1 = fmaxf(m1, x1);
+  }
+  template <int CTRL>
+  __device__ void add_lane() {
+    add(__uint_as_float(dpp<CTRL>(__float_as_uint(m1))), __uint_as_float(dpp<CTRL>(__float_as_uint(m2))));
+  }
+};
 
 // Four tokens' selections, t0 + lane / 16 each: lane c = lane % 16 < k gets
 // the expert of rank c and its weight. Lane c holds the experts
@@ -258,27 +261,24 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int E = a.E, k = a.k;
   const int64_t t = min(t0 + q, a.T - 1);
-  float l[NS], b[NS], lv[NJ][4];
+  // the sum over the router's K splits, the router's bias, the bias for balance
+  float l[NS], lv[NJ][4], bv[NJ][4];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) load_logits(a, t, 64 * j + 4 * c, lv[j]);
-#pragma unroll
-  for (int i = 0; i < NS; ++i) b[i] = 0.f;
-  if (a.balance) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) b[i] = a.balance[min(64 * (i >> 2) + 4 * c + (i & 3), E - 1)];
-  }
+  for (int i = 0; i < NS; ++i) lv[i >> 2][i & 3] = bv[i >> 2][i & 3] = 0.f;
+  if (a.balance) add_row<NJ>(a, a.balance, 4 * c, bv);
+  for (int sp = 0; sp < a.splits; ++sp) add_row<NJ>(a, a.partial + ((int64_t)sp * a.T + t) * E, 4 * c, lv);
+  if (a.rbias) add_row<NJ>(a, a.rbias, 4 * c, lv);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const float(&v)[4] = lv[j];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = 64 * j + 4 * c + u;
-      l[4 * j + u] = (e < E) & (v[u] == v[u]) ? v[u] : -INFINITY;
+      l[4 * j + u] = (e < E) & (lv[j][u] == lv[j][u]) ? lv[j][u] : -INFINITY;
     }
     if (a.logits_out && t0 + q < a.T) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (64 * j + 4 * c + u < E) a.logits_out[t * E + 64 * j + 4 * c + u] = v[u];
+        if (64 * j + 4 * c + u < E) a.logits_out[t * E + 64 * j + 4 * c + u] = lv[j][u];
     }
   }
   float mx = l[0];
@@ -295,13 +295,10 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
   float s[NS], top = 1.0f;
   if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));  // (-inf: 1 / inf)
+    for (int i = 0; i < NS; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
   } else {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const float p = __expf(l[i] == mx ? 0.f : l[i] - mx);
-      s[i] = l[i] == -INFINITY ? 0.f : p;
-    }
+    for (int i = 0; i < NS; ++i) s[i] = __expf(fminf(l[i] - mx, 0.f));  // (infinity - infinity: 1)
     float z[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) z[i] = s[i];
@@ -309,104 +306,122 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     for (int n = NS / 2; n > 0; n /= 2)
 #pragma unroll
       for (int i = 0; i < n; ++i) z[i] += z[i + n];
-    const float sum = row_sum(z[0]);
-    top = sum > 0.f ? 1.0f / sum : 0.f;
+    top = 1.0f / row_sum(z[0]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) s[i] *= top;
   }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) s[i] = l[i] == -INFINITY ? -INFINITY : s[i];
   float bmax = 0.f;  // the largest |bias| (a NaN is the largest of all, and leaves every token in doubt)
   if (a.balance) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) m = max(m, __float_as_uint(b[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < NS; ++i) {
+      const float b = bv[i >> 2][i & 3];
+      m = max(m, __float_as_uint(b) & 0x7FFFFFFFu);
+      s[i] += b;
+      if (!(s[i] == s[i])) s[i] = -INFINITY;
+    }
     bmax = __uint_as_float(row_max_u32(m));
   }
   const float range = top + bmax;
   const float err = (a.sigmoid ? 0x1p-21f : 0x1p-20f) * range;
   // a decision the fp32 keys cannot settle, and whether it is one of groups
   bool near = !(range < 1e30f), near_groups = near;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    s[i] = l[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-    if (!(s[i] == s[i])) s[i] = -INFINITY;
-  }
-  uint32_t in = ~0u;  // bit i: expert i's group is kept
+  uint64_t groups = 0;  // the token's kept groups
   if (a.n_groups > 1) {
     // group g: 2^lg lanes (up to sixteen groups), or lane g % 16
     const int size = a.group_size, lg = a.group_lanes_log2, p = c & ((1 << lg) - 1);
+    const bool quads = size % 4 == 0;
+    const int units = quads ? size / 4 : size;  // of a group
+    if (quads) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) L.v[q][key_at(64 * (i >> 2) + 4 * c + (i & 3))] = s[i];
+      for (int j = 0; j < NJ; ++j) {
+        const float x1 = fmaxf(s[4 * j], s[4 * j + 1]), n1 = fminf(s[4 * j], s[4 * j + 1]);
+        const float x2 = fmaxf(s[4 * j + 2], s[4 * j + 3]), n2 = fminf(s[4 * j + 2], s[4 * j + 3]);
+        *reinterpret_cast<f32x2*>(&L.v[q][2 * (16 * j + c)]) =
+            f32x2{fmaxf(x1, x2), fmaxf(fminf(x1, x2), fmaxf(n1, n2))};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) L.v[q][key_at(64 * (i >> 2) + 4 * c + (i & 3))] = s[i];
+    }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     float lo = INFINITY, hi = -INFINITY;
     for (int g = c >> lg; g < a.n_groups; g += 16) {
-      float m1 = -INFINITY, m2 = -INFINITY;
-      constexpr int kReads = 8;  // under way at once
-      for (int i0 = p; i0 < size; i0 += kReads << lg) {
-        float v[kReads];
-#pragma unroll
-        for (int j = 0; j < kReads; ++j) v[j] = L.v[q][key_at(g * size + min(i0 + (j << lg), size - 1))];
+      Top2 m;
+      constexpr int kReads = 4;  // under way at once
+      for (int i0 = p; i0 < units; i0 += kReads << lg) {
+        float v1[kReads], v2[kReads];
 #pragma unroll
         for (int j = 0; j < kReads; ++j) {
-          const float x = i0 + (j << lg) < size ? v[j] : -INFINITY;
-          m2 = fmaxf(m2, fminf(m1, x));
-          m1 = fmaxf(m1, x);
+          const int at = g * units + min(i0 + (j << lg), units - 1);
+          if (quads) {
+            const f32x2 v = *reinterpret_cast<const f32x2*>(&L.v[q][2 * at]);
+            v1[j] = v.x;
+            v2[j] = v.y;
+          } else {
+            v1[j] = L.v[q][key_at(at)];
+            v2[j] = -INFINITY;
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kReads; ++j)
+          if (i0 + (j << lg) < units) m.add(v1[j], v2[j]);
       }
       // over the group's lanes (all that hold a part agree after each step)
-      auto join = [&](uint32_t o1, uint32_t o2) {
-        const float x1 = __uint_as_float(o1), x2 = __uint_as_float(o2);
-        m2 = fmaxf(fmaxf(m2, x2), fminf(m1, x1));
-        m1 = fmaxf(m1, x1);
-      };
-      const auto u = [](float f) { return __float_as_uint(f); };
-      if (lg >= 1) join(dpp<0xB1>(u(m1)), dpp<0xB1>(u(m2)));
-      if (lg >= 2) join(dpp<0x4E>(u(m1)), dpp<0x4E>(u(m2)));
-      if (lg >= 3) join(dpp<0x141>(u(m1)), dpp<0x141>(u(m2)));
-      if (lg >= 4) join(dpp<0x140>(u(m1)), dpp<0x140>(u(m2)));
-      if (p == 0) L.group[q][g] = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
+      if (lg >= 1) m.add_lane<0xB1>();
+      if (lg >= 2) m.add_lane<0x4E>();
+      if (lg >= 3) m.add_lane<0x141>();
+      if (p == 0) L.group[q][g] = a.group_top2 && m.m2 > -INFINITY ? m.m1 + m.m2 : m.m1;
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    for (int g = c; g < a.n_groups; g += 16) {
+    for (int g0 = 0; g0 < a.n_groups; g0 += 16) {
+      const int g = g0 + c;
       const float mine = L.group[q][g];
       int rank = 0;
       for (int o0 = 0; o0 < a.n_groups; o0 += 8) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = L.group[q][min(o0 + j, a.n_groups - 1)];
+        const f32x4 va = *reinterpret_cast<const f32x4*>(&L.group[q][o0]);
+        const f32x4 vb = *reinterpret_cast<const f32x4*>(&L.group[q][o0 + 4]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+          const float v = j < 4 ? va[j & 3] : vb[j & 3];
           const int o = o0 + j;
-          rank += (o < a.n_groups) & ((v[j] > mine) | ((v[j] == mine) & (o < g)));
+          rank += (o < a.n_groups) & ((v > mine) | ((v == mine) & (o < g)));
         }
       }
-      const bool kept = rank < a.topk_groups;
-      L.kept[q][g] = kept;
-      if (kept)
-        lo = fminf(lo, mine);
-      else
-        hi = fmaxf(hi, mine);
+      const bool is = g < a.n_groups, kept = is && rank < a.topk_groups;
+      groups |= (__ballot(kept) >> (16 * q) & 0xFFFFull) << g0;
+      lo = kept ? fminf(lo, mine) : lo;
+      hi = is && !kept ? fmaxf(hi, mine) : hi;
     }
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     lo = row_min(lo);
     hi = row_max(hi);
     near_groups |= hi > -INFINITY && !(lo - hi > 4.0f * err);
     near |= near_groups;
-    in = 0u;
+    if (quads) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int e = 64 * (i >> 2) + 4 * c + (i & 3);
-      const uint32_t kept = L.kept[q][group_of(a, min(e, E - 1))];
-      in |= (e < E ? kept : 0u) << i;
+      for (int j = 0; j < NJ; ++j) {
+        const bool kept = groups >> group_of(a, min(64 * j + 4 * c, E - 1)) & 1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[4 * j + u] = kept ? s[4 * j + u] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int e = 64 * (i >> 2) + 4 * c + (i & 3);
+        s[i] = groups >> group_of(a, min(e, E - 1)) & 1 ? s[i] : -INFINITY;
+      }
     }
   }
   // keys as 24-bit fixed point over the range (0: masked or out of the
-  // running), then the lane's slot and the lane: all keys of a token differ
+  // running, at least 1 otherwise), then the lane's slot and the lane: all
+  // keys of a token differ
   const float scale = 16777000.0f / (range + bmax);
   uint32_t key[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const bool out = (s[i] == -INFINITY) | !(in >> i & 1);
-    const uint32_t v = out ? 0u : 1u + (uint32_t)(fmaxf(s[i] + bmax, 0.f) * scale);
+    const uint32_t v = (uint32_t)fmaxf(__builtin_fmaf(s[i] + bmax, scale, 2.0f), 0.f);
     key[i] = v << 8 | (uint32_t)(i << 4) | (uint32_t)c;
   }
   // the lane's keys in descending order
@@ -425,34 +440,55 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
       }
   // k + 1 rounds: the row's largest head; its lane drops it
   constexpr int ND = NS < KD ? NS : KD;
-  uint32_t mine = 0, next = 0;  // the keys of rank c and c + 1
+  uint32_t mine = 0, m = 0;  // mine: the key of rank c
   for (int r = 0; r <= k; ++r) {
-    const uint32_t m = row_max_u32(key[0]);
+    m = row_max_u32(key[0]);
     mine = c == r ? m : mine;
-    next = c == r - 1 ? m : next;
     const bool own = key[0] == m;
 #pragma unroll
     for (int i = 0; i + 1 < ND; ++i) key[i] = own ? key[i + 1] : key[i];
     if constexpr (ND == NS) key[NS - 1] = own ? 0u : key[NS - 1];
   }
+  const uint32_t next = c == 15 ? m : dpp<0x101>(mine);  // of rank c + 1 (the lane above)
   // twice the bound in steps of the fixed point (16 u of the range is at most
   // 16 of the 2^24 steps over range + bias), and what the steps cut off
   const uint32_t close = (a.sigmoid ? 16 : 32) + 4;
   const uint32_t vm = mine >> 8, vn = next >> 8;
   if (c < k) near |= vm == 0 || (vn > 0 && vm - vn <= close);
   sel = 64 * (int)(mine >> 6 & 3) + 4 * (int)(mine & 15) + (int)(mine >> 4 & 3);
-  // the weights in 64 bits from the selected logits; where the fp32 sum over
-  // the experts is used (softmax, not renormalised) it errs by a few 2^-24
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     *reinterpret_cast<f32x4*>(&L.v[q][64 * j + 4 * c]) = f32x4{l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]};
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+  // in doubt: those tokens again, one at a time, by the whole wave
+  uint64_t doubt = __ballot(near && t0 + q < a.T);
+  const uint64_t doubt_groups = __ballot(near_groups);
+  while (doubt) {
+    const int row = __builtin_ctzll(doubt) >> 4;
+    doubt &= ~(0xFFFFull << (16 * row));
+    float l4[4], b4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      b4[i] = a.balance && e < E ? a.balance[e] : 0.f;
+      l4[i] = e < 64 * NJ ? L.v[row][e] : -INFINITY;
+    }
+    const float top4 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mx), 16 * row));
+    const uint64_t kept = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(groups >> 32), 16 * row) << 32 |
+                          (uint32_t)__builtin_amdgcn_readlane((uint32_t)groups, 16 * row);
+    int se = gate_select_exact(a, l4, b4, top4, !(doubt_groups >> (16 * row) & 0xFFFF), kept);
+    se = __shfl(se, c);
+    if (q == row) sel = se;
+  }
+  // the weights in 64 bits from the selected logits; where the fp32 sum over
+  // the experts is used (softmax, not renormalised) it errs by a few 2^-24
   double v = 0.0;
-  if (c < k) {
+  if (c < k && sel < kMaskedSel) {
     const float x = L.v[q][sel];
     const double e = exp(a.sigmoid ? -(double)x : (x == mx ? 0.0 : (double)x - (double)mx));
     v = a.sigmoid ? 1.0 / (1.0 + e) : e;
   }
+  sel &= kMaskedSel - 1;
   if (a.renorm) {
     const double sum = row_sum_f64(v);
     v = sum > 0.0 ? v / sum : 0.0;
@@ -460,120 +496,29 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     v *= (double)top;
   }
   w = (float)(v * (double)a.scale);
-  // in doubt: those tokens again, one at a time
-  uint64_t doubt = __ballot(near && t0 + q < a.T);
-  const uint64_t doubt_groups = __ballot(near_groups);
-  while (doubt) {
-    const int row = __builtin_ctzll(doubt) >> 4;
-    doubt &= ~(0xFFFFull << (16 * row));
-    float l4[4], b4[4], top4;
-    load_logits(a, t0 + row, 4 * lane, l4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = 4 * lane + i;
-      if (!(e < E && l4[i] == l4[i])) l4[i] = -INFINITY;
-      b4[i] = a.balance && e < E ? a.balance[e] : 0.f;
-    }
-    top4 = __shfl(mx, 16 * row);
-    int se;
-    float we;
-    gate_select_exact(a, l4, b4, top4, doubt_groups >> (16 * row) & 0xFFFF ? nullptr : L.kept[row], se, we);
-    se = __shfl(se, c);
-    we = __shfl(we, c);
-    if (q == row) {
-      sel = se;
-      w = we;
-    }
-  }
 }
 
-// Exclusive prefix sum of v over the first 256 threads of the block (total in
-// every thread); every thread calls it.
-__device__ inline int scan256(int v, int* scratch /* 4 ints */, int& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int inc = v;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int n = __shfl_up(inc, o);
-    if (lane >= o) inc += n;
-  }
-  if (lane == 63 && wave < 4) scratch[wave] = inc;
-  __syncthreads();
-  int base = 0;
-  total = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) base += scratch[w];
-    total += scratch[w];
-  }
-  __syncthreads();
-  return base + inc - v;
+// Inclusive prefix sum over the wave: within rows of sixteen lanes, then the
+// earlier rows' totals.
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // the lane 1 below, 0 outside the row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // rows 1, 3: the last lane of the row below
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // rows 2, 3: lane 31
+  return v;
 }
 
-struct PlaceLds {
-  int at[kGateWaves][256];  // per wave and expert: pairs, then the next position
-  int base[256];            // first position of each expert's pairs of this block
-  int scratch[4];
-};
-
-// Stable scatter of n pairs (first pair p0, experts pe) of one block, in
-// L.base order: wave w places a contiguous piece of them.
-__device__ inline void place_pairs(const GateScatter& a, PlaceLds& L, const int32_t* pe, int p0, int n) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int piece = (n + 64 * kGateWaves - 1) / (64 * kGateWaves) * 64;
-  const int f = min(wave * piece, n), end = min(f + piece, n);
-  for (int i = tid; i < kGateWaves * 256; i += kGateThreads) (&L.at[0][0])[i] = 0;
-  __syncthreads();
-  for (int i = f + lane; i < end; i += 64) atomicAdd(&L.at[wave][pe[i]], 1);
-  __syncthreads();
-  if (tid < a.E) {
-    int c[kGateWaves], run = L.base[tid];
-#pragma unroll
-    for (int w = 0; w < kGateWaves; ++w) c[w] = L.at[w][tid];
-#pragma unroll
-    for (int w = 0; w < kGateWaves; ++w) {
-      L.at[w][tid] = run;
-      run += c[w];
-    }
-  }
-  __syncthreads();
-  for (int i = f + lane; i < end; i += 64) {
-    const int e = pe[i];
-    const uint64_t peers = match_any((uint32_t)e, 8);
-    const int rank = __popcll(peers & lanemask_lt());
-    const int pos = L.at[wave][e] + rank;
-    a.perm[pos] = p0 + i;
-    a.inv_perm[p0 + i] = pos;
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    if (rank == 0) L.at[wave][e] += __popcll(peers);
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-  }
-}
-
-// Histogram, offsets and block map from each expert's total (thread e < E:
-// tot, and off, its first position); block b of nb writes the map entries of
-// experts b, b + nb, ...; block 0 the rest. Every thread calls it.
-__device__ inline void write_map(const GateScatter& a, PlaceLds& L, int tot, int off, int pairs, int b, int nb) {
-  const int tid = threadIdx.x, E = a.E;
-  int blocks_total;
-  const int blocks = tid < E ? (tot + a.block_m - 1) / a.block_m : 0;
-  const int first = scan256(blocks, L.scratch, blocks_total);
-  if (b == 0) {
-    if (tid < E) {
-      a.hist[tid] = tot;
-      a.offsets[tid] = off;
-    }
-    if (tid == 0) {
-      a.offsets[E] = pairs;
-      *a.num_blocks = blocks_total;
-    }
-  }
-  if (tid < E && tid % nb == b)
-    for (int i = 0; i < blocks; ++i) {
-      int* m = a.block_map + 3 * (int64_t)(first + i);
-      m[0] = tid;
-      m[1] = off + i * a.block_m;
-      m[2] = min(a.block_m, tot - i * a.block_m);
-    }
+// The block map's entry that begins at a pair, if one does: its position, its
+// place among the expert's pairs, their number and their first block.
+__device__ inline void write_block(const GateScatter& a, int e, int pos, int rank, int total, int first) {
+  const int lg = a.block_m == 32 ? 5 : 4;
+  if (rank & (a.block_m - 1)) return;
+  int* m = a.block_map + 3 * (int64_t)(first + (rank >> lg));
+  m[0] = e;
+  m[1] = pos;
+  m[2] = min(a.block_m, total - rank);
 }
 
 }  // namespace
@@ -613,19 +558,33 @@ __global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
 
 // Block: 16 waves, `pieces` consecutive pieces of 128 tokens. Every block sums
 // all rows of counts (256 rows of 256 bytes for 4096 and for 16384 tokens), a
-// wave a row at a time, a lane four experts.
+// wave a row at a time, a lane four experts. A token selects an expert at
+// most once, so the tokens of a piece that selected an expert are a 128-bit
+// mask, and a pair's place among them the bits below its token's.
 __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter a) {
-  __shared__ PlaceLds L;
-  __shared__ int32_t pe[kScatterTokens * kMaxGateK];
   __shared__ int part[2][kGateWaves][256];  // [total, before][wave]
+  __shared__ int base[256];                 // first position of each expert's pairs of the piece
+  __shared__ int total[256], first[256], first_block[256];
+  __shared__ int sums[2][4];
+  __shared__ u32x4 mask[256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = a.E, step = kScatterTokens * a.k;
   const int p0 = blockIdx.x * a.pieces * step, end = min(p0 + a.pieces * step, a.T * a.k);
   const int rows = (a.T + a.count_tokens - 1) / a.count_tokens;
   const int mine = blockIdx.x * a.pieces * (kScatterTokens / a.count_tokens);
+  constexpr int kPairs = kScatterTokens * kMaxGateK / kGateThreads;  // per thread and piece
+  int e[kPairs];
+  auto load = [&](int p) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const int i = tid + kGateThreads * j;
+      e[j] = i < step && p + i < end ? a.topk_idx[p + i] : -1;
+    }
+  };
+  load(p0);
   {
     int tot[4] = {0, 0, 0, 0}, bef[4] = {0, 0, 0, 0};
-    constexpr int kRows = 8;  // loads under way
+    constexpr int kRows = 16;  // loads under way
     for (int r0 = wave; r0 < rows; r0 += kRows * kGateWaves) {
       uint32_t v[kRows];
 #pragma unroll
@@ -642,66 +601,147 @@ __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter 
         }
       }
     }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      part[0][wave][4 * lane + h] = tot[h];
-      part[1][wave][4 * lane + h] = bef[h];
-    }
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<i32x4*>(&part[0][wave][4 * lane]) = i32x4{tot[0], tot[1], tot[2], tot[3]};
+    *reinterpret_cast<i32x4*>(&part[1][wave][4 * lane]) = i32x4{bef[0], bef[1], bef[2], bef[3]};
   }
-  for (int i = tid; i < min(step, end - p0); i += kGateThreads) pe[i] = a.topk_idx[p0 + i];
+  if (tid < 256) mask[tid] = u32x4{0u, 0u, 0u, 0u};
   __syncthreads();
-  int tot = 0, bef = 0;
-  if (tid < E)
+  // thread e: expert e's pairs, and its blocks of the map
+  int tot = 0, blocks = 0, scan = 0, scan_blocks = 0;
+  if (tid < 256) {
+    int bef = 0;
+#pragma unroll
     for (int w = 0; w < kGateWaves; ++w) {
       tot += part[0][w][tid];
       bef += part[1][w][tid];
     }
-  int pairs;
-  const int off = scan256(tot, L.scratch, pairs);
-  if (tid < E) L.base[tid] = off + bef;
-  write_map(a, L, tot, off, pairs, blockIdx.x, gridDim.x);
-  place_pairs(a, L, pe, p0, min(step, end - p0));
-  for (int p = p0 + step; p < end; p += step) {
-    __syncthreads();
-    if (tid < E) L.base[tid] = L.at[kGateWaves - 1][tid];  // where the last piece ended
-    for (int i = tid; i < min(step, end - p); i += kGateThreads) pe[i] = a.topk_idx[p + i];
-    __syncthreads();
-    place_pairs(a, L, pe, p, min(step, end - p));
+    blocks = (tot + a.block_m - 1) / a.block_m;
+    scan = wave_scan(tot);
+    scan_blocks = wave_scan(blocks);
+    if (lane == 63) {
+      sums[0][wave] = scan;
+      sums[1][wave] = scan_blocks;
+    }
+    base[tid] = bef;
+    total[tid] = tot;
   }
-}
-
-// One block of 16 waves: up to kGateSmallT = 64 tokens, four a wave.
-template <int NJ, int KD>
-__global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, GateScatter sc) {
-  __shared__ union {
-    SelectLds select[kGateWaves];
-    PlaceLds place;
-  } L;
-  __shared__ int32_t pe[kGateSmallT * kMaxGateK];
-  __shared__ int cnt[256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15;
-  if (tid < 256) cnt[tid] = 0;
+  const int magic = (65536 + a.k - 1) / a.k;  // i / k is i * magic / 2^16 for i < 2048
+  auto mark = [&] {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      const int t = (tid + kGateThreads * j) * magic >> 16;
+      if (e[j] >= 0) atomicOr(reinterpret_cast<uint32_t*>(&mask[e[j]]) + (t >> 5), 1u << (t & 31));
+    }
+  };
+  mark();
   __syncthreads();
-  const int t0 = 4 * wave, t = t0 + (lane >> 4);
-  if (t0 < a.T) {
-    int sel;
-    float w;
-    gate_select<NJ, KD>(a, t0, L.select[wave], sel, w);
-    if (t < a.T && c < a.k) {
-      const int pair = t * a.k + c;
-      a.topk_idx[pair] = sel;
-      a.topk_w[pair] = w;
-      pe[pair] = sel;
-      atomicAdd(&cnt[sel], 1);
+  if (tid < 256) {
+    for (int w = 0; w < wave; ++w) {
+      scan += sums[0][w];
+      scan_blocks += sums[1][w];
+    }
+    const int off = scan - tot;
+    base[tid] += off;
+    first[tid] = off;
+    first_block[tid] = scan_blocks - blocks;
+    if (blockIdx.x == 0) {
+      if (tid < E) {
+        a.hist[tid] = tot;
+        a.offsets[tid] = off;
+      }
+      if (tid == 255) {
+        a.offsets[E] = scan;
+        *a.num_blocks = scan_blocks;
+      }
     }
   }
   __syncthreads();
-  const int tot = tid < a.E ? cnt[tid] : 0;
-  int pairs;
-  const int off = scan256(tot, L.place.scratch, pairs);
-  if (tid < a.E) L.place.base[tid] = off;
-  write_map(sc, L.place, tot, off, pairs, 0, 1);
-  place_pairs(sc, L.place, pe, 0, pairs);
+  for (int p = p0; p < end; p += step) {
+    if (p > p0) {
+      __syncthreads();
+      if (tid < 256) {
+        const u32x4 m = mask[tid];
+        base[tid] += __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+        mask[tid] = u32x4{0u, 0u, 0u, 0u};
+      }
+      load(p);
+      __syncthreads();
+      mark();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      if (e[j] < 0) continue;
+      const int i = tid + kGateThreads * j, t = i * magic >> 16;
+      const u32x4 m = mask[e[j]];
+      int pos = base[e[j]];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t below = t >= 32 * (w + 1) ? ~0u : (t >= 32 * w ? (1u << (t & 31)) - 1u : 0u);
+        pos += __popc(m[w] & below);
+      }
+      a.perm[pos] = p + i;
+      a.inv_perm[p + i] = pos;
+      write_block(a, e[j], pos, pos - first[e[j]], total[e[j]], first_block[e[j]]);
+    }
+  }
+}
+
+// One block, a wave for every four tokens, up to kGateSmallT = 64: the
+// tokens that selected an expert are one 64-bit mask.
+template <int NJ, int KD>
+__global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, GateScatter sc) {
+  __shared__ SelectLds L[kGateWaves];
+  __shared__ uint64_t mask[256];
+  __shared__ int first[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, E = a.E;
+  for (int i = tid; i < 256; i += blockDim.x) mask[i] = 0;
+  const int t0 = 4 * wave, t = t0 + (lane >> 4), pair = t * a.k + c;
+  const bool is = t < a.T && c < a.k;
+  int sel;
+  float w;
+  gate_select<NJ, KD>(a, t0, L[wave], sel, w);
+  __syncthreads();
+  if (is) {
+    a.topk_idx[pair] = sel;
+    a.topk_w[pair] = w;
+    atomicOr(reinterpret_cast<unsigned long long*>(&mask[sel]), 1ull << t);
+  }
+  __syncthreads();
+  if (wave == 0) {  // lane: experts 4 lane + i; pairs and blocks (both at most 1024) are added up in one word
+    const int up = sc.block_m - 1, lg = sc.block_m == 32 ? 5 : 4;
+    int n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] = __popcll(mask[4 * lane + i]);
+      sum += n[i] + ((n[i] + up) >> lg << 16);
+    }
+    const int scan = wave_scan(sum);
+    int at = scan - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = 4 * lane + i;
+      first[x] = at;
+      if (x < E) {
+        sc.hist[x] = n[i];
+        sc.offsets[x] = at & 0xFFFF;
+      }
+      at += n[i] + ((n[i] + up) >> lg << 16);
+    }
+    if (lane == 63) {
+      sc.offsets[E] = scan & 0xFFFF;
+      *sc.num_blocks = scan >> 16;
+    }
+  }
+  __syncthreads();
+  if (is) {
+    const uint64_t tokens = mask[sel];
+    const int rank = __popcll(tokens & ((1ull << t) - 1)), pos = (first[sel] & 0xFFFF) + rank;
+    sc.perm[pos] = pair;
+    sc.inv_perm[pair] = pos;
+    write_block(sc, sel, pos, rank, __popcll(tokens), first[sel] >> 16);
+  }
 }
 
 // Selection blocks of 4 waves (16 tokens) up to 4096 tokens: they spread few
@@ -723,7 +763,8 @@ GateArgs prepared(const GateArgs& in) {
   a.group_magic = a.group_size > 1 ? (uint32_t)((0x100000000ull + a.group_size - 1) / a.group_size) : 0u;
   a.group_lanes_log2 = 0;
   while ((2 << a.group_lanes_log2) * a.n_groups <= 16) ++a.group_lanes_log2;
-  a.vectors = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.partial) & 15) == 0;
+  const auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  a.vectors = a.E % 4 == 0 && ((bits(a.partial) | bits(a.rbias) | bits(a.balance)) & 15) == 0;
   return a;
 }
 
@@ -734,7 +775,7 @@ enum class GateLaunch { kTopk, kCounts, kSmall };
 template <GateLaunch L, int NJ, int KD>
 void launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
   if constexpr (L == GateLaunch::kSmall)
-    hipLaunchKernelGGL((gate_small_kernel<NJ, KD>), dim3(1), dim3(kGateThreads), 0, s, a, *sc);
+    hipLaunchKernelGGL((gate_small_kernel<NJ, KD>), dim3(1), dim3(64 * ((a.T + 3) / 4)), 0, s, a, *sc);
   else if (L == GateLaunch::kCounts && count_tokens(a.T) == 64)
     hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 16, true>), dim3((a.T + 63) / 64), dim3(1024), 0, s, a);
   else

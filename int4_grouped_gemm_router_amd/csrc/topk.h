@@ -25,10 +25,12 @@ __device__ inline uint32_t logit_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// v from another lane of the same row of 16 (DPP control CTRL).
+// v from another lane of the same row of 16 (DPP control CTRL), which has to be
+// active; 0 where the control names a lane outside the row. (The zero lets the
+// compiler fold the move into the operation that uses it.)
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
 // Maximum / minimum of v over the 64 lanes of a fully active wave, returned
