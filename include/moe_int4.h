@@ -354,7 +354,8 @@ typedef struct {
   const float* balance_bias; /* [E] fp32, or NULL */
 } moe_gate;
 
-/* moe_max_blocks and the workspace of moe_route_gated for a gate. */
+/* moe_max_blocks for a gate, and the workspace of moe_route_gated for up to T
+ * tokens. */
 int64_t moe_gate_max_blocks(const moe_gate* gate, int32_t T);
 int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes);
 

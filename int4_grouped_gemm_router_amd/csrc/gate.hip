@@ -744,14 +744,19 @@ __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, Ga
   }
 }
 
-// Selection blocks of 4 waves (16 tokens) up to 4096 tokens: they spread few
-// tokens over the chip (512 tokens: 10.2 us in blocks of 32, 13.9 in blocks of
-// 64). Blocks of 16 waves beyond: a quarter of the rows of counts, which every
-// scatter block sums (16384 tokens: 12.8 us with 512 rows, 9.7 with 256).
-static int count_tokens(int T) { return T <= 4096 ? 16 : 64; }
+// Tokens of a selection block, four a wave: as few as leave a block for each
+// of the 256 compute units, so that a unit's waves do not share its SIMDs
+// while others idle (2048 tokens: 10.3 us with the scatter in blocks of 16,
+// 13.4 in blocks of 64; 8192: 14.3 us in blocks of 32, 16.3 in blocks of
+// 64). More rows of counts than that cost every scatter block their sum (16384
+// tokens: 23.2 us in blocks of 16, 17.1 in blocks of 64).
+static int count_tokens(int T) { return T <= 4096 ? 16 : T <= 8192 ? 32 : 64; }
 
+// Enough for every smaller T too: 4096 tokens have as many rows as 16384.
 size_t gate_counts_bytes(int T) {
-  return T <= kGateSmallT ? 0 : (size_t)((T + count_tokens(T) - 1) / count_tokens(T)) * 256;
+  if (T <= kGateSmallT) return 0;
+  const int rows = (T + count_tokens(T) - 1) / count_tokens(T);
+  return (size_t)(T > 4096 && rows < 256 ? 256 : rows) * 256;
 }
 
 namespace {
@@ -778,6 +783,8 @@ void launch_gate(const GateArgs& a, const GateScatter* sc, hipStream_t s) {
     hipLaunchKernelGGL((gate_small_kernel<NJ, KD>), dim3(1), dim3(64 * ((a.T + 3) / 4)), 0, s, a, *sc);
   else if (L == GateLaunch::kCounts && count_tokens(a.T) == 64)
     hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 16, true>), dim3((a.T + 63) / 64), dim3(1024), 0, s, a);
+  else if (L == GateLaunch::kCounts && count_tokens(a.T) == 32)
+    hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 8, true>), dim3((a.T + 31) / 32), dim3(512), 0, s, a);
   else
     hipLaunchKernelGGL((gate_topk_kernel<NJ, KD, 4, L == GateLaunch::kCounts>), dim3((a.T + 15) / 16), dim3(256), 0, s, a);
 }

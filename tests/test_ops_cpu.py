@@ -103,6 +103,14 @@ def test_gate_refusals():
     assert L.moe_route_gated(by(g), FAKE, 1 << 27, by(ro), FAKE, 1 << 40, None) == B.MOE_EUNSUPPORTED
 
 
+def test_gate_workspace_serves_fewer_tokens():
+    n, most = ctypes.c_size_t(0), 0
+    for T in sorted([*range(0, 20000, 7), 64, 4096, 4097, 8192, 8193, 16384, 16385, 32769, 1 << 20]):
+        assert B.lib().moe_gate_workspace_bytes(by(_gate()), T, by(n)) == B.MOE_OK
+        assert n.value >= most, T
+        most = n.value
+
+
 def test_gated_layer_refusals():
     L = B.lib()
     d, w = B.dims(2048, 512), B.MoeLayerWeights(*([FAKE] * 7))
