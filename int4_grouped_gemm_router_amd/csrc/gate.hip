@@ -120,9 +120,18 @@ __device__ inline int group_of(const GateArgs& a, int e) {
 // One token's selection in 64 bits: lane j < k gets the expert of rank j, with
 // kMaskedSel added where it is masked. l: the lane's logits (-inf: masked), b:
 // their biases; kept: bit g: group g is kept (decided here if !groups_known).
+// least: no selected key is less (used if groups_known; NaN or -inf: not
+// known). The few keys that are not less are ranked by comparing all pairs,
+// from the wave's list in LDS; where there are too many, the largest is taken
+// k times (which takes five times as long).
+struct Candidate {
+  uint64_t key;
+  int e, pad;
+};
+constexpr int kCandidates = 64;
 constexpr int kMaskedSel = 256;
 __device__ int gate_select_exact(const GateArgs& a, const float (&l)[4], const float (&b)[4], float mx,
-                                 bool groups_known, uint64_t kept) {
+                                 bool groups_known, uint64_t kept, double least, Candidate* list) {
   const int lane = threadIdx.x & 63, E = a.E, k = a.k;
   double score[4];
   uint64_t key[4];
@@ -185,6 +194,33 @@ __device__ int gate_select_exact(const GateArgs& a, const float (&l)[4], const f
       if (e < E && !(kept >> group_of(a, e) & 1)) key[i] = 0;
     }
   }
+  const uint64_t bound = groups_known && least > -INFINITY ? key_order(least) : 0;
+  int n = 0, place[4];
+  bool is[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    is[i] = bound > 0 && key[i] >= bound;
+    const uint64_t lanes = __ballot(is[i]);
+    place[i] = n + __popcll(lanes & lanemask_lt());
+    n += __popcll(lanes);
+  }
+  if (n >= k && n <= kCandidates) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (is[i]) list[place[i]] = Candidate{key[i], 4 * lane + i, 0};
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    const Candidate mine = list[lane];
+    int rank = 0;
+    for (int o = 0; o < n; o += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Candidate x = list[o + j];  // (n <= 64: inside the list)
+        rank += (o + j < n) & ((x.key > mine.key) | ((x.key == mine.key) & (x.e < mine.e)));
+      }
+    }
+    // (the lanes past the candidates keep their own place, so all places differ; none is masked)
+    return __builtin_amdgcn_ds_permute(4 * (lane < n ? rank : lane), mine.e);
+  }
   int sel = 0;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0;
@@ -228,10 +264,14 @@ __device__ inline void add_row(const GateArgs& a, const float* row, int e, float
 
 // A wave's own LDS, per token: the keys for the groups (one word of padding
 // per sixteen spreads the groups over the banks), or the two largest of every
-// four consecutive keys; the groups' rank keys; then the logits.
+// four consecutive keys; the groups' rank keys; then the logits, and
+// the candidates of a token in doubt.
 struct SelectLds {
   float v[4][256 + 16];
-  float group[4][kMaxGateGroups];
+  union {
+    float group[4][kMaxGateGroups];
+    Candidate list[kCandidates];
+  };
 };
 __device__ inline int key_at(int e) { return e + (e >> 4); }
 
@@ -476,7 +516,12 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     const float top4 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mx), 16 * row));
     const uint64_t kept = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(groups >> 32), 16 * row) << 32 |
                           (uint32_t)__builtin_amdgcn_readlane((uint32_t)groups, 16 * row);
-    int se = gate_select_exact(a, l4, b4, top4, !(doubt_groups >> (16 * row) & 0xFFFF), kept);
+    // the lowest selected fp32 key, less what it and a fixed-point step may err
+    const uint32_t last = __builtin_amdgcn_readlane(vm, 16 * row + k - 1);
+    const double step = 1.0 / (double)__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * row));
+    const double least =
+        last > close + 4 ? ((double)last - 4.0 - (double)close) * step - (double)bmax : -(double)INFINITY;
+    int se = gate_select_exact(a, l4, b4, top4, !(doubt_groups >> (16 * row) & 0xFFFF), kept, least, L.list);
     se = __shfl(se, c);
     if (q == row) sel = se;
   }

@@ -293,6 +293,20 @@ def test_gate_keys_closer_than_fp32():
             _check_gate(l, _run_gate(l, **kw), **kw)
 
 
+@pytest.mark.parametrize("equal", [2, 9, 63, 64, 65, 100, 256])
+def test_gate_many_equal_keys(equal):
+    # `equal` experts share the largest key; with a bias, with groups and without
+    rng = np.random.default_rng(equal)
+    for T in (1, 70):
+        l = rng.normal(size=(T, 256)).astype(np.float32)
+        for t in range(T):
+            l[t, rng.permutation(256)[:equal]] = 5.0
+        for kw in (dict(score="softmax"), dict(score="sigmoid", bias=np.full(256, 0.25, np.float32)),
+                   dict(score="sigmoid", n_groups=8, topk_groups=4, group_score="top2"),
+                   dict(score="softmax", n_groups=32, topk_groups=9)):
+            _check_gate(l, _run_gate(l, top_k=8, **kw), top_k=8, **kw)
+
+
 def test_gate_softmax_agrees_with_moe_route():
     rng = np.random.default_rng(12)
     T, E = 1000, 256
