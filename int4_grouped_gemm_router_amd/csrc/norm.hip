@@ -75,45 +75,65 @@ __device__ inline uint32_t add_bits(uint32_t a, uint32_t b) {
 }
 __device__ inline uint32_t max_bits(uint32_t a, uint32_t b) { return max(a, b); }
 
-// Eight v / s rounded to int8 (the integer is in the low bits of
-// v / s + 1.5 2^23, rounded to even by that addition) or e4m3. `plain`: s is
-// normal and finite, and 1 / s its inverse; else 0 for s = 0, limited
-// quotients for the coarse scales below the normal range, and NaN or 0 where
-// the scale is not finite.
+// A group's scale and what its quotients are formed with. The values t of a
+// row are v up to the factor f (1 <= f < 2), which cancels in v / s = t Q / m
+// with m the largest |t| of the group: that quotient, corrected once, is
+// rounded correctly, where v / s from a rounded v and s is off by a few units
+// (and more 8-bit values land on the wrong side of a tie).
+struct Group {
+  float s, m, inv, f;
+  bool plain;  // m is far from under- and overflow
+};
 template <int OUT8>
-__device__ inline Bytes8 eight_bits(const float (&v)[kVec], float s, float inv, bool plain) {
+constexpr float kTop = OUT8 == kOut8Int8 ? 127.f : 448.f;
+
+template <int OUT8>
+__device__ inline Group group_of_max(float m, float f) {
+  Group g;
+  g.m = m;
+  g.f = f;
+  g.s = m * f / kTop<OUT8>;
+  g.plain = m >= 0x1p-100f && m < 0x1p100f;
+  g.inv = g.plain ? 1.0f / m : 0.f;
+  return g;
+}
+
+// The quotient of t before rounding; otherwise than plain: 0 for s = 0,
+// limited quotients for the coarse scales below the normal range, and NaN (or
+// 0 for int8) where the scale is not finite.
+template <int OUT8>
+__device__ inline float quotient(float t, const Group& g) {
+  constexpr float Q = kTop<OUT8>;
+  if (g.plain) {
+    const float n = t * Q, q = n * g.inv;  // (n is exact for 16-bit rows and weights)
+    return __builtin_fmaf(__builtin_fmaf(-q, g.m, n), g.inv, q);
+  }
+  float q = g.s == 0.f ? 0.f : t * g.f / g.s;
+  if (OUT8 == kOut8Int8 && !(g.s < INFINITY)) q = 0.f;
+  if (q > Q) q = Q;
+  if (q < -Q) q = -Q;
+  return OUT8 == kOut8Int8 && !(q == q) ? 0.f : q;
+}
+
+// Eight quotients rounded to int8 (the integer is in the low bits of
+// q + 1.5 2^23, rounded to even by that addition) or e4m3.
+template <int OUT8>
+__device__ inline Bytes8 eight_bits(const float (&t)[kVec], const Group& g) {
   Bytes8 o;
-  if (OUT8 == kOut8Int8) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = quotient<OUT8>(t[4 * h + i], g);
+    if (OUT8 == kOut8Int8) {
       uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float t = v[4 * h + i] * inv;
-        if (!plain) {
-          t = s > 0.f && s < INFINITY ? v[4 * h + i] / s : 0.f;
-          t = fminf(fmaxf(t, -127.f), 127.f);
-        }
-        b[i] = __float_as_uint(t + 12582912.0f);
-      }
+      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + 12582912.0f);
       const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0C);
       o.v[h] = lo | hi;
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float t[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        t[i] = v[4 * h + i] * inv;
-        if (!plain) {
-          t[i] = s == 0.f ? 0.f : v[4 * h + i] / s;
-          if (t[i] > 448.f) t[i] = 448.f;
-          if (t[i] < -448.f) t[i] = -448.f;
-        }
-      }
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
+    } else {
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
       o.v[h] = (uint32_t)w;
     }
   }
@@ -187,32 +207,34 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a) {
     ss = __uint_as_float(row_all<TPR>(__float_as_uint(ss), red, add_bits));
     const float r = 1.0f / sqrtf(ss / (float)H + a.eps);
 
-    auto store = [&](E* dst) {
+    auto store = [&](E* dst, auto value) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (lt + TPR * j) * kVec;
         if (c + kVec <= H) {
           Eight<E> o;
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) o.v[i] = R::put(v[j][i]);
+          for (int i = 0; i < kVec; ++i) o.v[i] = R::put(value(j, i));
           *reinterpret_cast<Eight<E>*>(dst + c) = o;
         } else {
 #pragma unroll
           for (int i = 0; i < kVec; ++i)
-            if (c + i < H) dst[c + i] = R::put(v[j][i]);
+            if (c + i < H) dst[c + i] = R::put(value(j, i));
         }
       }
     };
-    if (a.h_out) store(static_cast<E*>(a.h_out) + row * a.ld_h);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) v[j][i] = v[j][i] * r * w[j][i];
-    if (a.y) store(static_cast<E*>(a.y) + row * a.ld_y);
+    if (a.h_out) store(static_cast<E*>(a.h_out) + row * a.ld_h, [&](int j, int i) { return v[j][i]; });
+    if (a.y) store(static_cast<E*>(a.y) + row * a.ld_y, [&](int j, int i) { return v[j][i] * r * w[j][i]; });
     if constexpr (OUT8 != kOut8None) {
+      // v with the power of two in r only (both products are exact for 16-bit
+      // rows and weights): the rest of r is the group scale's factor
+      const float p = __uint_as_float(__float_as_uint(r) & 0x7F800000u), f = p > 0.f ? r / p : r;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[j][i] = v[j][i] * p * w[j][i];
       // |v| as ordered bits: their integer maximum is the largest magnitude,
       // with NaN above infinity (values past the row are 0)
-      const float Q = OUT8 == kOut8Int8 ? 127.f : 448.f;
       uint32_t m[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -245,10 +267,9 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a) {
       for (int j = 0; j < NV; ++j) {
         const int c = (lt + TPR * j) * kVec;
         if (c >= H) continue;
-        const float s = __uint_as_float(m[j]) / Q;
-        const bool plain = s >= 0x1p-120f && s < INFINITY;
-        if (a.group ? c % a.group == 0 : c == 0) scales[a.group ? c / a.group : 0] = s;
-        const Bytes8 o = eight_bits<OUT8>(v[j], s, plain ? 1.0f / s : 0.f, plain);
+        const Group g = group_of_max<OUT8>(__uint_as_float(m[j]), f);
+        if (a.group ? c % a.group == 0 : c == 0) scales[a.group ? c / a.group : 0] = g.s;
+        const Bytes8 o = eight_bits<OUT8>(v[j], g);
         if (c + kVec <= H) {
           *reinterpret_cast<Bytes8*>(q + c) = o;
         } else {
