@@ -570,7 +570,10 @@ __device__ inline void write_block(const GateScatter& a, int e, int pos, int ran
 
 // Grid: ceil(T / (4 W)). Block: W waves, four tokens each. COUNTS: the block
 // writes its row of expert counts [grid][256] bytes (at most 64 each);
-// otherwise counts are added to chunk_hist (when given).
+// otherwise counts are added to chunk_hist (when given). 256 experts, eight
+// groups, sigmoid and bias: 6 us for 512 tokens (the chain of one wave), 17
+// for 16384 (vector instructions, about 1300 a wave); 60 experts, softmax,
+// 2049 tokens: 4.
 template <int NJ, int KD, int W, bool COUNTS>
 __global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
   __shared__ SelectLds L[W];
@@ -605,7 +608,8 @@ __global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
 // all rows of counts (256 rows of 256 bytes for 4096 and for 16384 tokens), a
 // wave a row at a time, a lane four experts. A token selects an expert at
 // most once, so the tokens of a piece that selected an expert are a 128-bit
-// mask, and a pair's place among them the bits below its token's.
+// mask, and a pair's place among them the bits below its token's. Latency
+// bounds it: 5 us for 512 tokens, 5.8 for 16384 (131072 pairs).
 __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter a) {
   __shared__ int part[2][kGateWaves][256];  // [total, before][wave]
   __shared__ int base[256];                 // first position of each expert's pairs of the piece
@@ -734,7 +738,9 @@ __global__ __launch_bounds__(kGateThreads) void gate_scatter_kernel(GateScatter 
 }
 
 // One block, a wave for every four tokens, up to kGateSmallT = 64: the
-// tokens that selected an expert are one 64-bit mask.
+// tokens that selected an expert are one 64-bit mask. 256 experts: 4.7 us for
+// one token, 8.1 for 64 (6.2 for one with a sigmoid, a bias and eight groups);
+// from there on two launches take no longer.
 template <int NJ, int KD>
 __global__ __launch_bounds__(kGateThreads) void gate_small_kernel(GateArgs a, GateScatter sc) {
   __shared__ SelectLds L[kGateWaves];

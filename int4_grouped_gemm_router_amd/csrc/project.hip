@@ -89,9 +89,11 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 // `entries`-th distinct adapter of the tile and every `parts`-th 16 ranks of
 // it; the eight waves split K in chunks of 128 inputs, kHeld of them at a time
 // in the wave's own part of LDS (no barrier: the wave waits for its copies).
-// Grid: token tiles x parts x entries (entries fastest). What counts is latency: the activations are
-// under way before the adapters are known and serve every entry while they
-// are held, and an entry's part of A is under way before its rank is known.
+// Grid: token tiles x parts x entries (entries fastest). What counts is
+// latency: the activations are under way before the adapters are known and
+// serve every entry while they are held, and an entry's part of A is under way
+// before its rank is known. K = 2048, rank 16: 2.9 us for one token, 5.6 for
+// 32 tokens of 32 adapters (2.1 MB of them), 7.7 for 4096 tokens.
 struct DownLds {
   static constexpr int kHeld = 2;
   u32x4 x[kPWaves][kHeld][4][64], a[kPWaves][kHeld][4][64];  // [wave][chunk][32 inputs][frag_slot]
@@ -188,7 +190,9 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 // of the tokens are dealt out over the waves too; their operands are loaded
 // ahead of the groups (NE adapters a wave, the first 32 ranks), and their
 // B_a z goes to a tile of its own, added last, so a token's result does not
-// depend on the others.
+// depend on the others. 4096 x 2048: 5.2 us for one token (latency of one
+// pass), 8.0 for 32 tokens with 32 adapters; 2048 x 2048 for 500 tokens: 13.6
+// (the expansion of the codes, which every 64 rows repeat).
 template <int MS, int CT, int D>
 struct SplitLds {
   static constexpr int kStride = 16 * CT + 4;  // floats; the pad spreads the rows over the banks
@@ -469,7 +473,8 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
 // weights per four of them. The unit of the pipeline is half a group (k half,
 // 32 inputs): in half h the products of h run while h + 2 is written to LDS,
 // and the first operands of h + 1 are read before the barrier that ends h
-// (h + 1 was complete at the barrier before).
+// (h + 1 was complete at the barrier before). 4096 tokens, 4096 x 2048: 62 to
+// 64 us (1.1 PFLOP/s), about 70 with adapters of rank 16.
 template <int RS>
 struct TileLds {
   u32x4 x[2][2][2 * RS][64];  // [group % 2][k half][16-token subtile][frag_slot]
