@@ -5,7 +5,8 @@
 //
 // Two launches: the adapters' first product z into the workspace (fp32 sums,
 // kept as two bf16 halves: 16 significant bits), then the projection, in
-// whose epilogue B_a z is a few more matrix-core operations per tile.
+// whose epilogue B_a z is a few more matrix-core operations per tile. One
+// launch for one to four tokens of low rank.
 //
 // Tokens are never sorted by adapter: a 16-token tile walks over the distinct
 // adapters of its tokens (one in a prompt, up to 16 in a batch of single
@@ -23,6 +24,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "topk.h"
 #include "wide_expand.h"
 
 namespace moe {
@@ -31,6 +33,11 @@ namespace {
 
 constexpr int kPWaves = 8;
 constexpr int kPThreads = 64 * kPWaves;
+// T R up to which the projection's blocks form z themselves, each reading all
+// of the adapters' rows, and the launch before them is spared: 4096 x 2048,
+// one token, rank 8 or 16 6.2 us against 7.4, rank 32 7.8 against 7.4 but one
+// launch fewer for the host (3.4 us); rank 64 11.6 against 7.8.
+constexpr int kFusedRows = 32;
 
 // The adapter of token t, or -1.
 __device__ inline int adapter_at(const ProjectArgs& a, int t) {
@@ -69,6 +76,17 @@ __device__ inline u32x4 rank_mask(u32x4 v, int left) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = left >= 2 * j + 2 ? v[j] : (left == 2 * j + 1 ? v[j] & 0xFFFFu : 0u);
   return v;
+}
+
+// Sum over the wave, in every lane.
+__device__ inline float sum_lanes(float v) {
+  const auto at = [](uint32_t u) { return __uint_as_float(u); };
+  v += at(dpp<0xB1>(__float_as_uint(v)));
+  v += at(dpp<0x4E>(__float_as_uint(v)));
+  v += at(dpp<0x141>(__float_as_uint(v)));
+  v += at(dpp<0x140>(__float_as_uint(v)));
+  const auto row = [&](int l) { return at(__builtin_amdgcn_readlane(__float_as_uint(v), l)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
 // Eight consecutive ranks from r0 of row `row` of a [rows][R] array, zero
@@ -190,9 +208,10 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 // of the tokens are dealt out over the waves too; their operands are loaded
 // ahead of the groups (NE adapters a wave, the first 32 ranks), and their
 // B_a z goes to a tile of its own, added last, so a token's result does not
-// depend on the others. 4096 x 2048: 5.2 us for one token (latency of one
-// pass), 8.0 for 32 tokens with 32 adapters; 2048 x 2048 for 500 tokens: 13.6
-// (the expansion of the codes, which every 64 rows repeat).
+// depend on the others. 4096 x 2048: 6.2 us for one token with an adapter of
+// rank 16 (latency of one pass, FUSED), 8.0 for 32 tokens with 32 adapters;
+// 2048 x 2048 for 500 tokens: 13.6 (the expansion of the codes, which every 64
+// rows repeat).
 template <int MS, int CT, int D>
 struct SplitLds {
   static constexpr int kStride = 16 * CT + 4;  // floats; the pad spreads the rows over the banks
@@ -203,10 +222,14 @@ struct SplitLds {
   };
 };
 
-template <int MS, int CT, int D, int NE>
+// FUSED (T R <= kFusedRows): every block forms z itself, a wave a rank's row of
+// A at a time, while its first codes are on their way.
+template <int MS, int CT, int D, int NE, bool FUSED>
 __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs a) {
   typedef SplitLds<MS, CT, D> Lds;
   __shared__ Lds L;
+  __shared__ float zs[FUSED ? kFusedRows : 1];  // [T][R]
+  static_assert(!FUSED || MS == 1, "the tokens are in one tile");
   constexpr int kSub = 4 / CT;  // blocks per 64-column wave tile
   constexpr int NW = CT == 4 ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -290,9 +313,23 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
       o.b[ct] = rank_chunk(a.B, (int64_t)e.ad * a.N + 64 * wt + 16 * (ct0 + ct) + c16, a.R, s + 8 * kb, a.R);
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
+      if constexpr (FUSED) break;  // (from LDS, by fused_z)
       const int64_t t = min(t0 + 16 * ms + c16, a.T - 1);
       o.zh[ms] = rank_chunk(z_hi(a), t, a.R, s + 8 * kb, a.R);
       o.zl[ms] = rank_chunk(z_lo(a), t, a.R, s + 8 * kb, a.R);
+    }
+  };
+  // z's halves in the place of the workspace's
+  auto fused_z = [&](int s, Operands& o) {
+    o.zh[0] = o.zl[0] = u32x4{0u, 0u, 0u, 0u};
+    const int r0 = s + 8 * kb;
+    if (c16 < a.T && r0 < a.R) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v0 = zs[c16 * a.R + r0 + 2 * j], v1 = zs[c16 * a.R + r0 + 2 * j + 1];
+        o.zh[0][j] = pack_bf16x2(v0, v1);
+        o.zl[0][j] = pack_bf16x2(v0 - bf16lo(o.zh[0][j]), v1 - bf16hi(o.zh[0][j]));
+      }
     }
   };
   Entry first[NE];
@@ -314,6 +351,54 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
       }
     }
     left = rem;
+  }
+  if constexpr (FUSED) {
+    constexpr int kRows = 2, kChunks = 4;  // rows at a time; 512 inputs each
+    const int n = a.T * a.R;
+    for (int i0 = wave; i0 < n; i0 += kRows * kPWaves) {
+      float sum[kRows] = {0.f, 0.f};
+      int ad[kRows], r[kRows];
+      const uint16_t *ap[kRows], *xp[kRows];
+#pragma unroll
+      for (int h = 0; h < kRows; ++h) {
+        const int i = min(i0 + kPWaves * h, n - 1), t = i / a.R;
+        r[h] = i - t * a.R;
+        ad[h] = __builtin_amdgcn_readlane(mine, t);
+        ap[h] = a.A + ((int64_t)max(ad[h], 0) * a.R + r[h]) * a.K;
+        xp[h] = a.x + t * a.ldx;
+      }
+      for (int k0 = 0; k0 < a.K; k0 += 512 * kChunks) {
+        u32x4 av[kRows][kChunks], xv[kRows][kChunks];
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          const int k = k0 + 512 * j + 8 * lane;
+#pragma unroll
+          for (int h = 0; h < kRows; ++h) {
+            av[h][j] = xv[h][j] = u32x4{0u, 0u, 0u, 0u};
+            if (k < a.K) {
+              av[h][j] = *reinterpret_cast<const u32x4*>(ap[h] + k);
+              xv[h][j] = *reinterpret_cast<const u32x4*>(xp[h] + k);
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+          for (int h = 0; h < kRows; ++h)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              sum[h] = __builtin_fmaf(bf16lo(av[h][j][u]), bf16lo(xv[h][j][u]), sum[h]);
+              sum[h] = __builtin_fmaf(bf16hi(av[h][j][u]), bf16hi(xv[h][j][u]), sum[h]);
+            }
+      }
+#pragma unroll
+      for (int h = 0; h < kRows; ++h) {
+        const float v = sum_lanes(sum[h]);
+        const bool is = ad[h] >= 0 && r[h] < rank_of(a, max(ad[h], 0));
+        if (lane == 0 && i0 + kPWaves * h < n)
+          zs[i0 + kPWaves * h] = is ? v * (a.scales ? a.scales[ad[h]] : 1.f) : 0.f;
+      }
+    }
   }
 
   // ---- W x
@@ -395,13 +480,14 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
     }
   }
   if (with) {
-    auto finish = [&](const Entry& e, int rank, const Operands& o0) {
+    auto finish = [&](const Entry& e, int rank, Operands& o0) {
       f32x4 d[MS][CT];
 #pragma unroll
       for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) d[ms][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-      auto add = [&](const Operands& o, int s) {
+      auto add = [&](Operands& o, int s) {
+        if constexpr (FUSED) fused_z(s, o);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           const u32x4 b = rank_mask(o.b[ct], rank - s - 8 * kb);
@@ -699,12 +785,12 @@ size_t project_ws_bytes(int /*N*/, int /*K*/, int R, int T) {
 
 namespace {
 
-template <int MS, int CT, int D, int NE>
+template <int MS, int CT, int D, int NE, bool FUSED = false>
 hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * (a.N / 64) * (4 / CT);
   const int64_t blocks = (units + 7) / 8 * 8;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((project_split_kernel<MS, CT, D, NE>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
+  hipLaunchKernelGGL((project_split_kernel<MS, CT, D, NE, FUSED>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -720,17 +806,6 @@ hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
-  if (a.adapter_of) {
-    // blocks for each rank tile and for several adapters of a token tile while
-    // there are compute units for them
-    const int64_t tiles = (a.T + 15) / 16;
-    int parts = (a.R + 15) / 16, entries = min(min(16, a.n), a.T);
-    while (parts > 1 && tiles * parts > 256) parts = (parts + 1) / 2;
-    while (entries > 1 && tiles * parts * entries > 256) entries = (entries + 1) / 2;
-    if (tiles * parts * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * parts * entries)), dim3(kPThreads), 0, s, a, entries,
-                       parts);
-  }
   // The kernel and tile that take least, from what each measured at K = 2048
   // (all of them grow with K alike): a start and a time per round of 256
   // units, one for each compute unit, in tenths of a microsecond. Small tiles
@@ -741,12 +816,17 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
   struct Tiling {
     int rows, cols, start, round;
     hipError_t (*launch)(const ProjectArgs&, hipStream_t);
+    hipError_t (*fused)(const ProjectArgs&, hipStream_t);
   };
   static const Tiling tilings[] = {
-      {16, 16, 22, 20, launch_split<1, 1, 4, 2>},   {16, 32, 24, 20, launch_split<1, 2, 4, 2>},
-      {16, 64, 15, 36, launch_split<1, 4, 4, 2>},   {32, 32, 12, 39, launch_split<2, 2, 2, 4>},
-      {32, 64, 6, 57, launch_split<2, 4, 2, 1>},    {64, 64, 0, 100, launch_split<4, 4, 2, 1>},
-      {128, 256, 0, 330, launch_tile<4>},           {256, 256, 0, 600, launch_tile<8>},
+      {16, 16, 22, 20, launch_split<1, 1, 4, 2>, launch_split<1, 1, 4, 2, true>},
+      {16, 32, 24, 20, launch_split<1, 2, 4, 2>, launch_split<1, 2, 4, 2, true>},
+      {16, 64, 15, 36, launch_split<1, 4, 4, 2>, launch_split<1, 4, 4, 2, true>},
+      {32, 32, 12, 39, launch_split<2, 2, 2, 4>, nullptr},
+      {32, 64, 6, 57, launch_split<2, 4, 2, 1>, nullptr},
+      {64, 64, 0, 100, launch_split<4, 4, 2, 1>, nullptr},
+      {128, 256, 0, 330, launch_tile<4>, nullptr},
+      {256, 256, 0, 600, launch_tile<8>, nullptr},
   };
   constexpr int kSplits = 6, kAll = 8;
   const int first = a.gemm == 2 ? kSplits : 0, last = a.gemm == 1 ? kSplits : kAll;
@@ -760,6 +840,18 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
       best = &t;
       least = cost;
     }
+  }
+  if (a.adapter_of && (int64_t)a.T * a.R <= kFusedRows && best->fused) return best->fused(a, s);
+  if (a.adapter_of) {
+    // blocks for each rank tile and for several adapters of a token tile while
+    // there are compute units for them
+    const int64_t tiles = (a.T + 15) / 16;
+    int parts = (a.R + 15) / 16, entries = min(min(16, a.n), a.T);
+    while (parts > 1 && tiles * parts > 256) parts = (parts + 1) / 2;
+    while (entries > 1 && tiles * parts * entries > 256) entries = (entries + 1) / 2;
+    if (tiles * parts * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * parts * entries)), dim3(kPThreads), 0, s, a, entries,
+                       parts);
   }
   return best->launch(a, s);
 }

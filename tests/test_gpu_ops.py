@@ -504,6 +504,30 @@ def test_project_real_sizes(T, N, K, R, n):
         _check_project(m, x, _project(m, x, ad, of), ad, of, wide=True)
 
 
+@pytest.mark.parametrize("N,K", [(64, 128), (192, 640), (4096, 2048), (6144, 2176), (12288, 512), (128, 16384)])
+def test_project_few_tokens(N, K):
+    # the projection's blocks form the adapters' first product themselves
+    m, n = _Matrix(N, K), 3
+    for T, R in ((1, 8), (1, 16), (1, 24), (1, 32), (1, 40), (2, 8), (2, 16), (3, 8), (4, 8), (5, 8), (1, 128)):
+        ad = _adapters(N, K, n, R)
+        x = _x(T, K)
+        for of in ((torch.arange(T) % n).to(torch.int32), torch.full((T,), 1, dtype=torch.int32),
+                   torch.full((T,), -1, dtype=torch.int32)):
+            for gemm in (B.GEMM_AUTO, B.GEMM_EXACT):
+                _check_project(m, x, _project(m, x, ad, of, gemm, pad=8), ad, of, wide=gemm != B.GEMM_EXACT)
+    # a NaN adapter, what lies behind a rank, and a token of NaN
+    A, Bm, _, scales = _adapters(N, K, 3, 8)
+    ranks = torch.tensor([8, 5, 8], dtype=torch.int32)
+    dirty = [A.clone(), Bm.clone(), ranks, scales]
+    dirty[0][2, 3], dirty[0][1, 5:], dirty[1][1, :, 5:] = float("nan"), float("inf"), float("nan")
+    x, of = _x(4, K), torch.tensor([1, 2, -1, 0], dtype=torch.int32)
+    clean = _project(m, x, (A, Bm, ranks, scales), of)
+    x[3] = float("nan")
+    y = _project(m, x, dirty, of)
+    assert torch.equal(y[[0, 2]], clean[[0, 2]])
+    assert y[1].isnan().all() and y[3].isnan().all()
+
+
 def test_project_adapter_names_out_of_range_mean_none():
     m, n = _Matrix(128, 256), 3
     ad = _adapters(128, 256, n, 8)
