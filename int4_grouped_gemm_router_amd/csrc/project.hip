@@ -45,9 +45,37 @@ __device__ inline int adapter_at(const ProjectArgs& a, int t) {
   return i >= 0 && i < a.n ? i : -1;
 }
 
-__device__ inline int rank_of(const ProjectArgs& a, int i) {
-  return a.ranks ? min(max(a.ranks[i], 0), a.R) : a.R;
-}
+// As the load and what is made of it, where other loads go in between.
+__device__ inline int rank_load(const ProjectArgs& a, int i) { return a.ranks ? a.ranks[i] : a.R; }
+__device__ inline int rank_value(const ProjectArgs& a, int v) { return min(max(v, 0), a.R); }
+__device__ inline int rank_of(const ProjectArgs& a, int i) { return rank_value(a, rank_load(a, i)); }
+
+// The distinct adapters of a wave's rows (lane r: row r's, or -1), in row
+// order, found for all rows at once from one ballot per bit of the adapters'
+// indices.
+struct Distinct {
+  int mine, n;      // n: how many
+  uint64_t same;    // the lane's: rows of its adapter
+  int place;        // of the lane's adapter, if its row is the first with it, else -1
+  __device__ Distinct(int adapter, int adapters) : mine(adapter) {
+    same = __ballot(mine >= 0);
+    for (int b = 0; b < 31 && (adapters - 1) >> b; ++b) {
+      const uint64_t bit = __ballot(mine >> b & 1);
+      same &= mine >> b & 1 ? bit : ~bit;
+    }
+    const bool is = mine >= 0 && !(same & lanemask_lt());
+    const uint64_t firsts = __ballot(is);
+    n = __popcll(firsts);
+    place = is ? __popcll(firsts & lanemask_lt()) : -1;
+  }
+  // The j-th (j < n) and its rows.
+  __device__ int at(int j, uint64_t& rows) const {
+    const int lane = __builtin_ctzll(__ballot(place == j));
+    rows = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(same >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((uint32_t)same, lane);
+    return __builtin_amdgcn_readlane(mine, lane);
+  }
+};
 
 // z's two halves [T][R]: the bf16 value nearest to z, and that of the rest.
 __device__ inline uint16_t* z_hi(const ProjectArgs& a) { return static_cast<uint16_t*>(a.ws); }
@@ -127,7 +155,7 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
   const int n_rt = (a.R + 15) / 16;
   const int entry = blockIdx.x % entries, part = blockIdx.x / entries % parts;
   const int t0 = blockIdx.x / entries / parts * 16;
-  const int mine = adapter_at(a, t0 + c16);
+  const int id = a.adapter_of[min(t0 + c16, a.T - 1)];
   const int chunks = a.K / 128, batches = (chunks + kPWaves * kHeld - 1) / (kPWaves * kHeld);
   const int slot = frag_slot(c16, kb);
   // wave w's chunks of a batch: w, w + 8 (chunks past the last repeat it and are not used)
@@ -144,27 +172,21 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
   const uint32_t xoff = (uint32_t)min(frag_row(lane), rows - 1) * (uint32_t)(a.ldx * 2) + 16 * frag_chunk(lane);
   int held = 0;
   copy(xres, xoff, 0, L.x[wave]);
-  uint64_t rem = __ballot(mine >= 0) & 0xFFFFull;
-  for (int j = 0; rem; ++j) {
-    const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
-    const uint64_t same = __ballot(mine == ad) & 0xFFFFull;
-    rem &= ~same;
-    if (j % entries != entry) continue;
+  const Distinct adapters(lane < rows && id >= 0 && id < a.n ? id : -1, a.n);
+  for (int j = entry; j < adapters.n; j += entries) {
+    uint64_t same;
+    const int ad = adapters.at(j, same);
     for (int rt = part; rt < n_rt; rt += parts) {
       const int ranks = min(16, a.R - 16 * rt);
       const rsrc_t ares = make_rsrc(a.A + ((int64_t)ad * a.R + 16 * rt) * a.K, (uint32_t)ranks * (uint32_t)a.K * 2);
       const uint32_t aoff = (uint32_t)min(frag_row(lane), ranks - 1) * (uint32_t)(a.K * 2) + 16 * frag_chunk(lane);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      int rank = 0;
-      float scale = 1.f;
+      const int rank_read = rank_load(a, ad);
+      const float scale = a.scales ? a.scales[ad] : 1.f;
       for (int b = 0; b < batches; ++b) {
         if (held != b) copy(xres, xoff, b, L.x[wave]);
         held = b;
         copy(ares, aoff, b, L.a[wave]);
-        if (b == 0) {
-          rank = rank_of(a, ad);
-          if (a.scales) scale = a.scales[ad];
-        }
         wait_loads<0>();
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
@@ -184,7 +206,7 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 #pragma unroll
           for (int w = 0; w < kPWaves; ++w) v += L.red[w][row][tid & 15];
           v *= scale;
-          if (r >= rank) v = 0.f;
+          if (r >= rank_value(a, rank_read)) v = 0.f;
           const uint16_t hi = f2bf(v);
           const int64_t at = (int64_t)(t0 + row) * a.R + r;
           z_hi(a)[at] = hi;
@@ -251,9 +273,7 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
   const ExpandConsts xk = expand_consts();
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 
-  int mine = -1;  // lane r: the adapter of row r
-  if (a.adapter_of && lane < 16 * MS) mine = adapter_at(a, t0 + lane);
-
+  const int id = a.adapter_of ? a.adapter_of[min(t0 + lane, a.T - 1)] : -1;
   const int rows = min(16 * MS, a.T - t0);
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)(((int64_t)(rows - 1) * a.ldx + a.K) * 2));
   uint32_t xoff[MS];
@@ -296,12 +316,11 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
     int ad;
     uint64_t same;  // its rows
   };
+  const int mine = lane < rows && id >= 0 && id < a.n ? id : -1;  // lane r: the adapter of row r
   const uint64_t with = __ballot(mine >= 0);  // rows with an adapter
-  auto entry = [&](uint64_t& rem) {
+  auto entry = [&](const Distinct& d, int j) {
     Entry e;
-    e.ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rem));
-    e.same = __ballot(mine == e.ad);
-    rem &= ~e.same;
+    e.ad = d.at(j, e.same);
     return e;
   };
   struct Operands {
@@ -334,23 +353,20 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
   };
   Entry first[NE];
   Operands ops[NE];
-  int rank_first[NE];
-  uint64_t left = 0;  // rows whose adapters come after the first NE of every wave
+  int rank_first[NE];  // (not yet limited)
+  int distinct = 0;
   if (with) {
-    uint64_t rem = with;
+    const Distinct d(mine, a.n);
+    distinct = d.n;
 #pragma unroll
     for (int k = 0; k < NE; ++k) {
       first[k].same = 0;
-      for (int j = 0; j < kPWaves && rem; ++j) {
-        const Entry e = entry(rem);
-        if (j == wave) first[k] = e;
-      }
-      if (first[k].same) {
-        rank_first[k] = rank_of(a, first[k].ad);
+      if (wave + kPWaves * k < distinct) {
+        first[k] = entry(d, wave + kPWaves * k);
+        rank_first[k] = rank_load(a, first[k].ad);
         load_operands(first[k], 0, ops[k]);
       }
     }
-    left = rem;
   }
   if constexpr (FUSED) {
     constexpr int kRows = 2, kChunks = 4;  // rows at a time; 512 inputs each
@@ -514,13 +530,15 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
     };
 #pragma unroll
     for (int k = 0; k < NE; ++k)
-      if (first[k].same) finish(first[k], rank_first[k], ops[k]);
-    for (int j = 0; left; ++j) {
-      const Entry e = entry(left);
-      if (j % kPWaves != wave) continue;
-      Operands o;
-      load_operands(e, 0, o);
-      finish(e, rank_of(a, e.ad), o);
+      if (first[k].same) finish(first[k], rank_value(a, rank_first[k]), ops[k]);
+    if (distinct > kPWaves * NE) {
+      const Distinct d(mine, a.n);
+      for (int j = wave + kPWaves * NE; j < distinct; j += kPWaves) {
+        const Entry e = entry(d, j);
+        Operands o;
+        load_operands(e, 0, o);
+        finish(e, rank_of(a, e.ad), o);
+      }
     }
   }
   __syncthreads();
