@@ -138,8 +138,8 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 // Grid: token tiles x parts x entries (entries fastest). What counts is
 // latency: the activations are under way before the adapters are known and
 // serve every entry while they are held, and an entry's part of A is under way
-// before its rank is known. K = 2048, rank 16: 2.9 us for one token, 5.6 for
-// 32 tokens of 32 adapters (2.1 MB of them), 7.7 for 4096 tokens.
+// before its rank is known. K = 2048, rank 16: 4.3 us for 32 tokens of 32
+// adapters (2.1 MB of them), 7.1 for 4096 tokens.
 struct DownLds {
   static constexpr int kHeld = 2;
   u32x4 x[kPWaves][kHeld][4][64], a[kPWaves][kHeld][4][64];  // [wave][chunk][32 inputs][frag_slot]
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 // ahead of the groups (NE adapters a wave, the first 32 ranks), and their
 // B_a z goes to a tile of its own, added last, so a token's result does not
 // depend on the others. 4096 x 2048: 6.2 us for one token with an adapter of
-// rank 16 (latency of one pass, FUSED), 8.0 for 32 tokens with 32 adapters;
+// rank 16 (latency of one pass, FUSED), 7.4 for 32 tokens with 32 adapters;
 // 2048 x 2048 for 500 tokens: 13.6 (the expansion of the codes, which every 64
 // rows repeat).
 template <int MS, int CT, int D>
