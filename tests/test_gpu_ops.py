@@ -561,6 +561,39 @@ def test_project_bad_values_reach_their_own_tokens_only(gemm):
         assert y[of == 2].isnan().any()
 
 
+@pytest.mark.parametrize("T", [1, 60, 300])
+def test_project_many_adapters(T):
+    # indices of more than eight bits, more distinct ones in a tile than a block's waves hold
+    N, K, n, R = 128, 256, 700, 8
+    m, ad, x = _Matrix(N, K), _adapters(N, K, n, R), _x(T, K)
+    of = torch.from_numpy(np.random.default_rng(T).permutation(n)[:T].astype(np.int32))
+    of[T // 2] = n - 1
+    for gemm in GEMMS:
+        _check_project(m, x, _project(m, x, ad, of, gemm), ad, of, wide=gemm != B.GEMM_EXACT)
+
+
+@pytest.mark.parametrize("T", [3, 130, 260])
+def test_widest_row_strides(T):
+    # rows 2^20 elements apart: offsets inside a tile reach 2^29 bytes
+    N, K, ld = 192, 256, 1 << 20
+    m, ad, x = _Matrix(N, K), _adapters(N, K, 3, 16), _x(T, K)
+    of = _runs(T, 3, T)
+    a = B.Adapters(*_dev(ad))
+    far = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    far[:, :K] = x.cuda()
+    out = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    for gemm in GEMMS:
+        B.moe_project(m.blob, N, K, far[:, :K], out[:, :N], T, a, of.cuda(), gemm, B.project_workspace(N, K, T, a))
+        torch.cuda.synchronize()
+        assert torch.equal(out[:, :N].cpu(), _project(m, x, ad, of, gemm))
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    B.moe_add_rmsnorm(B.norm(K), far[:, :K], w, T, y=out[:, :K])
+    near = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    B.moe_add_rmsnorm(B.norm(K), x.cuda(), w, T, y=near)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, :K], near)
+
+
 def test_project_results_do_not_depend_on_the_batch():
     # a token's result is the same bits alone in the call's tile and among others of the same call size
     m, n = _Matrix(256, 512), 5
