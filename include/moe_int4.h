@@ -360,8 +360,9 @@ int64_t moe_gate_max_blocks(const moe_gate* gate, int32_t T);
 int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes);
 
 /* moe_route with a gate: from fp32 logits [T][E] (device) every field of
- * `out` (k = gate->top_k, E = gate->E, block_m = gate->block_m). Results do
- * not depend on the workspace's contents. T = 0 is a no-op. */
+ * `out` (k = gate->top_k, E = gate->E, block_m = gate->block_m). T * top_k <
+ * 2^30 and T <= 2^28 - 64 (MOE_EUNSUPPORTED otherwise). Results do not depend
+ * on the workspace's contents. T = 0 is a no-op. */
 int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const moe_route_out* out,
                     void* ws, size_t ws_bytes, void* stream);
 

@@ -167,6 +167,9 @@ bool gate_ok(const moe_gate* g) {
          g->topk_groups * (g->E / g->n_groups) >= g->top_k;
 }
 
+// (the selection takes sixteen threads a token, and HIP fewer than 2^32 a launch)
+constexpr int32_t kMaxGateT = (1 << 28) - 64;
+
 // MOE_OK, or why the gate is refused.
 int check_gate(const moe_gate* g) {
   if (!g || (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) ||
@@ -683,7 +686,7 @@ int moe_gate_workspace_bytes(const moe_gate* gate, int32_t T, size_t* bytes) {
   const int rc = check_gate(gate);
   if (rc != MOE_OK) return rc;
   const moe_dims d = gate_dims(gate);
-  if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
+  if (T > kMaxGateT || too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
   *bytes = gate_ws_bytes(T);
   return MOE_OK;
 }
@@ -694,7 +697,7 @@ int moe_route_gated(const moe_gate* gate, const float* logits, int32_t T, const 
   const int rc = check_gate(gate);
   if (rc != MOE_OK) return rc;
   const moe_dims d = gate_dims(gate);
-  if (too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
+  if (T > kMaxGateT || too_many_pairs(&d, T)) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!logits || !route_out_ok(out) || !ws || !al4(logits) || !al16(ws)) return MOE_EINVAL;
   if (ws_bytes < gate_ws_bytes(T)) return MOE_EWORKSPACE;

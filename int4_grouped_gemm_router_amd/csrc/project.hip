@@ -21,6 +21,7 @@
 //   project_tile_kernel   256 x 256 tiles; each weight is expanded once per
 //                         tile to bf16 and shared through LDS by its 256
 //                         rows: many rows, where the matrix cores count
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels.h"
@@ -803,11 +804,16 @@ size_t project_ws_bytes(int /*N*/, int /*K*/, int R, int T) {
 
 namespace {
 
+// Tokens of one launch: HIP takes fewer than 2^32 threads, and the tilings
+// that this many tokens choose have at most 2^31 (64 x 64 with 65536 columns;
+// the adapters' first product: 2^23). Longer calls are several launches, over
+// the same workspace one after the other.
+constexpr int kLaunchTokens = 1 << 18;
+
 template <int MS, int CT, int D, int NE, bool FUSED = false>
 hipError_t launch_split(const ProjectArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * (a.N / 64) * (4 / CT);
   const int64_t blocks = (units + 7) / 8 * 8;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((project_split_kernel<MS, CT, D, NE, FUSED>), dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -816,7 +822,6 @@ template <int RS>
 hipError_t launch_tile(const ProjectArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 32 * RS - 1) / (32 * RS)) * ((a.N + 255) / 256);
   const int64_t blocks = (units + 7) / 8 * 8;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(project_tile_kernel<RS>, dim3((unsigned)blocks), dim3(kPThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -860,18 +865,28 @@ hipError_t launch_project(const ProjectArgs& a, hipStream_t s) {
     }
   }
   if (a.adapter_of && (int64_t)a.T * a.R <= kFusedRows && best->fused) return best->fused(a, s);
-  if (a.adapter_of) {
-    // blocks for each rank tile and for several adapters of a token tile while
-    // there are compute units for them
-    const int64_t tiles = (a.T + 15) / 16;
-    int parts = (a.R + 15) / 16, entries = min(min(16, a.n), a.T);
-    while (parts > 1 && tiles * parts > 256) parts = (parts + 1) / 2;
-    while (entries > 1 && tiles * parts * entries > 256) entries = (entries + 1) / 2;
-    if (tiles * parts * entries > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * parts * entries)), dim3(kPThreads), 0, s, a, entries,
-                       parts);
+  for (int64_t t0 = 0; t0 < a.T; t0 += kLaunchTokens) {
+    ProjectArgs c = a;
+    c.T = (int)std::min<int64_t>(kLaunchTokens, a.T - t0);
+    c.x += t0 * a.ldx;
+    c.y += t0 * a.ldy;
+    if (a.adapter_of) {
+      c.adapter_of += t0;
+      // blocks for each rank tile and for several adapters of a token tile while
+      // there are compute units for them
+      const int tiles = (c.T + 15) / 16;
+      int parts = (a.R + 15) / 16, entries = std::min(std::min(16, a.n), c.T);
+      while (parts > 1 && tiles * parts > 256) parts = (parts + 1) / 2;
+      while (entries > 1 && tiles * parts * entries > 256) entries = (entries + 1) / 2;
+      hipLaunchKernelGGL(adapter_down_kernel, dim3((unsigned)(tiles * parts * entries)), dim3(kPThreads), 0, s, c, entries,
+                         parts);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    const hipError_t e = best->launch(c, s);
+    if (e != hipSuccess) return e;
   }
-  return best->launch(a, s);
+  return hipSuccess;
 }
 
 }  // namespace moe

@@ -594,6 +594,26 @@ def test_widest_row_strides(T):
     assert torch.equal(out[:, :K], near)
 
 
+@pytest.mark.parametrize("T", [(1 << 18) + 300, 1 << 27])
+def test_project_more_tokens_than_a_launch_takes(T):
+    # a launch has fewer than 2^32 threads; the adapters' first product takes 32 a token
+    N, K, R = 64, 128, 8
+    m, ad = _Matrix(N, K), _adapters(N, K, 3, R, full_rank=True)
+    a = B.Adapters(*_dev(ad))
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_()
+    of = (torch.arange(T, dtype=torch.int32, device="cuda") % 5 - 1).clamp_(max=2)
+    y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = B.project_workspace(N, K, T, a)
+    ws.fill_(0xFF)
+    B.moe_project(m.blob, N, K, x, y, T, a, of, B.GEMM_AUTO, ws)
+    for t0 in (0, (1 << 18) - 40, T // 2 - 40, T - 80):
+        at = slice(t0, t0 + 80)
+        _check_project(m, x[at].cpu(), y[at].cpu(), ad, of[at].cpu(), wide=True)
+    assert (y[T] == 7.0).all()
+    del x, of, y, ws
+    torch.cuda.empty_cache()
+
+
 def test_project_results_do_not_depend_on_the_batch():
     # a token's result is the same bits alone in the call's tile and among others of the same call size
     m, n = _Matrix(256, 512), 5

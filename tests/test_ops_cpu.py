@@ -103,6 +103,18 @@ def test_gate_refusals():
     assert L.moe_route_gated(by(g), FAKE, 1 << 27, by(ro), FAKE, 1 << 40, None) == B.MOE_EUNSUPPORTED
 
 
+def test_gate_refuses_more_tokens_than_a_launch_takes():
+    # sixteen threads a token, fewer than 2^32 a launch
+    L, n, most = B.lib(), ctypes.c_size_t(0), (1 << 28) - 64
+    ro = B.MoeRouteOut(*([FAKE] * 8))
+    for k in (1, 2, 3):
+        g = _gate(E=4, top_k=k)
+        assert L.moe_gate_workspace_bytes(by(g), most, by(n)) == B.MOE_OK
+        assert L.moe_gate_workspace_bytes(by(g), most + 1, by(n)) == B.MOE_EUNSUPPORTED
+        assert L.moe_route_gated(by(g), FAKE, most + 1, by(ro), FAKE, 1 << 40, None) == B.MOE_EUNSUPPORTED
+        assert L.moe_route_gated(by(g), FAKE, most, by(ro), FAKE, 0, None) == B.MOE_EWORKSPACE
+
+
 def test_gate_workspace_serves_fewer_tokens():
     n, most = ctypes.c_size_t(0), 0
     for T in sorted([*range(0, 20000, 7), 64, 4096, 4097, 8192, 8193, 16384, 16385, 32769, 1 << 20]):
