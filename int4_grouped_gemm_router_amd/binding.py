@@ -462,7 +462,7 @@ def _types_of(code):
     if _types is None:
         import torch
         _types = ((torch.bfloat16,), (torch.float16,), (torch.float32,), (), (torch.int8, torch.uint8),
-                  (torch.float8_e4m3fn, torch.uint8), (torch.bfloat16, torch.int16))
+                  (torch.float8_e4m3fn, torch.uint8), (torch.bfloat16, torch.int16, torch.uint16))
     if not 0 <= code < len(_types) or not _types[code]:
         raise ValueError(f"element type {code} is not known")
     return _types[code]
@@ -496,6 +496,13 @@ def _flat(t, n, dtype, name, dev=None):
     if dev is not None and t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
     return t.data_ptr()
+
+
+def _bits(t, n, dtypes, name, dev):
+    """Address of at least n contiguous values of one of `dtypes`, on GPU `dev`."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {n} contiguous values of {dtypes[0]} are needed, got {list(t.shape)} of {t.dtype}")
+    return _flat(t, n, t.dtype, name, dev)
 
 
 def _gpu(t):
@@ -591,26 +598,43 @@ def moe_route_gated(g: MoeGate, logits, T: int, out: RouteBuffers, ws, stream=No
     _call("moe_route_gated", dev, stream, ctypes.byref(g), lp, T, ctypes.byref(out.struct), wp, ws.numel())
 
 
+def _layer_args(d, g, w, x, y, T, last, logits_out, route_out, ws):
+    """The gated layer's pointer arguments after their checks; last: tokens that route_out describes."""
+    dev, bits = x.get_device(), _types_of(_BF16_BITS)
+    xp, yp = _bits(x, T * d.H, bits, "x", dev), _bits(y, T * d.H, bits, "y", dev)
+    lp = None if logits_out is None else _flat(logits_out, T * d.E, _types_of(F32)[0], "logits_out", dev)
+    ro = wp = None
+    wn = 0
+    if route_out is not None:
+        if (route_out.topk_idx.numel() < last * d.top_k or route_out.hist.numel() < d.E or
+                route_out.block_map.shape[0] < (last * d.top_k + d.block_m - 1) // d.block_m + d.E):
+            raise ValueError(f"route_out: buffers of {last} tokens of this layer are needed")
+        if route_out.topk_idx.get_device() != dev:
+            raise ValueError("route_out: on another device than x")
+        ro = ctypes.byref(route_out.struct)
+    if ws is not None:
+        wn, wp = ws.numel(), _flat(ws, 0, _types_of(BITS8 + OUT8_INT8)[1], "ws", dev)
+    for name, t in w.t.items():
+        if t.get_device() != dev:
+            raise ValueError(f"weights: {name} on {t.device}, other tensors on device {dev}: one GPU is needed")
+    _bias_on(g, dev)
+    return ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), xp, yp, lp, ro, wp, wn
+
+
 def moe_prefill_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, chunk_T: int = 0,
                             logits_out=None, route_out: RouteBuffers | None = None, ws=None, stream=None):
     """moe_prefill_layer routed by a gate."""
-    _bias_on(g, _gpu(x))
-    ro = ctypes.byref(route_out.struct) if route_out is not None else None
-    _check(lib().moe_prefill_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
-                                         _ptr(y), T, chunk_T, _ptr(logits_out), ro, _ptr(ws),
-                                         0 if ws is None else ws.numel(), _stream(stream)),
-           "moe_prefill_layer_gated")
+    chunk = chunk_T if 0 < chunk_T < T else T
+    last = T - (T - 1) // chunk * chunk if T > 0 else 0
+    dp, gp, sp, xp, yp, lp, ro, wp, wn = _layer_args(d, g, w, x, y, T, last, logits_out, route_out, ws)
+    _call("moe_prefill_layer_gated", _gpu(x), stream, dp, gp, sp, xp, yp, T, chunk_T, lp, ro, wp, wn)
 
 
 def moe_decode_layer_gated(d: MoeDims, g: MoeGate, w: DeviceWeights, x, y, T: int, logits_out=None,
                            route_out: RouteBuffers | None = None, ws=None, stream=None):
     """moe_decode_layer routed by a gate."""
-    _bias_on(g, _gpu(x))
-    ro = ctypes.byref(route_out.struct) if route_out is not None else None
-    _check(lib().moe_decode_layer_gated(ctypes.byref(d), ctypes.byref(g), ctypes.byref(w.struct), _ptr(x),
-                                        _ptr(y), T, _ptr(logits_out), ro, _ptr(ws),
-                                        0 if ws is None else ws.numel(), _stream(stream)),
-           "moe_decode_layer_gated")
+    dp, gp, sp, xp, yp, lp, ro, wp, wn = _layer_args(d, g, w, x, y, T, T, logits_out, route_out, ws)
+    _call("moe_decode_layer_gated", _gpu(x), stream, dp, gp, sp, xp, yp, T, lp, ro, wp, wn)
 
 
 class Adapters:

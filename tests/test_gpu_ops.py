@@ -390,6 +390,21 @@ def test_gate_binding_checks_tensors():
         B.moe_route_gated(ok, logits.cpu(), T, out, ws)
 
 
+def test_gated_layer_binding_wants_one_device():
+    _, w, _ = synth.generate("tiny_t32", with_x=False)
+    dw, T = B.DeviceWeights.from_logical(w), 2
+    d, g, x = dw.dims, B.gate(w.E, 8), torch.zeros((T, w.H), dtype=torch.int16, device="cuda")
+    for f, mode in ((B.moe_prefill_layer_gated, B.MODE_PREFILL), (B.moe_decode_layer_gated, B.MODE_DECODE)):
+        ws = B.workspace(d, T, mode)
+        for bad in (dict(y=x.cpu()), dict(ws=ws.cpu()), dict(logits_out=torch.zeros((T, w.E))),
+                    dict(route_out=B.RouteBuffers(d, T, device="cpu"))):
+            a = {**dict(y=torch.empty_like(x), ws=ws), **bad}
+            with pytest.raises(ValueError, match=next(iter(bad))):
+                f(d, g, dw, x, a.pop("y"), T, **a)
+        with pytest.raises(ValueError, match="weights"):
+            f(d, g, B.DeviceWeights.from_logical(w, device="cpu"), x, torch.empty_like(x), T, ws=ws)
+
+
 def test_gated_layer_with_the_softmax_rule_is_the_layer():
     _, w, _ = synth.generate("tiny_t32", with_x=False)
     dw = B.DeviceWeights.from_logical(w)

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from int4_grouped_gemm_router_amd import binding as B
+from int4_grouped_gemm_router_amd import synth
 
 FAKE = 0x10000  # never dereferenced: every call below returns before any launch
 by = ctypes.byref
@@ -148,6 +149,42 @@ def test_gated_layer_refusals():
     assert prefill(d, _gate(), n=ws - 1) == B.MOE_EWORKSPACE
     assert decode(d, _gate()) == B.MOE_EWORKSPACE
     assert decode(d, _gate(), T=5) == B.MOE_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("f,mode", [(B.moe_prefill_layer_gated, B.MODE_PREFILL), (B.moe_decode_layer_gated, B.MODE_DECODE)])
+def test_gated_layer_binding_checks_tensors(f, mode):
+    _, w, _ = synth.generate("tiny_t32", with_x=False)
+    dw, T = B.DeviceWeights.from_logical(w, device="cpu"), 3
+    d, g = dw.dims, B.gate(w.E, 8)
+    x = torch.zeros((T, w.H), dtype=torch.bfloat16)
+    ok = dict(x=x, y=torch.empty_like(x), logits_out=torch.empty((T, w.E)), route_out=B.RouteBuffers(d, T, device="cpu"),
+              ws=B.workspace(d, T, mode, device="cpu"))
+
+    def call(**kw):
+        a = {**ok, **kw}
+        f(d, g, dw, a.pop("x"), a.pop("y"), T, **a)
+
+    for kw in (dict(x=x.float()), dict(x=x.half()), dict(x=x[:2]), dict(x=torch.zeros((T, 2 * w.H), dtype=x.dtype)[:, ::2]),
+               dict(y=x[:2].clone()), dict(y=x.float()), dict(y=torch.zeros((w.H, T), dtype=x.dtype).t()),
+               dict(logits_out=torch.empty((T - 1, w.E))), dict(logits_out=torch.empty((T, w.E), dtype=torch.float64)),
+               dict(route_out=B.RouteBuffers(d, T - 1, device="cpu")), dict(ws=ok["ws"].view(torch.int32)),
+               dict(ws=ok["ws"][::2])):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            call(**kw)
+    for dtype in (torch.bfloat16, torch.int16, torch.uint16):      # the checks pass; there is no CPU path
+        with pytest.raises(ValueError, match="on a GPU"):
+            call(x=x.view(dtype), y=x.clone().view(dtype))
+
+
+def test_gated_prefill_binding_wants_the_last_chunks_buffers():
+    _, w, _ = synth.generate("tiny_t32", with_x=False)
+    dw, T, chunk = B.DeviceWeights.from_logical(w, device="cpu"), 50, 16
+    x, g = torch.zeros((T, w.H), dtype=torch.bfloat16), B.gate(w.E, 8)
+    for tokens, match in ((2, "on a GPU"), (1, "route_out")):      # 50 = 3 * 16 + 2
+        with pytest.raises(ValueError, match=match):
+            B.moe_prefill_layer_gated(dw.dims, g, dw, x, torch.empty_like(x), T, chunk,
+                                      route_out=B.RouteBuffers(dw.dims, tokens, device="cpu"),
+                                      ws=B.workspace(dw.dims, chunk, B.MODE_PREFILL, device="cpu"))
 
 
 def _project(blob=FAKE, N=128, K=256, x=FAKE, ldx=256, y=FAKE, ldy=128, T=4, ad=None, of=None, gemm=0, ws=FAKE, n=1 << 30):
