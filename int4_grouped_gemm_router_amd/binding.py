@@ -485,8 +485,8 @@ def _rows(t, T, width, dtypes, dev, name):
         raise ValueError(f"{name}: the values of a row have to be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
-    # the stride of a single row says nothing
-    return t.data_ptr(), (stride[0] if T > 1 else max(stride[0], width))
+    # the stride of a single row says nothing (it may be any)
+    return t.data_ptr(), (stride[0] if T > 1 else width)
 
 
 def _flat(t, n, dtype, name, dev=None):

@@ -173,6 +173,27 @@ def test_norm_in_place(H):
     assert torch.equal(xd, h0)
 
 
+def test_one_row_of_any_stride():
+    # the last token of a prompt [1, S, H]: its row stride, S H, is more than 2^20; and a stride that is no multiple of 8
+    H, N, S = 2048, 64, 600
+    prompt = torch.randn((1, S, H), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    w, m = torch.ones(H, dtype=torch.bfloat16, device="cuda"), _Matrix(N, H)
+    far, near = prompt[:, -1], prompt[:, -1].clone()
+    assert far.stride(0) > 1 << 20
+    odd = torch.zeros(H + 1, dtype=torch.bfloat16, device="cuda").as_strided((1, H), (H + 1, 1))
+    odd.copy_(near)
+    want, wide = torch.empty_like(near), torch.empty((1, N), dtype=torch.bfloat16, device="cuda")
+    B.moe_add_rmsnorm(B.norm(H), near, w, 1, y=want)
+    B.moe_project(m.blob, N, H, near, wide, 1, ws=B.project_workspace(N, H, 1))
+    for x in (far, odd):
+        got, p = torch.empty_like(near), torch.empty_like(wide)
+        B.moe_project(m.blob, N, H, x, p, 1, ws=B.project_workspace(N, H, 1))
+        B.moe_add_rmsnorm(B.norm(H), x, w, 1, y=got)
+        B.moe_add_rmsnorm(B.norm(H), x, w, 1, y=x.as_strided((1, H), (H, 1), x.storage_offset()))   # in place
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(x, want) and torch.equal(p, wide)
+
+
 # ------------------------------------------------------------------ gated routing
 
 SCORES = {"softmax": B.SCORE_SOFTMAX, "sigmoid": B.SCORE_SIGMOID}
