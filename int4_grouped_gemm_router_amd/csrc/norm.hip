@@ -77,9 +77,11 @@ __device__ inline uint32_t max_bits(uint32_t a, uint32_t b) { return max(a, b); 
 
 // A group's scale and what its quotients are formed with. The values t of a
 // row are v up to the factor f (1 <= f < 2), which cancels in v / s = t Q / m
-// with m the largest |t| of the group: that quotient, corrected once, is
-// rounded correctly, where v / s from a rounded v and s is off by a few units
-// (and more 8-bit values land on the wrong side of a tie).
+// with m the largest |t| of the group: that quotient of t and m, corrected
+// once, is rounded correctly, where v / s from a rounded v and s is off by a
+// few units (and more 8-bit values land on the wrong side of a tie). t itself
+// is exact for 16-bit rows and weights without an offset, else rounded once
+// or twice.
 struct Group {
   float s, m, inv, f;
   bool plain;  // m is far from under- and overflow
@@ -105,8 +107,10 @@ template <int OUT8>
 __device__ inline float quotient(float t, const Group& g) {
   constexpr float Q = kTop<OUT8>;
   if (g.plain) {
-    const float n = t * Q, q = n * g.inv;  // (n is exact for 16-bit rows and weights)
-    return __builtin_fmaf(__builtin_fmaf(-q, g.m, n), g.inv, q);
+    // t Q = n + e exactly (products of fp16 have 22 bits, and Q up to seven
+    // more), so that the remainder t Q - q m is rounded only once
+    const float n = t * Q, e = __builtin_fmaf(t, Q, -n), q = n * g.inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, g.m, n) + e, g.inv, q);
   }
   float q = g.s == 0.f ? 0.f : t * g.f / g.s;
   if (OUT8 == kOut8Int8 && !(g.s < INFINITY)) q = 0.f;
@@ -227,7 +231,8 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(NormArgs a) {
     if (a.y) store(static_cast<E*>(a.y) + row * a.ld_y, [&](int j, int i) { return v[j][i] * r * w[j][i]; });
     if constexpr (OUT8 != kOut8None) {
       // v with the power of two in r only (both products are exact for 16-bit
-      // rows and weights): the rest of r is the group scale's factor
+      // rows and weights without an offset): the rest of r is the group scale's
+      // factor
       const float p = __uint_as_float(__float_as_uint(r) & 0x7F800000u), f = p > 0.f ? r / p : r;
 #pragma unroll
       for (int j = 0; j < NV; ++j)

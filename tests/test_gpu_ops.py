@@ -133,6 +133,18 @@ def test_norm_zero_and_tiny_rows(out8, group):
     _norm_case(4, 256, dtype="f32", residual=False, out8=out8, group=group, x=x)
 
 
+def test_norm_int8_ties_of_wide_products():
+    # fp16 rows times fp16 weights have up to 22 bits and Q seven more: in a group of weight w with the largest value
+    # 254 w, (2 k + 1) w is exactly k + 1/2 steps and goes to the even one, whatever w is (the row's factor cancels)
+    H, group = 16384, 128
+    x = torch.cat([torch.arange(1, 254, 2), torch.tensor([254])]).repeat(H // group)[None].to(torch.float16)
+    w = ((1025 + 8 * torch.arange(H // group)) / 1024).repeat_interleave(group).to(torch.float16)
+    q = torch.zeros((1, H), dtype=torch.int8, device="cuda")
+    s = torch.zeros((1, H // group), device="cuda")
+    B.moe_add_rmsnorm(B.norm(H, dtype=torch.float16, out8=B.OUT8_INT8, group=group), x.cuda(), w.cuda(), 1, q=q, scales=s)
+    assert torch.equal(q.cpu().double(), torch.round(x.double() / 2))      # (torch rounds ties to even)
+
+
 def test_norm_nan_and_infinity_stay_in_their_row():
     T, H = 4, 512
     x = torch.randn(T, H, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
