@@ -19,6 +19,8 @@
 //   gate_scatter  per piece of tokens: totals and bases per expert from those
 //                 counts, a stable scatter, and a share of the block map
 //   gate_small    both in one block, for up to kGateSmallT tokens
+#include <cfloat>
+
 #include "kernels.h"
 #include "topk.h"
 
@@ -352,21 +354,42 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
   }
 #pragma unroll
   for (int i = 0; i < NS; ++i) s[i] = l[i] == -INFINITY ? -INFINITY : s[i];
-  float bmax = 0.f;  // the largest |bias| (a NaN is the largest of all, and leaves every token in doubt)
+  // What the fixed-point keys below span, [lowest, lowest + width], and the
+  // largest magnitude in it. Biases up to 1: all that keys can be. Else (a
+  // bias that masks an expert is -inf or NaN, or far below the others) the
+  // token's own keys, down to eight scores' range below its best one: what lies
+  // lower is selected only where little else is left, and then in 64 bits.
+  float lowest = 0.f, width = top, range = top;
   if (a.balance) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const float b = bv[i >> 2][i & 3];
-      m = max(m, __float_as_uint(b) & 0x7FFFFFFFu);
+      m = max(m, __float_as_uint(b) & 0x7FFFFFFFu);  // (NaN is the largest of all)
       s[i] += b;
       if (!(s[i] == s[i])) s[i] = -INFINITY;
     }
-    bmax = __uint_as_float(row_max_u32(m));
+    const float bmax = __uint_as_float(row_max_u32(m));
+    if (bmax <= 1.0f) {  // (the same in every lane)
+      lowest = -bmax;
+      range = top + bmax;
+      width = range + bmax;
+    } else {
+      float hi = s[0];
+#pragma unroll
+      for (int i = 1; i < NS; ++i) hi = fmaxf(hi, s[i]);
+      hi = row_max(hi);
+      lowest = hi;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) lowest = s[i] > hi - 8.0f ? fminf(lowest, s[i]) : lowest;
+      lowest = row_min(lowest);
+      range = fmaxf(top, fmaxf(fabsf(hi), fabsf(lowest)));
+      width = hi - lowest + 0x1p-21f * range;  // (not 0 where all keys are equal)
+    }
   }
-  const float range = top + bmax;
   const float err = (a.sigmoid ? 0x1p-21f : 0x1p-20f) * range;
   // a decision the fp32 keys cannot settle, and whether it is one of groups
+  // (all are where the best key is infinite or there is none)
   bool near = !(range < 1e30f), near_groups = near;
   uint64_t groups = 0;  // the token's kept groups
   if (a.n_groups > 1) {
@@ -413,7 +436,8 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
       if (lg >= 1) m.add_lane<0xB1>();
       if (lg >= 2) m.add_lane<0x4E>();
       if (lg >= 3) m.add_lane<0x141>();
-      if (p == 0) L.group[q][g] = a.group_top2 && m.m2 > -INFINITY ? m.m1 + m.m2 : m.m1;
+      // (a sum of keys is above what groups of masked experts have)
+      if (p == 0) L.group[q][g] = a.group_top2 && m.m2 > -INFINITY ? fmaxf(m.m1 + m.m2, -FLT_MAX) : m.m1;
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     for (int g0 = 0; g0 < a.n_groups; g0 += 16) {
@@ -437,7 +461,9 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     }
     lo = row_min(lo);
     hi = row_max(hi);
-    near_groups |= hi > -INFINITY && !(lo - hi > 4.0f * err);
+    // (groups whose keys are below `lowest` err by 2 u of what they are larger)
+    const float larger = fmaxf(fabsf(lo) + fabsf(hi) - 4.0f * range, 0.f);
+    near_groups |= hi > -INFINITY && !(lo - hi > 4.0f * err + 0x1p-22f * larger);
     near |= near_groups;
     if (quads) {
 #pragma unroll
@@ -454,14 +480,14 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
       }
     }
   }
-  // keys as 24-bit fixed point over the range (0: masked or out of the
-  // running, at least 1 otherwise), then the lane's slot and the lane: all
-  // keys of a token differ
-  const float scale = 16777000.0f / (range + bmax);
+  // keys as 24-bit fixed point (0: masked, out of the running or below
+  // `lowest`, at least 1 otherwise), then the lane's slot and the lane: all keys
+  // of a token differ
+  const float scale = 16777000.0f / width;
   uint32_t key[NS];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const uint32_t v = (uint32_t)fmaxf(__builtin_fmaf(s[i] + bmax, scale, 2.0f), 0.f);
+    const uint32_t v = (uint32_t)fmaxf(__builtin_fmaf(s[i] - lowest, scale, 2.0f), 0.f);
     key[i] = v << 8 | (uint32_t)(i << 4) | (uint32_t)c;
   }
   // the lane's keys in descending order
@@ -490,11 +516,11 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     if constexpr (ND == NS) key[NS - 1] = own ? 0u : key[NS - 1];
   }
   const uint32_t next = c == 15 ? m : dpp<0x101>(mine);  // of rank c + 1 (the lane above)
-  // twice the bound in steps of the fixed point (16 u of the range is at most
-  // 16 of the 2^24 steps over range + bias), and what the steps cut off
-  const uint32_t close = (a.sigmoid ? 16 : 32) + 4;
+  // twice the bound in steps of the fixed point (all of them where it is more),
+  // and what the steps cut off
+  const uint32_t close = (uint32_t)fminf(2.0f * err * scale, 0x1p24f) + 5;
   const uint32_t vm = mine >> 8, vn = next >> 8;
-  if (c < k) near |= vm == 0 || (vn > 0 && vm - vn <= close);
+  if (c < k) near |= vm == 0 || vm - vn <= close;
   sel = 64 * (int)(mine >> 6 & 3) + 4 * (int)(mine & 15) + (int)(mine >> 4 & 3);
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
@@ -519,8 +545,9 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     // the lowest selected fp32 key, less what it and a fixed-point step may err
     const uint32_t last = __builtin_amdgcn_readlane(vm, 16 * row + k - 1);
     const double step = 1.0 / (double)__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), 16 * row));
-    const double least =
-        last > close + 4 ? ((double)last - 4.0 - (double)close) * step - (double)bmax : -(double)INFINITY;
+    const uint32_t off = __builtin_amdgcn_readlane(close, 16 * row) + 4;
+    const double from = (double)__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lowest), 16 * row));
+    const double least = last > off ? (double)(last - off) * step + from : -(double)INFINITY;
     int se = gate_select_exact(a, l4, b4, top4, !(doubt_groups >> (16 * row) & 0xFFFF), kept, least, L.list);
     se = __shfl(se, c);
     if (q == row) sel = se;

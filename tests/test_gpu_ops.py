@@ -340,6 +340,80 @@ def test_gate_many_equal_keys(equal):
             _check_gate(l, _run_gate(l, top_k=8, **kw), top_k=8, **kw)
 
 
+def _mask_bias(rng, E, kind, share):
+    """Balance biases in which a share of the experts is masked in one of several ways."""
+    bias = rng.uniform(-0.05, 0.05, E).astype(np.float32)
+    far = {"inf": [-np.inf], "nan": [np.nan], "1e4": [-1e4], "1e9": [-1e9], "max": [-3e38], "2": [-2.0, -1.0],
+           "mixed": [-np.inf, np.nan, -9.0, -1e3, -1e9, -3e38], "above": [1e9, 50.0], "plus": [np.inf]}[kind]
+    at = rng.permutation(E)[: max(1, int(E * share))]
+    bias[at] = rng.choice(np.array(far, np.float32), size=len(at))
+    return bias
+
+
+@pytest.mark.parametrize("share", [0.0, 0.3, 0.8, 0.985])
+@pytest.mark.parametrize("kind", ["inf", "nan", "1e4", "1e9", "max", "2", "mixed", "above", "plus"])
+def test_gate_biases_that_mask_experts(kind, share):
+    # one expert, a part of them, so many that some groups have none left, and all but a few
+    for T, E in ((3, 256), (70, 256), (40, 128), (40, 64)):
+        rng = np.random.default_rng(T + E + int(100 * share))
+        bias = _mask_bias(rng, E, kind, share)
+        for score in ("softmax", "sigmoid"):
+            l = _logits(rng, T, E, "plain")
+            for kw in (dict(), dict(n_groups=8, topk_groups=4, group_score="top2"),
+                       dict(n_groups=16, topk_groups=5, group_score="max", renorm=False), dict(n_groups=32, topk_groups=9)):
+                kw = dict(top_k=8, score=score, bias=bias, **kw)
+                if kw.get("topk_groups", 1) * (E // kw.get("n_groups", 1)) >= 8:
+                    _check_gate(l, _run_gate(l, **kw), **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_large_biases_of_one_size(score):
+    # keys whose bias hides most of the score's bits, or all of them
+    for offset in (5.0, 300.0, 1e6, -1e6, -1e20, 1e29, -1e31):
+        rng = np.random.default_rng(int(abs(offset)) % 1000)
+        l = _logits(rng, 50, 256, "plain")
+        bias = (rng.uniform(-0.05, 0.05, 256) + offset).astype(np.float32)
+        for kw in (dict(), dict(n_groups=8, topk_groups=4, group_score="top2")):
+            kw = dict(top_k=8, score=score, bias=bias, **kw)
+            _check_gate(l, _run_gate(l, **kw), **kw)
+
+
+def _graph_us(f, n=20):
+    for _ in range(3):
+        f()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(n):
+            f()
+    best = float("inf")
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / n * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("masked", [-np.inf, np.nan, -1e4, -1e9])
+def test_gate_masking_an_expert_costs_no_decisions_in_64_bits(masked):
+    # decided in 64 bits, every token of a call, the routing took three times as long
+    T, E = 16384, 256
+    rng = np.random.default_rng(8)
+    logits = torch.from_numpy(_logits(rng, T, E, "plain")).cuda()
+    us = []
+    for value in (None, masked):
+        bias = rng.uniform(-0.05, 0.05, E).astype(np.float32)
+        if value is not None:
+            bias[E // 3] = value
+        g = B.gate(E, 8, score=B.SCORE_SIGMOID, n_groups=8, topk_groups=4, group_score=B.GROUP_TOP2,
+                   balance_bias=torch.from_numpy(bias).cuda())
+        out, ws = B.RouteBuffers(g, T), B.gate_workspace(g, T)
+        us.append(_graph_us(lambda: B.moe_route_gated(g, logits, T, out, ws)))
+    assert us[1] < 1.6 * us[0], us
+
+
 def test_gate_softmax_agrees_with_moe_route():
     rng = np.random.default_rng(12)
     T, E = 1000, 256
