@@ -6,7 +6,7 @@
 // Two launches: the adapters' first product z into the workspace (fp32 sums,
 // kept as two bf16 halves: 16 significant bits), then the projection, in
 // whose epilogue B_a z is a few more matrix-core operations per tile. One
-// launch for one to four tokens of low rank.
+// launch for one or two tokens of low rank.
 //
 // Tokens are never sorted by adapter: a 16-token tile walks over the distinct
 // adapters of its tokens (one in a prompt, up to 16 in a batch of single
@@ -35,10 +35,10 @@ namespace {
 constexpr int kPWaves = 8;
 constexpr int kPThreads = 64 * kPWaves;
 // T R up to which the projection's blocks form z themselves, each reading all
-// of the adapters' rows, and the launch before them is spared: 4096 x 2048,
-// one token, rank 8 or 16 6.2 us against 7.4, rank 32 7.8 against 7.4 but one
-// launch fewer for the host (3.4 us); rank 64 11.6 against 7.8.
-constexpr int kFusedRows = 32;
+// of the adapters' rows, and the launch before them is spared: two rows a wave,
+// one pass. N 512 to 12288 and K 512 to 16384, in a graph: 0.82 to 0.98 of the
+// two launches' time (4096 x 16384: 1.04); 32 rows, two passes, 1.04 to 1.5.
+constexpr int kFusedRows = 2 * kPWaves;
 
 // The adapter of token t, or -1.
 __device__ inline int adapter_at(const ProjectArgs& a, int t) {
@@ -245,8 +245,8 @@ struct SplitLds {
   };
 };
 
-// FUSED (T R <= kFusedRows): every block forms z itself, a wave a rank's row of
-// A at a time, while its first codes are on their way.
+// FUSED (T R <= kFusedRows): every block forms z itself, a wave one or two of
+// the adapters' rows.
 template <int MS, int CT, int D, int NE, bool FUSED>
 __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs a) {
   typedef SplitLds<MS, CT, D> Lds;
@@ -371,50 +371,49 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
   }
   if constexpr (FUSED) {
     constexpr int kRows = 2, kChunks = 4;  // rows at a time; 512 inputs each
-    const int n = a.T * a.R;
-    for (int i0 = wave; i0 < n; i0 += kRows * kPWaves) {
-      float sum[kRows] = {0.f, 0.f};
-      int ad[kRows], r[kRows];
-      const uint16_t *ap[kRows], *xp[kRows];
+    static_assert(kRows * kPWaves == kFusedRows, "one pass");
+    const int n = a.T * a.R;  // (at least 8: one row a wave)
+    float sum[kRows] = {0.f, 0.f};
+    int ad[kRows], r[kRows];
+    const uint16_t *ap[kRows], *xp[kRows];
 #pragma unroll
-      for (int h = 0; h < kRows; ++h) {
-        const int i = min(i0 + kPWaves * h, n - 1), t = i / a.R;
-        r[h] = i - t * a.R;
-        ad[h] = __builtin_amdgcn_readlane(mine, t);
-        ap[h] = a.A + ((int64_t)max(ad[h], 0) * a.R + r[h]) * a.K;
-        xp[h] = a.x + t * a.ldx;
-      }
-      for (int k0 = 0; k0 < a.K; k0 += 512 * kChunks) {
-        u32x4 av[kRows][kChunks], xv[kRows][kChunks];
+    for (int h = 0; h < kRows; ++h) {
+      const int i = min(wave + kPWaves * h, n - 1), t = i / a.R;
+      r[h] = i - t * a.R;
+      ad[h] = __builtin_amdgcn_readlane(mine, t);
+      ap[h] = a.A + ((int64_t)max(ad[h], 0) * a.R + r[h]) * a.K;
+      xp[h] = a.x + t * a.ldx;
+    }
+    for (int k0 = 0; k0 < a.K; k0 += 512 * kChunks) {
+      u32x4 av[kRows][kChunks], xv[kRows][kChunks];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-          const int k = k0 + 512 * j + 8 * lane;
+      for (int j = 0; j < kChunks; ++j) {
+        const int k = k0 + 512 * j + 8 * lane;
 #pragma unroll
-          for (int h = 0; h < kRows; ++h) {
-            av[h][j] = xv[h][j] = u32x4{0u, 0u, 0u, 0u};
-            if (k < a.K) {
-              av[h][j] = *reinterpret_cast<const u32x4*>(ap[h] + k);
-              xv[h][j] = *reinterpret_cast<const u32x4*>(xp[h] + k);
-            }
+        for (int h = 0; h < kRows; ++h) {
+          av[h][j] = xv[h][j] = u32x4{0u, 0u, 0u, 0u};
+          if (k < a.K) {
+            av[h][j] = *reinterpret_cast<const u32x4*>(ap[h] + k);
+            xv[h][j] = *reinterpret_cast<const u32x4*>(xp[h] + k);
           }
         }
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j)
-#pragma unroll
-          for (int h = 0; h < kRows; ++h)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              sum[h] = __builtin_fmaf(bf16lo(av[h][j][u]), bf16lo(xv[h][j][u]), sum[h]);
-              sum[h] = __builtin_fmaf(bf16hi(av[h][j][u]), bf16hi(xv[h][j][u]), sum[h]);
-            }
       }
 #pragma unroll
-      for (int h = 0; h < kRows; ++h) {
-        const float v = sum_lanes(sum[h]);
-        const bool is = ad[h] >= 0 && r[h] < rank_of(a, max(ad[h], 0));
-        if (lane == 0 && i0 + kPWaves * h < n)
-          zs[i0 + kPWaves * h] = is ? v * (a.scales ? a.scales[ad[h]] : 1.f) : 0.f;
-      }
+      for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+        for (int h = 0; h < kRows; ++h)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            sum[h] = __builtin_fmaf(bf16lo(av[h][j][u]), bf16lo(xv[h][j][u]), sum[h]);
+            sum[h] = __builtin_fmaf(bf16hi(av[h][j][u]), bf16hi(xv[h][j][u]), sum[h]);
+          }
+    }
+#pragma unroll
+    for (int h = 0; h < kRows; ++h) {
+      const float v = sum_lanes(sum[h]);
+      const bool is = ad[h] >= 0 && r[h] < rank_of(a, max(ad[h], 0));
+      if (lane == 0 && wave + kPWaves * h < n)
+        zs[wave + kPWaves * h] = is ? v * (a.scales ? a.scales[ad[h]] : 1.f) : 0.f;
     }
   }
 

@@ -39,6 +39,24 @@ def _behind(full, T, W, fill=7.0):
     return bool((f[T:] == fill).all() and (f[:T, W:] == fill).all())
 
 
+def _graph_us(f, n=20):
+    for _ in range(3):
+        f()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(n):
+            f()
+    best = float("inf")
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / n * 1e3)
+    return best
+
+
 # ------------------------------------------------------------------ residual add + RMS norm
 
 def _norm_case(T, H, dtype="bf16", weight=None, residual=True, y=True, out8=B.OUT8_NONE, group=0, offset=0.0, pad=0,
@@ -378,24 +396,6 @@ def test_gate_large_biases_of_one_size(score):
             _check_gate(l, _run_gate(l, **kw), **kw)
 
 
-def _graph_us(f, n=20):
-    for _ in range(3):
-        f()
-    g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
-        for _ in range(n):
-            f()
-    best = float("inf")
-    for _ in range(7):
-        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        a.record()
-        g.replay()
-        b.record()
-        torch.cuda.synchronize()
-        best = min(best, a.elapsed_time(b) / n * 1e3)
-    return best
-
-
 @pytest.mark.parametrize("masked", [-np.inf, np.nan, -1e4, -1e9])
 def test_gate_masking_an_expert_costs_no_decisions_in_64_bits(masked):
     # decided in 64 bits, every token of a call, the routing took three times as long
@@ -648,6 +648,20 @@ def test_project_few_tokens(N, K):
     y = _project(m, x, dirty, of)
     assert torch.equal(y[[0, 2]], clean[[0, 2]])
     assert y[1].isnan().all() and y[3].isnan().all()
+
+
+@pytest.mark.parametrize("T,R", [(1, 32), (2, 16), (4, 8)])
+def test_project_one_launch_only_where_it_is_faster(T, R):
+    # with T R = 32 rows every block read them all in two passes: 1.5 times the two launches' time, which more rows take
+    N, K, n = 512, 16384, 4
+    m, x = _Matrix(N, K), _x(T, K).cuda()
+    y, of = torch.empty((T, N), dtype=torch.bfloat16, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+    us = []
+    for r in (R, R + 8):
+        a = B.Adapters(*_dev(_adapters(N, K, n, r, full_rank=True)))
+        ws = B.project_workspace(N, K, T, a)
+        us.append(_graph_us(lambda: B.moe_project(m.blob, N, K, x, y, T, a, of, ws=ws)))
+    assert us[0] < 1.25 * us[1], us
 
 
 def test_project_adapter_names_out_of_range_mean_none():
