@@ -140,6 +140,13 @@ def test_norm_matches_64_bits(c):
     _norm_case(**c)
 
 
+@pytest.mark.parametrize("T,H", [(70001, 64), (20001, 500), (17003, 1024), (4999, 2048), (6001, 2056), (4100, 4104)])
+@pytest.mark.parametrize("out8,group", [(B.OUT8_INT8, 0), (B.OUT8_E4M3, 32)])
+def test_norm_blocks_take_rows_in_turn(T, H, out8, group):
+    # more rows than the grid holds at once, for each number of threads a row
+    _norm_case(T, H, out8=out8, group=group if H % 32 == 0 else 0)
+
+
 @pytest.mark.parametrize("out8,group", [(B.OUT8_INT8, 0), (B.OUT8_E4M3, 64)])
 def test_norm_zero_and_tiny_rows(out8, group):
     # rows of zeros (scale 0, q 0), rows far below eps, and one large value among zeros
@@ -476,6 +483,53 @@ def test_gated_layer(T, chunk):
         got = synth.bf16_bits_to_f32(y.cpu().numpy().view(np.uint16)).astype(np.float64)
         rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
         assert rel <= 5e-3, f"{name}: {rel}"     # the layer's own bar
+
+
+def _check_gated_layer(w, dw, d, T, mode, tokens=None):
+    """One call of the layer with a gate; y of `tokens` (all by default) against the oracle's experts."""
+    rng = np.random.default_rng(900 + T + w.H)
+    x = synth.make_x(rng, T, w.H)
+    bias = rng.uniform(-0.05, 0.05, w.E).astype(np.float32)
+    bias[5] = -np.inf                                          # an expert that is never selected
+    g = B.gate(w.E, 8, score=B.SCORE_SIGMOID, n_groups=8, topk_groups=4, group_score=B.GROUP_TOP2, scale=2.5,
+               balance_bias=torch.from_numpy(bias).cuda())
+    y = torch.full((T + 1, w.H), 0x5A5A, dtype=torch.int16, device="cuda")
+    logits, ro = torch.empty((T, w.E), device="cuda"), B.RouteBuffers(d, T)
+    f = B.moe_decode_layer_gated if mode == B.MODE_DECODE else B.moe_prefill_layer_gated
+    ws = B.workspace(d, T, mode)
+    ws.fill_(0xA5)
+    f(d, g, dw, torch.from_numpy(x).cuda(), y, T, logits_out=logits, route_out=ro, ws=ws)
+    torch.cuda.synchronize()
+    assert (y[T] == 0x5A5A).all()
+    idx, wsel = gate_ref(logits.cpu().numpy(), bias=bias, **GATE_DSV)
+    meta = ro.to_numpy()
+    assert np.array_equal(meta["topk_idx"], idx)
+    assert (np.abs(meta["topk_w"] - wsel) <= np.abs(wsel) * (16 * U32) + 1e-37).all()
+    check_route_meta(meta, idx, w.E, 8, 32)
+    at = np.arange(T) if tokens is None else np.linspace(0, T - 1, tokens).astype(int)
+    ref = _layer_ref(x[at], w, idx[at], wsel[at])
+    got = synth.bf16_bits_to_f32(y[:T].cpu().numpy().view(np.uint16)).astype(np.float64)[at]
+    rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+    assert rel <= 5e-3, rel                                    # the layer's own bar
+
+
+def test_gated_layer_real_size():
+    _, w, _ = synth.generate("prefill_t512", with_x=False)
+    dw = B.DeviceWeights.from_logical(w)
+    for T in (1, 2, 3, 4):
+        _check_gated_layer(w, dw, dw.dims, T, B.MODE_DECODE)
+    _check_gated_layer(w, dw, dw.dims, 2, B.MODE_PREFILL)
+    for gemm in (B.GEMM_EXACT, B.GEMM_WIDE):
+        _check_gated_layer(w, dw, B.dims(w.H, w.I, w.E, gemm=gemm), 512, B.MODE_PREFILL, tokens=16)
+
+
+@pytest.mark.parametrize("H,I,E", [(256, 128, 64), (1024, 256, 128), (4096, 128, 64), (768, 384, 192)])
+def test_gated_layer_other_sizes(H, I, E):
+    w = synth.make_weights(np.random.default_rng(H), H, I, E)
+    dw = B.DeviceWeights.from_logical(w)
+    for T in (1, 2, 4):
+        _check_gated_layer(w, dw, dw.dims, T, B.MODE_DECODE)
+    _check_gated_layer(w, dw, dw.dims, 37, B.MODE_PREFILL)
 
 
 def test_gate_binding_checks_tensors():
