@@ -532,6 +532,40 @@ def test_gated_layer_other_sizes(H, I, E):
     _check_gated_layer(w, dw, dw.dims, 37, B.MODE_PREFILL)
 
 
+@pytest.mark.parametrize("T", [1, 4, 33])
+def test_gated_layer_without_its_optional_outputs(T):
+    _, w, _ = synth.generate("tiny_t32", with_x=False)
+    dw, d = B.DeviceWeights.from_logical(w), B.dims(w.H, w.I, w.E)
+    x = torch.from_numpy(synth.make_x(np.random.default_rng(T), T, w.H)).cuda()
+    g = B.gate(w.E, 8, score=B.SCORE_SIGMOID)
+    for f, mode in ((B.moe_prefill_layer_gated, B.MODE_PREFILL), (B.moe_decode_layer_gated, B.MODE_DECODE)):
+        if mode == B.MODE_DECODE and T > 4:
+            continue
+        y = [torch.empty((T, w.H), dtype=torch.int16, device="cuda") for _ in range(2)]
+        f(d, g, dw, x, y[0], T, ws=B.workspace(d, T, mode))
+        f(d, g, dw, x, y[1], T, logits_out=torch.empty((T, w.E), device="cuda"), route_out=B.RouteBuffers(d, T),
+          ws=B.workspace(d, T, mode))
+        assert torch.equal(*y)
+
+
+@pytest.mark.parametrize("E", [256, 60])
+def test_gate_logits_and_biases_at_any_word(E):
+    rng, T = np.random.default_rng(E), 100
+    l, bias = _logits(rng, T, E, "plain"), rng.uniform(-0.05, 0.05, E).astype(np.float32)
+    want = _run_gate(l, 8, "sigmoid", bias=bias)
+    for lo, bo in ((1, 0), (0, 3), (2, 1)):
+        lt = torch.zeros(T * E + 3, device="cuda")[lo : lo + T * E].view(T, E)
+        bt = torch.zeros(E + 3, device="cuda")[bo : bo + E]
+        lt.copy_(torch.from_numpy(l))
+        bt.copy_(torch.from_numpy(bias))
+        g = B.gate(E, 8, score=B.SCORE_SIGMOID, balance_bias=bt)
+        out = B.RouteBuffers(g, T)
+        B.moe_route_gated(g, lt, T, out, B.gate_workspace(g, T))
+        got = out.to_numpy()
+        for name in want:
+            assert np.array_equal(got[name], want[name]), name
+
+
 def test_gate_binding_checks_tensors():
     _, w, _ = synth.generate("tiny_t32", with_x=False)
     dw, T = B.DeviceWeights.from_logical(w), 2
@@ -725,6 +759,26 @@ def test_project_adapter_names_out_of_range_mean_none():
         of = torch.tensor(([n, -7, 2 ** 31 - 1, -2 ** 31, 1] * 8)[:T], dtype=torch.int32)
         as_none = torch.where((of >= 0) & (of < n), of, torch.full_like(of, -1))
         assert torch.equal(_project(m, _x(T, 256), ad, of), _project(m, _x(T, 256), ad, as_none))
+
+
+def test_project_ranks_out_of_range_are_limited():
+    N, K, n, R = 128, 256, 5, 16
+    m, (A, Bm, _, scales) = _Matrix(N, K), _adapters(N, K, n, R)
+    ranks = torch.tensor([-1, 17, 2 ** 31 - 1, -2 ** 31, 9], dtype=torch.int32)
+    for T in (1, 2, 40, 300):
+        x, of = _x(T, K), torch.arange(T, dtype=torch.int32) % n
+        if T == 1:
+            of[0] = 2
+        assert torch.equal(_project(m, x, (A, Bm, ranks, scales), of), _project(m, x, (A, Bm, ranks.clamp(0, R), scales), of))
+
+
+@pytest.mark.parametrize("gemm", [B.GEMM_EXACT, B.GEMM_WIDE])
+def test_project_widest(gemm):
+    N, K, n, R = 65536, 128, 2, 8
+    m, ad = _Matrix(N, K), _adapters(N, K, n, R)
+    for T in (1, 3, 70):
+        x, of = _x(T, K), torch.arange(T, dtype=torch.int32) % (n + 1) - 1
+        _check_project(m, x, _project(m, x, ad, of, gemm), ad, of, wide=gemm == B.GEMM_WIDE)
 
 
 @pytest.mark.parametrize("gemm", GEMMS)
