@@ -309,7 +309,10 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
     sb[s] = bload(wres, c16 * 16, sbase + g * kSbBytes);
   };
 #pragma unroll
-  for (int s = 0; s < D; ++s) load(s);
+  for (int s = 0; s < D; ++s) {
+    load(s);
+    __builtin_amdgcn_sched_barrier(0);  // the waits below count on the slots' order
+  }
 
   // ---- the wave's adapters: the distinct ones of the rows, in row order,
   // every eighth; the first NE's operands are loaded here
