@@ -553,7 +553,9 @@ __device__ void gate_select(const GateArgs& a, int t0, SelectLds& L, int& sel, f
     if (q == row) sel = se;
   }
   // the weights in 64 bits from the selected logits; where the fp32 sum over
-  // the experts is used (softmax, not renormalised) it errs by a few 2^-24
+  // the experts is used (softmax, not renormalised) it errs by a few 2^-24: the
+  // sum in 64 bits would need every expert's exponential in them (errors are
+  // 5.6e-8 of the weights, 2.6e-8 of a rounding's own)
   double v = 0.0;
   if (c < k && sel < kMaskedSel) {
     const float x = L.v[q][sel];
@@ -598,9 +600,10 @@ __device__ inline void write_block(const GateScatter& a, int e, int pos, int ran
 // Grid: ceil(T / (4 W)). Block: W waves, four tokens each. COUNTS: the block
 // writes its row of expert counts [grid][256] bytes (at most 64 each);
 // otherwise counts are added to chunk_hist (when given). 256 experts, eight
-// groups, sigmoid and bias: 6 us for 512 tokens (the chain of one wave), 17
-// for 16384 (vector instructions, about 1300 a wave); 60 experts, softmax,
-// 2049 tokens: 4.
+// groups, sigmoid and bias: 6 us for 512 tokens (the chain of one wave, about
+// 1300 vector instructions), 17 for 16384 (waves, four a SIMD, wait 0.52 of
+// their time, and vector instructions issue in 0.36 of the SIMDs'); 60 experts,
+// softmax, 2049 tokens: 4.
 template <int NJ, int KD, int W, bool COUNTS>
 __global__ __launch_bounds__(64 * W) void gate_topk_kernel(GateArgs a) {
   __shared__ SelectLds L[W];
@@ -894,7 +897,8 @@ hipError_t launch_gate_route(const GateArgs& in, const GateScatter& scatter, hip
   if (e != hipSuccess) return e;
   // One piece a block, and no more blocks than the chip holds at once, since
   // each sums all the counts (131072 tokens: 170 us with the selection in a
-  // block per piece, 133 in 512 blocks; 1048576 tokens: 4898 and 1025).
+  // block per piece, 133 in 512 blocks; 1048576 tokens: 4898 and 1025; both, with
+  // a sigmoid and eight groups, 125 and 926 since).
   const int all = (a.T + kScatterTokens - 1) / kScatterTokens;
   sc.pieces = (all + kScatterBlocks - 1) / kScatterBlocks;
   hipLaunchKernelGGL(gate_scatter_kernel, dim3((all + sc.pieces - 1) / sc.pieces), dim3(kGateThreads), 0, s, sc);

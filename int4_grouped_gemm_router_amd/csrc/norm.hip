@@ -6,7 +6,8 @@
 // One pass over memory: a row is held in the registers of 16, 64 or 256
 // threads (up to 16384 values), so x and residual are read once and every
 // output is written once; the sum of squares and v are fp32. The memory
-// traffic bounds it, and for a few rows the latency of one load, one
+// traffic bounds it up to 4096 values, the waves that their registers leave
+// room for in longer rows, and for a few rows the latency of one load, one
 // reduction and one store. Threads keep their weights over the rows they take
 // in turn.
 #include <type_traits>
@@ -291,8 +292,9 @@ namespace {
 
 template <class R, int TPR, int NV>
 void launch_shape(const NormArgs& a, hipStream_t s) {
-  // enough blocks to fill the chip eight waves deep on every SIMD; each takes
-  // rows in turn
+  // enough blocks for eight waves on every SIMD, where their registers leave
+  // room (for six to eight up to 4096 values, three to five from 4097 on, one or
+  // two from 8193); each takes rows in turn
   constexpr int kRows = kNormThreads / TPR;
   const int64_t blocks = ((int64_t)a.T + kRows - 1) / kRows;
   const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048)), block(kNormThreads);
@@ -316,7 +318,9 @@ void launch_shape(const NormArgs& a, hipStream_t s) {
 // One load of each input per thread where the threads of a block or of a wave
 // allow it, more blocks rather than longer rows per thread: rows of 2048
 // values by 256 threads take 2.4 us for one row, 4.8 for 1024, 51.5 for 16384
-// (5.2 TB/s), by one wave with four loads a lane 3.9, 6.3 and 54.7.
+// (5.2 TB/s), by one wave with four loads a lane 3.9, 6.3 and 54.7. As many
+// bytes in rows of 4096 values move at 5.0 TB/s, of 5120, 7168 and 8192 at 3.7,
+// 4.0 and 4.4, of 16384 at 2.3 (with e4m3 4.9, 3.2, 3.5, 3.9 and 1.9).
 template <class R>
 void launch_rows(const NormArgs& a, hipStream_t s) {
   if (a.H <= 128)

@@ -78,7 +78,9 @@ struct Distinct {
   }
 };
 
-// z's two halves [T][R]: the bf16 value nearest to z, and that of the rest.
+// z's two halves [T][R]: the bf16 value nearest to z, and that of the rest. They
+// enter the matrix cores as they are, and their 16 bits miss at most 2^-16 of z,
+// far below y's own rounding (2^-8).
 __device__ inline uint16_t* z_hi(const ProjectArgs& a) { return static_cast<uint16_t*>(a.ws); }
 __device__ inline uint16_t* z_lo(const ProjectArgs& a) { return z_hi(a) + (int64_t)a.T * a.R; }
 
@@ -140,7 +142,7 @@ __device__ inline u32x4 rank_chunk(const uint16_t* base, int64_t row, int R, int
 // latency: the activations are under way before the adapters are known and
 // serve every entry while they are held, and an entry's part of A is under way
 // before its rank is known. K = 2048, rank 16: 4.3 us for 32 tokens of 32
-// adapters (2.1 MB of them), 7.1 for 4096 tokens.
+// adapters (2.1 MB of them), 7.2 for 4096 tokens.
 struct DownLds {
   static constexpr int kHeld = 2;
   u32x4 x[kPWaves][kHeld][4][64], a[kPWaves][kHeld][4][64];  // [wave][chunk][32 inputs][frag_slot]
@@ -229,12 +231,14 @@ __global__ __launch_bounds__(kPThreads) void adapter_down_kernel(ProjectArgs a, 
 //   acc += s * x.(128 + q) + (b - 128 s) * sum(x)
 // which is x . (q s + b) with the weights used exactly. The distinct adapters
 // of the tokens are dealt out over the waves too; their operands are loaded
-// ahead of the groups (NE adapters a wave, the first 32 ranks), and their
-// B_a z goes to a tile of its own, added last, so a token's result does not
-// depend on the others. 4096 x 2048: 6.2 us for one token with an adapter of
-// rank 16 (latency of one pass, FUSED), 7.4 for 32 tokens with 32 adapters;
-// 2048 x 2048 for 500 tokens: 13.6 (the expansion of the codes, which every 64
-// rows repeat).
+// before the groups' products (NE adapters a wave, the first 32 ranks; the wait
+// for an adapter's rank, the same in every lane, stands before its operands and
+// drains the first groups' loads as well), and their B_a z goes to a tile of its
+// own, added last, so a token's result does not depend on the others. 4096 x
+// 2048: 7.4 us for one token with an adapter of rank 16 (latency of one pass,
+// FUSED), 7.4 for 32 tokens with 32 adapters; 2048 x 2048 for 500 tokens: 13.6
+// (one round of blocks, two waves a SIMD: waves wait 0.42 of their time, vector
+// instructions issue in 0.24 of the SIMDs' and matrix cores are busy in 0.11).
 template <int MS, int CT, int D>
 struct SplitLds {
   static constexpr int kStride = 16 * CT + 4;  // floats; the pad spreads the rows over the banks
@@ -580,8 +584,11 @@ __global__ __launch_bounds__(kPThreads, 2) void project_split_kernel(ProjectArgs
 // weights per four of them. The unit of the pipeline is half a group (k half,
 // 32 inputs): in half h the products of h run while h + 2 is written to LDS,
 // and the first operands of h + 1 are read before the barrier that ends h
-// (h + 1 was complete at the barrier before). 4096 tokens, 4096 x 2048: 62 to
-// 64 us (1.1 PFLOP/s), about 70 with adapters of rank 16.
+// (h + 1 was complete at the barrier before). 4096 tokens, 4096 x 2048: 60 to
+// 64 us (1.1 PFLOP/s), 69 with adapters of rank 16 (76 to 82 after the first
+// millisecond of such calls without a pause). The weights' one rounding leaves
+// an error of 1.9e-3, 1.7e-3 of it y's own; the split kernel, which has none,
+// takes three times as long.
 template <int RS>
 struct TileLds {
   u32x4 x[2][2][2 * RS][64];  // [group % 2][k half][16-token subtile][frag_slot]
