@@ -413,6 +413,174 @@ int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64
                 int64_t ldy, int32_t T, const moe_adapters* ad, const int32_t* adapter_of,
                 int32_t gemm, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- the mixer half of a block
+ *
+ * What stands between moe_add_rmsnorm and the layer in a block: a projection
+ * of 8-bit rows, rotary positions, linear attention with a decay for each
+ * head, and the norm after a block with its gate, its residual scale and the
+ * norm of the next block. They follow the conventions at the top of this
+ * file; none has a backward pass (the library trains nothing). */
+
+/* A projection by 8-bit integers with a scale for each token and each output:
+ *   y[t][n] = x_scales[t] * w_scales[n] * sum_k x[t][k] w[n][k] + bias[n]
+ * for x [T][K] with row stride ldx (bytes, a multiple of 16, from K to 2^20),
+ * as moe_add_rmsnorm and moe_gated_norm leave int8 rows with one scale a row,
+ * and w [N][K] row-major, contiguous; both 16-byte aligned, any value
+ * -128..127. x_scales [T], w_scales [N] and bias [N] (or null) fp32. y [T][N]
+ * of type dtype (MOE_BF16, MOE_F16 or MOE_F32), aligned to its element, with
+ * row stride ldy (elements, from N to 2^20). K % 64 == 0, 64..65536; N
+ * 1..2^18; T <= 2^30. Sums are exact (32-bit integers); the scales and the
+ * bias are applied in fp32 and the result is rounded once. x and y must not
+ * overlap. ws 16-byte aligned (null where moe_project_int8_workspace_bytes
+ * gives 0); its contents do not matter. T = 0 is a no-op. */
+int moe_project_int8_workspace_bytes(int32_t N, int32_t K, int32_t T, size_t* bytes);
+int moe_project_int8(const int8_t* w, const float* w_scales, const float* bias, int32_t N, int32_t K,
+                     const int8_t* x, int64_t ldx, const float* x_scales, void* y, int64_t ldy,
+                     int32_t dtype, int32_t T, void* ws, size_t ws_bytes, void* stream);
+
+/* Frequencies of rotary positions: pair i of a turned part of rot_dim values
+ * turns by radians[i] = base^(-2i / rot_dim) per position, and for long
+ * contexts by less (factor >= 1):
+ *   MOE_ROPE_LINEAR  radians / factor
+ *   MOE_ROPE_NTK     the base times factor^(rot_dim / (rot_dim - 2))
+ *   MOE_ROPE_YARN    ("YaRN: Efficient Context Window Extension of Large
+ *                    Language Models", Peng et al., section 3) with r the
+ *                    turns of a pair over `context` positions and
+ *                    c = clamp((r - slow) / (fast - slow), 0, 1):
+ *                    radians (c + (1 - c) / factor), and the magnitude
+ *                    0.1 ln(factor) + 1 on cosine and sine (else 1)
+ * base > 0 and finite; context > 0 and fast > slow for YARN; rot_dim even, 2 to
+ * 1024 (more than 2 for NTK). radians [rot_dim / 2] and magnitude on the host. */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_NTK 2
+#define MOE_ROPE_YARN 3
+typedef struct {
+  int32_t kind;
+  double base, factor, context, slow, fast;
+} moe_rope_scaling;
+int moe_rope_radians(const moe_rope_scaling* scaling, int32_t rot_dim, double* radians,
+                     float* magnitude);
+
+/* radians[n] per position (finite) as whole numbers of 2^-64 turns, modulo one
+ * turn (host -> host): with them a position times a frequency is exact. */
+int moe_rope_turns(const double* radians, int32_t n, uint64_t* turns);
+
+/* Heads of head_dim values (2..1024), whose first rot_dim (even, 2..head_dim)
+ * are turned: pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved;
+ * inverse != 0 turns by the opposite angles. magnitude is a factor on cosine
+ * and sine (finite). turns: device, [rot_dim / 2], 8-byte aligned. */
+typedef struct {
+  int32_t head_dim, rot_dim, dtype, interleaved, inverse;
+  float magnitude;
+  const uint64_t* turns;
+} moe_rotary;
+
+/* Rotary positions of T tokens: with f the turns of a pair (a, b) per position
+ *   a' = m (a cos(2 pi f p) - b sin(2 pi f p)), b' = m (a sin(..) + b cos(..))
+ * p = positions[t] (device, int32, any value). q [T][q_heads][head_dim] and,
+ * unless null, k [T][k_heads][head_dim], heads contiguous within rows of
+ * strides ldq and ldk (elements, from heads * head_dim to 2^20), aligned to
+ * their element; q_out and k_out the same with ldqo and ldko. q_out may be q
+ * and k_out k, with the same stride; the values behind rot_dim are copied to
+ * another buffer and left alone in place. Any other overlap of an output with
+ * another argument is not allowed (q and k may be parts of one row, and so may
+ * the outputs). 1..1024 heads each. Angles err by at most 2^-32 turns however
+ * far the position; sums in fp32, one rounding. T <= 2^30; T = 0 is a no-op. */
+int moe_rope(const moe_rotary* rope, const void* q, int64_t ldq, void* q_out, int64_t ldqo,
+             int32_t q_heads, const void* k, int64_t ldk, void* k_out, int64_t ldko,
+             int32_t k_heads, const int32_t* positions, int32_t T, void* stream);
+
+/* Linear attention: v_heads states of [qk_dim][v_dim], v_heads a multiple of
+ * qk_heads (1..1024), qk_dim and v_dim multiples of 8, 8..256. Value head h
+ * uses the queries and keys of head h / (v_heads / qk_heads). scale finite. */
+typedef struct {
+  int32_t qk_heads, v_heads, qk_dim, v_dim;
+  float scale;
+} moe_linear;
+
+/* Linear attention over sequences, per value head:
+ *   S_t = exp(g_t) S_(t-1) + k_t v_t^T,   o_t = scale * q_t S_t
+ * q, k [T][qk_heads][qk_dim], v, o [T][v_heads][v_dim] bf16, 16-byte aligned,
+ * heads contiguous within rows of strides ldq, ldk, ldv, ldo (elements,
+ * multiples of 8, at most 2^20). g = log_decay, fp32: [T][v_heads] with row
+ * stride ld_decay (v_heads..2^20), or [v_heads] for all tokens with ld_decay
+ * 0. Any g is allowed: -inf forgets everything before the token.
+ * Sequence i holds the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
+ * (device, int32 [n_seqs + 1], not decreasing, from 0; values are limited to
+ * 0..T); rows of o behind the last are left as they were. Its state starts as
+ * state_in[slots_in[i]] and ends as state_out[slots_out[i]]: fp32
+ * [n][v_heads][qk_dim][v_dim], 16-byte aligned, n = n_in and n_out. Null
+ * slots stand for i; a slot outside 0..n-1 (-1) starts from zeros or is not
+ * kept, and so is every one of a null state. An empty sequence's state is
+ * copied. state_in may be state_out; a slot that one sequence writes must not
+ * be read or written by another (any number may read the same one).
+ * n_seqs <= 65536, T <= 2^30. States, sums and decays are fp32 or more; the
+ * state's update keeps 24 significant bits of v's decayed rows, and for o the
+ * state and the decayed products of q and k are rounded to bf16 as operands
+ * of the matrix cores (o's own type). ws 16-byte aligned, of
+ * moe_linear_workspace_bytes (null where that is 0); its contents do not
+ * matter, and a workspace for T tokens and n_seqs serves fewer. o must not
+ * overlap any input. n_seqs = 0 is a no-op. */
+int moe_linear_workspace_bytes(const moe_linear* linear, int32_t n_seqs, int32_t T, size_t* bytes);
+int moe_linear_attention(const moe_linear* linear, const uint16_t* q, int64_t ldq, const uint16_t* k,
+                         int64_t ldk, const uint16_t* v, int64_t ldv, const float* log_decay,
+                         int64_t ld_decay, const int32_t* cu_seqlens, int32_t n_seqs,
+                         const float* state_in, const int32_t* slots_in, int32_t n_in,
+                         float* state_out, const int32_t* slots_out, int32_t n_out, uint16_t* o,
+                         int64_t ldo, int32_t T, void* ws, size_t ws_bytes, void* stream);
+
+/* The same for T sequences of one token each (decode): token t is sequence t.
+ * No operand is rounded on the way to o. T <= 65536; T = 0 is a no-op. */
+int moe_linear_attention_step(const moe_linear* linear, const uint16_t* q, int64_t ldq,
+                              const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                              const float* log_decay, int64_t ld_decay, const float* state_in,
+                              const int32_t* slots_in, int32_t n_in, float* state_out,
+                              const int32_t* slots_out, int32_t n_out, uint16_t* o, int64_t ldo,
+                              int32_t T, void* stream);
+
+/* Gates of moe_gated_norm: none, z / (1 + exp(-z)), 1 / (1 + exp(-z)). */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_SILU 1
+#define MOE_GATE_SIGMOID 2
+
+/* Rows of H values (1..16384) of type dtype; the type of weight, next_weight
+ * and channel_scale (the rows' or MOE_F32). normalize: whether the first norm
+ * is taken, over `group` consecutive values (0: the row, or 32, 64, 128 or
+ * 256, dividing H). gate: a MOE_GATE_*; gate_per_row: one gate value a row
+ * instead of H. next: whether the second norm is taken. out8 and out8_group as
+ * out8 and group of moe_norm. eps and next_eps > 0, all others finite. */
+typedef struct {
+  int32_t H, dtype, weight_dtype, normalize, group, gate, gate_per_row, next, out8, out8_group;
+  float eps, weight_offset, scale, next_eps, next_offset;
+} moe_block_norm;
+
+/* The norm after a block (or of its heads) with its gate, the residual add
+ * with a scale, and the norm before the next block, per row of T:
+ *   u = x / sqrt(mean_group(x^2) + eps) * (weight + weight_offset)   normalize
+ *   v = scale * channel_scale * u * act(gate) + residual
+ *   h = v, rounded to the rows' type
+ *   v = v / sqrt(mean_row(v^2) + next_eps) * (next_weight + next_offset)  next
+ *   y = v, rounded to the rows' type
+ *   q, scales: v in 8 bits, as moe_add_rmsnorm forms them
+ * in fp32, each output rounded once (the second norm takes the sum before it
+ * is rounded to h). x, residual, gate [T][H] ([T] for gate_per_row), h_out, y
+ * and q with row strides ldx, ld_residual, ld_gate (from 1 for gate_per_row),
+ * ld_h, ld_y, ld_q in elements, up to 2^20. weight [group] ([H] for group 0)
+ * or null (the first norm without a weight; always null without a norm),
+ * channel_scale [H] or null, next_weight [H] with next. gate is given unless
+ * MOE_GATE_NONE. residual may be null, and so may h_out and y (y only with
+ * next); q and scales are both given with an 8-bit output; one output at least.
+ * h_out and y may each be x, residual or a gate [T][H], with the same row
+ * stride (each row is read whole before it is written; y over h_out leaves
+ * y); any other overlap of an output with another argument is not allowed.
+ * Pointers need their element's alignment only. T = 0 is a no-op. */
+int moe_gated_norm(const moe_block_norm* norm, const void* x, int64_t ldx, const void* weight,
+                   const void* gate, int64_t ld_gate, const void* channel_scale,
+                   const void* residual, int64_t ld_residual, const void* next_weight, void* h_out,
+                   int64_t ld_h, void* y, int64_t ld_y, void* q, int64_t ld_q, float* scales,
+                   int32_t T, void* stream);
+
 /* Static description of an error code. */
 const char* moe_strerror(int code);
 

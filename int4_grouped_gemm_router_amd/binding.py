@@ -27,6 +27,8 @@ BF16, F16, F32 = 0, 1, 2
 OUT8_NONE, OUT8_INT8, OUT8_E4M3 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+GATE_NONE, GATE_SILU, GATE_SIGMOID = 0, 1, 2
 HEADER_BYTES = 256
 
 _i32 = ctypes.c_int32
@@ -34,6 +36,7 @@ _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 
 class MoeDims(ctypes.Structure):
@@ -65,6 +68,25 @@ class MoeGate(ctypes.Structure):
 
 class MoeAdapters(ctypes.Structure):
     _fields_ = [("n", _i32), ("R", _i32), ("A", _vp), ("B", _vp), ("ranks", _vp), ("scales", _vp)]
+
+
+class MoeRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", _i32), ("base", _f64), ("factor", _f64), ("context", _f64), ("slow", _f64), ("fast", _f64)]
+
+
+class MoeRotary(ctypes.Structure):
+    _fields_ = [("head_dim", _i32), ("rot_dim", _i32), ("dtype", _i32), ("interleaved", _i32), ("inverse", _i32),
+                ("magnitude", _f32), ("turns", _vp)]
+
+
+class MoeLinear(ctypes.Structure):
+    _fields_ = [("qk_heads", _i32), ("v_heads", _i32), ("qk_dim", _i32), ("v_dim", _i32), ("scale", _f32)]
+
+
+class MoeBlockNorm(ctypes.Structure):
+    _fields_ = [("H", _i32), ("dtype", _i32), ("weight_dtype", _i32), ("normalize", _i32), ("group", _i32),
+                ("gate", _i32), ("gate_per_row", _i32), ("next", _i32), ("out8", _i32), ("out8_group", _i32),
+                ("eps", _f32), ("weight_offset", _f32), ("scale", _f32), ("next_eps", _f32), ("next_offset", _f32)]
 
 
 class MoeError(RuntimeError):
@@ -128,6 +150,18 @@ def lib():
         L.moe_project_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, P(_sz)]
         L.moe_project.argtypes = [_vp, _i32, _i32, _vp, _i64, _vp, _i64, _i32, P(MoeAdapters), _vp, _i32,
                                   _vp, _sz, _vp]
+        L.moe_project_int8_workspace_bytes.argtypes = [_i32, _i32, _i32, P(_sz)]
+        L.moe_project_int8.argtypes = [_vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _vp, _sz, _vp]
+        L.moe_rope_radians.argtypes = [P(MoeRopeScaling), _i32, _vp, P(_f32)]
+        L.moe_rope_turns.argtypes = [_vp, _i32, _vp]
+        L.moe_rope.argtypes = [P(MoeRotary)] + [_vp, _i64, _vp, _i64, _i32] * 2 + [_vp, _i32, _vp]
+        L.moe_linear_workspace_bytes.argtypes = [P(MoeLinear), _i32, _i32, P(_sz)]
+        states = [_vp, _vp, _i32] * 2
+        L.moe_linear_attention.argtypes = ([P(MoeLinear)] + [_vp, _i64] * 4 + [_vp, _i32] + states +
+                                           [_vp, _i64, _i32, _vp, _sz, _vp])
+        L.moe_linear_attention_step.argtypes = [P(MoeLinear)] + [_vp, _i64] * 4 + states + [_vp, _i64, _i32, _vp]
+        L.moe_gated_norm.argtypes = [P(MoeBlockNorm), _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp,
+                                     _i64, _vp, _i64, _vp, _i32, _vp]
         L.moe_strerror.argtypes = [ctypes.c_int]
         L.moe_strerror.restype = ctypes.c_char_p
         L.moe_test_dequant.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]
@@ -138,7 +172,10 @@ def lib():
                      "moe_prefill_layer_unfused", "moe_ceiling_read", "moe_ceiling_mfma",
                      "moe_decode_layer_noalloc", "moe_add_rmsnorm", "moe_gate_workspace_bytes",
                      "moe_route_gated", "moe_prefill_layer_gated", "moe_decode_layer_gated",
-                     "moe_project_workspace_bytes", "moe_project"):
+                     "moe_project_workspace_bytes", "moe_project", "moe_project_int8_workspace_bytes",
+                     "moe_project_int8", "moe_rope_radians", "moe_rope_turns", "moe_rope",
+                     "moe_linear_workspace_bytes", "moe_linear_attention", "moe_linear_attention_step",
+                     "moe_gated_norm"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -689,3 +726,197 @@ def moe_project(blob, N: int, K: int, x, y, T: int, adapters: Adapters | None = 
         wn = ws.numel()
         wp = _flat(ws, 0, torch.uint8, "ws", dev)
     _call("moe_project", _gpu(x), stream, blob.data_ptr(), N, K, xp, ldx, yp, ldy, T, ap, op, gemm, wp, wn)
+
+
+# ------------------------------------------------------------------ the mixer half of a block
+#
+# Checks and streams as above.
+
+def project_int8_workspace(N, K, T, device="cuda"):
+    """Workspace of moe_project_int8 for up to T tokens, or None where none is needed."""
+    import torch
+    n = _sz(0)
+    _check(lib().moe_project_int8_workspace_bytes(N, K, T, ctypes.byref(n)), "moe_project_int8_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+
+
+def moe_project_int8(w, w_scales, x, x_scales, y, T: int, bias=None, ws=None, stream=None):
+    """y[t] = x_scales[t] w_scales (w x[t]) + bias for int8 rows x [T, K] (moe_add_rmsnorm's q and scales) and
+    int8 weights w [N, K]; y bfloat16, float16 or float32."""
+    import torch
+    dev = x.get_device()
+    if w.dim() != 2:
+        raise ValueError(f"w: [N, K] is needed, got {list(w.shape)}")
+    N, K = w.shape
+    code = _type_code(y.dtype)
+    wp = _flat(w, N * K, torch.int8, "w", dev)
+    sp = _flat(w_scales, N, torch.float32, "w_scales", dev)
+    xp, ldx = _rows(x, T, K, _types_of(BITS8 + OUT8_INT8), dev, "x")
+    xs = _flat(x_scales, T, torch.float32, "x_scales", dev)
+    yp, ldy = _rows(y, T, N, _types_of(code), dev, "y")
+    bp = None if bias is None else _flat(bias, N, torch.float32, "bias", dev)
+    kp, kn = (None, 0) if ws is None else (_flat(ws, 0, torch.uint8, "ws", dev), ws.numel())
+    _call("moe_project_int8", _gpu(x), stream, wp, sp, bp, N, K, xp, ldx, xs, yp, ldy, code, T, kp, kn)
+
+
+def rope_radians(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, context=0.0, slow=1.0, fast=32.0):
+    """(radians per position of each pair, float64; the factor on cosine and sine) of scaled rotary positions."""
+    out, m = np.empty(max(rot_dim, 0) // 2, np.float64), _f32(0)
+    s = MoeRopeScaling(scaling, base, factor, context, slow, fast)
+    _check(lib().moe_rope_radians(ctypes.byref(s), rot_dim, _ptr(out), ctypes.byref(m)), "moe_rope_radians")
+    return out, m.value
+
+
+def rope(head_dim, rot_dim=None, dtype=BF16, interleaved=False, inverse=False, base=10000.0, scaling=ROPE_PLAIN,
+         factor=1.0, context=0.0, slow=1.0, fast=32.0, radians=None, magnitude=None, device="cuda") -> MoeRotary:
+    """How moe_rope turns heads of head_dim values, the first rot_dim (None: all) of them. The frequencies are those of
+    rope_radians, or `radians` [rot_dim / 2] of a model's own (then magnitude is 1 unless given)."""
+    import torch
+    rot = head_dim if rot_dim is None else rot_dim
+    if radians is None:
+        radians, m = rope_radians(rot, base, scaling, factor, context, slow, fast)
+    else:
+        radians, m = np.ascontiguousarray(radians, np.float64), 1.0
+        if radians.shape != (rot // 2,):
+            raise ValueError(f"radians: {rot // 2} values are needed, got {list(radians.shape)}")
+    turns = np.empty(len(radians), np.uint64)
+    _check(lib().moe_rope_turns(_ptr(radians), len(radians), _ptr(turns)), "moe_rope_turns")
+    table = torch.from_numpy(turns.view(np.int64)).to(device)
+    r = MoeRotary(head_dim, rot, _type_code(dtype), int(interleaved), int(inverse), m if magnitude is None else magnitude,
+                  table.data_ptr())
+    r.table = table  # kept alive with the plan
+    return r
+
+
+def _heads(t, T, heads, dim, dtypes, dev, name):
+    """Address and row stride of a [>= T, heads, dim] (or [>= T, heads * dim]) tensor whose rows are contiguous."""
+    if t.dim() == 3:
+        shape, stride = t.shape, t.stride()
+        if shape[1] != heads or shape[2] != dim or ((stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1)):
+            raise ValueError(f"{name}: [{T}, {heads}, {dim}] with contiguous heads is needed, got {list(shape)} of "
+                             f"strides {list(stride)}")
+        if t.dtype not in dtypes or shape[0] < T:
+            raise ValueError(f"{name}: [{T}, {heads}, {dim}] of {dtypes[0]} is needed, got {list(shape)} of {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
+        return t.data_ptr(), (stride[0] if T > 1 else heads * dim)
+    return _rows(t, T, heads * dim, dtypes, dev, name)
+
+
+def moe_rope(r: MoeRotary, positions, T: int, q, k=None, q_out=None, k_out=None, stream=None):
+    """Turns q [T, q_heads, head_dim] and k [T, k_heads, head_dim] by their tokens' positions (int32), into q_out and
+    k_out or in place."""
+    import torch
+    dev, types, D = q.get_device(), _types_of(r.dtype), r.head_dim
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    args = []
+    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            _need(o is None, f"{name}_out without {name}")
+            args += [None, 0, None, 0, 0]
+            continue
+        heads = t.shape[1] if t.dim() == 3 else t.shape[-1] // D
+        p, ld = _heads(t, T, heads, D, types, dev, name)
+        po, ldo = (p, ld) if o is t else _heads(o, T, heads, D, types, dev, name + "_out")
+        args += [p, ld, po, ldo, heads]
+    pp = _flat(positions, T, torch.int32, "positions", dev)
+    table = getattr(r, "table", None)
+    if table is not None and table.get_device() != dev:
+        raise ValueError(f"rope: its frequencies are on {table.device}, the tensors on device {dev}: one GPU is needed")
+    _call("moe_rope", _gpu(q), stream, ctypes.byref(r), *args, pp, T)
+
+
+def linear_attention(qk_heads, v_heads, qk_dim, v_dim, scale=None) -> MoeLinear:
+    """Heads of moe_linear_attention (scale None: qk_dim ** -0.5)."""
+    return MoeLinear(qk_heads, v_heads, qk_dim, v_dim, qk_dim ** -0.5 if scale is None else scale)
+
+
+def linear_attention_workspace(l: MoeLinear, n_seqs: int, T: int, device="cuda"):
+    """Workspace of moe_linear_attention for up to n_seqs sequences of T tokens together, or None where none is needed."""
+    import torch
+    n = _sz(0)
+    _check(lib().moe_linear_workspace_bytes(ctypes.byref(l), n_seqs, T, ctypes.byref(n)), "moe_linear_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+
+
+def _linear_args(l, q, k, v, log_decay, o, T, n_seqs, state_in, slots_in, state_out, slots_out):
+    import torch
+    dev, bits = q.get_device(), _types_of(_BF16_BITS)
+    rows = []
+    for t, heads, dim, name in ((q, l.qk_heads, l.qk_dim, "q"), (k, l.qk_heads, l.qk_dim, "k"), (v, l.v_heads, l.v_dim, "v"),
+                                (o, l.v_heads, l.v_dim, "o")):
+        rows += _heads(t, T, heads, dim, bits, dev, name)
+    if log_decay.dim() == 1:
+        rows[6:6] = [_flat(log_decay, l.v_heads, torch.float32, "log_decay", dev), 0]
+        _need(log_decay.numel() == l.v_heads, "log_decay: [v_heads] or [T, v_heads] is needed")
+    else:
+        rows[6:6] = _rows(log_decay, T, l.v_heads, _types_of(F32), dev, "log_decay")
+    states = []
+    for s, slots, name in ((state_in, slots_in, "in"), (state_out, slots_out, "out")):
+        if s is None:
+            _need(slots is None, f"slots_{name} without state_{name}")
+            states += [None, None, 0]
+            continue
+        if s.dim() != 4 or tuple(s.shape[1:]) != (l.v_heads, l.qk_dim, l.v_dim):
+            raise ValueError(f"state_{name}: [slots, {l.v_heads}, {l.qk_dim}, {l.v_dim}] is needed, got {list(s.shape)}")
+        sp = _flat(s, 0, torch.float32, f"state_{name}", dev)
+        states += [sp, None if slots is None else _flat(slots, n_seqs, torch.int32, f"slots_{name}", dev), s.shape[0]]
+    return dev, rows, states
+
+
+def moe_linear_attention(l: MoeLinear, q, k, v, log_decay, o, cu_seqlens, T: int, state_in=None, slots_in=None,
+                         state_out=None, slots_out=None, ws=None, stream=None):
+    """o = linear attention of the sequences that cu_seqlens [n + 1] (int32) cuts T tokens into; log_decay
+    [T, v_heads] or [v_heads]. Their states start as state_in[slots_in] and end as state_out[slots_out]."""
+    import torch
+    n = cu_seqlens.numel() - 1
+    _need(n >= 0, "cu_seqlens: n + 1 values are needed")
+    dev, rows, states = _linear_args(l, q, k, v, log_decay, o, T, n, state_in, slots_in, state_out, slots_out)
+    cp = _flat(cu_seqlens, n + 1, torch.int32, "cu_seqlens", dev)
+    wp, wn = (None, 0) if ws is None else (_flat(ws, 0, torch.uint8, "ws", dev), ws.numel())
+    _call("moe_linear_attention", _gpu(q), stream, ctypes.byref(l), *rows[:8], cp, n, *states, *rows[8:], T, wp, wn)
+
+
+def moe_linear_attention_step(l: MoeLinear, q, k, v, log_decay, o, T: int, state_in=None, slots_in=None, state_out=None,
+                              slots_out=None, stream=None):
+    """One token of each of T sequences (decode): moe_linear_attention with a token a sequence."""
+    dev, rows, states = _linear_args(l, q, k, v, log_decay, o, T, T, state_in, slots_in, state_out, slots_out)
+    _call("moe_linear_attention_step", _gpu(q), stream, ctypes.byref(l), *rows[:8], *states, *rows[8:], T)
+
+
+def gated_norm(H, dtype=BF16, weight_dtype=None, normalize=True, group=0, eps=1e-6, weight_offset=0.0, gate=GATE_NONE,
+               gate_per_row=False, scale=1.0, next_norm=False, next_eps=1e-6, next_offset=0.0, out8=OUT8_NONE,
+               out8_group=0) -> MoeBlockNorm:
+    """What moe_gated_norm does to rows of H values (dtype: a torch type or BF16 / F16 / F32)."""
+    code = _type_code(dtype)
+    return MoeBlockNorm(H, code, code if weight_dtype is None else _type_code(weight_dtype), int(normalize), group, gate,
+                        int(gate_per_row), int(next_norm), out8, out8_group, eps, weight_offset, scale, next_eps,
+                        next_offset)
+
+
+def moe_gated_norm(n: MoeBlockNorm, x, T: int, weight=None, gate=None, channel_scale=None, residual=None,
+                   next_weight=None, h_out=None, y=None, q=None, scales=None, stream=None):
+    """h = residual + scale channel_scale act(gate) norm(x), y = norm(h) of T rows, and q, scales: that in 8 bits."""
+    H, types, wtypes, dev = n.H, _types_of(n.dtype), _types_of(n.weight_dtype), x.get_device()
+    xp, ldx = _rows(x, T, H, types, dev, "x")
+    gp = rp = hp = yp = qp = sp = None
+    ldg = ldr = ldh = ldy = ldq = 0
+    if gate is not None:
+        if n.gate_per_row and gate.dim() == 1:
+            gate = gate[:, None]
+        gp, ldg = _rows(gate, T, 1 if n.gate_per_row else H, types, dev, "gate")
+    if residual is not None:
+        rp, ldr = _rows(residual, T, H, types, dev, "residual")
+    if h_out is not None:
+        hp, ldh = _rows(h_out, T, H, types, dev, "h_out")
+    if y is not None:
+        yp, ldy = _rows(y, T, H, types, dev, "y")
+    if q is not None:
+        qp, ldq = _rows(q, T, H, _types_of(BITS8 + (n.out8 or OUT8_INT8)), dev, "q")
+    if scales is not None:
+        sp = _flat(scales, T * (H // n.out8_group if n.out8_group else 1), _types_of(F32)[0], "scales", dev)
+    wp = None if weight is None else _flat(weight, n.group or H, wtypes[0], "weight", dev)
+    cp = None if channel_scale is None else _flat(channel_scale, H, wtypes[0], "channel_scale", dev)
+    np_ = None if next_weight is None else _flat(next_weight, H, wtypes[0], "next_weight", dev)
+    _call("moe_gated_norm", _gpu(x), stream, ctypes.byref(n), xp, ldx, wp, gp, ldg, cp, rp, ldr, np_, hp, ldh, yp, ldy, qp,
+          ldq, sp, T)

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmoe_int4.so")
 SOURCES = ["abi.hip", "route.hip", "gemm.hip", "gemm_wide.hip", "decode.hip", "pack.hip", "ceiling.hip",
-           "norm.hip", "gate.hip", "project.hip"]
+           "norm.hip", "gate.hip", "project.hip", "abi_mixer.hip", "project_int8.hip", "rope.hip", "linear.hip",
+           "gated.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

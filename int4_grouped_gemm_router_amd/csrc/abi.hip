@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/moe_int4.h"
+#include "checks.h"
 #include "kernels.h"
 
 using namespace moe;
@@ -126,13 +127,6 @@ size_t route_ws(const moe_dims* d, int T, void* ws, int32_t** chunk_hist) {
   return c.used;
 }
 
-// The kernels move activations, outputs, workspace pieces and packed weights
-// in 16-byte vectors and everything else in 4-byte words; a misaligned
-// pointer is rejected before anything is enqueued (null passes: null checks
-// are separate).
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
 // (token, slot) pair indices are 32-bit in the kernels
 constexpr int64_t kMaxPairs = int64_t(1) << 30;
 bool too_many_pairs(const moe_dims* d, int64_t T) { return T * d->top_k >= kMaxPairs; }
@@ -148,10 +142,6 @@ bool weights_aligned(const moe_layer_weights* w) {
   return al16(w->router_w3) && al16(w->router_w) && al4(w->router_bias) && al16(w->experts_gate_up) &&
          al16(w->experts_down) && al16(w->shared_gate_up) && al16(w->shared_down);
 }
-
-// Row strides of the operators around the layer (elements): in-tile offsets
-// of a few hundred rows stay 32-bit in the kernels.
-constexpr int64_t kMaxRowStride = int64_t(1) << 20;
 
 bool project_dims_ok(int N, int K) {
   return N > 0 && N % 64 == 0 && N <= 65536 && K > 0 && K % 128 == 0 && K <= 16384;
@@ -216,7 +206,6 @@ moe_dims gate_dims(const moe_gate* g) {
   return d;
 }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 // Optional timing hook: records events[i] before the i-th kernel launch and
 // one more after the last launch.

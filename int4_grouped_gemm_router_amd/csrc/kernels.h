@@ -181,6 +181,68 @@ struct ProjectArgs {
 size_t project_ws_bytes(int N, int K, int R, int T);
 hipError_t launch_project(const ProjectArgs& a, hipStream_t s);
 
+// ---- the mixer half of a block
+
+constexpr int kInt8MaxK = 65536, kInt8MaxN = 1 << 18;
+
+struct Int8Args {
+  const int8_t *w, *x;       // [N][K], [T] with row stride ldx
+  const float *w_scales, *x_scales, *bias;  // [N], [T], [N] or null
+  void* y;                   // [T], row stride ldy
+  void* ws;                  // int8_ws_bytes
+  int64_t ldx, ldy;
+  int N, K, T, dtype;
+};
+size_t int8_ws_bytes(int N, int K, int T);
+hipError_t launch_project_int8(const Int8Args& a, hipStream_t s);
+
+struct RopeArgs {
+  const void* x[2];          // queries, keys: [T][heads][D], row stride ldx
+  void* y[2];
+  const int32_t* positions;  // [T]
+  const uint64_t* turns;     // [rot / 2]
+  int64_t ldx[2], ldy[2];
+  int heads[2], copy[2];     // copy: the values behind the turned part go to another buffer
+  int T, D, rot, dtype, interleaved;
+  uint32_t flip;             // sign bit of the sine's factor
+  float magnitude;
+  // set by the launcher
+  uint32_t items, per_token, per_token_magic, units, units_magic;
+  int turn_units;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
+constexpr int kLinearMaxDim = 256;
+
+struct LinearArgs {
+  const uint16_t *q, *k, *v;  // [T][heads][dim], row strides ldq, ldk, ldv
+  const float* decay;         // [v_heads], or [T] with row stride ld_decay
+  const int32_t* cu_seqlens;  // [n_seqs + 1], or null: a token a sequence
+  const float* state_in;      // [n_in][v_heads][qk_dim][v_dim] or null
+  float* state_out;           // [n_out][v_heads][qk_dim][v_dim] or null
+  const int32_t *slots_in, *slots_out;  // [n_seqs], or null: the sequence's index
+  uint16_t* o;                // [T][v_heads][v_dim], row stride ldo
+  void* ws;                   // linear_ws_bytes
+  int64_t ldq, ldk, ldv, ldo, ld_decay;
+  int n_seqs, n_in, n_out, T, qk_heads, v_heads, qk_dim, v_dim;
+  float scale;
+};
+size_t linear_ws_bytes(const LinearArgs& a);
+hipError_t launch_linear_attention(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_step(const LinearArgs& a, hipStream_t s);
+
+constexpr int kGateNone = 0, kGateSilu = 1, kGateSigmoid = 2;
+
+struct GatedArgs {
+  const void *x, *weight, *gate, *channel, *residual, *next_weight;  // all but x: or null
+  void *h_out, *y, *q;
+  float* scales;
+  int64_t ldx, ld_gate, ld_residual, ld_h, ld_y, ld_q;
+  int T, H, dtype, weight_f32, normalize, group, gate_kind, gate_per_row, next, out8, out8_group;
+  float eps, weight_offset, scale, next_eps, next_offset;
+};
+hipError_t launch_gated_norm(const GatedArgs& a, hipStream_t s);
+
 // ev (optional): four events recorded before each of the three launches and after the last.
 // gate (optional): a routing rule in the place of the softmax top-k (its sizes
 // are a's; no events then). Requires k == 8.
