@@ -226,6 +226,9 @@ struct LinearArgs {
   int64_t ldq, ldk, ldv, ldo, ld_decay;
   int n_seqs, n_in, n_out, T, qk_heads, v_heads, qk_dim, v_dim;
   float scale;
+  // set by the launcher: tokens of a window and how many windows; whether the
+  // states that sequences over several windows start from are copied
+  int window, windows, copied;
 };
 size_t linear_ws_bytes(const LinearArgs& a);
 hipError_t launch_linear_attention(const LinearArgs& a, hipStream_t s);

@@ -4,7 +4,10 @@
 //
 // for each value head, whose queries and keys are those of the key head
 // v_head * qk_heads / v_heads. States are fp32 [qk_dim][v_dim].
+#include <algorithm>
+
 #include "kernels.h"
+#include "wide_expand.h"
 
 namespace moe {
 
@@ -95,9 +98,519 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(LinearArgs a) {
   }
 }
 
-size_t linear_ws_bytes(const LinearArgs& /*a*/) { return 0; }
+// ------------------------------------------------------------------ prompts: chunks of 32 tokens
 
 namespace {
+
+constexpr int kChunk = 32;
+constexpr int kNowhere = INT32_MIN;  // a buffer offset past every end: such loads give zeros
+constexpr float kLog2e = 1.44269504f;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// 4 bytes a lane straight to LDS, as bload_lds does 16.
+__device__ inline void bload_lds4(rsrc_t r, void* dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, (int)voff, 0, 0, 0);
+}
+
+// Four values of one column from four rows of LDS: the sixteen lanes of a group
+// read four rows of sixteen values (lane l row l / 4, values 4 (l % 4) ..) and
+// lane l gets column l of the four.
+__device__ inline u32x2 column4(const void* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+// Rows of R 16-byte pieces lie in LDS without gaps, piece c of row r at
+// c ^ swizzle(r): sixteen rows' same piece, and eight rows' same pair of
+// pieces, are then in different banks.
+template <int R>
+__device__ inline int swizzle(int r) {
+  return R >= 16 ? 2 * (r & 7) | (r >> 3 & 1) : 2 * (r >> 1 & 3) | (r >> 3 & 1);
+}
+
+// A tensor's 32 rows as the lanes of a wave copy them to LDS, 64 pieces an
+// instruction; wave w takes every fourth instruction.
+template <int R>
+struct RowCopy {
+  static constexpr int kN = kChunk * R / 256;  // instructions a wave
+  int off[kN];
+  __device__ void init(int wave, int lane, int dim, int64_t ld) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int slot = 64 * (4 * i + wave) + lane, row = slot / R, c = (slot % R) ^ swizzle<R>(row);
+      off[i] = 8 * c < dim ? row * (int)(ld * 2) + 16 * c : kNowhere;
+    }
+  }
+  // base: the first row's values; records: bytes up to the end of the last row's
+  __device__ void issue(u32x4* dst, const uint16_t* base, uint32_t records, int wave) const {
+    const rsrc_t r = make_rsrc(base, records);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) bload_lds(r, dst + 64 * (4 * i + wave), (uint32_t)off[i], 0);
+  }
+};
+
+// A chunk: up to 32 tokens of one sequence.
+struct Item {
+  int t0, count, seq, flags;
+};
+constexpr int kItem = 1;    // there is one
+constexpr int kFirst = 2;   // the first of its sequence in the window: the state is loaded
+constexpr int kMiddle = 4;  // its sequence began in an earlier window
+constexpr int kLast = 8;    // the last of its sequence: the state is kept
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The first of the n sorted values that is not less than v, or n. By all lanes
+// of a wave, 64 at a time.
+__device__ inline int first_at_least(const int32_t* p, int n, int v) {
+  int lo = 0, len = n;  // the answer is in lo .. lo + len
+  const int lane = threadIdx.x & 63;
+  while (len > 0) {
+    const int step = (len + 63) / 64, at = lo + min((lane + 1) * step, len) - 1;
+    const int below = __popcll(__ballot(p[at] < v));  // whole steps below v
+    if (below == 64) return lo + len;
+    lo += min(below * step, len);
+    len = min(step - 1, n - lo);
+  }
+  return lo;
+}
+
+// The chunks of window w, one after the other.
+struct Walk {
+  int w, begin, end, seq, pos, stop, flags;
+  bool last_window, open;
+  __device__ Walk(const LinearArgs& a, int w_) : w(w_) {
+    begin = w * a.window;
+    last_window = w == a.windows - 1;
+    end = min(begin + a.window, a.T);
+    seq = begin > 0 ? max(uniform(first_at_least(a.cu_seqlens, a.n_seqs, begin)) - 1, 0) : 0;
+    open = false;
+    pos = stop = flags = 0;
+  }
+  __device__ Item next(const LinearArgs& a) {
+    while (!open) {
+      if (seq >= a.n_seqs) return Item{0, 0, 0, 0};
+      int b, e;
+      bounds(a, seq, b, e);
+      b = uniform(b);
+      e = uniform(e);
+      if (b >= end && !last_window) return Item{0, 0, 0, 0};
+      ++seq;
+      if (b < begin && e <= begin) continue;  // before the window
+      if (b == e) {
+        // no token: its state only moves, if it does
+        const int si = a.state_in ? uniform(slot_of(a.slots_in, seq - 1, a.n_in)) : -1;
+        const int so = a.state_out ? uniform(slot_of(a.slots_out, seq - 1, a.n_out)) : -1;
+        if (so < 0 || (a.state_in == a.state_out && si == so)) continue;
+        return Item{0, 0, seq - 1, kItem | kFirst | kLast};
+      }
+      open = true;
+      pos = max(b, begin);
+      stop = min(e, end);
+      flags = kItem | kFirst | (b < begin ? kMiddle : 0) | (e <= end ? kLast : 0);
+    }
+    Item it{pos, min(kChunk, stop - pos), seq - 1, flags & ~kLast};
+    pos += it.count;
+    if (pos >= stop) {
+      it.flags |= flags & kLast;
+      open = false;
+    }
+    flags &= ~kFirst;
+    return it;
+  }
+};
+
+// Whether sequence i has tokens from `end` on.
+__device__ inline bool walk_goes_on(const LinearArgs& a, int i, int end) {
+  int b, e;
+  bounds(a, i, b, e);
+  return uniform(e) > end;
+}
+
+// Where windows keep what they pass on (LinearArgs::ws): per window, whether
+// its last sequence goes on behind it, whether that sequence began in it, and
+// which one it is; the sequence's decay over the window for each head; its
+// state: first what the window adds to a state of zeros, then the state at the
+// window's end; and a copy of the state it starts from.
+struct Passed {
+  int32_t* meta;  // [windows][4]
+  float *decay, *state, *start;
+};
+__host__ __device__ inline int64_t state_values(const LinearArgs& a) { return (int64_t)a.v_heads * a.qk_dim * a.v_dim; }
+__host__ __device__ inline Passed passed(const LinearArgs& a) {
+  Passed p;
+  p.meta = static_cast<int32_t*>(a.ws);
+  p.decay = reinterpret_cast<float*>(p.meta) + 4 * (int64_t)a.windows;
+  p.state = p.decay + ((int64_t)a.windows * a.v_heads + 3) / 4 * 4;
+  p.start = p.state + a.windows * state_values(a);
+  return p;
+}
+
+}  // namespace
+
+// Block: one window of tokens, one value head, 64 NT columns of its state, of
+// which each of the four waves holds 16 NT in registers as accumulators of the
+// matrix cores. With G the running sum of g in a chunk, G_n its last,
+//   O = scale (diag(e^G) Q S + (Q K^T .* e^(G_i - G_j), i >= j) V)
+//   S = e^(G_n) S + K^T diag(e^(G_n - G_j)) V
+// O is formed as its transpose. S is a matrix operand as it lies in the
+// accumulators (lane group g holds rows 4 g .. 4 g + 3 of each sixteen), since
+// the products over its rows take the queries in the same order; so are the
+// decayed products of queries and keys, which every wave forms for itself (12
+// of its 80 matrix operations a chunk) so that nothing but the rows goes
+// through LDS. STATE: only S, from zeros, of the sequence that goes on behind
+// the window.
+template <int DK, int NT, int ST, bool STATE>
+__global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
+  constexpr int RQ = DK / 8, RV = 8 * NT, kCols = 64 * NT;
+  __shared__ struct {
+    struct {
+      u32x4 q[STATE ? 1 : kChunk * RQ], k[kChunk * RQ], v[kChunk * RV];
+    } tile[ST];
+    float g[4][64];
+    struct {
+      float G[kChunk], w[kChunk];  // G and w_j = G_n - G_j's power, base 2
+      float total;                 // e^(G_n)
+      float log_total;             // G_n
+    } dec[2];
+  } L;
+  static_assert(ST == 3, "tile c + 2 goes where tile c - 1 was");
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int c16 = lane & 15, g4 = lane >> 4;
+  const int slices = (a.v_dim + kCols - 1) / kCols;
+  // heads that share queries and keys, and slices of a head, follow each other in one XCD
+  const int units = (STATE ? a.windows - 1 : a.windows) * a.v_heads * slices;
+  const int per = (units + 7) / 8, u = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || u >= units) return;
+  const int slice = u % slices, head = u / slices % a.v_heads, w = u / slices / a.v_heads;
+  const int kh = head / (a.v_heads / a.qk_heads), col0 = slice * kCols, cols = min(kCols, a.v_dim - col0);
+  const Passed ps = passed(a);
+
+  Walk walk(a, w);
+  float sum = 0.f;  // of the window's logarithms (STATE)
+  if constexpr (STATE) {
+    // the sequence with tokens on both sides of the window's end
+    int b = 0, e = 0;
+    const int i = max(uniform(first_at_least(a.cu_seqlens, a.n_seqs, walk.end)) - 1, 0);
+    bounds(a, i, b, e);
+    b = uniform(b);
+    e = uniform(e);
+    const bool goes_on = b < walk.end && e > walk.end;
+    if (head == 0 && slice == 0 && tid < 4)
+      ps.meta[4 * w + tid] = tid == 0 ? goes_on : tid == 1 ? b >= walk.begin : tid == 2 ? i : 0;
+    if (!goes_on) return;
+    walk.seq = i;
+  }
+  const uint16_t* qb = a.q + (int64_t)kh * a.qk_dim;
+  const uint16_t* kb = a.k + (int64_t)kh * a.qk_dim;
+  const uint16_t* vb = a.v + (int64_t)head * a.v_dim + col0;
+  RowCopy<RQ> cq, ck;
+  RowCopy<RV> cv;
+  if constexpr (!STATE) cq.init(wave, lane, a.qk_dim, a.ldq);
+  ck.init(wave, lane, a.qk_dim, a.ldk);
+  cv.init(wave, lane, cols, a.ldv);
+  constexpr int kLoads = (STATE ? 1 : 2) * RowCopy<RQ>::kN + RowCopy<RV>::kN;
+
+  auto records = [](const Item& it, int64_t ld, int dim) {
+    return it.count ? (uint32_t)(((it.count - 1) * ld + dim) * 2) : 0u;
+  };
+  // (every item, also one that is not there, issues the same number of loads: the waits count on it)
+  auto load_tile = [&](const Item& it, int st) {
+    const int64_t t = it.t0;
+    if constexpr (!STATE) cq.issue(L.tile[st].q, qb + t * a.ldq, records(it, a.ldq, a.qk_dim), wave);
+    ck.issue(L.tile[st].k, kb + t * a.ldk, records(it, a.ldk, a.qk_dim), wave);
+    cv.issue(L.tile[st].v, vb + t * a.ldv, records(it, a.ldv, cols), wave);
+  };
+  auto load_g = [&](const Item& it, int slot) {
+    if (wave != 0) return;
+    const rsrc_t r = make_rsrc(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
+    bload_lds4(r, L.g[slot], lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
+  };
+  // The chunk's running sums, in base 2 and 64 bits: differences of large sums
+  // keep the precision of small ones. 2^-288 and less is 0 either way.
+  auto decays = [&](int slot, int to) {
+    float g = L.g[slot][lane] * kLog2e;
+    g = g < -288.f ? -288.f : g;
+    // (log2(e) to 64 bits where it matters)
+    double G = g == -288.f ? (double)g : (double)L.g[slot][lane] * 1.4426950408889634;
+#pragma unroll
+    for (int o = 1; o < kChunk; o *= 2) {
+      const double p = __shfl_up(G, o);
+      if ((lane & 31) >= o) G += p;
+    }
+    const double total = __shfl(G, 31);
+    if (lane < kChunk) {
+      L.dec[to].G[lane] = (float)G;
+      L.dec[to].w[lane] = __builtin_amdgcn_exp2f((float)(total - G));
+      if (lane == 0) {
+        L.dec[to].total = __builtin_amdgcn_exp2f((float)total);
+        L.dec[to].log_total = (float)total;
+      }
+    }
+  };
+
+  Item q0 = walk.next(a), q1 = walk.next(a), q2 = walk.next(a), q3;
+  if (!(q0.flags & kItem)) return;
+  load_g(q0, 0);
+  load_g(q1, 1);
+  load_g(q2, 2);
+  load_tile(q0, 0);
+  load_tile(q1, 1);
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  if (wave == 0) decays(0, 0);
+
+  f32x4 S[DK / 16][NT];
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) S[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // where this lane's part of a state is: rows 16 i + 4 g4 + r, column col + 16 n
+  const int col = col0 + (wave * NT) * 16 + c16;
+  auto each_of_state = [&](auto f) {
+    // (hidden from the optimiser, which otherwise keeps every element's place in registers over the loop)
+    int row0 = 4 * g4, step = a.v_dim;
+    asm volatile("" : "+v"(row0), "+s"(step));
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + row0 + r < a.qk_dim && col + 16 * n < a.v_dim)
+            S[i][n][r] = f(S[i][n][r], (16 * i + row0 + r) * step + col + 16 * n);
+  };
+  const int64_t head_state = (int64_t)a.qk_dim * a.v_dim;
+
+  u32x2 out[2][NT];
+  Item written{0, 0, 0, 0};
+  auto store_out = [&] {
+    if constexpr (STATE) return;
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+      if (16 * it + c16 < written.count) {
+        uint16_t* p = a.o + (int64_t)(written.t0 + 16 * it + c16) * a.ldo + (int64_t)head * a.v_dim;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int c = col0 + (wave * NT + n) * 16 + 4 * g4;
+          if (c < a.v_dim) *reinterpret_cast<u32x2*>(p + c) = out[it][n];
+        }
+      }
+  };
+
+  int st = 0;
+  for (int c = 0;; ++c) {
+    // Tile c and its decays are in LDS and no wave reads tile c - 1 any more.
+    // (The newest loads, tile c + 1's, may be under way: a turn issues a tile's
+    // loads after all its other memory operations.)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    store_out();
+    if (!STATE && (q0.flags & kFirst)) {
+      const float* from = nullptr;
+      if (q0.flags & kMiddle) {
+        from = ps.state + (w - 1) * state_values(a);
+      } else {
+        const int si = a.state_in ? uniform(slot_of(a.slots_in, q0.seq, a.n_in)) : -1;
+        // (the copy, where a later window's block may have written the state by now)
+        if (si >= 0) from = a.copied && walk_goes_on(a, q0.seq, walk.end) ? ps.start + w * state_values(a) : a.state_in + si * state_values(a);
+      }
+      if (from)
+        each_of_state([&](float, int at) { return from[head * head_state + at]; });
+      else
+        each_of_state([](float, int) { return 0.f; });
+    }
+    q3 = walk.next(a);
+    load_g(q3, (c + 3) & 3);
+    load_tile(q2, st == 0 ? 2 : st - 1);
+    if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1);
+
+    const auto& T = L.tile[st];
+    const auto& D = L.dec[c & 1];
+    // values and their weights: lane's column, tokens 4 g4 + r and 16 + 4 g4 + r
+    const int vrow = 4 * g4 + (c16 >> 2);
+    u32x4 vf[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int piece = (2 * (wave * NT + n) + (c16 >> 1 & 1)) ^ swizzle<RV>(vrow);
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.v[vrow * RV + piece]) + 8 * (c16 & 1);
+      const u32x2 lo = column4(p), hi = column4(p + 16 * RV * 16);
+      vf[n] = u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
+    if constexpr (!STATE) {
+      // queries, and their products with the keys: rows (keys) x columns (queries)
+      u32x4 qf[2][DK / 32];
+      f32x4 p00{0.f, 0.f, 0.f, 0.f}, p01 = p00, p11 = p00;
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        const int piece = (4 * s + (g4 >> 1)) ^ swizzle<RQ>(c16);
+        const int at0 = (c16 * RQ + piece) * 16 + 8 * (g4 & 1), at1 = at0 ^ 32;
+        u32x4 kf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* tq = reinterpret_cast<const uint8_t*>(T.q) + h * (16 * RQ * 16);
+          const uint8_t* tk = reinterpret_cast<const uint8_t*>(T.k) + h * (16 * RQ * 16);
+          const u32x2 x = *reinterpret_cast<const u32x2*>(tq + at0), y = *reinterpret_cast<const u32x2*>(tq + at1);
+          qf[h][s] = u32x4{x.x, x.y, y.x, y.y};
+          const u32x2 z = *reinterpret_cast<const u32x2*>(tk + at0), t = *reinterpret_cast<const u32x2*>(tk + at1);
+          kf[h] = u32x4{z.x, z.y, t.x, t.y};
+        }
+        p00 = mfma16(kf[0], qf[0][s], p00);
+        p01 = mfma16(kf[0], qf[1][s], p01);
+        p11 = mfma16(kf[1], qf[1][s], p11);
+      }
+      // the state's part of the output, before this chunk enters the state
+      f32x4 oa[2][NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) oa[0][n] = oa[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const f32x4 x = S[2 * s][n], y = S[2 * s + 1][n];
+          const u32x4 sb = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+          oa[0][n] = mfma16(sb, qf[0][s], oa[0][n]);
+          oa[1][n] = mfma16(sb, qf[1][s], oa[1][n]);
+        }
+      const float Gi0 = D.G[c16], Gi1 = D.G[16 + c16];
+      const f32x4 Gj0 = *reinterpret_cast<const f32x4*>(&D.G[4 * g4]), Gj1 = *reinterpret_cast<const f32x4*>(&D.G[16 + 4 * g4]);
+      float w00[4], w01[4], w11[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        w00[r] = 4 * g4 + r <= c16 ? p00[r] * __builtin_amdgcn_exp2f(Gi0 - Gj0[r]) : 0.f;
+        w01[r] = p01[r] * __builtin_amdgcn_exp2f(Gi1 - Gj0[r]);
+        w11[r] = 4 * g4 + r <= c16 ? p11[r] * __builtin_amdgcn_exp2f(Gi1 - Gj1[r]) : 0.f;
+      }
+      const u32x4 pa0 = {pack_bf16x2(w00[0], w00[1]), pack_bf16x2(w00[2], w00[3]), 0u, 0u};
+      const u32x4 pa1 = {pack_bf16x2(w01[0], w01[1]), pack_bf16x2(w01[2], w01[3]), pack_bf16x2(w11[0], w11[1]),
+                         pack_bf16x2(w11[2], w11[3])};
+      const float e0 = __builtin_amdgcn_exp2f(Gi0), e1 = __builtin_amdgcn_exp2f(Gi1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        oa[0][n] = mfma16(vf[n], pa0, oa[0][n] * e0);
+        oa[1][n] = mfma16(vf[n], pa1, oa[1][n] * e1);
+#pragma unroll
+        for (int it = 0; it < 2; ++it)
+          out[it][n] = u32x2{pack_bf16x2(a.scale * oa[it][n][0], a.scale * oa[it][n][1]),
+                             pack_bf16x2(a.scale * oa[it][n][2], a.scale * oa[it][n][3])};
+      }
+      written = q0;
+    }
+    // the chunk enters the state: the decayed values in three bf16 parts, which
+    // hold all 24 bits of them
+    u32x4 part[NT][3];
+    {
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[4 * g4]), w1 = *reinterpret_cast<const f32x4*>(&D.w[16 + 4 * g4]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const f32x4 ww = p < 2 ? w0 : w1;
+          float x[2] = {bf16lo(vf[n][p]) * ww[2 * (p & 1)], bf16hi(vf[n][p]) * ww[2 * (p & 1) + 1]};
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            part[n][k][p] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302);
+#pragma unroll
+            for (int e = 0; e < 2 && k < 2; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xFFFF0000u);
+          }
+        }
+    }
+    const float total = D.total;
+    if constexpr (STATE) sum += D.log_total;
+    const int krow = 4 * g4 + (c16 >> 2);
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) {
+      const int piece = (2 * i + (c16 >> 1 & 1)) ^ swizzle<RQ>(krow);
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.k[krow * RQ + piece]) + 8 * (c16 & 1);
+      const u32x2 lo = column4(p), hi = column4(p + 16 * RQ * 16);
+      const u32x4 kt = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * total;
+#pragma unroll
+      for (int k = 2; k >= 0; --k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[i][n] = mfma16(kt, part[n][k], S[i][n]);
+    }
+    if (!STATE && (q0.flags & kLast)) {
+      const int so = a.state_out ? uniform(slot_of(a.slots_out, q0.seq, a.n_out)) : -1;
+      if (so >= 0) {
+        float* to = a.state_out + so * state_values(a) + head * head_state;
+        each_of_state([&](float s, int at) { return to[at] = s; });
+      }
+    }
+    if (!(q1.flags & kItem)) break;
+    q0 = q1;
+    q1 = q2;
+    q2 = q3;
+    st = st == 2 ? 0 : st + 1;
+  }
+  // (the copies into LDS that are under way end before the block does)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  store_out();
+  if constexpr (STATE) {
+    float* to = ps.state + w * state_values(a) + head * head_state;
+    each_of_state([&](float s, int at) { return to[at] = s; });
+    if (slice == 0 && tid == 0) ps.decay[w * a.v_heads + head] = __builtin_amdgcn_exp2f(sum);
+  }
+}
+
+// What windows pass on: S at the end of each, from what each adds. Thread: four
+// values of one head's state, window after window.
+__global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
+  const Passed ps = passed(a);
+  const int head = blockIdx.y;
+  const int64_t head_state = (int64_t)a.qk_dim * a.v_dim, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= head_state) return;
+  const int64_t stride = state_values(a), off = head * head_state + at;
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = 8;
+  for (int w0 = 0; w0 < a.windows - 1; w0 += kAhead) {
+    f32x4 add[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      add[j] = *reinterpret_cast<const f32x4*>(ps.state + min(w0 + j, a.windows - 2) * stride + off);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int w = w0 + j;
+      if (w >= a.windows - 1 || !ps.meta[4 * w]) continue;
+      if (ps.meta[4 * w + 1]) {
+        const int si = a.state_in ? slot_of(a.slots_in, ps.meta[4 * w + 2], a.n_in) : -1;
+        S = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (si >= 0) S = *reinterpret_cast<const f32x4*>(a.state_in + si * stride + off);
+        if (a.copied) *reinterpret_cast<f32x4*>(ps.start + w * stride + off) = S;
+      }
+      S = S * ps.decay[w * a.v_heads + head] + add[j];
+      *reinterpret_cast<f32x4*>(ps.state + w * stride + off) = S;
+    }
+  }
+}
+
+namespace {
+
+constexpr int kMinWindow = 64;
+
+int chunk_cols(const LinearArgs& a) { return a.qk_dim > 128 || a.v_dim <= 64 ? 64 : 128; }
+// Windows for up to T tokens: enough for two blocks on each compute unit.
+int most_windows(const LinearArgs& a) {
+  const int per = a.v_heads * ((a.v_dim + chunk_cols(a) - 1) / chunk_cols(a));
+  const int64_t by_blocks = std::max(1, 512 / per), by_tokens = ((int64_t)a.T + kMinWindow - 1) / kMinWindow;
+  return (int)std::max<int64_t>(1, std::min(by_blocks, by_tokens));
+}
+void set_windows(LinearArgs& a) {
+  const int most = most_windows(a);
+  a.window = (int)std::max<int64_t>(kMinWindow, ((int64_t)a.T + most - 1) / most + (kChunk - 1)) / kChunk * kChunk;
+  a.windows = std::max(1, (a.T + a.window - 1) / a.window);
+}
+
+template <int DK, int NT>
+hipError_t launch_chunks(const LinearArgs& a, hipStream_t s) {
+  const int slices = (a.v_dim + 64 * NT - 1) / (64 * NT), per = a.v_heads * slices;
+  const auto grid = [](int units) { return dim3((units + 7) / 8 * 8); };
+  if (a.windows > 1) {
+    hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, true>), grid((a.windows - 1) * per), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(linear_pass_kernel, dim3((a.qk_dim * a.v_dim + 1023) / 1024, a.v_heads), dim3(256), 0, s, a);
+  }
+  hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, false>), grid(a.windows * per), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
 
 hipError_t launch_walk(const LinearArgs& a, hipStream_t s) {
   const dim3 grid(a.n_seqs, a.v_heads, (a.v_dim + kStepCols - 1) / kStepCols), block(256);
@@ -112,7 +625,23 @@ hipError_t launch_walk(const LinearArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_linear_attention(const LinearArgs& a, hipStream_t s) { return launch_walk(a, s); }
+size_t linear_ws_bytes(const LinearArgs& a) {
+  const int64_t n = most_windows(a);
+  if (n <= 1) return 0;
+  return (size_t)(n * (16 + 4 * (int64_t)a.v_heads + 8 * state_values(a)) + 16);
+}
+
+hipError_t launch_linear_attention(const LinearArgs& in, hipStream_t s) {
+  LinearArgs a = in;
+  set_windows(a);
+  // states written where others are read: sequences that go over several windows start from a copy
+  const uintptr_t ib = reinterpret_cast<uintptr_t>(a.state_in), ob = reinterpret_cast<uintptr_t>(a.state_out);
+  const uintptr_t bytes = 4 * (uintptr_t)state_values(a);
+  a.copied = a.windows > 1 && a.state_in && a.state_out && ib < ob + a.n_out * bytes && ob < ib + a.n_in * bytes;
+  if (a.qk_dim > 128) return launch_chunks<256, 1>(a, s);
+  if (a.v_dim <= 64) return a.qk_dim <= 64 ? launch_chunks<64, 1>(a, s) : launch_chunks<128, 1>(a, s);
+  return a.qk_dim <= 64 ? launch_chunks<64, 2>(a, s) : launch_chunks<128, 2>(a, s);
+}
 hipError_t launch_linear_step(const LinearArgs& a, hipStream_t s) { return launch_walk(a, s); }
 
 }  // namespace moe
