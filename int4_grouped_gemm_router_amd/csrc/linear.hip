@@ -108,9 +108,21 @@ constexpr float kLog2e = 1.44269504f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// 4 bytes a lane straight to LDS, as bload_lds does 16.
-__device__ inline void bload_lds4(rsrc_t r, void* dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, (int)voff, 0, 0, 0);
+// 16 or 4 bytes a lane straight to LDS (from dst on, lane after lane), as
+// assembly: before a transposing read of LDS the compiler waits for every copy
+// it knows of, also those into other tiles. The kernel's own waits count them.
+__device__ inline u32x4 words_of(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+__device__ inline uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ inline void copy16_to_lds(u32x4 r, uint32_t dst, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(voff), "s"(r) : "m0", "memory");
+}
+__device__ inline void copy4_to_lds(u32x4 r, uint32_t dst, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(dst), "v"(voff), "s"(r) : "m0", "memory");
 }
 
 // Four values of one column from four rows of LDS: the sixteen lanes of a group
@@ -143,9 +155,10 @@ struct RowCopy {
   }
   // base: the first row's values; records: bytes up to the end of the last row's
   __device__ void issue(u32x4* dst, const uint16_t* base, uint32_t records, int wave) const {
-    const rsrc_t r = make_rsrc(base, records);
+    const u32x4 r = words_of(base, records);
+    const uint32_t to = lds_offset(dst) + 1024 * wave;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) bload_lds(r, dst + 64 * (4 * i + wave), (uint32_t)off[i], 0);
+    for (int i = 0; i < kN; ++i) copy16_to_lds(r, to + 4096 * i, (uint32_t)off[i]);
   }
 };
 
@@ -158,7 +171,23 @@ constexpr int kFirst = 2;   // the first of its sequence in the window: the stat
 constexpr int kMiddle = 4;  // its sequence began in an earlier window
 constexpr int kLast = 8;    // the last of its sequence: the state is kept
 
+// v from another lane, as dpp, in the rows of sixteen that ROWS names; 0 elsewhere.
+template <int CTRL, int ROWS>
+__device__ inline double dpp64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// A state is kept as f times what the registers hold, so that a chunk's decay
+// mostly costs one product instead of one per element: f takes the decays until
+// it is far from 1, then the elements take it over.
+__device__ inline bool keeps(float f) { return f >= 0x1p-20f && f <= 0x1p20f; }
+__device__ inline float factor_after(float f, float decay) { return keeps(f * decay) ? f * decay : 1.f; }
+
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline float uniform_f(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(int, v))); }
 
 // The first of the n sorted values that is not less than v, or n. By all lanes
 // of a wave, 64 at a time.
@@ -229,7 +258,7 @@ __device__ inline bool walk_goes_on(const LinearArgs& a, int i, int end) {
 
 // Where windows keep what they pass on (LinearArgs::ws): per window, whether
 // its last sequence goes on behind it, whether that sequence began in it, and
-// which one it is; the sequence's decay over the window for each head; its
+// the slot of the state it began with; the sequence's decay over the window for each head; its
 // state: first what the window adds to a state of zeros, then the state at the
 // window's end; and a copy of the state it starts from.
 struct Passed {
@@ -254,8 +283,9 @@ __host__ __device__ inline Passed passed(const LinearArgs& a) {
 //   O = scale (diag(e^G) Q S + (Q K^T .* e^(G_i - G_j), i >= j) V)
 //   S = e^(G_n) S + K^T diag(e^(G_n - G_j)) V
 // O is formed as its transpose. S is a matrix operand as it lies in the
-// accumulators (lane group g holds rows 4 g .. 4 g + 3 of each sixteen), since
-// the products over its rows take the queries in the same order; so are the
+// accumulators: of each 32 rows lane group g holds rows 8 g .. 8 g + 7, the ones
+// that a matrix operand wants of it, because the keys enter the update with
+// their columns in that order. So are the
 // decayed products of queries and keys, which every wave forms for itself (12
 // of its 80 matrix operations a chunk) so that nothing but the rows goes
 // through LDS. STATE: only S, from zeros, of the sequence that goes on behind
@@ -269,9 +299,9 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     } tile[ST];
     float g[4][64];
     struct {
-      float G[kChunk], w[kChunk];  // G and w_j = G_n - G_j's power, base 2
-      float total;                 // e^(G_n)
-      float log_total;             // G_n
+      float G[kChunk], Gs[kChunk];  // G in base 2, and with log2 |scale| added
+      float w[kChunk];              // e^(G_n - G_j) / the state's factor after the chunk
+      float total, log_total;       // e^(G_n), G_n in base 2
     } dec[2];
   } L;
   static_assert(ST == 3, "tile c + 2 goes where tile c - 1 was");
@@ -296,8 +326,12 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     b = uniform(b);
     e = uniform(e);
     const bool goes_on = b < walk.end && e > walk.end;
-    if (head == 0 && slice == 0 && tid < 4)
-      ps.meta[4 * w + tid] = tid == 0 ? goes_on : tid == 1 ? b >= walk.begin : tid == 2 ? i : 0;
+    if (head == 0 && slice == 0 && tid == 0) {
+      const int si = a.state_in ? slot_of(a.slots_in, i, a.n_in) : -1;
+      ps.meta[4 * w] = goes_on;
+      ps.meta[4 * w + 1] = b >= walk.begin;
+      ps.meta[4 * w + 2] = si;
+    }
     if (!goes_on) return;
     walk.seq = i;
   }
@@ -323,27 +357,31 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   };
   auto load_g = [&](const Item& it, int slot) {
     if (wave != 0) return;
-    const rsrc_t r = make_rsrc(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
-    bload_lds4(r, L.g[slot], lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
+    const u32x4 r = words_of(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
+    copy4_to_lds(r, lds_offset(L.g[slot]), lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
   };
   // The chunk's running sums, in base 2 and 64 bits: differences of large sums
   // keep the precision of small ones. 2^-288 and less is 0 either way.
-  auto decays = [&](int slot, int to) {
-    float g = L.g[slot][lane] * kLog2e;
-    g = g < -288.f ? -288.f : g;
-    // (log2(e) to 64 bits where it matters)
-    double G = g == -288.f ? (double)g : (double)L.g[slot][lane] * 1.4426950408889634;
-#pragma unroll
-    for (int o = 1; o < kChunk; o *= 2) {
-      const double p = __shfl_up(G, o);
-      if ((lane & 31) >= o) G += p;
-    }
-    const double total = __shfl(G, 31);
+  const float log_scale = __log2f(fabsf(a.scale));
+  const uint32_t sign = __float_as_uint(a.scale) & 0x80000000u;
+  auto decays = [&](int slot, int to, float f) {
+    const float g = L.g[slot][lane];
+    double G = g * kLog2e < -288.f ? -288.0 : (double)g * 1.4426950408889634;
+    G += dpp64<0x111, 0xF>(G);  // the lane before, two, four, eight before in rows of sixteen
+    G += dpp64<0x112, 0xF>(G);
+    G += dpp64<0x114, 0xF>(G);
+    G += dpp64<0x118, 0xF>(G);
+    G += dpp64<0x142, 0xA>(G);  // the first row's last, to the second
+    const uint64_t last = __builtin_bit_cast(uint64_t, G);
+    const double total = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 31) << 32 |
+                                                        (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 31));
+    const float e = __builtin_amdgcn_exp2f((float)total);
     if (lane < kChunk) {
       L.dec[to].G[lane] = (float)G;
-      L.dec[to].w[lane] = __builtin_amdgcn_exp2f((float)(total - G));
+      L.dec[to].Gs[lane] = (float)(G + log_scale);
+      L.dec[to].w[lane] = __builtin_amdgcn_exp2f((float)(total - G)) * (1.0f / factor_after(f, e));
       if (lane == 0) {
-        L.dec[to].total = __builtin_amdgcn_exp2f((float)total);
+        L.dec[to].total = e;
         L.dec[to].log_total = (float)total;
       }
     }
@@ -357,27 +395,41 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   load_tile(q0, 0);
   load_tile(q1, 1);
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (wave == 0) decays(0, 0);
+  if (wave == 0) decays(0, 0, 1.f);
 
   f32x4 S[DK / 16][NT];
 #pragma unroll
   for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n) S[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // where this lane's part of a state is: rows 16 i + 4 g4 + r, column col + 16 n
+  // where this lane's part of a state is: rows 32 (i / 2) + 8 g4 + 4 (i % 2) + r, column col + 16 n
   const int col = col0 + (wave * NT) * 16 + c16;
+  // (by buffer accesses: rows past the state are past its end, columns are sent
+  // there; loads give zeros and stores are dropped, without a branch between)
+  const uint32_t head_bytes = (uint32_t)(a.qk_dim * a.v_dim * 4);
   auto each_of_state = [&](auto f) {
     // (hidden from the optimiser, which otherwise keeps every element's place in registers over the loop)
-    int row0 = 4 * g4, step = a.v_dim;
+    int row0 = 8 * g4, step = a.v_dim * 4;
     asm volatile("" : "+v"(row0), "+s"(step));
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t at = col + 16 * n < a.v_dim ? (uint32_t)(row0 * step + (col + 16 * n) * 4) : (uint32_t)kNowhere;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * i + row0 + r < a.qk_dim && col + 16 * n < a.v_dim)
-            S[i][n][r] = f(S[i][n][r], (16 * i + row0 + r) * step + col + 16 * n);
+        for (int r = 0; r < 4; ++r) S[i][n][r] = f(S[i][n][r], at + (uint32_t)((32 * (i >> 1) + 4 * (i & 1) + r) * step));
+    }
+  };
+  auto load_state = [&](const float* p) {
+    const rsrc_t r = make_rsrc(p, head_bytes);
+    each_of_state([&](float, uint32_t at) { return __uint_as_float(bload1(r, at, 0)); });
+  };
+  auto store_state = [&](float* p, float f) {
+    const rsrc_t r = make_rsrc(p, head_bytes);
+    each_of_state([&](float s, uint32_t at) {
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s * f), r, (int)at, 0, 0);
+      return s;
+    });
   };
   const int64_t head_state = (int64_t)a.qk_dim * a.v_dim;
 
@@ -398,6 +450,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   };
 
   int st = 0;
+  float f = 1.f;
   for (int c = 0;; ++c) {
     // Tile c and its decays are in LDS and no wave reads tile c - 1 any more.
     // (The newest loads, tile c + 1's, may be under way: a turn issues a tile's
@@ -405,6 +458,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
     store_out();
     if (!STATE && (q0.flags & kFirst)) {
+      f = 1.f;
       const float* from = nullptr;
       if (q0.flags & kMiddle) {
         from = ps.state + (w - 1) * state_values(a);
@@ -414,17 +468,21 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
         if (si >= 0) from = a.copied && walk_goes_on(a, q0.seq, walk.end) ? ps.start + w * state_values(a) : a.state_in + si * state_values(a);
       }
       if (from)
-        each_of_state([&](float, int at) { return from[head * head_state + at]; });
+        load_state(from + head * head_state);
       else
-        each_of_state([](float, int) { return 0.f; });
+        each_of_state([](float, uint32_t) { return 0.f; });
+      // (a wait the compiler sees: it has none to add in every turn, which would be for the tiles too)
+      __builtin_amdgcn_s_waitcnt(0);
     }
     q3 = walk.next(a);
     load_g(q3, (c + 3) & 3);
     load_tile(q2, st == 0 ? 2 : st - 1);
-    if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1);
-
     const auto& T = L.tile[st];
     const auto& D = L.dec[c & 1];
+    const float f_before = f, decayed = f * uniform_f(D.total);
+    f = keeps(decayed) ? decayed : 1.f;
+    if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1, !STATE && (q1.flags & kFirst) ? 1.f : f);
+
     // values and their weights: lane's column, tokens 4 g4 + r and 16 + 4 g4 + r
     const int vrow = 4 * g4 + (c16 >> 2);
     u32x4 vf[NT];
@@ -441,17 +499,12 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       f32x4 p00{0.f, 0.f, 0.f, 0.f}, p01 = p00, p11 = p00;
 #pragma unroll
       for (int s = 0; s < DK / 32; ++s) {
-        const int piece = (4 * s + (g4 >> 1)) ^ swizzle<RQ>(c16);
-        const int at0 = (c16 * RQ + piece) * 16 + 8 * (g4 & 1), at1 = at0 ^ 32;
+        const int at = c16 * RQ + ((4 * s + g4) ^ swizzle<RQ>(c16));
         u32x4 kf[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* tq = reinterpret_cast<const uint8_t*>(T.q) + h * (16 * RQ * 16);
-          const uint8_t* tk = reinterpret_cast<const uint8_t*>(T.k) + h * (16 * RQ * 16);
-          const u32x2 x = *reinterpret_cast<const u32x2*>(tq + at0), y = *reinterpret_cast<const u32x2*>(tq + at1);
-          qf[h][s] = u32x4{x.x, x.y, y.x, y.y};
-          const u32x2 z = *reinterpret_cast<const u32x2*>(tk + at0), t = *reinterpret_cast<const u32x2*>(tk + at1);
-          kf[h] = u32x4{z.x, z.y, t.x, t.y};
+          qf[h][s] = T.q[at + h * (16 * RQ)];
+          kf[h] = T.k[at + h * (16 * RQ)];
         }
         p00 = mfma16(kf[0], qf[0][s], p00);
         p01 = mfma16(kf[0], qf[1][s], p01);
@@ -470,7 +523,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           oa[0][n] = mfma16(sb, qf[0][s], oa[0][n]);
           oa[1][n] = mfma16(sb, qf[1][s], oa[1][n]);
         }
-      const float Gi0 = D.G[c16], Gi1 = D.G[16 + c16];
+      const float Gi0 = D.Gs[c16], Gi1 = D.Gs[16 + c16];
       const f32x4 Gj0 = *reinterpret_cast<const f32x4*>(&D.G[4 * g4]), Gj1 = *reinterpret_cast<const f32x4*>(&D.G[16 + 4 * g4]);
       float w00[4], w01[4], w11[4];
 #pragma unroll
@@ -479,18 +532,20 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
         w01[r] = p01[r] * __builtin_amdgcn_exp2f(Gi1 - Gj0[r]);
         w11[r] = 4 * g4 + r <= c16 ? p11[r] * __builtin_amdgcn_exp2f(Gi1 - Gj1[r]) : 0.f;
       }
-      const u32x4 pa0 = {pack_bf16x2(w00[0], w00[1]), pack_bf16x2(w00[2], w00[3]), 0u, 0u};
-      const u32x4 pa1 = {pack_bf16x2(w01[0], w01[1]), pack_bf16x2(w01[2], w01[3]), pack_bf16x2(w11[0], w11[1]),
-                         pack_bf16x2(w11[2], w11[3])};
-      const float e0 = __builtin_amdgcn_exp2f(Gi0), e1 = __builtin_amdgcn_exp2f(Gi1);
+      // (the scale's sign, in both halves)
+      const uint32_t flip = sign | sign >> 16;
+      const u32x4 pa0 = {pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
+      const u32x4 pa1 = {pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
+                         pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
+      const float fs = __uint_as_float(__float_as_uint(f_before) ^ sign);
+      const float e0 = __builtin_amdgcn_exp2f(Gi0) * fs, e1 = __builtin_amdgcn_exp2f(Gi1) * fs;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         oa[0][n] = mfma16(vf[n], pa0, oa[0][n] * e0);
         oa[1][n] = mfma16(vf[n], pa1, oa[1][n] * e1);
 #pragma unroll
         for (int it = 0; it < 2; ++it)
-          out[it][n] = u32x2{pack_bf16x2(a.scale * oa[it][n][0], a.scale * oa[it][n][1]),
-                             pack_bf16x2(a.scale * oa[it][n][2], a.scale * oa[it][n][3])};
+          out[it][n] = u32x2{pack_bf16x2(oa[it][n][0], oa[it][n][1]), pack_bf16x2(oa[it][n][2], oa[it][n][3])};
       }
       written = q0;
     }
@@ -513,28 +568,35 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           }
         }
     }
-    const float total = D.total;
     if constexpr (STATE) sum += D.log_total;
+    if (!keeps(decayed)) {
+      asm volatile("");  // (keeps the products in the branch)
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * decayed;
+    }
     const int krow = 4 * g4 + (c16 >> 2);
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-      const int piece = (2 * i + (c16 >> 1 & 1)) ^ swizzle<RQ>(krow);
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.k[krow * RQ + piece]) + 8 * (c16 & 1);
-      const u32x2 lo = column4(p), hi = column4(p + 16 * RQ * 16);
-      const u32x4 kt = {lo.x, lo.y, hi.x, hi.y};
+    for (int s = 0; s < DK / 32; ++s) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.k[krow * RQ + ((4 * s + (c16 & 3)) ^ swizzle<RQ>(krow))]);
+      u32x4 kt[2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * total;
+      for (int e = 0; e < 2; ++e) {
+        const u32x2 lo = column4(p + 8 * e), hi = column4(p + 8 * e + 16 * RQ * 16);
+        kt[e] = u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
+      // (the small parts first)
 #pragma unroll
       for (int k = 2; k >= 0; --k)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) S[i][n] = mfma16(kt, part[n][k], S[i][n]);
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) S[2 * s + e][n] = mfma16(kt[e], part[n][k], S[2 * s + e][n]);
     }
     if (!STATE && (q0.flags & kLast)) {
       const int so = a.state_out ? uniform(slot_of(a.slots_out, q0.seq, a.n_out)) : -1;
-      if (so >= 0) {
-        float* to = a.state_out + so * state_values(a) + head * head_state;
-        each_of_state([&](float s, int at) { return to[at] = s; });
-      }
+      if (so >= 0) store_state(a.state_out + so * state_values(a) + head * head_state, f);
     }
     if (!(q1.flags & kItem)) break;
     q0 = q1;
@@ -546,8 +608,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   store_out();
   if constexpr (STATE) {
-    float* to = ps.state + w * state_values(a) + head * head_state;
-    each_of_state([&](float s, int at) { return to[at] = s; });
+    store_state(ps.state + w * state_values(a) + head * head_state, f);
     if (slice == 0 && tid == 0) ps.decay[w * a.v_heads + head] = __builtin_amdgcn_exp2f(sum);
   }
 }
@@ -563,21 +624,29 @@ __global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   constexpr int kAhead = 8;
   for (int w0 = 0; w0 < a.windows - 1; w0 += kAhead) {
-    f32x4 add[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      add[j] = *reinterpret_cast<const f32x4*>(ps.state + min(w0 + j, a.windows - 2) * stride + off);
+    f32x4 add[kAhead], start[kAhead];
+    int on[kAhead], begins[kAhead];
+    float decay[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int w = w0 + j;
-      if (w >= a.windows - 1 || !ps.meta[4 * w]) continue;
-      if (ps.meta[4 * w + 1]) {
-        const int si = a.state_in ? slot_of(a.slots_in, ps.meta[4 * w + 2], a.n_in) : -1;
-        S = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (si >= 0) S = *reinterpret_cast<const f32x4*>(a.state_in + si * stride + off);
+      const int w = min(w0 + j, a.windows - 2);
+      add[j] = *reinterpret_cast<const f32x4*>(ps.state + w * stride + off);
+      on[j] = uniform(w0 + j < a.windows - 1 ? ps.meta[4 * w] : 0);
+      begins[j] = uniform(ps.meta[4 * w + 1]);
+      decay[j] = ps.decay[w * a.v_heads + head];
+      const int si = uniform(ps.meta[4 * w + 2]);
+      start[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (on[j] && begins[j] && si >= 0) start[j] = *reinterpret_cast<const f32x4*>(a.state_in + si * stride + off);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!on[j]) continue;
+      const int64_t w = w0 + j;
+      if (begins[j]) {
+        S = start[j];
         if (a.copied) *reinterpret_cast<f32x4*>(ps.start + w * stride + off) = S;
       }
-      S = S * ps.decay[w * a.v_heads + head] + add[j];
+      S = S * decay[j] + add[j];
       *reinterpret_cast<f32x4*>(ps.state + w * stride + off) = S;
     }
   }
