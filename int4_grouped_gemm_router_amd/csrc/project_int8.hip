@@ -7,7 +7,9 @@
 // matrix operation takes of an operand; a wave copies it from the rows straight
 // to LDS, four lanes a row (sixteen lanes that each read another row cost the
 // address unit four times as long), and reads it back in the matrix cores'
-// order. Two kernels:
+// order. Three kernels:
+//   int8_vector_kernel one to four tokens: whole rows of weights straight to
+//                      registers, dot products of four in the vector units
 //   int8_split_kernel  a block's eight waves split K and join through LDS:
 //                      few rows, where bytes and latency count
 //   int8_tile_kernel   256 x 256 tiles, both operands shared through a ring of
@@ -17,6 +19,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "topk.h"
 #include "wide_expand.h"
 
 namespace moe {
@@ -76,6 +79,89 @@ __device__ inline void put_eight(const Int8Args& a, int64_t at, const float (&v)
 
 }  // namespace
 
+// One to four tokens. Wave (r, p) of a block takes kRows outputs and the p-th
+// of KS parts of K, in pieces of 16 inputs a lane: whole KBs of a row at a
+// time, the next turn's pieces under way while this one's are multiplied, four
+// at a time, in the vector units. The lanes' sums are joined by DPP, the parts'
+// in LDS.
+constexpr int kVecRows = 4;
+
+template <int T, int KS>
+__global__ __launch_bounds__(kIThreads) void int8_vector_kernel(Int8Args a) {
+  constexpr int kGroups = kIWaves / KS;  // row groups of a block
+  __shared__ int red[kIWaves][kVecRows][T];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = wave % KS, n0 = ((int)blockIdx.x * kGroups + wave / KS) * kVecRows;
+  // this part's pieces: from p0 on, n of them
+  const int pieces = a.K / 16, p0 = (int)((int64_t)pieces * part / KS), n = (int)((int64_t)pieces * (part + 1) / KS) - p0;
+  const u32x4* w[kVecRows];
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r) w[r] = reinterpret_cast<const u32x4*>(a.w + (int64_t)min(n0 + r, a.N - 1) * a.K) + p0;
+  const u32x4* x[T];
+#pragma unroll
+  for (int t = 0; t < T; ++t) x[t] = reinterpret_cast<const u32x4*>(a.x + t * a.ldx) + p0;
+  int acc[kVecRows][T] = {};
+  u32x4 wv[2][kVecRows], xv[2][T];
+  auto load = [&](int s, int at) {
+    // (pieces past the part repeat its last one, whose tokens are put to zero)
+    const int i = min(at + lane, n - 1);
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) wv[s][r] = __builtin_nontemporal_load(w[r] + i);
+#pragma unroll
+    for (int t = 0; t < T; ++t) xv[s][t] = x[t][i];
+  };
+  auto multiply = [&](int s, int at) {
+    const bool in = at + lane < n;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int xd = in ? (int)xv[s][t][d] : 0;
+#pragma unroll
+        for (int r = 0; r < kVecRows; ++r) acc[r][t] = __builtin_amdgcn_sdot4((int)wv[s][r][d], xd, acc[r][t], false);
+      }
+    }
+  };
+  load(0, 0);
+  for (int at = 0; at < n; at += 128) {
+    if (at + 64 < n) load(1, at + 64);
+    multiply(0, at);
+    if (at + 64 >= n) break;
+    if (at + 128 < n) load(0, at + 128);
+    multiply(1, at + 64);
+  }
+  // (lane l of sixteen rows' sums; every lane gets its row's)
+#pragma unroll
+  for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      int v = acc[r][t];
+      v += (int)dpp<0xB1>((uint32_t)v);
+      v += (int)dpp<0x4E>((uint32_t)v);
+      v += (int)dpp<0x141>((uint32_t)v);
+      v += (int)dpp<0x140>((uint32_t)v);
+      v = __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+          __builtin_amdgcn_readlane(v, 48);
+      if (lane == 0) red[wave][r][t] = v;
+    }
+  __syncthreads();
+  if (tid >= kGroups * kVecRows * T) return;
+  const int r = tid % kVecRows, g = tid / kVecRows % kGroups, tt = tid / (kVecRows * kGroups);
+  const int row = ((int)blockIdx.x * kGroups + g) * kVecRows + r;
+  if (row >= a.N) return;
+  int s = 0;
+#pragma unroll
+  for (int p = 0; p < KS; ++p) s += red[g * KS + p][r][tt];
+  float v = (float)s * a.x_scales[tt] * a.w_scales[row];
+  if (a.bias) v += a.bias[row];
+  const int64_t at = tt * a.ldy + row;
+  if (a.dtype == kNormF32)
+    static_cast<float*>(a.y)[at] = v;
+  else
+    static_cast<uint16_t*>(a.y)[at] = a.dtype == kNormBf16 ? f2bf(v) : __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
 // A block owns 16 MS tokens and 16 CT outputs; wave w takes the w-th eighth of
 // the steps on its own, D steps ahead in its own ring in LDS (no barrier: the
 // wave waits for its copies), and the eight partial tiles are added in LDS.
@@ -113,6 +199,22 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
   for (int m = 0; m < MS; ++m) xoff[m] = (uint32_t)min(16 * m + (lane >> 2), rows - 1) * (uint32_t)a.ldx + 16 * piece_of(lane);
 #pragma unroll
   for (int c = 0; c < CT; ++c) woff[c] = (uint32_t)min(16 * c + (lane >> 2), cols - 1) * (uint32_t)a.K + 16 * piece_of(lane);
+  // what the thread scales and stores in the end: eight outputs of a token,
+  // whose scales are under way before the rows are
+  constexpr int kEights = 16 * MS * 2 * CT;
+  static_assert(kEights <= kIThreads, "one each at most");
+  const int er = tid / (2 * CT), ec = tid % (2 * CT) * 8;
+  const bool stores = er < rows && ec < cols;
+  float xs = 0.f, ws[8], bias[8];
+  if (stores) {
+    xs = a.x_scales[t0 + er];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = min(n0 + ec + i, a.N - 1);
+      ws[i] = a.w_scales[n];
+      bias[i] = a.bias ? a.bias[n] : 0.f;
+    }
+  }
   int next = 0;
   auto load = [&](int s) {
     // (steps past the last repeat it and are not used)
@@ -162,25 +264,16 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
     for (int c = 0; c < CT; ++c)
       *reinterpret_cast<i32x4*>(&L.red[wave][16 * m + c16][16 * c + 4 * kb]) = acc[m][c];
   __syncthreads();
-  constexpr int kEights = 16 * MS * 2 * CT;
-  for (int e = tid; e < kEights; e += kIThreads) {
-    const int r = e / (2 * CT), c = e % (2 * CT) * 8;
-    if (r >= rows || c >= cols) continue;
-    i32x4 s[2] = {};
+  if (!stores) return;
+  i32x4 s[2] = {};
 #pragma unroll
-    for (int w = 0; w < kIWaves; ++w)
+  for (int w = 0; w < kIWaves; ++w)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] += *reinterpret_cast<const i32x4*>(&L.red[w][r][c + 4 * h]);
-    const float xs = a.x_scales[t0 + r];
-    float v[8];
+    for (int h = 0; h < 2; ++h) s[h] += *reinterpret_cast<const i32x4*>(&L.red[w][er][ec + 4 * h]);
+  float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = min(n0 + c + i, a.N - 1);
-      v[i] = (float)s[i >> 2][i & 3] * xs * a.w_scales[n];
-      if (a.bias) v[i] += a.bias[n];
-    }
-    put_eight(a, (int64_t)(t0 + r) * a.ldy + n0 + c, v, a.N - n0 - c);
-  }
+  for (int i = 0; i < 8; ++i) v[i] = (float)s[i >> 2][i & 3] * xs * ws[i] + bias[i];
+  put_eight(a, (int64_t)(t0 + er) * a.ldy + n0 + ec, v, a.N - n0 - ec);
 }
 
 // Many rows: tiles of 32 RS tokens x 256 outputs, eight waves of 16 RS x 64. A
@@ -340,6 +433,29 @@ size_t int8_ws_bytes(int /*N*/, int /*K*/, int /*T*/) { return 0; }
 
 namespace {
 
+constexpr int kVecTokens = 4;
+
+template <int T, int KS>
+hipError_t launch_vector(const Int8Args& a, hipStream_t s) {
+  constexpr int kOut = kIWaves / KS * kVecRows;
+  hipLaunchKernelGGL((int8_vector_kernel<T, KS>), dim3((a.N + kOut - 1) / kOut), dim3(kIThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t launch_vector_parts(const Int8Args& a, hipStream_t s) {
+  // a KB of a row for each wave, as long as the waves are not more than what
+  // keeps the memory busy: one token, 12288 x 2048 with K in 1, 2, 4, 8 parts 6.3,
+  // 6.2, 6.6, 8.8 us, 2048 x 4096 5.1, 4.3, 3.9, 4.0, 4096 x 8192 10.6, 8.7, 7.4,
+  // 7.3, 12288 x 512 3.7, 4.0, 5.5, 8.1; four tokens, 12288 x 2048 7.9, 8.6, 11.4,
+  // 19.6, 2048 x 4096 7.0, 5.7, 5.1, 5.5
+  const auto fits = [&](int parts) { return a.K >= 1024 * parts && (int64_t)a.N / kVecRows * parts <= 4096; };
+  if (fits(8)) return launch_vector<T, 8>(a, s);
+  if (fits(4)) return launch_vector<T, 4>(a, s);
+  if (fits(2)) return launch_vector<T, 2>(a, s);
+  return launch_vector<T, 1>(a, s);
+}
+
 template <int MS, int CT, int D>
 hipError_t launch_split(const Int8Args& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * ((a.N + 16 * CT - 1) / (16 * CT));
@@ -354,6 +470,8 @@ hipError_t launch_tile(const Int8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// A start and a time per round of 256 units, one for each compute unit, in
+// tenths of a microsecond, measured at K = 2048 (all of them grow with K alike).
 struct Tiling {
   int rows, cols, start, round;
   hipError_t (*launch)(const Int8Args&, hipStream_t);
@@ -362,14 +480,27 @@ struct Tiling {
 }  // namespace
 
 hipError_t launch_project_int8(const Int8Args& in, hipStream_t s) {
+  // Small tiles start fastest and lose when there are many, in us: 16 tokens by
+  // 4096 outputs 4.9 in 16 x 16 tiles, 5.8 in 32 x 32, 8.1 in 64 x 64; 16 by
+  // 12288 11.2, 11.6 and 11.0 (16 x 64: 9.8); 64 by 4096 8.5, 6.6, 9.3; 256 by
+  // 4096 33, 16, 11.2 and 18 in 128 x 256; 512 by 12288 59 in 64 x 64, 27 in 128
+  // x 256, 34 in 256 x 256; 4096 by 12288 482, 159, 117.
   static const Tiling tilings[] = {
-      {16, 16, 22, 20, launch_split<1, 1, 4>}, {16, 32, 24, 20, launch_split<1, 2, 4>}, {16, 64, 15, 36, launch_split<1, 4, 4>},
-      {32, 32, 12, 39, launch_split<2, 2, 2>}, {32, 64, 6, 57, launch_split<2, 4, 2>},  {64, 64, 0, 100, launch_split<4, 4, 2>},
-      {128, 256, 0, 330, launch_tile<4>},      {256, 256, 0, 600, launch_tile<8>},
+      {16, 16, 28, 19, launch_split<1, 1, 2>}, {16, 32, 35, 20, launch_split<1, 2, 2>}, {16, 64, 30, 40, launch_split<1, 4, 2>},
+      {32, 32, 27, 39, launch_split<2, 2, 2>}, {32, 64, 20, 54, launch_split<2, 4, 2>}, {64, 64, 0, 100, launch_split<4, 4, 2>},
+      {128, 256, 0, 260, launch_tile<4>},      {256, 256, 0, 385, launch_tile<8>},
   };
   Int8Args a = in;
   const int eb = a.dtype == kNormF32 ? 4 : 2;
   a.wide = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy * eb % 16 == 0;
+  if (a.T <= kVecTokens) {
+    switch (a.T) {
+      case 1: return launch_vector_parts<1>(a, s);
+      case 2: return launch_vector_parts<2>(a, s);
+      case 3: return launch_vector_parts<3>(a, s);
+      default: return launch_vector_parts<4>(a, s);
+    }
+  }
   const Tiling* best = nullptr;
   int64_t least = 0;
   for (const Tiling& t : tilings) {
