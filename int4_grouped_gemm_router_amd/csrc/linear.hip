@@ -5,6 +5,7 @@
 // for each value head, whose queries and keys are those of the key head
 // v_head * qk_heads / v_heads. States are fp32 [qk_dim][v_dim].
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "wide_expand.h"
@@ -103,6 +104,7 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(LinearArgs a) {
 namespace {
 
 constexpr int kChunk = 32;
+constexpr int kMaxWindows = 512;
 constexpr int kNowhere = INT32_MIN;  // a buffer offset past every end: such loads give zeros
 constexpr float kLog2e = 1.44269504f;
 
@@ -162,15 +164,6 @@ struct RowCopy {
   }
 };
 
-// A chunk: up to 32 tokens of one sequence.
-struct Item {
-  int t0, count, seq, flags;
-};
-constexpr int kItem = 1;    // there is one
-constexpr int kFirst = 2;   // the first of its sequence in the window: the state is loaded
-constexpr int kMiddle = 4;  // its sequence began in an earlier window
-constexpr int kLast = 8;    // the last of its sequence: the state is kept
-
 // v from another lane, as dpp, in the rows of sixteen that ROWS names; 0 elsewhere.
 template <int CTRL, int ROWS>
 __device__ inline double dpp64(double v) {
@@ -189,56 +182,92 @@ __device__ inline float factor_after(float f, float decay) { return keeps(f * de
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ inline float uniform_f(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(int, v))); }
 
-// The first of the n sorted values that is not less than v, or n. By all lanes
-// of a wave, 64 at a time.
-__device__ inline int first_at_least(const int32_t* p, int n, int v) {
-  int lo = 0, len = n;  // the answer is in lo .. lo + len
-  const int lane = threadIdx.x & 63;
-  while (len > 0) {
-    const int step = (len + 63) / 64, at = lo + min((lane + 1) * step, len) - 1;
-    const int below = __popcll(__ballot(p[at] < v));  // whole steps below v
-    if (below == 64) return lo + len;
-    lo += min(below * step, len);
-    len = min(step - 1, n - lo);
+// A chunk: up to 32 tokens of one sequence, and the slots of its states (-1: none).
+struct Item {
+  int t0, count, in, out, flags;
+};
+constexpr int kItem = 1;     // there is one
+constexpr int kFirst = 2;    // the first of its sequence in the window: the state is loaded
+constexpr int kMiddle = 4;   // its sequence began in an earlier window
+constexpr int kLast = 8;     // the last of its sequence: the state is kept
+constexpr int kGoesOn = 16;  // its sequence goes on behind the window
+
+// Sequences as a wave holds them: lane l has the beginning of sequence base + l
+// (which is also the end of the one before) and its slots, so that a walk over
+// up to 63 sequences waits for memory once. Whatever the arrays hold, bounds
+// are in 0..T and ends not before their beginnings.
+struct Sequences {
+  int base, begins, in, out;
+  __device__ void load(const LinearArgs& a, int first) {
+    base = first;
+    const int i = first + (int)(threadIdx.x & 63), n = min(i, a.n_seqs - 1);
+    begins = min(max(a.cu_seqlens[min(i, a.n_seqs)], 0), a.T);
+    const int si = a.state_in ? (a.slots_in ? a.slots_in[n] : n) : -1, so = a.state_out ? (a.slots_out ? a.slots_out[n] : n) : -1;
+    in = si >= 0 && si < a.n_in ? si : -1;
+    out = so >= 0 && so < a.n_out ? so : -1;
   }
-  return lo;
-}
+  __device__ void hold(const LinearArgs& a, int i) {
+    if (i < base || i > base + 62) load(a, i);
+  }
+  __device__ int begin(int i) const { return __builtin_amdgcn_readlane(begins, i - base); }
+  __device__ int end(int i) const { return max(__builtin_amdgcn_readlane(begins, i + 1 - base), begin(i)); }
+  __device__ int slot_in(int i) const { return __builtin_amdgcn_readlane(in, i - base); }
+  __device__ int slot_out(int i) const { return __builtin_amdgcn_readlane(out, i - base); }
+  // The last sequence that begins before token v > 0, or the first of all; held.
+  __device__ int before(const LinearArgs& a, int v) {
+    const int lane = threadIdx.x & 63;
+    if (a.n_seqs <= 63) return max(__popcll(__ballot(lane < a.n_seqs && begins < v)) - 1, 0);  // (all of them are held)
+    int lo = 0, len = a.n_seqs;  // the first that does not is in lo .. lo + len; 64 steps at a time
+    while (len > 0) {
+      const int step = (len + 63) / 64, at = lo + min((lane + 1) * step, len) - 1;
+      const int below = __popcll(__ballot(a.cu_seqlens[at] < v));  // whole steps below v
+      if (below == 64) {
+        lo += len;
+        break;
+      }
+      lo += min(below * step, len);
+      len = min(step - 1, a.n_seqs - lo);
+    }
+    const int i = max(uniform(lo) - 1, 0);
+    hold(a, i);
+    return i;
+  }
+};
 
 // The chunks of window w, one after the other.
 struct Walk {
-  int w, begin, end, seq, pos, stop, flags;
+  Sequences s;
+  int begin, end, seq, pos, stop, flags;
   bool last_window, open;
-  __device__ Walk(const LinearArgs& a, int w_) : w(w_) {
+  __device__ Walk(const LinearArgs& a, int w) {
     begin = w * a.window;
     last_window = w == a.windows - 1;
     end = min(begin + a.window, a.T);
-    seq = begin > 0 ? max(uniform(first_at_least(a.cu_seqlens, a.n_seqs, begin)) - 1, 0) : 0;
+    s.load(a, 0);
+    seq = begin > 0 ? s.before(a, begin) : 0;
     open = false;
     pos = stop = flags = 0;
   }
   __device__ Item next(const LinearArgs& a) {
     while (!open) {
-      if (seq >= a.n_seqs) return Item{0, 0, 0, 0};
-      int b, e;
-      bounds(a, seq, b, e);
-      b = uniform(b);
-      e = uniform(e);
-      if (b >= end && !last_window) return Item{0, 0, 0, 0};
+      if (seq >= a.n_seqs) return Item{0, 0, -1, -1, 0};
+      s.hold(a, seq);
+      const int b = s.begin(seq), e = s.end(seq);
+      if (b >= end && !last_window) return Item{0, 0, -1, -1, 0};
       ++seq;
       if (b < begin && e <= begin) continue;  // before the window
       if (b == e) {
         // no token: its state only moves, if it does
-        const int si = a.state_in ? uniform(slot_of(a.slots_in, seq - 1, a.n_in)) : -1;
-        const int so = a.state_out ? uniform(slot_of(a.slots_out, seq - 1, a.n_out)) : -1;
+        const int si = s.slot_in(seq - 1), so = s.slot_out(seq - 1);
         if (so < 0 || (a.state_in == a.state_out && si == so)) continue;
-        return Item{0, 0, seq - 1, kItem | kFirst | kLast};
+        return Item{0, 0, si, so, kItem | kFirst | kLast};
       }
       open = true;
       pos = max(b, begin);
       stop = min(e, end);
-      flags = kItem | kFirst | (b < begin ? kMiddle : 0) | (e <= end ? kLast : 0);
+      flags = kItem | kFirst | (b < begin ? kMiddle : 0) | (e <= end ? kLast : kGoesOn);
     }
-    Item it{pos, min(kChunk, stop - pos), seq - 1, flags & ~kLast};
+    Item it{pos, min(kChunk, stop - pos), s.slot_in(seq - 1), s.slot_out(seq - 1), flags & ~kLast};
     pos += it.count;
     if (pos >= stop) {
       it.flags |= flags & kLast;
@@ -248,13 +277,6 @@ struct Walk {
     return it;
   }
 };
-
-// Whether sequence i has tokens from `end` on.
-__device__ inline bool walk_goes_on(const LinearArgs& a, int i, int end) {
-  int b, e;
-  bounds(a, i, b, e);
-  return uniform(e) > end;
-}
 
 // Where windows keep what they pass on (LinearArgs::ws): per window, whether
 // its last sequence goes on behind it, whether that sequence began in it, and
@@ -320,14 +342,10 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   float sum = 0.f;  // of the window's logarithms (STATE)
   if constexpr (STATE) {
     // the sequence with tokens on both sides of the window's end
-    int b = 0, e = 0;
-    const int i = max(uniform(first_at_least(a.cu_seqlens, a.n_seqs, walk.end)) - 1, 0);
-    bounds(a, i, b, e);
-    b = uniform(b);
-    e = uniform(e);
-    const bool goes_on = b < walk.end && e > walk.end;
+    const int i = walk.s.before(a, walk.end), b = walk.s.begin(i);
+    const bool goes_on = b < walk.end && walk.s.end(i) > walk.end;
+    const int si = walk.s.slot_in(i);
     if (head == 0 && slice == 0 && tid == 0) {
-      const int si = a.state_in ? slot_of(a.slots_in, i, a.n_in) : -1;
       ps.meta[4 * w] = goes_on;
       ps.meta[4 * w + 1] = b >= walk.begin;
       ps.meta[4 * w + 2] = si;
@@ -394,8 +412,6 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   load_g(q2, 2);
   load_tile(q0, 0);
   load_tile(q1, 1);
-  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (wave == 0) decays(0, 0, 1.f);
 
   f32x4 S[DK / 16][NT];
 #pragma unroll
@@ -433,8 +449,25 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   };
   const int64_t head_state = (int64_t)a.qk_dim * a.v_dim;
 
+  // (the copy, where a later window's block may have written the state by now)
+  auto first_state = [&](const Item& it) {
+    const float* from = nullptr;
+    if (it.flags & kMiddle)
+      from = ps.state + (w - 1) * state_values(a);
+    else if (it.in >= 0)
+      from = a.copied && (it.flags & kGoesOn) ? ps.start + w * state_values(a) : a.state_in + it.in * state_values(a);
+    if (from)
+      load_state(from + head * head_state);
+    else
+      each_of_state([](float, uint32_t) { return 0.f; });
+  };
+  if constexpr (!STATE) first_state(q0);
+  __builtin_amdgcn_s_waitcnt(0);  // (the compiler sees it, as below)
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  if (wave == 0) decays(0, 0, 1.f);
+
   u32x2 out[2][NT];
-  Item written{0, 0, 0, 0};
+  Item written{0, 0, 0, 0, 0};
   auto store_out = [&] {
     if constexpr (STATE) return;
 #pragma unroll
@@ -457,20 +490,9 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     // loads after all its other memory operations.)
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
     store_out();
-    if (!STATE && (q0.flags & kFirst)) {
+    if (!STATE && c > 0 && (q0.flags & kFirst)) {
       f = 1.f;
-      const float* from = nullptr;
-      if (q0.flags & kMiddle) {
-        from = ps.state + (w - 1) * state_values(a);
-      } else {
-        const int si = a.state_in ? uniform(slot_of(a.slots_in, q0.seq, a.n_in)) : -1;
-        // (the copy, where a later window's block may have written the state by now)
-        if (si >= 0) from = a.copied && walk_goes_on(a, q0.seq, walk.end) ? ps.start + w * state_values(a) : a.state_in + si * state_values(a);
-      }
-      if (from)
-        load_state(from + head * head_state);
-      else
-        each_of_state([](float, uint32_t) { return 0.f; });
+      first_state(q0);
       // (a wait the compiler sees: it has none to add in every turn, which would be for the tiles too)
       __builtin_amdgcn_s_waitcnt(0);
     }
@@ -595,8 +617,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           for (int n = 0; n < NT; ++n) S[2 * s + e][n] = mfma16(kt[e], part[n][k], S[2 * s + e][n]);
     }
     if (!STATE && (q0.flags & kLast)) {
-      const int so = a.state_out ? uniform(slot_of(a.slots_out, q0.seq, a.n_out)) : -1;
-      if (so >= 0) store_state(a.state_out + so * state_values(a) + head * head_state, f);
+      if (q0.out >= 0) store_state(a.state_out + q0.out * state_values(a) + head * head_state, f);
     }
     if (!(q1.flags & kItem)) break;
     q0 = q1;
@@ -614,41 +635,62 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
 }
 
 // What windows pass on: S at the end of each, from what each adds. Thread: four
-// values of one head's state, window after window.
+// values of one head's state, window after window; what the next eight windows
+// add is under way meanwhile.
 __global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
+  __shared__ struct {
+    int on, begins, slot;
+    float decay;
+  } meta[kMaxWindows];
   const Passed ps = passed(a);
-  const int head = blockIdx.y;
-  const int64_t head_state = (int64_t)a.qk_dim * a.v_dim, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= head_state) return;
+  const int head = blockIdx.y, n = a.windows - 1;
+  for (int w = threadIdx.x; w < n; w += 256) {
+    meta[w].on = ps.meta[4 * w];
+    meta[w].begins = ps.meta[4 * w + 1];
+    meta[w].slot = ps.meta[4 * w + 2];
+    meta[w].decay = ps.decay[w * a.v_heads + head];
+  }
+  const int64_t head_state = (int64_t)a.qk_dim * a.v_dim;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t stride = state_values(a), off = head * head_state + at;
-  f32x4 S = {0.f, 0.f, 0.f, 0.f};
   constexpr int kAhead = 8;
-  for (int w0 = 0; w0 < a.windows - 1; w0 += kAhead) {
-    f32x4 add[kAhead], start[kAhead];
-    int on[kAhead], begins[kAhead];
-    float decay[kAhead];
+  f32x4 add[2][kAhead], start[2][kAhead];
+  auto load = [&](auto s_, int w0) {
+    constexpr int s = decltype(s_)::value;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int w = min(w0 + j, a.windows - 2);
-      add[j] = *reinterpret_cast<const f32x4*>(ps.state + w * stride + off);
-      on[j] = uniform(w0 + j < a.windows - 1 ? ps.meta[4 * w] : 0);
-      begins[j] = uniform(ps.meta[4 * w + 1]);
-      decay[j] = ps.decay[w * a.v_heads + head];
-      const int si = uniform(ps.meta[4 * w + 2]);
-      start[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (on[j] && begins[j] && si >= 0) start[j] = *reinterpret_cast<const f32x4*>(a.state_in + si * stride + off);
+      const int w = min(w0 + j, n - 1);
+      add[s][j] = *reinterpret_cast<const f32x4*>(ps.state + w * stride + off);
+      start[s][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (meta[w].on && meta[w].begins && meta[w].slot >= 0)
+        start[s][j] = *reinterpret_cast<const f32x4*>(a.state_in + meta[w].slot * stride + off);
     }
+  };
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  auto pass = [&](auto s_, int w0) {
+    constexpr int s = decltype(s_)::value;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (!on[j]) continue;
-      const int64_t w = w0 + j;
-      if (begins[j]) {
-        S = start[j];
+      const int w = w0 + j;
+      if (w >= n || !meta[w].on) continue;
+      if (meta[w].begins) {
+        S = start[s][j];
         if (a.copied) *reinterpret_cast<f32x4*>(ps.start + w * stride + off) = S;
       }
-      S = S * decay[j] + add[j];
+      S = S * meta[w].decay + add[s][j];
       *reinterpret_cast<f32x4*>(ps.state + w * stride + off) = S;
     }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  __syncthreads();
+  if (at >= head_state) return;
+  load(I0{}, 0);
+  for (int w0 = 0; w0 < n; w0 += 2 * kAhead) {
+    load(I1{}, w0 + kAhead);
+    pass(I0{}, w0);
+    load(I0{}, w0 + 2 * kAhead);
+    pass(I1{}, w0 + kAhead);
   }
 }
 
@@ -660,7 +702,7 @@ int chunk_cols(const LinearArgs& a) { return a.qk_dim > 128 || a.v_dim <= 64 ? 6
 // Windows for up to T tokens: enough for two blocks on each compute unit.
 int most_windows(const LinearArgs& a) {
   const int per = a.v_heads * ((a.v_dim + chunk_cols(a) - 1) / chunk_cols(a));
-  const int64_t by_blocks = std::max(1, 512 / per), by_tokens = ((int64_t)a.T + kMinWindow - 1) / kMinWindow;
+  const int64_t by_blocks = std::max(1, kMaxWindows / per), by_tokens = ((int64_t)a.T + kMinWindow - 1) / kMinWindow;
   return (int)std::max<int64_t>(1, std::min(by_blocks, by_tokens));
 }
 void set_windows(LinearArgs& a) {
