@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "topk.h"
 #include "wide_expand.h"
 
 namespace moe {
@@ -164,20 +165,17 @@ struct RowCopy {
   }
 };
 
-// v from another lane, as dpp, in the rows of sixteen that ROWS names; 0 elsewhere.
-template <int CTRL, int ROWS>
-__device__ inline double dpp64(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// v from a lane of the same row of sixteen, as dpp; 0 past the row.
+template <int CTRL>
+__device__ inline float shifted(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
 }
 
-// A state is kept as f times what the registers hold, so that a chunk's decay
-// mostly costs one product instead of one per element: f takes the decays until
-// it is far from 1, then the elements take it over.
-__device__ inline bool keeps(float f) { return f >= 0x1p-20f && f <= 0x1p20f; }
-__device__ inline float factor_after(float f, float decay) { return keeps(f * decay) ? f * decay : 1.f; }
+// A state is 2^f times what the registers hold, so that a chunk's decay mostly
+// costs one sum instead of a product per element: f takes the decays until it
+// is far from 0, then the elements take it over.
+__device__ inline bool keeps(float f) { return f >= -4.f && f <= 4.f; }
+__device__ inline float factor_after(float f, float decay) { return keeps(f + decay) ? f + decay : 0.f; }
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ inline float uniform_f(float v) { return __builtin_bit_cast(float, uniform(__builtin_bit_cast(int, v))); }
@@ -321,9 +319,9 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     } tile[ST];
     float g[4][64];
     struct {
-      float G[kChunk], Gs[kChunk];  // G in base 2, and with log2 |scale| added
-      float w[kChunk];              // e^(G_n - G_j) / the state's factor after the chunk
-      float total, log_total;       // e^(G_n), G_n in base 2
+      float G[kChunk], Gs[kChunk];  // the sums of g in base 2, and with log2 |scale| added
+      float w[kChunk];              // e^(G_n - G_j) over the state's factor after the chunk
+      float total;                  // G_n
     } dec[2];
   } L;
   static_assert(ST == 3, "tile c + 2 goes where tile c - 1 was");
@@ -366,7 +364,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   auto records = [](const Item& it, int64_t ld, int dim) {
     return it.count ? (uint32_t)(((it.count - 1) * ld + dim) * 2) : 0u;
   };
-  // (every item, also one that is not there, issues the same number of loads: the waits count on it)
+  // (every item, also one that is not there, has the same number of loads: the waits count on it)
   auto load_tile = [&](const Item& it, int st) {
     const int64_t t = it.t0;
     if constexpr (!STATE) cq.issue(L.tile[st].q, qb + t * a.ldq, records(it, a.ldq, a.qk_dim), wave);
@@ -378,30 +376,33 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     const u32x4 r = words_of(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
     copy4_to_lds(r, lds_offset(L.g[slot]), lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
   };
-  // The chunk's running sums, in base 2 and 64 bits: differences of large sums
-  // keep the precision of small ones. 2^-288 and less is 0 either way.
+  // The chunk's sums in base 2. A weight's exponent is a sum from its own token
+  // on, so that small ones are precise beside large ones; the sums from the
+  // front weigh products that are rounded to bf16. 2^-288 and less is 0 here.
   const float log_scale = __log2f(fabsf(a.scale));
   const uint32_t sign = __float_as_uint(a.scale) & 0x80000000u;
-  auto decays = [&](int slot, int to, float f) {
-    const float g = L.g[slot][lane];
-    double G = g * kLog2e < -288.f ? -288.0 : (double)g * 1.4426950408889634;
-    G += dpp64<0x111, 0xF>(G);  // the lane before, two, four, eight before in rows of sixteen
-    G += dpp64<0x112, 0xF>(G);
-    G += dpp64<0x114, 0xF>(G);
-    G += dpp64<0x118, 0xF>(G);
-    G += dpp64<0x142, 0xA>(G);  // the first row's last, to the second
-    const uint64_t last = __builtin_bit_cast(uint64_t, G);
-    const double total = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 31) << 32 |
-                                                        (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 31));
-    const float e = __builtin_amdgcn_exp2f((float)total);
+  auto decays = [&](int slot, int to, float lf) {
+    float g = L.g[slot][lane] * kLog2e;
+    g = g < -288.f ? -288.f : g;
+    const float front = g + shifted<0x111>(g);  // of this lane and up to 1, 3, 7, 15 before it, in rows of sixteen
+    float G = front + shifted<0x112>(front);
+    G += shifted<0x114>(G);
+    G += shifted<0x118>(G);
+    float R = g + shifted<0x101>(g);  // of this lane and up to 1, 3, 7, 15 behind it, then without this lane
+    R += shifted<0x102>(R);
+    R += shifted<0x104>(R);
+    R += shifted<0x108>(R);
+    R = shifted<0x101>(R);
+    const float first = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 15));
+    const float second = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 31));
+    if (lane >= 16) G += first;
+    if (lane < 16) R += second;
+    const float total = first + second;
     if (lane < kChunk) {
-      L.dec[to].G[lane] = (float)G;
-      L.dec[to].Gs[lane] = (float)(G + log_scale);
-      L.dec[to].w[lane] = __builtin_amdgcn_exp2f((float)(total - G)) * (1.0f / factor_after(f, e));
-      if (lane == 0) {
-        L.dec[to].total = e;
-        L.dec[to].log_total = (float)total;
-      }
+      L.dec[to].G[lane] = G;
+      L.dec[to].Gs[lane] = G + log_scale;
+      L.dec[to].w[lane] = __builtin_amdgcn_exp2f(R - factor_after(lf, total));
+      if (lane == 0) L.dec[to].total = total;
     }
   };
 
@@ -464,46 +465,67 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   if constexpr (!STATE) first_state(q0);
   __builtin_amdgcn_s_waitcnt(0);  // (the compiler sees it, as below)
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (wave == 0) decays(0, 0, 1.f);
+  if (wave == 0) decays(0, 0, 0.f);
 
-  u32x2 out[2][NT];
+  // The output of a turn, stored in the next. A lane has four columns of two
+  // tiles (of columns, or of tokens where there is one tile of columns); by
+  // exchanging the odd rows of sixteen lanes of the one with the even rows of the
+  // other it has eight neighbouring columns of one, and stores 16 bytes: 4 x 8
+  // bytes a lane instead took 50 us more for 16384 tokens of 32 heads of 128.
+  // Every turn has them, dropped where there is nothing to store: the waits count
+  // on it, so that a turn waits for stores two turns old and not for its last.
+  constexpr int kStores = STATE ? 0 : NT;
+  u32x4 out[NT];
   Item written{0, 0, 0, 0, 0};
+  auto side_by_side = [](u32x2 x, u32x2 y) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const auto s = __builtin_amdgcn_permlane16_swap(x[i], y[i], false, false);
+      r[i] = s[0];
+      r[2 + i] = s[1];
+    }
+    return r;
+  };
+  uint32_t store_at[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int row = NT == 2 ? 16 * i + c16 : 16 * (g4 & 1) + c16;
+    const int c = wave * NT * 16 + (NT == 2 ? 16 * (g4 & 1) : 0) + 8 * (g4 >> 1);
+    store_at[i] = c < cols ? (uint32_t)(row * (int)(a.ldo * 2) + c * 2) : (uint32_t)kNowhere;
+  }
   auto store_out = [&] {
     if constexpr (STATE) return;
+    const rsrc_t r = make_rsrc(a.o + written.t0 * a.ldo + (int64_t)head * a.v_dim + col0, records(written, a.ldo, cols));
 #pragma unroll
-    for (int it = 0; it < 2; ++it)
-      if (16 * it + c16 < written.count) {
-        uint16_t* p = a.o + (int64_t)(written.t0 + 16 * it + c16) * a.ldo + (int64_t)head * a.v_dim;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int c = col0 + (wave * NT + n) * 16 + 4 * g4;
-          if (c < a.v_dim) *reinterpret_cast<u32x2*>(p + c) = out[it][n];
-        }
-      }
+    for (int i = 0; i < NT; ++i) __builtin_amdgcn_raw_buffer_store_b128(out[i], r, (int)store_at[i], 0, 0);
   };
 
   int st = 0;
-  float f = 1.f;
+  float f = 0.f;
   for (int c = 0;; ++c) {
     // Tile c and its decays are in LDS and no wave reads tile c - 1 any more.
-    // (The newest loads, tile c + 1's, may be under way: a turn issues a tile's
-    // loads after all its other memory operations.)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
-    store_out();
+    // (What was issued after tile c's loads may be under way: the stores of two
+    // turns, which follow a turn's loads, and tile c + 1's loads.)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads + 2 * kStores) : "memory");
     if (!STATE && c > 0 && (q0.flags & kFirst)) {
-      f = 1.f;
+      f = 0.f;
       first_state(q0);
       // (a wait the compiler sees: it has none to add in every turn, which would be for the tiles too)
       __builtin_amdgcn_s_waitcnt(0);
     }
-    q3 = walk.next(a);
-    load_g(q3, (c + 3) & 3);
-    load_tile(q2, st == 0 ? 2 : st - 1);
     const auto& T = L.tile[st];
     const auto& D = L.dec[c & 1];
-    const float f_before = f, decayed = f * uniform_f(D.total);
-    f = keeps(decayed) ? decayed : 1.f;
-    if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1, !STATE && (q1.flags & kFirst) ? 1.f : f);
+    const float f_before = f, decayed = f + uniform_f(D.total);
+    f = keeps(decayed) ? decayed : 0.f;
+    // what is to come: in the middle of the turn, when the first operands are on their way
+    auto ahead = [&] {
+      q3 = walk.next(a);
+      load_g(q3, (c + 3) & 3);
+      load_tile(q2, st == 0 ? 2 : st - 1);
+      store_out();
+      if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1, !STATE && (q1.flags & kFirst) ? 0.f : f);
+    };
 
     // values and their weights: lane's column, tokens 4 g4 + r and 16 + 4 g4 + r
     const int vrow = 4 * g4 + (c16 >> 2);
@@ -545,6 +567,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           oa[0][n] = mfma16(sb, qf[0][s], oa[0][n]);
           oa[1][n] = mfma16(sb, qf[1][s], oa[1][n]);
         }
+      ahead();
       const float Gi0 = D.Gs[c16], Gi1 = D.Gs[16 + c16];
       const f32x4 Gj0 = *reinterpret_cast<const f32x4*>(&D.G[4 * g4]), Gj1 = *reinterpret_cast<const f32x4*>(&D.G[16 + 4 * g4]);
       float w00[4], w01[4], w11[4];
@@ -559,18 +582,23 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       const u32x4 pa0 = {pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
       const u32x4 pa1 = {pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
                          pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
-      const float fs = __uint_as_float(__float_as_uint(f_before) ^ sign);
+      const float fs = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f_before)) ^ sign);
       const float e0 = __builtin_amdgcn_exp2f(Gi0) * fs, e1 = __builtin_amdgcn_exp2f(Gi1) * fs;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         oa[0][n] = mfma16(vf[n], pa0, oa[0][n] * e0);
         oa[1][n] = mfma16(vf[n], pa1, oa[1][n] * e1);
-#pragma unroll
-        for (int it = 0; it < 2; ++it)
-          out[it][n] = u32x2{pack_bf16x2(oa[it][n][0], oa[it][n][1]), pack_bf16x2(oa[it][n][2], oa[it][n][3])};
+      }
+      auto packed = [](const f32x4& v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
+      if constexpr (NT == 2) {
+        out[0] = side_by_side(packed(oa[0][0]), packed(oa[0][1]));
+        out[1] = side_by_side(packed(oa[1][0]), packed(oa[1][1]));
+      } else {
+        out[0] = side_by_side(packed(oa[0][0]), packed(oa[1][0]));
       }
       written = q0;
     }
+    if constexpr (STATE) ahead();
     // the chunk enters the state: the decayed values in three bf16 parts, which
     // hold all 24 bits of them
     u32x4 part[NT][3];
@@ -590,34 +618,40 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           }
         }
     }
-    if constexpr (STATE) sum += D.log_total;
+    if constexpr (STATE) sum += D.total;
     if (!keeps(decayed)) {
       asm volatile("");  // (keeps the products in the branch)
+      const float by = __builtin_amdgcn_exp2f(decayed);
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * decayed;
+        for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * by;
     }
     const int krow = 4 * g4 + (c16 >> 2);
-#pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
+    u32x4 kt[2][2];
+    auto columns = [&](int s) {
       const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.k[krow * RQ + ((4 * s + (c16 & 3)) ^ swizzle<RQ>(krow))]);
-      u32x4 kt[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const u32x2 lo = column4(p + 8 * e), hi = column4(p + 8 * e + 16 * RQ * 16);
-        kt[e] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        kt[s & 1][e] = u32x4{lo.x, lo.y, hi.x, hi.y};
       }
+    };
+    columns(0);
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      if (s + 1 < DK / 32) columns(s + 1);
       // (the small parts first)
 #pragma unroll
       for (int k = 2; k >= 0; --k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) S[2 * s + e][n] = mfma16(kt[e], part[n][k], S[2 * s + e][n]);
+          for (int n = 0; n < NT; ++n) S[2 * s + e][n] = mfma16(kt[s & 1][e], part[n][k], S[2 * s + e][n]);
+      __builtin_amdgcn_sched_barrier(0);  // (else the reads sink to their uses)
     }
     if (!STATE && (q0.flags & kLast)) {
-      if (q0.out >= 0) store_state(a.state_out + q0.out * state_values(a) + head * head_state, f);
+      if (q0.out >= 0) store_state(a.state_out + q0.out * state_values(a) + head * head_state, __builtin_amdgcn_exp2f(f));
     }
     if (!(q1.flags & kItem)) break;
     q0 = q1;
@@ -629,7 +663,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   store_out();
   if constexpr (STATE) {
-    store_state(ps.state + w * state_values(a) + head * head_state, f);
+    store_state(ps.state + w * state_values(a) + head * head_state, __builtin_amdgcn_exp2f(f));
     if (slice == 0 && tid == 0) ps.decay[w * a.v_heads + head] = __builtin_amdgcn_exp2f(sum);
   }
 }
