@@ -230,6 +230,7 @@ struct LinearArgs {
   // set by the launcher: tokens of a window and how many windows; whether the
   // states that sequences over several windows start from are copied
   int window, windows, copied;
+  int short_tokens;  // sequences of at most so many tokens are walked through
 };
 size_t linear_ws_bytes(const LinearArgs& a);
 hipError_t launch_linear_attention(const LinearArgs& a, hipStream_t s);

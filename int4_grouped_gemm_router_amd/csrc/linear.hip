@@ -30,73 +30,84 @@ __device__ inline int slot_of(const int32_t* slots, int i, int n) {
 }  // namespace
 
 // Block: one sequence, one value head, 32 columns of its state in registers:
-// thread (r, c) holds rows r + 32 p, columns 4 c .. 4 c + 3. Token after token.
+// thread (r, c) holds rows r + 32 p, columns 4 c .. 4 c + 3. Token after token,
+// the next token's rows under way. The states' bytes bound it: 48 sequences of
+// 32 heads of 128 x 128 move 202 MB.
 template <int NP>
 __global__ __launch_bounds__(256) void linear_walk_kernel(LinearArgs a) {
-  __shared__ float part[4][kStepCols];
+  __shared__ float part[2][4][kStepCols];
   const int tid = threadIdx.x, wave = tid >> 6, c = tid & 7, r = tid >> 3;
   const int col = blockIdx.z * kStepCols + 4 * c;
   const int head = blockIdx.y, seq = blockIdx.x, kh = head / (a.v_heads / a.qk_heads);
   const bool in = col < a.v_dim;
   int begin, end;
   bounds(a, seq, begin, end);
+  const int si = a.state_in ? slot_of(a.slots_in, seq, a.n_in) : -1, so = a.state_out ? slot_of(a.slots_out, seq, a.n_out) : -1;
+  if (end - begin > a.short_tokens) return;
+  if (begin == end && (so < 0 || (a.state_in == a.state_out && si == so))) return;
   const int64_t state = (int64_t)a.qk_dim * a.v_dim;
-  float S[NP][4] = {};
-  const int si = a.state_in ? slot_of(a.slots_in, seq, a.n_in) : -1;
+  f32x4 S[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (si >= 0 && in) {
     const float* p = a.state_in + ((int64_t)si * a.v_heads + head) * state + col;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      if (r + 32 * i < a.qk_dim) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p + (int64_t)(r + 32 * i) * a.v_dim);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] = v[j];
-      }
+      if (r + 32 * i < a.qk_dim) S[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + (int64_t)(r + 32 * i) * a.v_dim));
   }
-  for (int t = begin; t < end; ++t) {
+  uint16_t kn[NP], qn[NP];
+  u32x2 vn = {0u, 0u};
+  float gn = 0.f;
+  auto load = [&](int t) {
     const uint16_t* q = a.q + (int64_t)t * a.ldq + (int64_t)kh * a.qk_dim;
     const uint16_t* k = a.k + (int64_t)t * a.ldk + (int64_t)kh * a.qk_dim;
-    float v[4] = {}, o[4] = {};
-    if (in) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(a.v + (int64_t)t * a.ldv + (int64_t)head * a.v_dim + col);
-      v[0] = bf16lo(w.x);
-      v[1] = bf16hi(w.x);
-      v[2] = bf16lo(w.y);
-      v[3] = bf16hi(w.y);
-    }
-    const float d = expf(a.decay[a.ld_decay ? (int64_t)t * a.ld_decay + head : head]);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      if (r + 32 * i >= a.qk_dim) continue;
-      const float kv = bf16f(k[r + 32 * i]), qv = bf16f(q[r + 32 * i]);
+      const int row = min(r + 32 * i, a.qk_dim - 1);
+      kn[i] = k[row];
+      qn[i] = q[row];
+    }
+    if (in) vn = *reinterpret_cast<const u32x2*>(a.v + (int64_t)t * a.ldv + (int64_t)head * a.v_dim + col);
+    gn = a.decay[a.ld_decay ? (int64_t)t * a.ld_decay + head : head];
+  };
+  if (begin < end) load(begin);
+  for (int t = begin; t < end; ++t) {
+    const float v[4] = {bf16lo(vn.x), bf16hi(vn.x), bf16lo(vn.y), bf16hi(vn.y)}, d = expf(gn);
+    float kv[NP], qv[NP], o[4] = {};
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      kv[i] = r + 32 * i < a.qk_dim ? bf16f(kn[i]) : 0.f;
+      qv[i] = r + 32 * i < a.qk_dim ? bf16f(qn[i]) : 0.f;
+    }
+    if (t + 1 < end) load(t + 1);
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        S[i][j] = __builtin_fmaf(kv, v[j], S[i][j] * d);
-        o[j] = __builtin_fmaf(qv, S[i][j], o[j]);
+        S[i][j] = __builtin_fmaf(kv[i], v[j], S[i][j] * d);
+        o[j] = __builtin_fmaf(qv[i], S[i][j], o[j]);
       }
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       o[j] += __shfl_xor(o[j], 8);
       o[j] += __shfl_xor(o[j], 16);
       o[j] += __shfl_xor(o[j], 32);
     }
+    // (two sets of sums: a token's are read while the next one's are written)
+    auto& sums = part[t & 1];
     if ((tid & 63) < 8)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[wave][4 * c + j] = o[j];
+      for (int j = 0; j < 4; ++j) sums[wave][4 * c + j] = o[j];
     __syncthreads();
-    if (tid < kStepCols && blockIdx.z * kStepCols + tid < a.v_dim)
+    if (tid < kStepCols && (int)blockIdx.z * kStepCols + tid < a.v_dim)
       a.o[(int64_t)t * a.ldo + (int64_t)head * a.v_dim + blockIdx.z * kStepCols + tid] =
-          f2bf(a.scale * ((part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid])));
-    __syncthreads();
+          f2bf(a.scale * ((sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid])));
   }
-  const int so = a.state_out ? slot_of(a.slots_out, seq, a.n_out) : -1;
   if (so >= 0 && in) {
     float* p = a.state_out + ((int64_t)so * a.v_heads + head) * state + col;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-      if (r + 32 * i < a.qk_dim)
-        *reinterpret_cast<f32x4*>(p + (int64_t)(r + 32 * i) * a.v_dim) = f32x4{S[i][0], S[i][1], S[i][2], S[i][3]};
+      if (r + 32 * i < a.qk_dim) *reinterpret_cast<f32x4*>(p + (int64_t)(r + 32 * i) * a.v_dim) = S[i];
   }
 }
 
@@ -253,7 +264,8 @@ struct Walk {
       const int b = s.begin(seq), e = s.end(seq);
       if (b >= end && !last_window) return Item{0, 0, -1, -1, 0};
       ++seq;
-      if (b < begin && e <= begin) continue;  // before the window
+      if (b < begin && e <= begin) continue;      // before the window
+      if (e - b <= a.short_tokens) continue;      // the other kernel's
       if (b == e) {
         // no token: its state only moves, if it does
         const int si = s.slot_in(seq - 1), so = s.slot_out(seq - 1);
@@ -341,7 +353,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   if constexpr (STATE) {
     // the sequence with tokens on both sides of the window's end
     const int i = walk.s.before(a, walk.end), b = walk.s.begin(i);
-    const bool goes_on = b < walk.end && walk.s.end(i) > walk.end;
+    const bool goes_on = b < walk.end && walk.s.end(i) > walk.end && walk.s.end(i) - b > a.short_tokens;
     const int si = walk.s.slot_in(i);
     if (head == 0 && slice == 0 && tid == 0) {
       ps.meta[4 * w] = goes_on;
@@ -730,19 +742,24 @@ __global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
 
 namespace {
 
-constexpr int kMinWindow = 64;
+constexpr int kManySeqs = 8, kShortTokens = 8;
 
 int chunk_cols(const LinearArgs& a) { return a.qk_dim > 128 || a.v_dim <= 64 ? 64 : 128; }
-// Windows for up to T tokens: enough for two blocks on each compute unit.
-int most_windows(const LinearArgs& a) {
+// Windows for T tokens: enough for two blocks on each compute unit, of 64 tokens
+// at least, of 128 from 1024 tokens on, and one for up to 256 tokens, where two
+// launches more cost more than they save. 32 heads of 128 x 128, one window,
+// windows of 64, of 128, of 256: 256 tokens 23, 28, 34, 23 us; 512 tokens 42, 33,
+// 35, 48; 1024 tokens 79, 45, 40, 49; 2048 tokens 152, 56, 55, 54.
+int most_windows(const LinearArgs& a, int64_t T) {
   const int per = a.v_heads * ((a.v_dim + chunk_cols(a) - 1) / chunk_cols(a));
-  const int64_t by_blocks = std::max(1, kMaxWindows / per), by_tokens = ((int64_t)a.T + kMinWindow - 1) / kMinWindow;
-  return (int)std::max<int64_t>(1, std::min(by_blocks, by_tokens));
+  const int64_t least = T < 1024 ? 64 : 128;
+  if (T <= 256) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::max(1, kMaxWindows / per), (T + least - 1) / least));
 }
 void set_windows(LinearArgs& a) {
-  const int most = most_windows(a);
-  a.window = (int)std::max<int64_t>(kMinWindow, ((int64_t)a.T + most - 1) / most + (kChunk - 1)) / kChunk * kChunk;
-  a.windows = std::max(1, (a.T + a.window - 1) / a.window);
+  const int most = most_windows(a, a.T);
+  a.window = (int)((((int64_t)a.T + most - 1) / most + kChunk - 1) / kChunk * kChunk);
+  a.windows = std::max(1, (a.T + a.window - 1) / std::max(a.window, 1));
 }
 
 template <int DK, int NT>
@@ -757,6 +774,7 @@ hipError_t launch_chunks(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Sequences of at most a.short_tokens.
 hipError_t launch_walk(const LinearArgs& a, hipStream_t s) {
   const dim3 grid(a.n_seqs, a.v_heads, (a.v_dim + kStepCols - 1) / kStepCols), block(256);
   if (a.qk_dim <= 64)
@@ -771,13 +789,21 @@ hipError_t launch_walk(const LinearArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t linear_ws_bytes(const LinearArgs& a) {
-  const int64_t n = most_windows(a);
+  // (a workspace for T tokens serves fewer)
+  const int64_t n = std::max(most_windows(a, a.T), most_windows(a, std::min(a.T, 1023)));
   if (n <= 1) return 0;
   return (size_t)(n * (16 + 4 * (int64_t)a.v_heads + 8 * state_values(a)) + 16);
 }
 
 hipError_t launch_linear_attention(const LinearArgs& in, hipStream_t s) {
   LinearArgs a = in;
+  // Many sequences: those of a few tokens are walked through, a block for each,
+  // since they would follow each other in a window, at about 4 us each.
+  a.short_tokens = a.n_seqs >= kManySeqs ? kShortTokens : -1;
+  if (a.short_tokens >= 0) {
+    const hipError_t e = launch_walk(a, s);
+    if (e != hipSuccess || a.T <= 0) return e;
+  }
   set_windows(a);
   // states written where others are read: sequences that go over several windows start from a copy
   const uintptr_t ib = reinterpret_cast<uintptr_t>(a.state_in), ob = reinterpret_cast<uintptr_t>(a.state_out);
@@ -787,6 +813,11 @@ hipError_t launch_linear_attention(const LinearArgs& in, hipStream_t s) {
   if (a.v_dim <= 64) return a.qk_dim <= 64 ? launch_chunks<64, 1>(a, s) : launch_chunks<128, 1>(a, s);
   return a.qk_dim <= 64 ? launch_chunks<64, 2>(a, s) : launch_chunks<128, 2>(a, s);
 }
-hipError_t launch_linear_step(const LinearArgs& a, hipStream_t s) { return launch_walk(a, s); }
+
+hipError_t launch_linear_step(const LinearArgs& in, hipStream_t s) {
+  LinearArgs a = in;
+  a.short_tokens = 1;
+  return launch_walk(a, s);
+}
 
 }  // namespace moe
