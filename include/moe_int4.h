@@ -549,7 +549,8 @@ int moe_linear_attention_step(const moe_linear* linear, const uint16_t* q, int64
  * is taken, over `group` consecutive values (0: the row, or 32, 64, 128 or
  * 256, dividing H). gate: a MOE_GATE_*; gate_per_row: one gate value a row
  * instead of H. next: whether the second norm is taken. out8 and out8_group as
- * out8 and group of moe_norm. eps and next_eps > 0, all others finite. */
+ * out8 and group of moe_norm. eps and next_eps at least 2^-126, all others
+ * finite. */
 typedef struct {
   int32_t H, dtype, weight_dtype, normalize, group, gate, gate_per_row, next, out8, out8_group;
   float eps, weight_offset, scale, next_eps, next_offset;

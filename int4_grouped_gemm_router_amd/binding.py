@@ -550,10 +550,15 @@ def _gpu(t):
     return dev
 
 
+_entry = {}  # C entry points by name, as `_call` finds them
+
+
 def _call(name, dev, stream, *args):
     """The C entry point with a stream as its last argument, GPU `dev` being current."""
     import torch
-    f = getattr(lib(), name)
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(lib(), name)
     if dev == torch.cuda.current_device():
         code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
     else:
@@ -789,18 +794,18 @@ def rope(head_dim, rot_dim=None, dtype=BF16, interleaved=False, inverse=False, b
 
 
 def _heads(t, T, heads, dim, dtypes, dev, name):
-    """Address and row stride of a [>= T, heads, dim] (or [>= T, heads * dim]) tensor whose rows are contiguous."""
-    if t.dim() == 3:
-        shape, stride = t.shape, t.stride()
-        if shape[1] != heads or shape[2] != dim or ((stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1)):
-            raise ValueError(f"{name}: [{T}, {heads}, {dim}] with contiguous heads is needed, got {list(shape)} of "
-                             f"strides {list(stride)}")
-        if t.dtype not in dtypes or shape[0] < T:
-            raise ValueError(f"{name}: [{T}, {heads}, {dim}] of {dtypes[0]} is needed, got {list(shape)} of {t.dtype}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
-        return t.data_ptr(), (stride[0] if T > 1 else heads * dim)
-    return _rows(t, T, heads * dim, dtypes, dev, name)
+    """Address and row stride of a [>= T, heads, dim] (or [>= T, heads * dim]) tensor whose rows are contiguous, on GPU
+    `dev`."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        return _rows(t, T, heads * dim, dtypes, dev, name)
+    if t.dtype not in dtypes or shape[0] < T or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: [{T}, {heads}, {dim}] of {dtypes[0]} is needed, got {list(shape)} of {t.dtype}")
+    if (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a row have to be contiguous, got strides {list(stride)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on device {dev}: one GPU is needed")
+    return t.data_ptr(), (stride[0] if T > 1 else heads * dim)
 
 
 def moe_rope(r: MoeRotary, positions, T: int, q, k=None, q_out=None, k_out=None, stream=None):
@@ -808,17 +813,20 @@ def moe_rope(r: MoeRotary, positions, T: int, q, k=None, q_out=None, k_out=None,
     k_out or in place."""
     import torch
     dev, types, D = q.get_device(), _types_of(r.dtype), r.head_dim
-    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-    args = []
-    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            _need(o is None, f"{name}_out without {name}")
-            args += [None, 0, None, 0, 0]
-            continue
-        heads = t.shape[1] if t.dim() == 3 else t.shape[-1] // D
+
+    def heads_of(t, out, name):
+        shape = t.shape
+        heads = shape[1] if len(shape) == 3 else shape[-1] // max(D, 1)
         p, ld = _heads(t, T, heads, D, types, dev, name)
-        po, ldo = (p, ld) if o is t else _heads(o, T, heads, D, types, dev, name + "_out")
-        args += [p, ld, po, ldo, heads]
+        if out is None or out is t:
+            return p, ld, p, ld, heads
+        return (p, ld) + _heads(out, T, heads, D, types, dev, name + "_out") + (heads,)
+    args = heads_of(q, q_out, "q")
+    if k is not None:
+        args += heads_of(k, k_out, "k")
+    else:
+        _need(k_out is None, "k_out without k")
+        args += (None, 0, None, 0, 0)
     pp = _flat(positions, T, torch.int32, "positions", dev)
     table = getattr(r, "table", None)
     if table is not None and table.get_device() != dev:
@@ -839,29 +847,37 @@ def linear_attention_workspace(l: MoeLinear, n_seqs: int, T: int, device="cuda")
     return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
 
 
-def _linear_args(l, q, k, v, log_decay, o, T, n_seqs, state_in, slots_in, state_out, slots_out):
-    import torch
-    dev, bits = q.get_device(), _types_of(_BF16_BITS)
-    rows = []
-    for t, heads, dim, name in ((q, l.qk_heads, l.qk_dim, "q"), (k, l.qk_heads, l.qk_dim, "k"), (v, l.v_heads, l.v_dim, "v"),
-                                (o, l.v_heads, l.v_dim, "o")):
-        rows += _heads(t, T, heads, dim, bits, dev, name)
-    if log_decay.dim() == 1:
-        rows[6:6] = [_flat(log_decay, l.v_heads, torch.float32, "log_decay", dev), 0]
-        _need(log_decay.numel() == l.v_heads, "log_decay: [v_heads] or [T, v_heads] is needed")
-    else:
-        rows[6:6] = _rows(log_decay, T, l.v_heads, _types_of(F32), dev, "log_decay")
-    states = []
-    for s, slots, name in ((state_in, slots_in, "in"), (state_out, slots_out, "out")):
-        if s is None:
-            _need(slots is None, f"slots_{name} without state_{name}")
-            states += [None, None, 0]
-            continue
-        if s.dim() != 4 or tuple(s.shape[1:]) != (l.v_heads, l.qk_dim, l.v_dim):
-            raise ValueError(f"state_{name}: [slots, {l.v_heads}, {l.qk_dim}, {l.v_dim}] is needed, got {list(s.shape)}")
-        sp = _flat(s, 0, torch.float32, f"state_{name}", dev)
-        states += [sp, None if slots is None else _flat(slots, n_seqs, torch.int32, f"slots_{name}", dev), s.shape[0]]
-    return dev, rows, states
+def _state(s, slots, l, heads, n_seqs, dev, name):
+    """Addresses of a state and its slots, and how many states it has."""
+    if s is None:
+        _need(slots is None, f"slots_{name} without state_{name}")
+        return None, None, 0
+    shape, (f32,) = s.shape, _types_of(F32)
+    if len(shape) != 4 or shape[1] != heads or shape[2] != l.qk_dim or shape[3] != l.v_dim or s.dtype != f32 or not s.is_contiguous():
+        raise ValueError(f"state_{name}: contiguous [slots, {heads}, {l.qk_dim}, {l.v_dim}] of float32 is needed, got {list(shape)} "
+                         f"of {s.dtype}")
+    if s.get_device() != dev:
+        raise ValueError(f"state_{name}: on {s.device}, other tensors on device {dev}: one GPU is needed")
+    return s.data_ptr(), None if slots is None else _flat(slots, n_seqs, _i32_type(), f"slots_{name}", dev), shape[0]
+
+
+_int32 = None
+
+
+def _i32_type():
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    return _int32
+
+
+def _decay(g, T, heads, dev):
+    """Address and row stride of the logarithms of the decay."""
+    if g.dim() != 1:
+        return _rows(g, T, heads, _types_of(F32), dev, "log_decay")
+    _need(g.numel() == heads, "log_decay: [v_heads] or [T, v_heads] is needed")
+    return _flat(g, heads, _types_of(F32)[0], "log_decay", dev), 0
 
 
 def moe_linear_attention(l: MoeLinear, q, k, v, log_decay, o, cu_seqlens, T: int, state_in=None, slots_in=None,
@@ -871,17 +887,33 @@ def moe_linear_attention(l: MoeLinear, q, k, v, log_decay, o, cu_seqlens, T: int
     import torch
     n = cu_seqlens.numel() - 1
     _need(n >= 0, "cu_seqlens: n + 1 values are needed")
-    dev, rows, states = _linear_args(l, q, k, v, log_decay, o, T, n, state_in, slots_in, state_out, slots_out)
+    dev, bits, hk, hv, dk, dv = q.get_device(), _types_of(_BF16_BITS), l.qk_heads, l.v_heads, l.qk_dim, l.v_dim
+    qp, ldq = _heads(q, T, hk, dk, bits, dev, "q")
+    kp, ldk = _heads(k, T, hk, dk, bits, dev, "k")
+    vp, ldv = _heads(v, T, hv, dv, bits, dev, "v")
+    op, ldo = _heads(o, T, hv, dv, bits, dev, "o")
+    gp, ldg = _decay(log_decay, T, hv, dev)
+    si, sli, ni = _state(state_in, slots_in, l, hv, n, dev, "in")
+    so, slo, no = _state(state_out, slots_out, l, hv, n, dev, "out")
     cp = _flat(cu_seqlens, n + 1, torch.int32, "cu_seqlens", dev)
     wp, wn = (None, 0) if ws is None else (_flat(ws, 0, torch.uint8, "ws", dev), ws.numel())
-    _call("moe_linear_attention", _gpu(q), stream, ctypes.byref(l), *rows[:8], cp, n, *states, *rows[8:], T, wp, wn)
+    _call("moe_linear_attention", _gpu(q), stream, ctypes.byref(l), qp, ldq, kp, ldk, vp, ldv, gp, ldg, cp, n, si, sli, ni, so,
+          slo, no, op, ldo, T, wp, wn)
 
 
 def moe_linear_attention_step(l: MoeLinear, q, k, v, log_decay, o, T: int, state_in=None, slots_in=None, state_out=None,
                               slots_out=None, stream=None):
     """One token of each of T sequences (decode): moe_linear_attention with a token a sequence."""
-    dev, rows, states = _linear_args(l, q, k, v, log_decay, o, T, T, state_in, slots_in, state_out, slots_out)
-    _call("moe_linear_attention_step", _gpu(q), stream, ctypes.byref(l), *rows[:8], *states, *rows[8:], T)
+    dev, bits, hk, hv, dk, dv = q.get_device(), _types_of(_BF16_BITS), l.qk_heads, l.v_heads, l.qk_dim, l.v_dim
+    qp, ldq = _heads(q, T, hk, dk, bits, dev, "q")
+    kp, ldk = _heads(k, T, hk, dk, bits, dev, "k")
+    vp, ldv = _heads(v, T, hv, dv, bits, dev, "v")
+    op, ldo = _heads(o, T, hv, dv, bits, dev, "o")
+    gp, ldg = _decay(log_decay, T, hv, dev)
+    si, sli, ni = _state(state_in, slots_in, l, hv, T, dev, "in")
+    so, slo, no = _state(state_out, slots_out, l, hv, T, dev, "out")
+    _call("moe_linear_attention_step", dev if dev >= 0 else _gpu(q), stream, ctypes.byref(l), qp, ldq, kp, ldk, vp, ldv, gp, ldg,
+          si, sli, ni, so, slo, no, op, ldo, T)
 
 
 def gated_norm(H, dtype=BF16, weight_dtype=None, normalize=True, group=0, eps=1e-6, weight_offset=0.0, gate=GATE_NONE,

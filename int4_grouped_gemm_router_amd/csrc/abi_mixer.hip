@@ -268,7 +268,7 @@ int moe_gated_norm(const moe_block_norm* n, const void* x, int64_t ldx, const vo
                    int64_t ld_h, void* y, int64_t ld_y, void* q, int64_t ld_q, float* scales,
                    int32_t T, void* stream) {
   const auto flag = [](int f) { return f == 0 || f == 1; };
-  const auto eps_ok = [](float e) { return std::isfinite(e) && e > 0.f; };
+  const auto eps_ok = [](float e) { return std::isfinite(e) && e >= 0x1p-126f; };
   if (!n || T < 0 || !type_ok(n->dtype) || (n->weight_dtype != n->dtype && n->weight_dtype != MOE_F32) ||
       !flag(n->normalize) || !flag(n->gate_per_row) || !flag(n->next) || n->gate < MOE_GATE_NONE ||
       n->gate > MOE_GATE_SIGMOID || n->out8 < MOE_OUT8_NONE || n->out8 > MOE_OUT8_E4M3 || !eps_ok(n->eps) ||

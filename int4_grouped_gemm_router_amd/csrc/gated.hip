@@ -7,11 +7,12 @@
 //   s = max |v| / Q per 8-bit group,  q = v / s
 //
 // One pass over memory, as the plain norm does it: a row in the registers of
-// 16 to 1024 threads, eight consecutive values a thread and access, every
-// sum and v in fp32. A group of 32 to 256 values lies in 4 to 32 neighbouring
-// lanes, so the first norm needs no LDS unless it spans the row. The weights
-// of the first norm, the channels' scale and the scalar one are one factor a
-// value, kept over the rows that a thread takes in turn.
+// 16 to 1024 threads, eight consecutive values a thread and access (sixteen in
+// the longest rows), every sum and v in fp32. A group of 32 to 256 values lies in
+// 4 to 32 neighbouring lanes, so the first norm needs no LDS unless it spans the
+// row. The weights of the first norm, the channels' scale and the scalar one are
+// one factor a value, kept over the rows that a thread takes in turn. Memory
+// bounds it, and with a gate per value the exponentials come near.
 #include <type_traits>
 
 #include "kernels.h"
@@ -35,7 +36,20 @@ __device__ inline float exp_full(float z) {
   return p < INFINITY ? __builtin_fmaf(p, e * 0.693147181f, p) : p;
 }
 
-__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_full(-z)); }
+// For rows of 16 bits without the part that the product loses: it errs by
+// 2^-24 |z| log2(e), far below those rows' own 2^-9 or 2^-12.
+template <class R>
+__device__ inline float sigmoid(float z) {
+  const float e = sizeof(typename R::type) == 4 ? exp_full(-z) : __builtin_amdgcn_exp2f(z * -1.44269504f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// 1 / sqrt(x) for x >= 2^-126: the instruction's and one step of Newton's method.
+__device__ inline float inverse_root(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  const float e = __builtin_fmaf(-x * r, r, 1.0f);
+  return x < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
+}
 
 // The sum over the lanes that hold a group of `group` values (32, 64, 128 or
 // 256: 4, 8, 16 or 32 lanes), in each.
@@ -49,16 +63,60 @@ __device__ inline float group_sum(float s, int group) {
   return __uint_as_float(v);
 }
 
+// row_all with one barrier: s is not used again before another barrier that
+// every thread reaches after its reads here.
+template <int TPR, class F>
+__device__ inline uint32_t row_all_once(uint32_t v, uint32_t* s, F f) {
+  v = row_all<(TPR < 64 ? TPR : 64)>(v, s, f);
+  if constexpr (TPR >= 256) {
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = f(f(s[0], s[1]), f(s[2], s[3]));
+#pragma unroll
+    for (int w = 4; w < TPR / 64; w += 4) v = f(v, f(f(s[w], s[w + 1]), f(s[w + 2], s[w + 3])));
+  }
+  return v;
+}
+
 }  // namespace
 
-// Block: 256 threads, 256 / TPR rows at a time, or TPR and one; blocks take rows in turn.
-// Thread i of a row owns the eight values from (i + TPR j) * 8, j < NV.
-template <class R, int TPR, int NV, int OUT8>
-__global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArgs a) {
+// Block: 256 threads, 256 / TPR rows at a time, or TPR and one; blocks take
+// rows in turn. Thread i of a row owns the eight values from (i + TPR j) * 8,
+// j < NV. NEXT: the second norm. 64 registers for rows of 16 bits, so that eight
+// waves fit a SIMD: 16384 x 2048 with residual, second norm and int8 takes 65 us
+// (4.6 TB/s), with the 94 registers of a next row loaded ahead 73; 1500 x 4096
+// fp16, gated by heads of 128, 16 and 20.
+template <class R, int TPR, int NV, int OUT8, bool NEXT>
+__global__ __launch_bounds__(kGatedThreads<TPR>, NV == 1 && sizeof(typename R::type) == 2 ? 8 : 4) void gated_norm_kernel(GatedArgs a) {
   typedef typename R::type E;
-  __shared__ uint32_t red[16];
+  __shared__ uint32_t red[2][3][16];  // by turns: [turn % 2][which reduction][wave]
   constexpr int kRows = kGatedThreads<TPR> / TPR;
-  const int lt = threadIdx.x % TPR, H = a.H;
+  const int lt = kRows > 1 ? threadIdx.x % TPR : threadIdx.x, H = a.H;
+  const bool wide_gate = a.gate_kind && !a.gate_per_row;
+  Eight<E> xv[NV], gv[NV], rv[NV];
+  E row_gate = E(0);
+  auto load_rows = [&](int64_t row) {
+    auto load = [&](const void* p, int64_t ld, Eight<E> (&out)[NV]) {
+      const E* x = static_cast<const E*>(p) + row * ld;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (lt + TPR * j) * kVec;
+        if (c + kVec <= H) {
+          out[j] = *reinterpret_cast<const Eight<E>*>(x + c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) out[j].v[i] = c + i < H ? x[c + i] : E(0);
+        }
+      }
+    };
+    load(a.x, a.ldx, xv);
+    if (wide_gate) load(a.gate, a.ld_gate, gv);
+    if (a.gate_per_row) row_gate = static_cast<const E*>(a.gate)[row * a.ld_gate];
+    if (a.residual) load(a.residual, a.ld_residual, rv);
+  };
+  // (one row a block: the same for all threads, and so are its addresses)
+  const int64_t first = (int64_t)blockIdx.x * kRows + (kRows > 1 ? threadIdx.x / TPR : 0), step = (int64_t)gridDim.x * kRows;
+
   // p's values at c .. c + 7 (index masked by `mask`; group weights repeat), 0 past the row
   auto eight = [&](const void* p, bool f32, int c, int mask, float add, float (&out)[kVec]) {
     if (f32) {
@@ -88,10 +146,7 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
   for (int j = 0; j < NV; ++j) {
     const int c = (lt + TPR * j) * kVec;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      w[j][i] = a.scale;
-      nw[j][i] = 0.f;
-    }
+    for (int i = 0; i < kVec; ++i) w[j][i] = a.scale;
     if (a.channel) {
       float f[kVec];
       eight(a.channel, a.weight_f32, c, -1, 0.f, f);
@@ -104,93 +159,66 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
 #pragma unroll
       for (int i = 0; i < kVec; ++i) w[j][i] *= f[i];
     }
-    if (a.next) eight(a.next_weight, a.weight_f32, c, -1, a.next_offset, nw[j]);
+    if constexpr (NEXT) eight(a.next_weight, a.weight_f32, c, -1, a.next_offset, nw[j]);
   }
-  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; row < a.T; row += (int64_t)gridDim.x * kRows) {
-    Eight<E> xv[NV], gv[NV], rv[NV];
-    auto load = [&](const void* p, int64_t ld, Eight<E> (&out)[NV]) {
-      const E* x = static_cast<const E*>(p) + row * ld;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (lt + TPR * j) * kVec;
-        if (c + kVec <= H) {
-          out[j] = *reinterpret_cast<const Eight<E>*>(x + c);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) out[j].v[i] = c + i < H ? x[c + i] : E(0);
-        }
-      }
-    };
-    load(a.x, a.ldx, xv);
-    E row_gate = E(0);
-    if (a.gate_kind) {
-      if (a.gate_per_row)
-        row_gate = static_cast<const E*>(a.gate)[row * a.ld_gate];
-      else
-        load(a.gate, a.ld_gate, gv);
-    }
-    if (a.residual) load(a.residual, a.ld_residual, rv);
-
-    float v[NV][kVec];
+  int turn = 0;
+  for (int64_t row = first; row < a.T; row += step, turn ^= 1) {
+    load_rows(row);
+    float v[NV][kVec], g[NV][kVec], res[NV][kVec];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[j][i] = R::get(xv[j].v[i]);
+      for (int i = 0; i < kVec; ++i) {
+        v[j][i] = R::get(xv[j].v[i]);
+        g[j][i] = R::get(gv[j].v[i]);
+        res[j][i] = R::get(rv[j].v[i]);
+      }
+    const float zr = R::get(row_gate);
     auto squares = [&](int j) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) s = __builtin_fmaf(v[j][i], v[j][i], s);
       return s;
     };
+    auto multiply = [&](int j, float f) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[j][i] *= f;
+    };
     if (a.normalize) {
       if (a.group) {
+        const float of = 1.0f / (float)a.group;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const float r = 1.0f / sqrtf(group_sum(squares(j), a.group) / (float)a.group + a.eps);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] *= r;
-        }
+        for (int j = 0; j < NV; ++j) multiply(j, inverse_root(group_sum(squares(j), a.group) * of + a.eps));
       } else {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) ss += squares(j);
-        ss = __uint_as_float(row_all<TPR>(__float_as_uint(ss), red, add_bits));
-        const float r = 1.0f / sqrtf(ss / (float)H + a.eps);
+        ss = __uint_as_float(row_all_once<TPR>(__float_as_uint(ss), red[turn][0], add_bits));
+        const float r = inverse_root(ss * (1.0f / (float)H) + a.eps);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] *= r;
+        for (int j = 0; j < NV; ++j) multiply(j, r);
       }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) v[j][i] *= w[j][i];
-    if (a.gate_kind) {
-      const bool silu = a.gate_kind == kGateSilu;
-      if (a.gate_per_row) {
-        const float z = R::get(row_gate);
-        float f = sigmoid(z);
-        if (silu) f *= z;
+    const bool silu = a.gate_kind == kGateSilu;
+    if (wide_gate) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) v[j][i] *= f;
-      } else {
+        for (int i = 0; i < kVec; ++i) v[j][i] *= sigmoid<R>(g[j][i]) * (silu ? g[j][i] : 1.0f);
+    } else if (a.gate_kind) {
+      const float f = sigmoid<R>(zr) * (silu ? zr : 1.0f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            const float z = R::get(gv[j].v[i]);
-            v[j][i] *= sigmoid(z) * (silu ? z : 1.0f);
-          }
-      }
+      for (int j = 0; j < NV; ++j) multiply(j, f);
     }
     if (a.residual) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[j][i] += R::get(rv[j].v[i]);
+        for (int i = 0; i < kVec; ++i) v[j][i] += res[j][i];
     }
     auto store = [&](void* p, int64_t ld) {
       E* dst = static_cast<E*>(p) + row * ld;
@@ -209,32 +237,28 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
         }
       }
     };
-    if (a.next) {
-      // the sum of squares first: its reduction does not wait for h's stores
+    if (a.h_out) store(a.h_out, a.ld_h);
+    if constexpr (NEXT) {
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) ss += squares(j);
-      if (a.h_out) store(a.h_out, a.ld_h);
-      ss = __uint_as_float(row_all<TPR>(__float_as_uint(ss), red, add_bits));
-      const float r = 1.0f / sqrtf(ss / (float)H + a.next_eps);
+      ss = __uint_as_float(row_all_once<TPR>(__float_as_uint(ss), red[turn][1], add_bits));
+      const float r = inverse_root(ss * (1.0f / (float)H) + a.next_eps);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[j][i] = v[j][i] * r * nw[j][i];
       if (a.y) store(a.y, a.ld_y);
-    } else {
-      if (a.h_out) store(a.h_out, a.ld_h);
     }
     if constexpr (OUT8 != kOut8None) {
       // |v| as ordered bits: their integer maximum is the largest magnitude,
-      // with NaN above infinity (values past the row are left out)
+      // with NaN above infinity (values past the row are 0, or NaN with its sum)
       uint32_t m[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         m[j] = 0;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          m[j] = max(m[j], (lt + TPR * j) * kVec + i < H ? __float_as_uint(v[j][i]) & 0x7FFFFFFFu : 0u);
+        for (int i = 0; i < kVec; ++i) m[j] = max(m[j], __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
       }
       if (a.out8_group) {
 #pragma unroll
@@ -249,7 +273,7 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
         uint32_t all = m[0];
 #pragma unroll
         for (int j = 1; j < NV; ++j) all = max(all, m[j]);
-        all = row_all<TPR>(all, red, max_bits);
+        all = row_all_once<TPR>(all, red[turn][2], max_bits);
 #pragma unroll
         for (int j = 0; j < NV; ++j) m[j] = all;
       }
@@ -259,9 +283,9 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
       for (int j = 0; j < NV; ++j) {
         const int c = (lt + TPR * j) * kVec;
         if (c >= H) continue;
-        const Group g = group_of_max<OUT8>(__uint_as_float(m[j]), 1.0f);
-        if (a.out8_group ? c % a.out8_group == 0 : c == 0) scales[a.out8_group ? c / a.out8_group : 0] = g.s;
-        const Bytes8 o = eight_bits<OUT8>(v[j], g);
+        const Group gr = group_of_max<OUT8>(__uint_as_float(m[j]), 1.0f);
+        if (a.out8_group ? c % a.out8_group == 0 : c == 0) scales[a.out8_group ? c / a.out8_group : 0] = gr.s;
+        const Bytes8 o = eight_bits<OUT8>(v[j], gr);
         if (c + kVec <= H) {
           *reinterpret_cast<Bytes8*>(q + c) = o;
         } else {
@@ -276,17 +300,28 @@ __global__ __launch_bounds__(kGatedThreads<TPR>) void gated_norm_kernel(GatedArg
 
 namespace {
 
+template <class R, int TPR, int NV, int OUT8>
+void launch_next(const GatedArgs& a, dim3 grid, hipStream_t s) {
+  if (a.next)
+    hipLaunchKernelGGL((gated_norm_kernel<R, TPR, NV, OUT8, true>), grid, dim3(kGatedThreads<TPR>), 0, s, a);
+  else
+    hipLaunchKernelGGL((gated_norm_kernel<R, TPR, NV, OUT8, false>), grid, dim3(kGatedThreads<TPR>), 0, s, a);
+}
+
 template <class R, int TPR, int NV>
 void launch_shape(const GatedArgs& a, hipStream_t s) {
+  // twice the blocks that fill every SIMD with eight waves (2048 blocks of 256
+  // threads take 68 us where 4096 take 65 and 16384, a row each, 79)
   constexpr int kRows = kGatedThreads<TPR> / TPR;
+  constexpr int64_t kMost = 4096 * 256 / kGatedThreads<TPR>;
   const int64_t blocks = ((int64_t)a.T + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048)), block(kGatedThreads<TPR>);
+  const dim3 grid((unsigned)(blocks < kMost ? blocks : kMost));
   if (a.out8 == kOut8Int8)
-    hipLaunchKernelGGL((gated_norm_kernel<R, TPR, NV, kOut8Int8>), grid, block, 0, s, a);
+    launch_next<R, TPR, NV, kOut8Int8>(a, grid, s);
   else if (a.out8 == kOut8E4m3)
-    hipLaunchKernelGGL((gated_norm_kernel<R, TPR, NV, kOut8E4m3>), grid, block, 0, s, a);
+    launch_next<R, TPR, NV, kOut8E4m3>(a, grid, s);
   else
-    hipLaunchKernelGGL((gated_norm_kernel<R, TPR, NV, kOut8None>), grid, block, 0, s, a);
+    launch_next<R, TPR, NV, kOut8None>(a, grid, s);
 }
 
 template <class R>
@@ -295,14 +330,12 @@ void launch_rows(const GatedArgs& a, hipStream_t s) {
     launch_shape<R, 16, 1>(a, s);
   else if (a.H <= 512)
     launch_shape<R, 64, 1>(a, s);
-  else if (a.H <= 1024)
-    launch_shape<R, 64, 2>(a, s);
   else if (a.H <= 2048)
     launch_shape<R, 256, 1>(a, s);
   else if (a.H <= 4096)
-    launch_shape<R, 256, 2>(a, s);
+    launch_shape<R, 512, 1>(a, s);
   else if (a.H <= 8192)
-    launch_shape<R, 512, 2>(a, s);
+    launch_shape<R, 1024, 1>(a, s);
   else
     launch_shape<R, 1024, kNormMaxH / (1024 * kVec)>(a, s);
 }

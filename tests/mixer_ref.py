@@ -96,8 +96,10 @@ def gated_ref(x, c, weight=None, gate=None, channel=None, residual=None, next_we
     if gate is not None:
         z = gate.double()
         u = u * torch.sigmoid(z) * (z if c["gate"] == 1 else 1.0)
-        # the exponential (its part put back, its ulp, their product), 1 + e, the reciprocal's ulp, z and the product
-        rel += 10 * U32
+        # the exponential (its part put back, its ulp, their product), 1 + e, the reciprocal's ulp, z and the product; for
+        # rows of 16 bits nothing is put back: log2(e) and its product with z round, 2 u |z| log2(e) of the exponent in base
+        # 2, of which ln 2 reach the result
+        rel = rel + 10 * U32 + (2 * U32 * z.abs() if x.dtype != torch.float32 else 0.0)
     u = u * c["scale"] * (1.0 if channel is None else channel.double())
     rel += 4 * U32
     err = rel * u.abs() + 2.0 ** -126

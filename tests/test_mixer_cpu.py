@@ -265,7 +265,7 @@ def test_gated_refusals():
     n8 = B.gated_norm(64, out8=B.OUT8_INT8, out8_group=32)
     assert _gated(n8) == B.MOE_EINVAL and _gated(n8, q=FAKE, ldq=64) == B.MOE_EINVAL
     assert _gated(n8, q=FAKE, ldq=63, s=FAKE) == B.MOE_EINVAL and _gated(n8, q=FAKE, ldq=64, s=FAKE + 2) == B.MOE_EINVAL
-    for bad in (dict(eps=0.0), dict(next_eps=-1.0), dict(eps=math.nan), dict(weight_offset=math.inf), dict(scale=math.nan),
+    for bad in (dict(eps=0.0), dict(eps=1e-39), dict(next_eps=-1.0), dict(eps=math.nan), dict(weight_offset=math.inf), dict(scale=math.nan),
                 dict(next_offset=math.inf), dict(gate=3), dict(gate=-1), dict(out8=3)):
         assert _gated(B.gated_norm(64, **bad)) == B.MOE_EINVAL, bad
     for bad in (dict(H=0), dict(H=16385), dict(H=96, group=64), dict(H=96, group=48), dict(H=96, out8_group=64), dict(H=64, group=-32)):
