@@ -3,18 +3,17 @@
 // Sums are exact in 32-bit integers (K <= 65536, so at most 2^30); the scales
 // and the bias are applied in fp32 and the result is rounded once.
 //
-// Both operands are row-major. A fragment, 16 rows x 64 inputs, is what one
-// matrix operation takes of an operand; a wave copies it from the rows straight
-// to LDS, four lanes a row (sixteen lanes that each read another row cost the
-// address unit four times as long), and reads it back in the matrix cores'
-// order. Three kernels:
+// Both operands are row-major. A tile of 16 rows x 128 inputs is two matrix
+// operations' operand; a wave copies it from the rows straight to LDS, eight
+// lanes a row, so that each copy takes whole lines of 128 bytes (with 64 bytes a
+// row, a step of one operation, L2 delivers half as much: 4096 x 12288 x 2048 took
+// 115 us), and reads it back in the matrix cores' order. Three kernels:
 //   int8_vector_kernel one to four tokens: whole rows of weights straight to
 //                      registers, dot products of four in the vector units
-//   int8_split_kernel  a block's eight waves split K and join through LDS:
-//                      few rows, where bytes and latency count
-//   int8_tile_kernel   256 x 256 tiles, both operands shared through a ring of
-//                      four stages of 64 inputs: many rows, where the matrix
-//                      cores count
+//   int8_split_kernel  a block's waves split K and join through LDS: few rows,
+//                      where bytes and latency count
+//   int8_tile_kernel   256 x 256 tiles, both operands shared through two stages
+//                      of 128 inputs: many rows, where the matrix cores count
 #include <algorithm>
 #include <type_traits>
 
@@ -28,7 +27,8 @@ namespace {
 
 constexpr int kIWaves = 8;
 constexpr int kIThreads = 64 * kIWaves;
-constexpr int kStep = 64;  // inputs of a fragment
+constexpr int kStep = 128;  // inputs of a tile
+constexpr int kNowhere = INT32_MIN;  // a buffer offset past every end: such copies are zeros
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -38,11 +38,35 @@ __device__ inline i32x4 mfma16_i8(u32x4 a, u32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// Lane l of a copy takes piece piece_of(l) (16 inputs) of row l / 4 to slot l;
-// lane (c16, kb) of the matrix cores finds row c16, piece kb in slot_of(c16,
-// kb). The swizzle spreads the sixteen rows of one piece over the LDS banks.
-__device__ inline int piece_of(int l) { return (l & 3) ^ (l >> 4); }
-__device__ inline int slot_of(int c16, int kb) { return 4 * c16 + (kb ^ (c16 >> 2)); }
+// Copy h of a tile (rows 8 h .. 8 h + 7): lane l takes piece piece_of(h, l) (16
+// inputs) of row 8 h + l / 8 to slot 64 h + l. Lane (c16, kb) of the matrix
+// cores finds piece p of row c16 in slot_of(c16, p), p = kb + 4 half. The swizzle
+// puts the sixteen rows' same piece into different LDS banks.
+__device__ inline int piece_of(int h, int l) { return (l & 7) ^ (4 * h + (l >> 4)); }
+__device__ inline int slot_of(int c16, int p) { return 8 * c16 + (p ^ (c16 >> 1)); }
+
+// What a wave needs to copy N tiles of one operand, from the base of rows of ld
+// bytes: each lane's offsets. Rows past the last repeat it.
+template <int N>
+struct TileCopy {
+  uint32_t off[N][2];
+  __device__ void init(int lane, int first, int rows, int64_t ld) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        off[n][h] = (uint32_t)min(16 * (first + n) + 8 * h + (lane >> 3), rows - 1) * (uint32_t)ld + 16 * piece_of(h, lane);
+  }
+  // the tiles' inputs from k on, those from K on as zeros; tile n goes to dst + 128 n
+  __device__ void issue(rsrc_t r, u32x4* dst, int lane, int k, int K) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool past = k + 16 * piece_of(h, lane) >= K;
+#pragma unroll
+      for (int n = 0; n < N; ++n) bload_lds(r, dst + 128 * n + 64 * h, past ? (uint32_t)kNowhere : off[n][h], (uint32_t)k);
+    }
+  }
+};
 
 template <int N>
 __device__ inline void wait_copies() {
@@ -162,21 +186,21 @@ __global__ __launch_bounds__(kIThreads) void int8_vector_kernel(Int8Args a) {
     static_cast<uint16_t*>(a.y)[at] = a.dtype == kNormBf16 ? f2bf(v) : __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// A block owns 16 MS tokens and 16 CT outputs; wave w takes the w-th eighth of
-// the steps on its own, D steps ahead in its own ring in LDS (no barrier: the
-// wave waits for its copies), and the eight partial tiles are added in LDS.
-template <int MS, int CT, int D>
+// A block owns 16 MS tokens and 16 CT outputs; wave w takes the w-th of W parts
+// of the steps on its own, D steps ahead in its own ring in LDS (no barrier: the
+// wave waits for its copies), and the partial tiles are added in LDS.
+template <int MS, int CT, int D, int W>
 struct Int8SplitLds {
   static constexpr int kStride = 16 * CT + 4;  // the pad spreads the rows over the banks
   union {
-    u32x4 f[kIWaves][D][MS + CT][64];
-    int red[kIWaves][16 * MS][kStride];
+    u32x4 f[W][D][MS + CT][128];
+    int red[W][16 * MS][kStride];
   };
 };
 
-template <int MS, int CT, int D>
-__global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
-  typedef Int8SplitLds<MS, CT, D> Lds;
+template <int MS, int CT, int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void int8_split_kernel(Int8Args a) {
+  typedef Int8SplitLds<MS, CT, D, W> Lds;
   __shared__ Lds L;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -190,40 +214,35 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
   if (u >= u1) return;
   const int t0 = (int)(u % row_tiles) * (16 * MS), n0 = (int)(u / row_tiles) * (16 * CT);
   const int rows = min(16 * MS, a.T - t0), cols = min(16 * CT, a.N - n0);
-  const int G = a.K / kStep, g0 = (int)((int64_t)G * wave / kIWaves), ng = (int)((int64_t)G * (wave + 1) / kIWaves) - g0;
-  // (rows past the last repeat it and are not stored)
+  const int G = (a.K + kStep - 1) / kStep, g0 = (int)((int64_t)G * wave / W), ng = (int)((int64_t)G * (wave + 1) / W) - g0;
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)((rows - 1) * a.ldx + a.K));
   const rsrc_t wres = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)(cols * a.K));
-  uint32_t xoff[MS], woff[CT];
-#pragma unroll
-  for (int m = 0; m < MS; ++m) xoff[m] = (uint32_t)min(16 * m + (lane >> 2), rows - 1) * (uint32_t)a.ldx + 16 * piece_of(lane);
-#pragma unroll
-  for (int c = 0; c < CT; ++c) woff[c] = (uint32_t)min(16 * c + (lane >> 2), cols - 1) * (uint32_t)a.K + 16 * piece_of(lane);
+  TileCopy<MS> xc;
+  TileCopy<CT> wc;
+  xc.init(lane, 0, rows, a.ldx);
+  wc.init(lane, 0, cols, a.K);
   // what the thread scales and stores in the end: eight outputs of a token,
   // whose scales are under way before the rows are
-  constexpr int kEights = 16 * MS * 2 * CT;
-  static_assert(kEights <= kIThreads, "one each at most");
-  const int er = tid / (2 * CT), ec = tid % (2 * CT) * 8;
-  const bool stores = er < rows && ec < cols;
-  float xs = 0.f, ws[8], bias[8];
-  if (stores) {
-    xs = a.x_scales[t0 + er];
+  constexpr int kEights = 16 * MS * 2 * CT, kEach = (kEights + 64 * W - 1) / (64 * W);
+  float xs[kEach], ws[kEach][8], bias[kEach][8];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int er = min((tid + 64 * W * e) / (2 * CT), rows - 1), ec = (tid + 64 * W * e) % (2 * CT) * 8;
+    xs[e] = a.x_scales[t0 + er];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int n = min(n0 + ec + i, a.N - 1);
-      ws[i] = a.w_scales[n];
-      bias[i] = a.bias ? a.bias[n] : 0.f;
+      ws[e][i] = a.w_scales[n];
+      bias[e][i] = a.bias ? a.bias[n] : 0.f;
     }
   }
   int next = 0;
   auto load = [&](int s) {
     // (steps past the last repeat it and are not used)
-    const uint32_t k = (uint32_t)(g0 + min(next, max(ng - 1, 0))) * kStep;
+    const int k = (g0 + min(next, max(ng - 1, 0))) * kStep;
     ++next;
-#pragma unroll
-    for (int c = 0; c < CT; ++c) bload_lds(wres, &L.f[wave][s][MS + c][0], woff[c], k);
-#pragma unroll
-    for (int m = 0; m < MS; ++m) bload_lds(xres, &L.f[wave][s][m][0], xoff[m], k);
+    wc.issue(wres, L.f[wave][s][MS], lane, k, a.K);
+    xc.issue(xres, L.f[wave][s][0], lane, k, a.K);
   };
 #pragma unroll
   for (int s = 0; s < D; ++s) {
@@ -235,21 +254,24 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
   for (int m = 0; m < MS; ++m)
 #pragma unroll
     for (int c = 0; c < CT; ++c) acc[m][c] = i32x4{0, 0, 0, 0};
-  const int sl = slot_of(c16, kb);
   for (int g = 0; g < ng; g += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
       if (g + s < ng) {
-        wait_copies<(D - 1) * (MS + CT)>();
-        u32x4 x[MS], w[CT];
+        wait_copies<(D - 1) * 2 * (MS + CT)>();
 #pragma unroll
-        for (int m = 0; m < MS; ++m) x[m] = L.f[wave][s][m][sl];
+        for (int h = 0; h < 2; ++h) {
+          const int sl = slot_of(c16, kb + 4 * h);
+          u32x4 x[MS], w[CT];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) w[c] = L.f[wave][s][MS + c][sl];
+          for (int m = 0; m < MS; ++m) x[m] = L.f[wave][s][m][sl];
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
+          for (int c = 0; c < CT; ++c) w[c] = L.f[wave][s][MS + c][sl];
 #pragma unroll
-          for (int c = 0; c < CT; ++c) acc[m][c] = mfma16_i8(w[c], x[m], acc[m][c]);
+          for (int m = 0; m < MS; ++m)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[m][c] = mfma16_i8(w[c], x[m], acc[m][c]);
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next copies
         load(s);
         __builtin_amdgcn_sched_barrier(0);
@@ -264,26 +286,30 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_split_kernel(Int8Args a) {
     for (int c = 0; c < CT; ++c)
       *reinterpret_cast<i32x4*>(&L.red[wave][16 * m + c16][16 * c + 4 * kb]) = acc[m][c];
   __syncthreads();
-  if (!stores) return;
-  i32x4 s[2] = {};
 #pragma unroll
-  for (int w = 0; w < kIWaves; ++w)
+  for (int e = 0; e < kEach; ++e) {
+    const int er = (tid + 64 * W * e) / (2 * CT), ec = (tid + 64 * W * e) % (2 * CT) * 8;
+    if (er >= rows || ec >= cols) continue;
+    i32x4 s[2] = {};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] += *reinterpret_cast<const i32x4*>(&L.red[w][er][ec + 4 * h]);
-  float v[8];
+    for (int w = 0; w < W; ++w)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)s[i >> 2][i & 3] * xs * ws[i] + bias[i];
-  put_eight(a, (int64_t)(t0 + er) * a.ldy + n0 + ec, v, a.N - n0 - ec);
+      for (int h = 0; h < 2; ++h) s[h] += *reinterpret_cast<const i32x4*>(&L.red[w][er][ec + 4 * h]);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)s[i >> 2][i & 3] * xs[e] * ws[e][i] + bias[e][i];
+    put_eight(a, (int64_t)(t0 + er) * a.ldy + n0 + ec, v, a.N - n0 - ec);
+  }
 }
 
 // Many rows: tiles of 32 RS tokens x 256 outputs, eight waves of 16 RS x 64. A
-// stage holds the tile's fragments of one step; step i is multiplied while
-// step i + 1, which is in LDS already, gives its first operands and step i + 3
-// is copied to where step i - 1 was. One barrier a step.
+// stage holds the tile's rows of one step of 128 inputs. One barrier a step,
+// before the products of its last two subtiles: from there on the next step's
+// operands are read, and the copies of the step after it go to where this one was.
 template <int RS>
 struct Int8TileLds {
-  static constexpr int kFrags = 2 * RS + 16;
-  u32x4 f[4][kFrags][64];  // [stage][tokens' subtiles, then outputs'][slot]
+  static constexpr int kTiles = 2 * RS + 16;
+  u32x4 f[2][kTiles][128];  // [stage][tokens' subtiles, then outputs'][slot]
 };
 
 template <int RS>
@@ -294,7 +320,7 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_tile_kernel(Int8Args a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, kb = lane >> 4;
   const int wr = wave >> 2, wc = wave & 3;
-  const int G = a.K / kStep;
+  const int G = (a.K + kStep - 1) / kStep;
   const int row_tiles = (a.T + 32 * RS - 1) / (32 * RS), col_tiles = (a.N + 255) / 256;
   // XCD x takes a contiguous range of units, column tiles fastest: the rows of
   // few row tiles stay in its L2
@@ -307,24 +333,19 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_tile_kernel(Int8Args a) {
   const rsrc_t xres = make_rsrc(a.x + (int64_t)t0 * a.ldx, (uint32_t)((rows - 1) * a.ldx + a.K));
   const rsrc_t wres = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)(cols * a.K));
   // wave w copies tokens' subtiles w RS / 4 .. and outputs' 2 w, 2 w + 1
-  constexpr int kX = RS / 4, kCopies = kX + 2;
-  uint32_t xoff[kX], woff[2];
-#pragma unroll
-  for (int f = 0; f < kX; ++f)
-    xoff[f] = (uint32_t)min(16 * (wave * kX + f) + (lane >> 2), rows - 1) * (uint32_t)a.ldx + 16 * piece_of(lane);
-#pragma unroll
-  for (int f = 0; f < 2; ++f)
-    woff[f] = (uint32_t)min(16 * (2 * wave + f) + (lane >> 2), cols - 1) * (uint32_t)a.K + 16 * piece_of(lane);
+  constexpr int kX = RS / 4;
+  TileCopy<kX> xc;
+  TileCopy<2> oc;
+  xc.init(lane, wave * kX, rows, a.ldx);
+  oc.init(lane, 2 * wave, cols, a.K);
   // the steps are taken in turn from a start that depends on the column tile:
   // rows a multiple of 4 KB apart have one step of every row in the same L2
   // channel, and blocks in step would all wait for it
   int gk = (int)((int64_t)(u % col_tiles) * G / col_tiles);
   // (steps past the last wrap around and are not used)
   auto load = [&](int st) {
-#pragma unroll
-    for (int f = 0; f < kX; ++f) bload_lds(xres, &L.f[st][wave * kX + f][0], xoff[f], (uint32_t)gk * kStep);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) bload_lds(wres, &L.f[st][2 * RS + 2 * wave + f][0], woff[f], (uint32_t)gk * kStep);
+    xc.issue(xres, L.f[st][wave * kX], lane, gk * kStep, a.K);
+    oc.issue(wres, L.f[st][2 * RS + 2 * wave], lane, gk * kStep, a.K);
     gk = gk + 1 < G ? gk + 1 : 0;
   };
   i32x4 acc[RS][4];
@@ -334,56 +355,62 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_tile_kernel(Int8Args a) {
     for (int c = 0; c < 4; ++c) acc[m][c] = i32x4{0, 0, 0, 0};
   load(0);
   load(1);
-  load(2);
+  constexpr int kCopies = 2 * (kX + 2);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kCopies) : "memory");
-  const int sl = slot_of(c16, kb);
+  const int sl[2] = {slot_of(c16, kb), slot_of(c16, kb + 4)};
   // token operands are read kAhead subtiles ahead of their products, the
-  // outputs' over the second half of a step
+  // outputs' over the end of the half before
   constexpr int kAhead = 3, kRing = 4;
   u32x4 av[kRing], bw[2][4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) bw[0][c] = L.f[0][2 * RS + 4 * wc + c][sl];
+  for (int c = 0; c < 4; ++c) bw[0][c] = L.f[0][2 * RS + 4 * wc + c][sl[0]];
 #pragma unroll
-  for (int m = 0; m < kAhead; ++m) av[m] = L.f[0][wr * RS + m][sl];
+  for (int m = 0; m < kAhead; ++m) av[m] = L.f[0][wr * RS + m][sl[0]];
+  auto products = [&](int h, int m) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[m][c] = mfma16_i8(bw[h][c], av[m % kRing], acc[m][c]);
+    // (without these fences the compiler gathers the reads and spills)
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto step = [&](auto S_) {
-    constexpr int S = decltype(S_)::value, Sn = (S + 1) & 3, B = S & 1;
-    load((S + 3) & 3);
+    constexpr int S = decltype(S_)::value, Sn = 1 - S;
+    auto token = [&](int st, int h, int m) { av[m % kRing] = L.f[st][wr * RS + m][sl[h]]; };
+    auto output = [&](int st, int h, int c) { bw[h][c] = L.f[st][2 * RS + 4 * wc + c][sl[h]]; };
 #pragma unroll
     for (int m = 0; m < RS; ++m) {
       const int fa = m + kAhead;
-      av[fa % kRing] = fa < RS ? L.f[S][wr * RS + fa][sl] : L.f[Sn][wr * RS + fa - RS][sl];
+      token(S, fa < RS ? 0 : 1, fa % RS);
       if (m >= RS / 2) {
 #pragma unroll
-        for (int q = 0; q < 8 / RS; ++q) {
-          const int c = (m - RS / 2) * (8 / RS) + q;
-          bw[1 - B][c] = L.f[Sn][2 * RS + 4 * wc + c][sl];
-        }
+        for (int q = 0; q < 8 / RS; ++q) output(S, 1, (m - RS / 2) * (8 / RS) + q);
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][c] = mfma16_i8(bw[B][c], av[m % kRing], acc[m][c]);
-      // (without these fences the compiler gathers the reads and spills)
-      __builtin_amdgcn_sched_barrier(0);
+      products(0, m);
     }
-    // Before any wave goes on: step i + 2 is in LDS (the copies of step i + 3
-    // may be under way), and this wave's reads of step i are done (LDS answers
-    // in order; the last quarter's reads, of step i + 1, may be under way).
-    static_assert(RS == 8 || RS == 4, "reads after the last of this step");
-    if constexpr (RS == 8)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(4)\n\ts_barrier" ::"n"(kCopies) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(3)\n\ts_barrier" ::"n"(kCopies) : "memory");
+#pragma unroll
+    for (int m = 0; m < RS - 2; ++m) {
+      if (m + kAhead < RS) token(S, 1, m + kAhead);
+      products(1, m);
+    }
+    // Every wave has read this step, and the next one is in LDS.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    load(S);
+    token(Sn, 0, 0);
+    token(Sn, 0, 1);
+    output(Sn, 0, 0);
+    output(Sn, 0, 1);
+    products(1, RS - 2);
+    token(Sn, 0, 2);
+    output(Sn, 0, 2);
+    output(Sn, 0, 3);
+    products(1, RS - 1);
   };
-  for (int g = 0;; g += 4) {
+  for (int g = 0;; g += 2) {
     step(std::integral_constant<int, 0>{});
     if (g + 1 >= G) break;
     step(std::integral_constant<int, 1>{});
     if (g + 2 >= G) break;
-    step(std::integral_constant<int, 2>{});
-    if (g + 3 >= G) break;
-    step(std::integral_constant<int, 3>{});
-    if (g + 4 >= G) break;
   }
-  // (the last copies and reads of the ring end here, in every wave)
+  // (the last copies and reads of the stages end here, in every wave)
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // lane: token c16 of each subtile, outputs 4 kb .. 4 kb + 3 of each sixteen;
@@ -456,10 +483,10 @@ hipError_t launch_vector_parts(const Int8Args& a, hipStream_t s) {
   return launch_vector<T, 1>(a, s);
 }
 
-template <int MS, int CT, int D>
+template <int MS, int CT, int D, int W>
 hipError_t launch_split(const Int8Args& a, hipStream_t s) {
   const int64_t units = (int64_t)((a.T + 16 * MS - 1) / (16 * MS)) * ((a.N + 16 * CT - 1) / (16 * CT));
-  hipLaunchKernelGGL((int8_split_kernel<MS, CT, D>), dim3((unsigned)((units + 7) / 8 * 8)), dim3(kIThreads), 0, s, a);
+  hipLaunchKernelGGL((int8_split_kernel<MS, CT, D, W>), dim3((unsigned)((units + 7) / 8 * 8)), dim3(64 * W), 0, s, a);
   return hipGetLastError();
 }
 
@@ -481,14 +508,15 @@ struct Tiling {
 
 hipError_t launch_project_int8(const Int8Args& in, hipStream_t s) {
   // Small tiles start fastest and lose when there are many, in us: 16 tokens by
-  // 4096 outputs 4.9 in 16 x 16 tiles, 5.8 in 32 x 32, 8.1 in 64 x 64; 16 by
-  // 12288 11.2, 11.6 and 11.0 (16 x 64: 9.8); 64 by 4096 8.5, 6.6, 9.3; 256 by
-  // 4096 33, 16, 11.2 and 18 in 128 x 256; 512 by 12288 59 in 64 x 64, 27 in 128
-  // x 256, 34 in 256 x 256; 4096 by 12288 482, 159, 117.
+  // 4096 outputs 4.5 in 16 x 16 tiles, 5.0 in 32 x 32, 7.2 in 64 x 64; 16 by 12288
+  // 8.9, 9.3, 9.4 (16 x 64: 7.8); 64 by 4096 7.3, 5.2, 7.5; 256 by 4096 19, 11, 7.9
+  // and 18 in 128 x 256; 512 by 12288 43 in 64 x 64, 26 in 128 x 256, 33 in 256 x
+  // 256; 4096 by 12288 369, 154, 113.
   static const Tiling tilings[] = {
-      {16, 16, 28, 19, launch_split<1, 1, 2>}, {16, 32, 35, 20, launch_split<1, 2, 2>}, {16, 64, 30, 40, launch_split<1, 4, 2>},
-      {32, 32, 27, 39, launch_split<2, 2, 2>}, {32, 64, 20, 54, launch_split<2, 4, 2>}, {64, 64, 0, 100, launch_split<4, 4, 2>},
-      {128, 256, 0, 260, launch_tile<4>},      {256, 256, 0, 385, launch_tile<8>},
+      {16, 16, 30, 10, launch_split<1, 1, 2, 4>}, {16, 32, 33, 14, launch_split<1, 2, 2, 4>},
+      {16, 64, 30, 24, launch_split<1, 4, 2, 4>}, {32, 32, 33, 19, launch_split<2, 2, 2, 4>},
+      {32, 64, 20, 41, launch_split<2, 4, 2, 4>}, {64, 64, 8, 71, launch_split<4, 4, 2, 4>},
+      {128, 256, 0, 257, launch_tile<4>},         {256, 256, 0, 372, launch_tile<8>},
   };
   Int8Args a = in;
   const int eb = a.dtype == kNormF32 ? 4 : 2;
