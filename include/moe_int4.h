@@ -518,7 +518,10 @@ typedef struct {
  * n_seqs <= 65536, T <= 2^30. States, sums and decays are fp32 or more; the
  * state's update keeps 24 significant bits of v's decayed rows, and for o the
  * state and the decayed products of q and k are rounded to bf16 as operands
- * of the matrix cores (o's own type). ws 16-byte aligned, of
+ * of the matrix cores (o's own type). |v| is below 2^120. A NaN or infinity in
+ * a token's row reaches that token's o and, from k, v or g, the later ones of
+ * its sequence and its state (as NaN or infinity; from v in its own column
+ * only), nothing else. ws 16-byte aligned, of
  * moe_linear_workspace_bytes (null where that is 0); its contents do not
  * matter, and a workspace for T tokens and n_seqs serves fewer. o must not
  * overlap any input. n_seqs = 0 is a no-op. */

@@ -121,6 +121,7 @@ constexpr int kNowhere = INT32_MIN;  // a buffer offset past every end: such loa
 constexpr float kLog2e = 1.44269504f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // 16 or 4 bytes a lane straight to LDS (from dst on, lane after lane), as
 // assembly: before a transposing read of LDS the compiler waits for every copy
@@ -461,6 +462,10 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     });
   };
   const int64_t head_state = (int64_t)a.qk_dim * a.v_dim;
+  auto state_operand = [&](int s, int n) {
+    const f32x4 x = S[2 * s][n], y = S[2 * s + 1][n];
+    return u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+  };
 
   // (the copy, where a later window's block may have written the state by now)
   auto first_state = [&](const Item& it) {
@@ -506,6 +511,15 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     const int c = wave * NT * 16 + (NT == 2 ? 16 * (g4 & 1) : 0) + 8 * (g4 >> 1);
     store_at[i] = c < cols ? (uint32_t)(row * (int)(a.ldo * 2) + c * 2) : (uint32_t)kNowhere;
   }
+  auto keep_out = [&](const f32x4 (&o)[2][NT]) {
+    auto packed = [](const f32x4& v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
+    if constexpr (NT == 2) {
+      out[0] = side_by_side(packed(o[0][0]), packed(o[0][1]));
+      out[1] = side_by_side(packed(o[1][0]), packed(o[1][1]));
+    } else {
+      out[0] = side_by_side(packed(o[0][0]), packed(o[1][0]));
+    }
+  };
   auto store_out = [&] {
     if constexpr (STATE) return;
     const rsrc_t r = make_rsrc(a.o + written.t0 * a.ldo + (int64_t)head * a.v_dim + col0, records(written, a.ldo, cols));
@@ -549,6 +563,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       const u32x2 lo = column4(p), hi = column4(p + 16 * RV * 16);
       vf[n] = u32x4{lo.x, lo.y, hi.x, hi.y};
     }
+    u32x4 pa0, pa1;
     if constexpr (!STATE) {
       // queries, and their products with the keys: rows (keys) x columns (queries)
       u32x4 qf[2][DK / 32];
@@ -574,8 +589,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const f32x4 x = S[2 * s][n], y = S[2 * s + 1][n];
-          const u32x4 sb = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+          const u32x4 sb = state_operand(s, n);
           oa[0][n] = mfma16(sb, qf[0][s], oa[0][n]);
           oa[1][n] = mfma16(sb, qf[1][s], oa[1][n]);
         }
@@ -591,9 +605,9 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       }
       // (the scale's sign, in both halves)
       const uint32_t flip = sign | sign >> 16;
-      const u32x4 pa0 = {pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
-      const u32x4 pa1 = {pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
-                         pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
+      pa0 = u32x4{pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
+      pa1 = u32x4{pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
+                  pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
       const float fs = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f_before)) ^ sign);
       const float e0 = __builtin_amdgcn_exp2f(Gi0) * fs, e1 = __builtin_amdgcn_exp2f(Gi1) * fs;
 #pragma unroll
@@ -601,13 +615,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
         oa[0][n] = mfma16(vf[n], pa0, oa[0][n] * e0);
         oa[1][n] = mfma16(vf[n], pa1, oa[1][n] * e1);
       }
-      auto packed = [](const f32x4& v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
-      if constexpr (NT == 2) {
-        out[0] = side_by_side(packed(oa[0][0]), packed(oa[0][1]));
-        out[1] = side_by_side(packed(oa[1][0]), packed(oa[1][1]));
-      } else {
-        out[0] = side_by_side(packed(oa[0][0]), packed(oa[1][0]));
-      }
+      keep_out(oa);
       written = q0;
     }
     if constexpr (STATE) ahead();
@@ -631,9 +639,64 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
         }
     }
     if constexpr (STATE) sum += D.total;
-    if (!keeps(decayed)) {
+    // An infinity or NaN among the values met products of zero, which carried it
+    // to earlier tokens: the output is formed again, token after token.
+    bool again = false;
+    if constexpr (!STATE) {
+      u16x2 top = {0, 0};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, vf[n][p] & 0x7FFF7FFFu));
+      again = __ballot(max(top.x, top.y) >= 0x7F80) != 0;
+    }
+    if (again || !keeps(decayed)) {
+      if (!STATE && again) {
+        int q = c16;
+        asm volatile("" : "+v"(q));  // (nothing of this is prepared outside)
+        const float fs = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f_before)) ^ sign);
+        const float e[2] = {__builtin_amdgcn_exp2f(D.Gs[q]) * fs, __builtin_amdgcn_exp2f(D.Gs[16 + q]) * fs};
+        const int at = q * RQ, sw = swizzle<RQ>(q);
+        f32x4 oa[2][NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) oa[0][n] = oa[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s) {
+          const u32x4 q0_ = T.q[at + ((4 * s + g4) ^ sw)], q1_ = T.q[at + ((4 * s + g4) ^ sw) + 16 * RQ];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const u32x4 sb = state_operand(s, n);
+            oa[0][n] = mfma16(sb, q0_, oa[0][n]);
+            oa[1][n] = mfma16(sb, q1_, oa[1][n]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          oa[0][n] = oa[0][n] * e[0];
+          oa[1][n] = oa[1][n] * e[1];
+        }
+#pragma unroll 1
+        for (int j = 0; j < kChunk; ++j) {
+          // token j in an operand: word 2 (j / 16) + j / 2 % 2 of lane group j / 4 % 4
+          const uint32_t half = g4 == (j >> 2 & 3) ? (j & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+          const int word = 2 * (j >> 4) + (j >> 1 & 1);
+          auto only = [&](const u32x4& x) {
+            return u32x4{word == 0 ? x.x & half : 0u, word == 1 ? x.y & half : 0u, word == 2 ? x.z & half : 0u, word == 3 ? x.w & half : 0u};
+          };
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const f32x4 y0 = mfma16(only(vf[n]), only(pa0), oa[0][n]), y1 = mfma16(only(vf[n]), only(pa1), oa[1][n]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              oa[0][n][r] = q >= j ? y0[r] : oa[0][n][r];
+              oa[1][n][r] = 16 + q >= j ? y1[r] : oa[1][n][r];
+            }
+          }
+        }
+        keep_out(oa);
+      }
       asm volatile("");  // (keeps the products in the branch)
-      const float by = __builtin_amdgcn_exp2f(decayed);
+      const float by = keeps(decayed) ? 1.f : __builtin_amdgcn_exp2f(decayed);
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i)
 #pragma unroll

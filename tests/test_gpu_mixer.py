@@ -81,7 +81,7 @@ INT8_CASES = [
     dict(T=257, N=4097, K=192, dtype="f32"), dict(T=500, N=2000, K=4096, dtype="f16", bias=True, pad=64),
     dict(T=600, N=1536, K=2048, pad=32), dict(T=1000, N=2048, K=1024), dict(T=1025, N=6000, K=704, ypad=2),
     dict(T=2049, N=2304, K=512), dict(T=4096, N=4096, K=128), dict(T=5, N=300, K=65536), dict(T=300, N=320, K=16384),
-    dict(T=3, N=1 << 18, K=64), dict(T=40000, N=48, K=64), dict(T=1, N=40, K=65536, extreme=True, dtype="f32"),
+    dict(T=3, N=1 << 18, K=64), dict(T=40000, N=48, K=64), dict(T=(1 << 18) + 37, N=16, K=64, ypad=2), dict(T=1, N=40, K=65536, extreme=True, dtype="f32"),
     dict(T=300, N=300, K=65536, extreme=True, dtype="f32"), dict(T=20, N=80, K=65536, extreme=True),
 ]
 
@@ -283,7 +283,12 @@ LINEAR_CASES = [
     dict(lengths=[70, 3, 0, 65], slots=[-1, 2, 99, 2]), dict(lengths=[70, 3, 0, 65], slots=[5, 1, 0, 2], inplace=True),
     dict(lengths=[700, 3, 400], slots=[1, -1, 3], inplace=True, Hv=2), dict(lengths=[100, 20], start=False),
     dict(lengths=[100, 20], keep=False), dict(lengths=[600, 20], start=False, keep=False),
-    dict(lengths=[128], scale=1.0, strong=0.1), dict(lengths=[400], scale=-0.5, strong=0.5),
+    dict(lengths=[128], scale=1.0, strong=0.1), dict(lengths=[400], scale=-0.5, strong=0.5), dict(lengths=[70], scale=0.0),
+    # many sequences, short ones beside long ones, in place and not
+    dict(lengths=[1] * 20 + [300] + [8, 9, 0, 7] + [2] * 9), dict(lengths=[5, 600, 0, 8, 0, 9, 1, 1, 64, 3], inplace=True, Hv=2),
+    dict(lengths=[0] * 9), dict(lengths=[0] * 9, behind=2, inplace=True), dict(lengths=[3] * 12, slots=[-1, 13] + [4] * 10, behind=5),
+    dict(lengths=[20] * 100, Hk=1, Hv=2, dk=32, dv=64), dict(lengths=[0, 33, 8, 15, 1, 40] * 30, Hk=1, Hv=2, dk=64, dv=32, inplace=True),
+    dict(lengths=[8] * 70 + [400], Hk=1, Hv=1, dk=32, dv=32), dict(lengths=[1] * 130, Hk=1, Hv=2, dk=40, dv=72, per_token=False),
 ]
 
 
@@ -338,6 +343,40 @@ def test_linear_nan_stays_in_its_head_and_sequence():
     assert torch.equal(o1[:, 1], o0[:, 1]) and torch.equal(o1[70:], o0[70:]) and torch.equal(o1[:40, 0], o0[:40, 0])
     assert o1[40:70, 0].isnan().all() and S1[0, 0].isnan().all()
     assert torch.equal(S1[1], S0[1]) and torch.equal(S1[0, 1], S0[0, 1])
+
+
+@pytest.mark.parametrize("D,Hv,value", [(64, 2, math.nan), (64, 2, math.inf), (128, 2, -math.inf), (40, 1, math.nan), (256, 1, math.inf)])
+def test_linear_not_finite_values_reach_no_earlier_token(D, Hv, value):
+    """A NaN or infinity of one token's value, key or query reaches that token and, but for the query, its later ones,
+    never an earlier token, another sequence or (a value) another column."""
+    T, at = 200, 75
+    q, k, v, g = _linear_inputs(T, Hv, Hv, D, D, True, 17)
+    plan, cu = B.linear_attention(Hv, Hv, D, D), torch.tensor([0, 50, 150, 200], dtype=torch.int32, device="cuda")
+    ws = B.linear_attention_workspace(plan, 3, T)
+
+    def run(q, k, v):
+        o, S = torch.empty((T, Hv, D), dtype=torch.bfloat16, device="cuda"), torch.empty((3, Hv, D, D), device="cuda")
+        B.moe_linear_attention(plan, q.cuda(), k.cuda(), v.cuda(), g.cuda(), o, cu, T, state_out=S, ws=ws)
+        return o.cpu(), S.cpu()
+    o0, S0 = run(q, k, v)
+    for which in range(3):
+        bad = [t.clone() for t in (q, k, v)]
+        bad[which][at, 0, 5] = value
+        o, S = run(*bad)
+        same = torch.ones((T, Hv, D), dtype=torch.bool)
+        if which == 0:
+            same[at, 0] = False
+        elif which == 1:
+            same[at:150, 0] = False
+        else:
+            same[at:150, 0, 5] = False
+        assert torch.equal(o[same], o0[same]), which
+        assert not o[~same].isfinite().any(), which
+        assert torch.equal(S[[0, 2]], S0[[0, 2]])
+        if which == 0:
+            assert torch.equal(S, S0)
+        elif which == 2:
+            assert not S[1, 0, :, 5].isfinite().any() and torch.equal(S[1, 0, :, :5], S0[1, 0, :, :5])
 
 
 def test_linear_offsets_out_of_order_stay_in_range():
