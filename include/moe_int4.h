@@ -505,7 +505,8 @@ typedef struct {
  * heads contiguous within rows of strides ldq, ldk, ldv, ldo (elements,
  * multiples of 8, at most 2^20). g = log_decay, fp32: [T][v_heads] with row
  * stride ld_decay (v_heads..2^20), or [v_heads] for all tokens with ld_decay
- * 0. Any g is allowed: -inf forgets everything before the token.
+ * 0. A g of -inf forgets everything before the token; where g is above 0, exp
+ * of its sum over a sequence has to be finite.
  * Sequence i holds the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
  * (device, int32 [n_seqs + 1], not decreasing, from 0; values are limited to
  * 0..T); rows of o behind the last are left as they were. Its state starts as

@@ -227,9 +227,10 @@ struct LinearArgs {
   int64_t ldq, ldk, ldv, ldo, ld_decay;
   int n_seqs, n_in, n_out, T, qk_heads, v_heads, qk_dim, v_dim;
   float scale;
-  // set by the launcher: tokens of a window and how many windows; whether the
-  // states that sequences over several windows start from are copied
-  int window, windows, copied;
+  // set by the launcher: tokens of a window, how many windows, and over how many
+  // blocks the sequences of a single one are spread; whether the states that
+  // sequences over several windows start from are copied
+  int window, windows, strands, copied;
   int short_tokens;  // sequences of at most so many tokens are walked through
 };
 size_t linear_ws_bytes(const LinearArgs& a);

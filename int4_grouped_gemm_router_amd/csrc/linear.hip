@@ -244,19 +244,20 @@ struct Sequences {
   }
 };
 
-// The chunks of window w, one after the other.
+// The chunks of window w, one after the other; of one window, those of every
+// a.strands-th sequence.
 struct Walk {
   Sequences s;
-  int begin, end, seq, pos, stop, flags;
+  int begin, end, seq, of, pos, stop, flags;  // of: the chunks' sequence, seq: the next one
   bool last_window, open;
-  __device__ Walk(const LinearArgs& a, int w) {
+  __device__ Walk(const LinearArgs& a, int w, int strand) {
     begin = w * a.window;
     last_window = w == a.windows - 1;
     end = min(begin + a.window, a.T);
     s.load(a, 0);
-    seq = begin > 0 ? s.before(a, begin) : 0;
+    seq = begin > 0 ? s.before(a, begin) : strand;
     open = false;
-    pos = stop = flags = 0;
+    of = pos = stop = flags = 0;
   }
   __device__ Item next(const LinearArgs& a) {
     while (!open) {
@@ -264,12 +265,13 @@ struct Walk {
       s.hold(a, seq);
       const int b = s.begin(seq), e = s.end(seq);
       if (b >= end && !last_window) return Item{0, 0, -1, -1, 0};
-      ++seq;
+      of = seq;
+      seq += a.strands;
       if (b < begin && e <= begin) continue;      // before the window
       if (e - b <= a.short_tokens) continue;      // the other kernel's
       if (b == e) {
         // no token: its state only moves, if it does
-        const int si = s.slot_in(seq - 1), so = s.slot_out(seq - 1);
+        const int si = s.slot_in(of), so = s.slot_out(of);
         if (so < 0 || (a.state_in == a.state_out && si == so)) continue;
         return Item{0, 0, si, so, kItem | kFirst | kLast};
       }
@@ -278,7 +280,7 @@ struct Walk {
       stop = min(e, end);
       flags = kItem | kFirst | (b < begin ? kMiddle : 0) | (e <= end ? kLast : kGoesOn);
     }
-    Item it{pos, min(kChunk, stop - pos), s.slot_in(seq - 1), s.slot_out(seq - 1), flags & ~kLast};
+    Item it{pos, min(kChunk, stop - pos), s.slot_in(of), s.slot_out(of), flags & ~kLast};
     pos += it.count;
     if (pos >= stop) {
       it.flags |= flags & kLast;
@@ -342,14 +344,15 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   const int c16 = lane & 15, g4 = lane >> 4;
   const int slices = (a.v_dim + kCols - 1) / kCols;
   // heads that share queries and keys, and slices of a head, follow each other in one XCD
-  const int units = (STATE ? a.windows - 1 : a.windows) * a.v_heads * slices;
+  const int units = (STATE ? a.windows - 1 : a.windows * a.strands) * a.v_heads * slices;
   const int per = (units + 7) / 8, u = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per || u >= units) return;
-  const int slice = u % slices, head = u / slices % a.v_heads, w = u / slices / a.v_heads;
+  const int slice = u % slices, head = u / slices % a.v_heads, part_of = u / slices / a.v_heads;
+  const int w = a.strands > 1 ? 0 : part_of, strand = a.strands > 1 ? part_of : 0;
   const int kh = head / (a.v_heads / a.qk_heads), col0 = slice * kCols, cols = min(kCols, a.v_dim - col0);
   const Passed ps = passed(a);
 
-  Walk walk(a, w);
+  Walk walk(a, w, strand);
   float sum = 0.f;  // of the window's logarithms (STATE)
   if constexpr (STATE) {
     // the sequence with tokens on both sides of the window's end
@@ -807,22 +810,36 @@ namespace {
 
 constexpr int kManySeqs = 8, kShortTokens = 8;
 
-int chunk_cols(const LinearArgs& a) { return a.qk_dim > 128 || a.v_dim <= 64 ? 64 : 128; }
+// Columns of a state a block holds. Half of them where that fills the chip
+// better than it costs in keys and queries read again: turns, states and their
+// passing take less time. 128 x 128, 128 columns against 64: 4 heads of 150
+// tokens 20.4, 16.2 us, of 16384 88, 69; 32 heads of 600 tokens 42.9, 37.9, of
+// 1777 56.5, 51.0, of 4096 75.7, 82.2; 64 heads of 1100 tokens 67.1, 62.3, of
+// 1777 79.0, 80.2; 12 heads of 4096 tokens 56.3, 52.3, of 16384 102, 112.
+int chunk_cols(const LinearArgs& a, int64_t T) {
+  return a.qk_dim > 128 || a.v_dim <= 64 || T * a.v_heads <= 96 * 1024 ? 64 : 128;
+}
 // Windows for T tokens: enough for two blocks on each compute unit, of 64 tokens
-// at least, of 128 from 1024 tokens on, and one for up to 256 tokens, where two
-// launches more cost more than they save. 32 heads of 128 x 128, one window,
-// windows of 64, of 128, of 256: 256 tokens 23, 28, 34, 23 us; 512 tokens 42, 33,
-// 35, 48; 1024 tokens 79, 45, 40, 49; 2048 tokens 152, 56, 55, 54.
+// at least, of 128 from 1024 tokens on; one for few tokens, where two launches
+// more cost more than they save, the more so the more heads the windows' states
+// are passed for. One sequence of heads of 128 x 128, one window against
+// windows: 12 heads of 257 tokens 20.2, 22.7 us, of 320 22.1, 23.0, of 384 25.4,
+// 23.9; 32 heads of 384 tokens 26.1, 30.1, of 512 33.3, 31.6; 64 heads of 640
+// tokens 40.8, 44.4, of 768 47.6, 47.3. Windows of at least 64, 96, 128 tokens:
+// 32 heads of 600 tokens 43, 39, 41 us; 16 heads of 4096 tokens 60, 60, 59.
 int most_windows(const LinearArgs& a, int64_t T) {
-  const int per = a.v_heads * ((a.v_dim + chunk_cols(a) - 1) / chunk_cols(a));
+  const int per = a.v_heads * ((a.v_dim + chunk_cols(a, T) - 1) / chunk_cols(a, T));
   const int64_t least = T < 1024 ? 64 : 128;
-  if (T <= 256) return 1;
+  if (T <= 256 + 4 * std::min(per, 128)) return 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::max(1, kMaxWindows / per), (T + least - 1) / least));
 }
 void set_windows(LinearArgs& a) {
   const int most = most_windows(a, a.T);
   a.window = (int)((((int64_t)a.T + most - 1) / most + kChunk - 1) / kChunk * kChunk);
   a.windows = std::max(1, (a.T + a.window - 1) / std::max(a.window, 1));
+  // one window's sequences need not follow each other
+  const int per = a.v_heads * ((a.v_dim + chunk_cols(a, a.T) - 1) / chunk_cols(a, a.T));
+  a.strands = a.windows > 1 ? 1 : std::max(1, std::min(a.n_seqs, kMaxWindows / per));
 }
 
 template <int DK, int NT>
@@ -833,7 +850,7 @@ hipError_t launch_chunks(const LinearArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, true>), grid((a.windows - 1) * per), dim3(256), 0, s, a);
     hipLaunchKernelGGL(linear_pass_kernel, dim3((a.qk_dim * a.v_dim + 1023) / 1024, a.v_heads), dim3(256), 0, s, a);
   }
-  hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, false>), grid(a.windows * per), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, false>), grid(a.windows * a.strands * per), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -873,7 +890,7 @@ hipError_t launch_linear_attention(const LinearArgs& in, hipStream_t s) {
   const uintptr_t bytes = 4 * (uintptr_t)state_values(a);
   a.copied = a.windows > 1 && a.state_in && a.state_out && ib < ob + a.n_out * bytes && ob < ib + a.n_in * bytes;
   if (a.qk_dim > 128) return launch_chunks<256, 1>(a, s);
-  if (a.v_dim <= 64) return a.qk_dim <= 64 ? launch_chunks<64, 1>(a, s) : launch_chunks<128, 1>(a, s);
+  if (chunk_cols(a, a.T) == 64) return a.qk_dim <= 64 ? launch_chunks<64, 1>(a, s) : launch_chunks<128, 1>(a, s);
   return a.qk_dim <= 64 ? launch_chunks<64, 2>(a, s) : launch_chunks<128, 2>(a, s);
 }
 

@@ -287,7 +287,7 @@ LINEAR_CASES = [
     # many sequences, short ones beside long ones, in place and not
     dict(lengths=[1] * 20 + [300] + [8, 9, 0, 7] + [2] * 9), dict(lengths=[5, 600, 0, 8, 0, 9, 1, 1, 64, 3], inplace=True, Hv=2),
     dict(lengths=[0] * 9), dict(lengths=[0] * 9, behind=2, inplace=True), dict(lengths=[3] * 12, slots=[-1, 13] + [4] * 10, behind=5),
-    dict(lengths=[20] * 100, Hk=1, Hv=2, dk=32, dv=64), dict(lengths=[0, 33, 8, 15, 1, 40] * 30, Hk=1, Hv=2, dk=64, dv=32, inplace=True),
+    dict(lengths=[20] * 100, Hk=1, Hv=2, dk=32, dv=64), dict(lengths=[9] * 28, dk=32, dv=72, slots=[27] * 3 + [-1] * 25), dict(lengths=[0, 11, 0, 0, 9, 200, 8], Hk=1, Hv=2, inplace=True), dict(lengths=[0, 33, 8, 15, 1, 40] * 30, Hk=1, Hv=2, dk=64, dv=32, inplace=True),
     dict(lengths=[8] * 70 + [400], Hk=1, Hv=1, dk=32, dv=32), dict(lengths=[1] * 130, Hk=1, Hv=2, dk=40, dv=72, per_token=False),
 ]
 
