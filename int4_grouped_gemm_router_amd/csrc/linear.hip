@@ -116,6 +116,7 @@ __global__ __launch_bounds__(256) void linear_walk_kernel(LinearArgs a) {
 namespace {
 
 constexpr int kChunk = 32;
+constexpr int kChunkThreads = 320;  // four waves that compute, one that fetches for them
 constexpr int kMaxWindows = 512;
 constexpr int kNowhere = INT32_MIN;  // a buffer offset past every end: such loads give zeros
 constexpr float kLog2e = 1.44269504f;
@@ -155,25 +156,25 @@ __device__ inline int swizzle(int r) {
   return R >= 16 ? 2 * (r & 7) | (r >> 3 & 1) : 2 * (r >> 1 & 3) | (r >> 3 & 1);
 }
 
-// A tensor's 32 rows as the lanes of a wave copy them to LDS, 64 pieces an
-// instruction; wave w takes every fourth instruction.
+// A tensor's 32 rows as the lanes of one wave copy them to LDS, 64 pieces an
+// instruction.
 template <int R>
 struct RowCopy {
-  static constexpr int kN = kChunk * R / 256;  // instructions a wave
+  static constexpr int kN = kChunk * R / 64;  // instructions
   int off[kN];
-  __device__ void init(int wave, int lane, int dim, int64_t ld) {
+  __device__ void init(int lane, int dim, int64_t ld) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int slot = 64 * (4 * i + wave) + lane, row = slot / R, c = (slot % R) ^ swizzle<R>(row);
+      const int slot = 64 * i + lane, row = slot / R, c = (slot % R) ^ swizzle<R>(row);
       off[i] = 8 * c < dim ? row * (int)(ld * 2) + 16 * c : kNowhere;
     }
   }
   // base: the first row's values; records: bytes up to the end of the last row's
-  __device__ void issue(u32x4* dst, const uint16_t* base, uint32_t records, int wave) const {
+  __device__ void issue(u32x4* dst, const uint16_t* base, uint32_t records) const {
     const u32x4 r = words_of(base, records);
-    const uint32_t to = lds_offset(dst) + 1024 * wave;
+    const uint32_t to = lds_offset(dst);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) copy16_to_lds(r, to + 4096 * i, (uint32_t)off[i]);
+    for (int i = 0; i < kN; ++i) copy16_to_lds(r, to + 1024 * i, (uint32_t)off[i]);
   }
 };
 
@@ -259,7 +260,7 @@ struct Walk {
     open = false;
     of = pos = stop = flags = 0;
   }
-  __device__ Item next(const LinearArgs& a) {
+  __device__ __forceinline__ Item next(const LinearArgs& a) {
     while (!open) {
       if (seq >= a.n_seqs) return Item{0, 0, -1, -1, 0};
       s.hold(a, seq);
@@ -320,13 +321,21 @@ __host__ __device__ inline Passed passed(const LinearArgs& a) {
 // O is formed as its transpose. S is a matrix operand as it lies in the
 // accumulators: of each 32 rows lane group g holds rows 8 g .. 8 g + 7, the ones
 // that a matrix operand wants of it, because the keys enter the update with
-// their columns in that order. So are the
-// decayed products of queries and keys, which every wave forms for itself (12
-// of its 80 matrix operations a chunk) so that nothing but the rows goes
-// through LDS. STATE: only S, from zeros, of the sequence that goes on behind
-// the window.
+// their columns in that order. So are the decayed products of queries and keys,
+// which every wave forms for itself (12 of its 76 matrix operations a chunk), so
+// that nothing but the rows goes through LDS. A fifth wave walks over the
+// sequences, copies rows two chunks ahead and forms the decays of the next
+// chunk; the four wait for nothing but it, once a chunk. (With that work spread
+// over the four, a chunk of a lone block took 1.7 us instead of 1.1; 16 heads of
+// 300 tokens 21.7, 15.8 us, 32 heads of 16384 tokens alike.) STATE: only S, from
+// zeros, of the sequence that goes on behind the window.
+//
+// Latency bounds it: 16384 tokens of 32 heads of 128 x 128 in 16 windows take 61,
+// 13 and 125 us for the states, their passing and the outputs, which move 0.18,
+// 0.05 and 0.46 GB (3.0 to 3.8 TB/s); matrix cores are busy 0.22 of the time,
+// vector instructions issue in 0.31 of it, LDS is read in 0.17.
 template <int DK, int NT, int ST, bool STATE>
-__global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
+__global__ __launch_bounds__(kChunkThreads, DK == 128 ? 3 : 2) void linear_chunk_kernel(LinearArgs a) {
   constexpr int RQ = DK / 8, RV = 8 * NT, kCols = 64 * NT;
   __shared__ struct {
     struct {
@@ -338,7 +347,10 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       float w[kChunk];              // e^(G_n - G_j) over the state's factor after the chunk
       float total;                  // G_n
     } dec[2];
+    Item item[4];
   } L;
+  // (three waves a SIMD leave 168 registers each)
+  constexpr bool kTight = DK == 128 && NT == 2 && !STATE;
   static_assert(ST == 3, "tile c + 2 goes where tile c - 1 was");
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
@@ -352,83 +364,130 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   const int kh = head / (a.v_heads / a.qk_heads), col0 = slice * kCols, cols = min(kCols, a.v_dim - col0);
   const Passed ps = passed(a);
 
-  Walk walk(a, w, strand);
-  float sum = 0.f;  // of the window's logarithms (STATE)
-  if constexpr (STATE) {
-    // the sequence with tokens on both sides of the window's end
-    const int i = walk.s.before(a, walk.end), b = walk.s.begin(i);
-    const bool goes_on = b < walk.end && walk.s.end(i) > walk.end && walk.s.end(i) - b > a.short_tokens;
-    const int si = walk.s.slot_in(i);
-    if (head == 0 && slice == 0 && tid == 0) {
-      ps.meta[4 * w] = goes_on;
-      ps.meta[4 * w + 1] = b >= walk.begin;
-      ps.meta[4 * w + 2] = si;
-    }
-    if (!goes_on) return;
-    walk.seq = i;
-  }
-  const uint16_t* qb = a.q + (int64_t)kh * a.qk_dim;
-  const uint16_t* kb = a.k + (int64_t)kh * a.qk_dim;
-  const uint16_t* vb = a.v + (int64_t)head * a.v_dim + col0;
-  RowCopy<RQ> cq, ck;
-  RowCopy<RV> cv;
-  if constexpr (!STATE) cq.init(wave, lane, a.qk_dim, a.ldq);
-  ck.init(wave, lane, a.qk_dim, a.ldk);
-  cv.init(wave, lane, cols, a.ldv);
-  constexpr int kLoads = (STATE ? 1 : 2) * RowCopy<RQ>::kN + RowCopy<RV>::kN;
-
   auto records = [](const Item& it, int64_t ld, int dim) {
     return it.count ? (uint32_t)(((it.count - 1) * ld + dim) * 2) : 0u;
   };
-  // (every item, also one that is not there, has the same number of loads: the waits count on it)
-  auto load_tile = [&](const Item& it, int st) {
-    const int64_t t = it.t0;
-    if constexpr (!STATE) cq.issue(L.tile[st].q, qb + t * a.ldq, records(it, a.ldq, a.qk_dim), wave);
-    ck.issue(L.tile[st].k, kb + t * a.ldk, records(it, a.ldk, a.qk_dim), wave);
-    cv.issue(L.tile[st].v, vb + t * a.ldv, records(it, a.ldv, cols), wave);
-  };
-  auto load_g = [&](const Item& it, int slot) {
-    if (wave != 0) return;
-    const u32x4 r = words_of(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
-    copy4_to_lds(r, lds_offset(L.g[slot]), lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
-  };
-  // The chunk's sums in base 2. A weight's exponent is a sum from its own token
-  // on, so that small ones are precise beside large ones; the sums from the
-  // front weigh products that are rounded to bf16. 2^-288 and less is 0 here.
-  const float log_scale = __log2f(fabsf(a.scale));
-  const uint32_t sign = __float_as_uint(a.scale) & 0x80000000u;
-  auto decays = [&](int slot, int to, float lf) {
-    float g = L.g[slot][lane] * kLog2e;
-    g = g < -288.f ? -288.f : g;
-    const float front = g + shifted<0x111>(g);  // of this lane and up to 1, 3, 7, 15 before it, in rows of sixteen
-    float G = front + shifted<0x112>(front);
-    G += shifted<0x114>(G);
-    G += shifted<0x118>(G);
-    float R = g + shifted<0x101>(g);  // of this lane and up to 1, 3, 7, 15 behind it, then without this lane
-    R += shifted<0x102>(R);
-    R += shifted<0x104>(R);
-    R += shifted<0x108>(R);
-    R = shifted<0x101>(R);
-    const float first = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 15));
-    const float second = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 31));
-    if (lane >= 16) G += first;
-    if (lane < 16) R += second;
-    const float total = first + second;
-    if (lane < kChunk) {
-      L.dec[to].G[lane] = G;
-      L.dec[to].Gs[lane] = G + log_scale;
-      L.dec[to].w[lane] = __builtin_amdgcn_exp2f(R - factor_after(lf, total));
-      if (lane == 0) L.dec[to].total = total;
+  if (wave == 4) {
+    // The wave that fetches: turn c is between the barriers c and c + 1, in which
+    // the others compute chunk c; in it this one has the copies of chunk c + 2 set
+    // out and forms the decays of chunk c + 1.
+    Walk walk(a, w, strand);
+    bool any = true;
+    if constexpr (STATE) {
+      // the sequence with tokens on both sides of the window's end
+      const int i = walk.s.before(a, walk.end), b = walk.s.begin(i);
+      any = b < walk.end && walk.s.end(i) > walk.end && walk.s.end(i) - b > a.short_tokens;
+      const int si = walk.s.slot_in(i);
+      if (head == 0 && slice == 0 && lane == 0) {
+        ps.meta[4 * w] = any;
+        ps.meta[4 * w + 1] = b >= walk.begin;
+        ps.meta[4 * w + 2] = si;
+      }
+      walk.seq = i;
     }
-  };
+    if (!any) walk.seq = a.n_seqs;  // (no chunk)
+    Item q0 = walk.next(a), q1 = walk.next(a), q2 = walk.next(a), q3;
+    auto pass_on = [&](const Item& it, int slot) {
+      if (lane == 0) L.item[slot] = it;
+    };
+    pass_on(q0, 0);
+    pass_on(q1, 1);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (!(q0.flags & kItem)) return;
+    const uint16_t* qb = a.q + (int64_t)kh * a.qk_dim;
+    const uint16_t* kb = a.k + (int64_t)kh * a.qk_dim;
+    const uint16_t* vb = a.v + (int64_t)head * a.v_dim + col0;
+    RowCopy<RQ> cq, ck;
+    RowCopy<RV> cv;
+    if constexpr (!STATE) cq.init(lane, a.qk_dim, a.ldq);
+    ck.init(lane, a.qk_dim, a.ldk);
+    cv.init(lane, cols, a.ldv);
+    // (every item, also one that is not there, has the same number of copies: the waits count on it)
+    constexpr int kLoads = (STATE ? 1 : 2) * RowCopy<RQ>::kN + RowCopy<RV>::kN;
+    static_assert(kLoads + 1 < 64, "what a wait can count");
+    auto load_tile = [&](const Item& it, int st) {
+      const int64_t t = it.t0;
+      if constexpr (!STATE) cq.issue(L.tile[st].q, qb + t * a.ldq, records(it, a.ldq, a.qk_dim));
+      ck.issue(L.tile[st].k, kb + t * a.ldk, records(it, a.ldk, a.qk_dim));
+      cv.issue(L.tile[st].v, vb + t * a.ldv, records(it, a.ldv, cols));
+    };
+    auto load_g = [&](const Item& it, int slot) {
+      const u32x4 r = words_of(a.decay + it.t0 * a.ld_decay + head, it.count ? (uint32_t)((it.count - 1) * a.ld_decay + 1) * 4u : 0u);
+      copy4_to_lds(r, lds_offset(L.g[slot]), lane < it.count ? (uint32_t)(lane * a.ld_decay) * 4u : (uint32_t)kNowhere);
+    };
+    // The chunk's sums in base 2. A weight's exponent is a sum from its own token
+    // on, so that small ones are precise beside large ones; the sums from the
+    // front weigh products that are rounded to bf16. 2^-288 and less is 0 here.
+    const float log_scale = __log2f(fabsf(a.scale));
+    auto decays = [&](int slot, int to, float lf) -> float {
+      float g = L.g[slot][lane] * kLog2e;
+      g = g < -288.f ? -288.f : g;
+      const float front = g + shifted<0x111>(g);  // of this lane and up to 1, 3, 7, 15 before it, in rows of sixteen
+      float G = front + shifted<0x112>(front);
+      G += shifted<0x114>(G);
+      G += shifted<0x118>(G);
+      float R = g + shifted<0x101>(g);  // of this lane and up to 1, 3, 7, 15 behind it, then without this lane
+      R += shifted<0x102>(R);
+      R += shifted<0x104>(R);
+      R += shifted<0x108>(R);
+      R = shifted<0x101>(R);
+      const float first = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 15));
+      const float second = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, G), 31));
+      if (lane >= 16) G += first;
+      if (lane < 16) R += second;
+      const float total = first + second;
+      if (lane < kChunk) {
+        L.dec[to].G[lane] = G;
+        L.dec[to].Gs[lane] = G + log_scale;
+        L.dec[to].w[lane] = __builtin_amdgcn_exp2f(R - factor_after(lf, total));
+        if (lane == 0) L.dec[to].total = total;
+      }
+      return total;
+    };
 
-  Item q0 = walk.next(a), q1 = walk.next(a), q2 = walk.next(a), q3;
+    load_g(q0, 0);
+    load_g(q1, 1);
+    load_g(q2, 2);
+    load_tile(q0, 0);
+    load_tile(q1, 1);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads > 63 ? 63 : 2 * kLoads) : "memory");
+    float total = decays(0, 0, 0.f), f = 0.f;
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+    int st = 2;
+    for (int c = 0;; ++c) {
+      // Chunk c is in LDS (what was issued after its rows: the decays of chunk
+      // c + 2 and the rows of chunk c + 1).
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads + 1) : "memory");
+      if (!(q1.flags & kItem)) break;
+      pass_on(q2, (c + 2) & 3);
+      q3 = walk.next(a);
+      load_g(q3, (c + 3) & 3);
+      load_tile(q2, st);
+      if (!STATE && (q0.flags & kFirst)) f = 0.f;
+      f = factor_after(f, total);
+      total = decays((c + 1) & 3, (c + 1) & 1, !STATE && (q1.flags & kFirst) ? 0.f : f);
+      q0 = q1;
+      q1 = q2;
+      q2 = q3;
+      st = st == 2 ? 0 : st + 1;
+    }
+    // (the copies into LDS that are under way end before the block does)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return;
+  }
+
+  // The waves that compute, before the one that fetches where they share a SIMD
+  // (16384 tokens of 32 heads 202 -> 199 us).
+  __builtin_amdgcn_s_setprio(2);
+  auto item_of = [&](int slot) {
+    const Item& it = L.item[slot];
+    return Item{uniform(it.t0), uniform(it.count), uniform(it.in), uniform(it.out), uniform(it.flags)};
+  };
+  asm volatile("s_barrier" ::: "memory");
+  Item q0 = item_of(0), q1;
   if (!(q0.flags & kItem)) return;
-  load_g(q0, 0);
-  load_g(q1, 1);
-  load_g(q2, 2);
-  load_tile(q0, 0);
-  load_tile(q1, 1);
+  const uint32_t sign = __float_as_uint(a.scale) & 0x80000000u;
+  float sum = 0.f;  // of the window's logarithms (STATE)
 
   f32x4 S[DK / 16][NT];
 #pragma unroll
@@ -442,7 +501,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
   const uint32_t head_bytes = (uint32_t)(a.qk_dim * a.v_dim * 4);
   auto each_of_state = [&](auto f) {
     // (hidden from the optimiser, which otherwise keeps every element's place in registers over the loop)
-    int row0 = 8 * g4, step = a.v_dim * 4;
+    int row0 = 8 * g4, step = uniform(a.v_dim * 4);
     asm volatile("" : "+v"(row0), "+s"(step));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -483,20 +542,11 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
       each_of_state([](float, uint32_t) { return 0.f; });
   };
   if constexpr (!STATE) first_state(q0);
-  __builtin_amdgcn_s_waitcnt(0);  // (the compiler sees it, as below)
-  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-  if (wave == 0) decays(0, 0, 0.f);
-
-  // The output of a turn, stored in the next. A lane has four columns of two
-  // tiles (of columns, or of tokens where there is one tile of columns); by
-  // exchanging the odd rows of sixteen lanes of the one with the even rows of the
-  // other it has eight neighbouring columns of one, and stores 16 bytes: 4 x 8
-  // bytes a lane instead took 50 us more for 16384 tokens of 32 heads of 128.
-  // Every turn has them, dropped where there is nothing to store: the waits count
-  // on it, so that a turn waits for stores two turns old and not for its last.
-  constexpr int kStores = STATE ? 0 : NT;
-  u32x4 out[NT];
-  Item written{0, 0, 0, 0, 0};
+  // A lane has four columns of two tiles (of columns, or of tokens where there is
+  // one tile of columns); by exchanging the odd rows of sixteen lanes of the one
+  // with the even rows of the other it has eight neighbouring columns of one, and
+  // stores 16 bytes: 4 x 8 bytes a lane instead took 50 us more for 16384 tokens
+  // of 32 heads of 128.
   auto side_by_side = [](u32x2 x, u32x2 y) {
     u32x4 r;
 #pragma unroll
@@ -507,125 +557,148 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     }
     return r;
   };
-  uint32_t store_at[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int row = NT == 2 ? 16 * i + c16 : 16 * (g4 & 1) + c16;
+  uint32_t store_at;
+  {
+    const int row = NT == 2 ? c16 : 16 * (g4 & 1) + c16;
     const int c = wave * NT * 16 + (NT == 2 ? 16 * (g4 & 1) : 0) + 8 * (g4 >> 1);
-    store_at[i] = c < cols ? (uint32_t)(row * (int)(a.ldo * 2) + c * 2) : (uint32_t)kNowhere;
+    store_at = c < cols ? (uint32_t)(row * (int)(a.ldo * 2) + c * 2) : (uint32_t)kNowhere;
   }
-  auto keep_out = [&](const f32x4 (&o)[2][NT]) {
+  auto store_out = [&](const f32x4 (&y)[2][NT]) {
     auto packed = [](const f32x4& v) { return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
-    if constexpr (NT == 2) {
-      out[0] = side_by_side(packed(o[0][0]), packed(o[0][1]));
-      out[1] = side_by_side(packed(o[1][0]), packed(o[1][1]));
-    } else {
-      out[0] = side_by_side(packed(o[0][0]), packed(o[1][0]));
+    uint16_t* o = a.o + q0.t0 * a.ldo + (int64_t)head * a.v_dim + col0;
+    Item rows = q0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const u32x4 out = NT == 2 ? side_by_side(packed(y[i][0]), packed(y[i][NT - 1])) : side_by_side(packed(y[0][0]), packed(y[1][0]));
+      __builtin_amdgcn_raw_buffer_store_b128(out, make_rsrc(o, records(rows, a.ldo, cols)), (int)store_at, 0, 0);
+      o += 16 * a.ldo;
+      rows.count = max(rows.count - 16, 0);
     }
   };
-  auto store_out = [&] {
-    if constexpr (STATE) return;
-    const rsrc_t r = make_rsrc(a.o + written.t0 * a.ldo + (int64_t)head * a.v_dim + col0, records(written, a.ldo, cols));
-#pragma unroll
-    for (int i = 0; i < NT; ++i) __builtin_amdgcn_raw_buffer_store_b128(out[i], r, (int)store_at[i], 0, 0);
-  };
+
+  // Where a lane reads in a tile, in bytes: the keys' columns (row krow, pieces 4 s
+  // + c16 % 4) and the values' (the same row, pieces of this wave's tiles); its
+  // query and key are row c16, pieces 4 s + g4. Steps of s and of tiles change
+  // bits that nothing else sets, also under the swizzle.
+  const int krow = 4 * g4 + (c16 >> 2);
+  const int key_at = 16 * (krow * RQ + ((c16 & 3) ^ swizzle<RQ>(krow)));
+  const int value_at = 16 * (krow * RV + ((2 * NT * wave + (c16 >> 1 & 1)) ^ swizzle<RV>(krow))) + 8 * (c16 & 1);
+  auto piece = [](const u32x4* tile, int at) { return *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(tile) + at); };
 
   int st = 0;
   float f = 0.f;
   for (int c = 0;; ++c) {
-    // Tile c and its decays are in LDS and no wave reads tile c - 1 any more.
-    // (What was issued after tile c's loads may be under way: the stores of two
-    // turns, which follow a turn's loads, and tile c + 1's loads.)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads + 2 * kStores) : "memory");
+    // Tile c and its decays are in LDS, and no wave reads tile c - 1 any more.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (!STATE && c > 0 && (q0.flags & kFirst)) {
       f = 0.f;
       first_state(q0);
-      // (a wait the compiler sees: it has none to add in every turn, which would be for the tiles too)
+      // (a wait the compiler sees: it has none to add in every turn, which would be for the stores too)
       __builtin_amdgcn_s_waitcnt(0);
     }
     const auto& T = L.tile[st];
     const auto& D = L.dec[c & 1];
     const float f_before = f, decayed = f + uniform_f(D.total);
     f = keeps(decayed) ? decayed : 0.f;
-    // what is to come: in the middle of the turn, when the first operands are on their way
-    auto ahead = [&] {
-      q3 = walk.next(a);
-      load_g(q3, (c + 3) & 3);
-      load_tile(q2, st == 0 ? 2 : st - 1);
-      store_out();
-      if (wave == (c & 3)) decays((c + 1) & 3, (c + 1) & 1, !STATE && (q1.flags & kFirst) ? 0.f : f);
-    };
+    q1 = item_of((c + 1) & 3);
 
-    // values and their weights: lane's column, tokens 4 g4 + r and 16 + 4 g4 + r
-    const int vrow = 4 * g4 + (c16 >> 2);
-    u32x4 vf[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int piece = (2 * (wave * NT + n) + (c16 >> 1 & 1)) ^ swizzle<RV>(vrow);
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.v[vrow * RV + piece]) + 8 * (c16 & 1);
+    // (hidden, so that places are formed again in each turn instead of filling registers over the loop)
+    int ka = key_at, va = value_at, row = c16;
+    if constexpr (kTight) asm volatile("" : "+v"(row), "+v"(ka), "+v"(va));
+    int ra = 16 * (row * RQ + (g4 ^ swizzle<RQ>(row)));
+    // values: this lane's column, tokens 4 g4 + r and 16 + 4 g4 + r
+    auto values = [&](int n, int at) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(T.v) + (at ^ 32 * n);
       const u32x2 lo = column4(p), hi = column4(p + 16 * RV * 16);
-      vf[n] = u32x4{lo.x, lo.y, hi.x, hi.y};
-    }
-    u32x4 pa0, pa1;
-    if constexpr (!STATE) {
-      // queries, and their products with the keys: rows (keys) x columns (queries)
-      u32x4 qf[2][DK / 32];
-      f32x4 p00{0.f, 0.f, 0.f, 0.f}, p01 = p00, p11 = p00;
-#pragma unroll
-      for (int s = 0; s < DK / 32; ++s) {
-        const int at = c16 * RQ + ((4 * s + g4) ^ swizzle<RQ>(c16));
-        u32x4 kf[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          qf[h][s] = T.q[at + h * (16 * RQ)];
-          kf[h] = T.k[at + h * (16 * RQ)];
-        }
-        p00 = mfma16(kf[0], qf[0][s], p00);
-        p01 = mfma16(kf[0], qf[1][s], p01);
-        p11 = mfma16(kf[1], qf[1][s], p11);
-      }
-      // the state's part of the output, before this chunk enters the state
-      f32x4 oa[2][NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) oa[0][n] = oa[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < DK / 32; ++s)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const u32x4 sb = state_operand(s, n);
-          oa[0][n] = mfma16(sb, qf[0][s], oa[0][n]);
-          oa[1][n] = mfma16(sb, qf[1][s], oa[1][n]);
-        }
-      ahead();
-      const float Gi0 = D.Gs[c16], Gi1 = D.Gs[16 + c16];
+      return u32x4{lo.x, lo.y, hi.x, hi.y};
+    };
+    // products of the keys (rows) and queries (columns; lane c has two) with their decays, as operands
+    auto decayed_products = [&](const f32x4 (&p)[3], int c, u32x4 (&pa)[2]) {
+      const float Gi0 = D.Gs[c], Gi1 = D.Gs[16 + c];
       const f32x4 Gj0 = *reinterpret_cast<const f32x4*>(&D.G[4 * g4]), Gj1 = *reinterpret_cast<const f32x4*>(&D.G[16 + 4 * g4]);
       float w00[4], w01[4], w11[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        w00[r] = 4 * g4 + r <= c16 ? p00[r] * __builtin_amdgcn_exp2f(Gi0 - Gj0[r]) : 0.f;
-        w01[r] = p01[r] * __builtin_amdgcn_exp2f(Gi1 - Gj0[r]);
-        w11[r] = 4 * g4 + r <= c16 ? p11[r] * __builtin_amdgcn_exp2f(Gi1 - Gj1[r]) : 0.f;
+        w00[r] = 4 * g4 + r <= c ? p[0][r] * __builtin_amdgcn_exp2f(Gi0 - Gj0[r]) : 0.f;
+        w01[r] = p[1][r] * __builtin_amdgcn_exp2f(Gi1 - Gj0[r]);
+        w11[r] = 4 * g4 + r <= c ? p[2][r] * __builtin_amdgcn_exp2f(Gi1 - Gj1[r]) : 0.f;
       }
       // (the scale's sign, in both halves)
       const uint32_t flip = sign | sign >> 16;
-      pa0 = u32x4{pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
-      pa1 = u32x4{pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
-                  pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
+      pa[0] = u32x4{pack_bf16x2(w00[0], w00[1]) ^ flip, pack_bf16x2(w00[2], w00[3]) ^ flip, 0u, 0u};
+      pa[1] = u32x4{pack_bf16x2(w01[0], w01[1]) ^ flip, pack_bf16x2(w01[2], w01[3]) ^ flip,
+                    pack_bf16x2(w11[0], w11[1]) ^ flip, pack_bf16x2(w11[2], w11[3]) ^ flip};
+    };
+    // the state's part of the output, by the decays and the scale
+    auto scaled = [&](f32x4 (&o)[2][NT], int c) {
       const float fs = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f_before)) ^ sign);
-      const float e0 = __builtin_amdgcn_exp2f(Gi0) * fs, e1 = __builtin_amdgcn_exp2f(Gi1) * fs;
+      const float e0 = __builtin_amdgcn_exp2f(D.Gs[c]) * fs, e1 = __builtin_amdgcn_exp2f(D.Gs[16 + c]) * fs;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        oa[0][n] = mfma16(vf[n], pa0, oa[0][n] * e0);
-        oa[1][n] = mfma16(vf[n], pa1, oa[1][n] * e1);
+        o[0][n] = o[0][n] * e0;
+        o[1][n] = o[1][n] * e1;
       }
-      keep_out(oa);
-      written = q0;
+    };
+    // The state's part of the output (rows: columns of the state, columns: queries),
+    // before this chunk enters the state, and the decayed products as operands.
+    auto products = [&](int at0, int c, f32x4 (&oa)[2][NT], u32x4 (&pa)[2]) {
+      f32x4 p[3];
+      p[0] = p[1] = p[2] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) oa[0][n] = oa[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      u32x4 qf[kTight ? 1 : DK / 32][2];
+      auto of_state = [&](int s, const u32x4 (&q)[2]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const u32x4 sb = state_operand(s, n);
+          oa[0][n] = mfma16(sb, q[0], oa[0][n]);
+          oa[1][n] = mfma16(sb, q[1], oa[1][n]);
+        }
+      };
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        const int at = at0 ^ 64 * s;
+        u32x4 q[2], k[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          q[h] = piece(T.q + h * (16 * RQ), at);
+          k[h] = piece(T.k + h * (16 * RQ), at);
+        }
+        p[0] = mfma16(k[0], q[0], p[0]);
+        p[1] = mfma16(k[0], q[1], p[1]);
+        p[2] = mfma16(k[1], q[1], p[2]);
+        if constexpr (kTight) {
+          of_state(s, q);
+        } else {
+          qf[s][0] = q[0];
+          qf[s][1] = q[1];
+        }
+      }
+      if constexpr (!kTight) {
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s) of_state(s, qf[s]);
+      }
+      decayed_products(p, c, pa);
+      scaled(oa, c);
+    };
+    u32x4 vf[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) vf[n] = values(n, va);
+    if constexpr (!STATE) {
+      f32x4 oa[2][NT];
+      u32x4 pa[2];
+      products(ra, c16, oa, pa);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        oa[0][n] = mfma16(vf[n], pa[0], oa[0][n]);
+        oa[1][n] = mfma16(vf[n], pa[1], oa[1][n]);
+      }
+      store_out(oa);
     }
-    if constexpr (STATE) ahead();
     // the chunk enters the state: the decayed values in three bf16 parts, which
     // hold all 24 bits of them
     u32x4 part[NT][3];
-    {
+    auto make_parts = [&] {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[4 * g4]), w1 = *reinterpret_cast<const f32x4*>(&D.w[16 + 4 * g4]);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -640,7 +713,8 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
             for (int e = 0; e < 2 && k < 2; ++e) x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xFFFF0000u);
           }
         }
-    }
+    };
+    if constexpr (!kTight) make_parts();
     if constexpr (STATE) sum += D.total;
     // An infinity or NaN among the values met products of zero, which carried it
     // to earlier tokens: the output is formed again, token after token.
@@ -656,28 +730,13 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     if (again || !keeps(decayed)) {
       if (!STATE && again) {
         int q = c16;
-        asm volatile("" : "+v"(q));  // (nothing of this is prepared outside)
-        const float fs = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f_before)) ^ sign);
-        const float e[2] = {__builtin_amdgcn_exp2f(D.Gs[q]) * fs, __builtin_amdgcn_exp2f(D.Gs[16 + q]) * fs};
-        const int at = q * RQ, sw = swizzle<RQ>(q);
+        asm volatile("" : "+v"(q));  // (nothing of this is prepared or kept outside)
+        asm volatile("" : "+v"(ra), "+v"(va));
         f32x4 oa[2][NT];
+        u32x4 pa[2];
+        products(ra, q, oa, pa);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) oa[0][n] = oa[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < DK / 32; ++s) {
-          const u32x4 q0_ = T.q[at + ((4 * s + g4) ^ sw)], q1_ = T.q[at + ((4 * s + g4) ^ sw) + 16 * RQ];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const u32x4 sb = state_operand(s, n);
-            oa[0][n] = mfma16(sb, q0_, oa[0][n]);
-            oa[1][n] = mfma16(sb, q1_, oa[1][n]);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          oa[0][n] = oa[0][n] * e[0];
-          oa[1][n] = oa[1][n] * e[1];
-        }
+        for (int n = 0; n < NT; ++n) vf[n] = values(n, va);
 #pragma unroll 1
         for (int j = 0; j < kChunk; ++j) {
           // token j in an operand: word 2 (j / 16) + j / 2 % 2 of lane group j / 4 % 4
@@ -688,7 +747,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
           };
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const f32x4 y0 = mfma16(only(vf[n]), only(pa0), oa[0][n]), y1 = mfma16(only(vf[n]), only(pa1), oa[1][n]);
+            const f32x4 y0 = mfma16(only(vf[n]), only(pa[0]), oa[0][n]), y1 = mfma16(only(vf[n]), only(pa[1]), oa[1][n]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               oa[0][n][r] = q >= j ? y0[r] : oa[0][n][r];
@@ -696,7 +755,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
             }
           }
         }
-        keep_out(oa);
+        store_out(oa);
       }
       asm volatile("");  // (keeps the products in the branch)
       const float by = keeps(decayed) ? 1.f : __builtin_amdgcn_exp2f(decayed);
@@ -705,10 +764,10 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) S[i][n] = S[i][n] * by;
     }
-    const int krow = 4 * g4 + (c16 >> 2);
+    if constexpr (kTight) make_parts();
     u32x4 kt[2][2];
     auto columns = [&](int s) {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(&T.k[krow * RQ + ((4 * s + (c16 & 3)) ^ swizzle<RQ>(krow))]);
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(T.k) + (ka ^ 64 * s);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const u32x2 lo = column4(p + 8 * e), hi = column4(p + 8 * e + 16 * RQ * 16);
@@ -733,13 +792,8 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(LinearArgs a) {
     }
     if (!(q1.flags & kItem)) break;
     q0 = q1;
-    q1 = q2;
-    q2 = q3;
     st = st == 2 ? 0 : st + 1;
   }
-  // (the copies into LDS that are under way end before the block does)
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  store_out();
   if constexpr (STATE) {
     store_state(ps.state + w * state_values(a) + head * head_state, __builtin_amdgcn_exp2f(f));
     if (slice == 0 && tid == 0) ps.decay[w * a.v_heads + head] = __builtin_amdgcn_exp2f(sum);
@@ -812,25 +866,25 @@ constexpr int kManySeqs = 8, kShortTokens = 8;
 
 // Columns of a state a block holds. Half of them where that fills the chip
 // better than it costs in keys and queries read again: turns, states and their
-// passing take less time. 128 x 128, 128 columns against 64: 4 heads of 150
-// tokens 20.4, 16.2 us, of 16384 88, 69; 32 heads of 600 tokens 42.9, 37.9, of
-// 1777 56.5, 51.0, of 4096 75.7, 82.2; 64 heads of 1100 tokens 67.1, 62.3, of
-// 1777 79.0, 80.2; 12 heads of 4096 tokens 56.3, 52.3, of 16384 102, 112.
+// passing take less time. Heads of 128 x 128, 128 columns against 64: 16 heads of
+// 4096 tokens 58, 50 us, of 8192 82, 77; 32 heads of 1777 tokens 54, 47, of 4096
+// 81, 77, of 8192 120, 128; 64 heads of 1777 tokens 75.5, 73.4, of 2500 90.1,
+// 90.7, of 4096 124, 131.
 int chunk_cols(const LinearArgs& a, int64_t T) {
-  return a.qk_dim > 128 || a.v_dim <= 64 || T * a.v_heads <= 96 * 1024 ? 64 : 128;
+  return a.qk_dim > 128 || a.v_dim <= 64 || T * a.v_heads <= 144 * 1024 ? 64 : 128;
 }
 // Windows for T tokens: enough for two blocks on each compute unit, of 64 tokens
 // at least, of 128 from 1024 tokens on; one for few tokens, where two launches
 // more cost more than they save, the more so the more heads the windows' states
 // are passed for. One sequence of heads of 128 x 128, one window against
-// windows: 12 heads of 257 tokens 20.2, 22.7 us, of 320 22.1, 23.0, of 384 25.4,
-// 23.9; 32 heads of 384 tokens 26.1, 30.1, of 512 33.3, 31.6; 64 heads of 640
-// tokens 40.8, 44.4, of 768 47.6, 47.3. Windows of at least 64, 96, 128 tokens:
-// 32 heads of 600 tokens 43, 39, 41 us; 16 heads of 4096 tokens 60, 60, 59.
+// windows: 4 heads of 384 tokens 17.8, 18.7 us, of 448 20.0, 19.4; 16 heads of
+// 512 tokens 22.6, 23.2, of 768 31.7, 29.2; 32 heads of 768 tokens 32.4, 34.8, of
+// 1024 41.3, 38.2; 64 heads of 1024 tokens 41.9, 54.5. Windows of at least 64
+// and 128 tokens: 12 heads of 1024 tokens 29.3, 25.3, of 1777 35.8, 34.4.
 int most_windows(const LinearArgs& a, int64_t T) {
   const int per = a.v_heads * ((a.v_dim + chunk_cols(a, T) - 1) / chunk_cols(a, T));
   const int64_t least = T < 1024 ? 64 : 128;
-  if (T <= 256 + 4 * std::min(per, 128)) return 1;
+  if (T <= 384 + 6 * std::min(per, 128)) return 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::max(1, kMaxWindows / per), (T + least - 1) / least));
 }
 void set_windows(LinearArgs& a) {
@@ -847,10 +901,10 @@ hipError_t launch_chunks(const LinearArgs& a, hipStream_t s) {
   const int slices = (a.v_dim + 64 * NT - 1) / (64 * NT), per = a.v_heads * slices;
   const auto grid = [](int units) { return dim3((units + 7) / 8 * 8); };
   if (a.windows > 1) {
-    hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, true>), grid((a.windows - 1) * per), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, true>), grid((a.windows - 1) * per), dim3(kChunkThreads), 0, s, a);
     hipLaunchKernelGGL(linear_pass_kernel, dim3((a.qk_dim * a.v_dim + 1023) / 1024, a.v_heads), dim3(256), 0, s, a);
   }
-  hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, false>), grid(a.windows * a.strands * per), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((linear_chunk_kernel<DK, NT, 3, false>), grid(a.windows * a.strands * per), dim3(kChunkThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -288,6 +288,9 @@ LINEAR_CASES = [
     dict(lengths=[1] * 20 + [300] + [8, 9, 0, 7] + [2] * 9), dict(lengths=[5, 600, 0, 8, 0, 9, 1, 1, 64, 3], inplace=True, Hv=2),
     dict(lengths=[0] * 9), dict(lengths=[0] * 9, behind=2, inplace=True), dict(lengths=[3] * 12, slots=[-1, 13] + [4] * 10, behind=5),
     dict(lengths=[20] * 100, Hk=1, Hv=2, dk=32, dv=64), dict(lengths=[9] * 28, dk=32, dv=72, slots=[27] * 3 + [-1] * 25), dict(lengths=[0, 11, 0, 0, 9, 200, 8], Hk=1, Hv=2, inplace=True), dict(lengths=[0, 33, 8, 15, 1, 40] * 30, Hk=1, Hv=2, dk=64, dv=32, inplace=True),
+    # 128 columns of a state a block, one window and several
+    dict(lengths=[1, 150, 39], Hk=390, Hv=780, dk=16, dv=72), dict(lengths=[1000, 0, 700, 621], Hk=16, Hv=64, dk=16, dv=80, slots=[3, 1, 0, 5], inplace=True),
+    dict(lengths=[30, 1300, 991], Hk=32, Hv=64, dk=72, dv=72), dict(lengths=[1900, 700], Hk=60, Hv=60, dk=24, dv=136, per_token=False, behind=3),
     dict(lengths=[8] * 70 + [400], Hk=1, Hv=1, dk=32, dv=32), dict(lengths=[1] * 130, Hk=1, Hv=2, dk=40, dv=72, per_token=False),
 ]
 
@@ -345,7 +348,7 @@ def test_linear_nan_stays_in_its_head_and_sequence():
     assert torch.equal(S1[1], S0[1]) and torch.equal(S1[0, 1], S0[0, 1])
 
 
-@pytest.mark.parametrize("D,Hv,value", [(64, 2, math.nan), (64, 2, math.inf), (128, 2, -math.inf), (40, 1, math.nan), (256, 1, math.inf)])
+@pytest.mark.parametrize("D,Hv,value", [(64, 2, math.nan), (64, 2, math.inf), (128, 2, -math.inf), (40, 1, math.nan), (256, 1, math.inf), (72, 740, math.nan)])
 def test_linear_not_finite_values_reach_no_earlier_token(D, Hv, value):
     """A NaN or infinity of one token's value, key or query reaches that token and, but for the query, its later ones,
     never an earlier token, another sequence or (a value) another column."""
