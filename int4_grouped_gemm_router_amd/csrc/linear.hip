@@ -31,8 +31,9 @@ __device__ inline int slot_of(const int32_t* slots, int i, int n) {
 
 // Block: one sequence, one value head, 32 columns of its state in registers:
 // thread (r, c) holds rows r + 32 p, columns 4 c .. 4 c + 3. Token after token,
-// the next token's rows under way. The states' bytes bound it: 48 sequences of
-// 32 heads of 128 x 128 move 202 MB.
+// the next token's rows under way. The states' bytes bound it: 48 sequences of a
+// token of 32 heads of 128 x 128 move 202 MB in 41 us (4.9 TB/s; with states
+// loaded through the caches 47).
 template <int NP>
 __global__ __launch_bounds__(256) void linear_walk_kernel(LinearArgs a) {
   __shared__ float part[2][4][kStepCols];
@@ -330,10 +331,11 @@ __host__ __device__ inline Passed passed(const LinearArgs& a) {
 // 300 tokens 21.7, 15.8 us, 32 heads of 16384 tokens alike.) STATE: only S, from
 // zeros, of the sequence that goes on behind the window.
 //
-// Latency bounds it: 16384 tokens of 32 heads of 128 x 128 in 16 windows take 61,
-// 13 and 125 us for the states, their passing and the outputs, which move 0.18,
-// 0.05 and 0.46 GB (3.0 to 3.8 TB/s); matrix cores are busy 0.22 of the time,
-// vector instructions issue in 0.31 of it, LDS is read in 0.17.
+// Latency bounds it: 16384 tokens of 32 heads of 128 x 128 in 16 windows take 58
+// to 61, 13 and 125 to 138 us for the states, their passing and the outputs, which
+// move 0.18, 0.05 and 0.46 GB (3.0 to 3.8 TB/s); matrix cores are busy 0.31 (the
+// states) and 0.26 (the outputs) of the time, vector instructions issue in 0.37,
+// LDS is read in 0.17.
 template <int DK, int NT, int ST, bool STATE>
 __global__ __launch_bounds__(kChunkThreads, DK == 128 ? 3 : 2) void linear_chunk_kernel(LinearArgs a) {
   constexpr int RQ = DK / 8, RV = 8 * NT, kCols = 64 * NT;
@@ -802,7 +804,7 @@ __global__ __launch_bounds__(kChunkThreads, DK == 128 ? 3 : 2) void linear_chunk
 
 // What windows pass on: S at the end of each, from what each adds. Thread: four
 // values of one head's state, window after window; what the next eight windows
-// add is under way meanwhile.
+// add is under way meanwhile. Latency bounds it: 15 windows of 32 heads 13 us.
 __global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
   __shared__ struct {
     int on, begins, slot;

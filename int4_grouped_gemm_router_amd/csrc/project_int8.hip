@@ -9,11 +9,13 @@
 // row, a step of one operation, L2 delivers half as much: 4096 x 12288 x 2048 took
 // 115 us), and reads it back in the matrix cores' order. Three kernels:
 //   int8_vector_kernel one to four tokens: whole rows of weights straight to
-//                      registers, dot products of four in the vector units
+//                      registers, dot products of four in the vector units;
+//                      memory bounds it (1 x 12288 x 2048 5.7 us, 4.4 TB/s)
 //   int8_split_kernel  a block's waves split K and join through LDS: few rows,
-//                      where bytes and latency count
+//                      where bytes and latency count (500 x 2000 x 4096 12 us)
 //   int8_tile_kernel   256 x 256 tiles, both operands shared through two stages
 //                      of 128 inputs: many rows, where the matrix cores count
+//                      (4096 x 12288 x 2048 113 us, 1.83 POP/s; 4096^3 64, 2.15)
 #include <algorithm>
 #include <type_traits>
 

@@ -8,8 +8,9 @@
 // and a rest of at most an eighth of a turn, where the Taylor series of sine
 // and cosine to x^9 and x^10 err by less than 3e-9.
 //
-// Memory bounds long calls, one load and one store's latency short ones. A
-// thread owns eight pairs of a token (eight values from each half, or sixteen
+// Memory bounds long calls (16384 tokens of 40 heads of 128: 72 us, 4.6 TB/s),
+// one load and one store's latency short ones (4.2 us for one token). A thread
+// owns eight pairs of a token (eight values from each half, or sixteen
 // neighbouring ones) and, in long calls, four heads, over which it uses the
 // eight angles; the values behind the turned part are copied sixteen at a time
 // where the output is another buffer.
