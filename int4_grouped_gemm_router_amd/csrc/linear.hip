@@ -323,7 +323,7 @@ __host__ __device__ inline Passed passed(const LinearArgs& a) {
 // accumulators: of each 32 rows lane group g holds rows 8 g .. 8 g + 7, the ones
 // that a matrix operand wants of it, because the keys enter the update with
 // their columns in that order. So are the decayed products of queries and keys,
-// which every wave forms for itself (12 of its 76 matrix operations a chunk), so
+// which every wave forms for itself (12 of its 80 matrix operations a chunk), so
 // that nothing but the rows goes through LDS. A fifth wave walks over the
 // sequences, copies rows two chunks ahead and forms the decays of the next
 // chunk; the four wait for nothing but it, once a chunk. (With that work spread

@@ -696,3 +696,84 @@ def test_mixer_in_graphs_and_on_streams():
         ms[0].run()
     got = ms[0].outputs()
     assert all(torch.equal(got[n], want[0][n]) for n in want[0])
+
+
+def test_rows_past_two_to_the_31st():
+    """Rows a million elements apart, so that their offsets pass 32 bits: the same as rows side by side, bit for bit."""
+    ld, T = 1 << 20, 2100
+    g = torch.Generator().manual_seed(8)
+    far = torch.empty((T, ld), dtype=torch.bfloat16, device="cuda")
+    assert (T - 1) * ld > 1 << 31
+
+    def spread(t, at):
+        """t's rows in columns `at` on of `far`."""
+        v = far[:, at:at + t.shape[1]]
+        v.copy_(t)
+        return v
+    Hk, Hv, D = 1, 2, 64
+    q, k, v, decay = (t.cuda() for t in _linear_inputs(T, Hk, Hv, D, D, True, 5))
+    plan, cu = B.linear_attention(Hk, Hv, D, D), torch.tensor([0, 700, T], dtype=torch.int32, device="cuda")
+    ws = B.linear_attention_workspace(plan, 2, T)
+    o = torch.empty((T, Hv, D), dtype=torch.bfloat16, device="cuda")
+    B.moe_linear_attention(plan, q, k, v, decay, o, cu, T, ws=ws)
+    fo = far[:, 4096:4096 + Hv * D]
+    B.moe_linear_attention(plan, spread(q.flatten(1), 0), spread(k.flatten(1), 1024), spread(v.flatten(1), 2048), decay, fo, cu, T,
+                           ws=ws)
+    assert torch.equal(fo, o.flatten(1))
+    B.moe_linear_attention_step(plan, q, k, v, decay, o, T)
+    B.moe_linear_attention_step(plan, far[:, :Hk * D], far[:, 1024:1024 + Hk * D], far[:, 2048:2048 + Hv * D], decay, fo, T)
+    assert torch.equal(fo, o.flatten(1))
+
+    rope, pos = B.rope(D), torch.arange(T, dtype=torch.int32, device="cuda")
+    y = torch.empty_like(v)
+    B.moe_rope(rope, pos, T, v, q_out=y)
+    B.moe_rope(rope, pos, T, far[:, 2048:2048 + Hv * D])
+    assert torch.equal(far[:, 2048:2048 + Hv * D], y.flatten(1))
+
+    H = 128
+    n = B.gated_norm(H, gate=B.GATE_SILU, next_norm=True)
+    x, z, w = (torch.randn(s, generator=g).bfloat16().cuda() for s in ((T, H), (T, H), (H,)))
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    B.moe_gated_norm(n, x, T, weight=w, gate=z, residual=x, next_weight=w, h_out=h, y=y)
+    fh, fy = far[:, 8192:8192 + H], far[:, ld - H:]
+    xf = spread(x, 3)
+    B.moe_gated_norm(n, xf, T, weight=w, gate=spread(z, 5000), residual=xf, next_weight=w, h_out=fh, y=fy)
+    assert torch.equal(fh, h) and torch.equal(fy, y)
+
+    x8, w8 = (torch.randint(-128, 128, s, generator=g, dtype=torch.int8).cuda() for s in ((T, 256), (48, 256)))
+    xs, wsc = torch.rand(T, generator=g).cuda(), torch.rand(48, generator=g).cuda()
+    y = torch.empty((T, 48), dtype=torch.bfloat16, device="cuda")
+    B.moe_project_int8(w8, wsc, x8, xs, y, T)
+    far8 = torch.as_strided(far.view(torch.int8), (2 * T, 256), (ld, 1))  # (rows of a million bytes)
+    far8[T:].copy_(x8)
+    far8[:T].copy_(x8)
+    y2 = torch.empty((2 * T, 48), dtype=torch.bfloat16, device="cuda")
+    B.moe_project_int8(w8, wsc, far8, xs.repeat(2), y2, 2 * T)
+    assert torch.equal(y2[:T], y) and torch.equal(y2[T:], y)
+    fy = far[:, 1 << 19:(1 << 19) + 48]
+    B.moe_project_int8(w8, wsc, x8, xs, fy, T)
+    assert torch.equal(fy, y)
+
+
+def test_linear_states_past_two_to_the_31st():
+    """Slots at the end of a pool of more than 2^31 values: the same as in a small pool, bit for bit, in place."""
+    Hk, Hv, D, n = 2, 16, 128, 8200
+    assert n * Hv * D * D > 1 << 31
+    pool = torch.empty((n, Hv, D, D), device="cuda")
+    start = torch.randn((2, Hv, D, D), generator=torch.Generator().manual_seed(2)).cuda()
+    plan = B.linear_attention(Hk, Hv, D, D)
+    slots = torch.tensor([n - 1, n - 3], dtype=torch.int32, device="cuda")
+    for T, cu in ((2, None), (50, [0, 20, 50]), (1400, [0, 1390, 1400])):
+        q, k, v, g = (t.cuda() for t in _linear_inputs(T, Hk, Hv, D, D, True, T))
+        small, o, o2 = start.clone(), torch.empty_like(v), torch.empty_like(v)
+        pool[n - 1], pool[n - 3] = start[0], start[1]
+        if cu is None:
+            B.moe_linear_attention_step(plan, q, k, v, g, o, T, state_in=small, state_out=small)
+            B.moe_linear_attention_step(plan, q, k, v, g, o2, T, state_in=pool, slots_in=slots, state_out=pool, slots_out=slots)
+        else:
+            cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            ws = B.linear_attention_workspace(plan, 2, T)
+            B.moe_linear_attention(plan, q, k, v, g, o, cu, T, state_in=small, state_out=small, ws=ws)
+            B.moe_linear_attention(plan, q, k, v, g, o2, cu, T, state_in=pool, slots_in=slots, state_out=pool, slots_out=slots, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(pool[n - 1], small[0]) and torch.equal(pool[n - 3], small[1])
+        assert not torch.equal(small, start)
