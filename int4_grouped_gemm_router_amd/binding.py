@@ -858,7 +858,11 @@ def _state(s, slots, l, heads, n_seqs, dev, name):
                          f"of {s.dtype}")
     if s.get_device() != dev:
         raise ValueError(f"state_{name}: on {s.device}, other tensors on device {dev}: one GPU is needed")
-    return s.data_ptr(), None if slots is None else _flat(slots, n_seqs, _i32_type(), f"slots_{name}", dev), shape[0]
+    if slots is None:  # (the sequence's index: states past the pool's end would be lost without a word)
+        if shape[0] < n_seqs:
+            raise ValueError(f"state_{name}: {n_seqs} states are needed without slots, got {shape[0]}")
+        return s.data_ptr(), None, shape[0]
+    return s.data_ptr(), _flat(slots, n_seqs, _i32_type(), f"slots_{name}", dev), shape[0]
 
 
 _int32 = None
