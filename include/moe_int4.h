@@ -462,8 +462,9 @@ typedef struct {
 int moe_rope_radians(const moe_rope_scaling* scaling, int32_t rot_dim, double* radians,
                      float* magnitude);
 
-/* radians[n] per position (finite) as whole numbers of 2^-64 turns, modulo one
- * turn (host -> host): with them a position times a frequency is exact. */
+/* radians[n] per position (at most 2^61 either way) as whole numbers of 2^-64
+ * turns, modulo one turn, each the nearest or its neighbour (host -> host): the
+ * product of one and a position is exact. */
 int moe_rope_turns(const double* radians, int32_t n, uint64_t* turns);
 
 /* Heads of head_dim values (2..1024), whose first rot_dim (even, 2..head_dim)
@@ -485,8 +486,11 @@ typedef struct {
  * and k_out k, with the same stride; the values behind rot_dim are copied to
  * another buffer and left alone in place. Any other overlap of an output with
  * another argument is not allowed (q and k may be parts of one row, and so may
- * the outputs). 1..1024 heads each. Angles err by at most 2^-32 turns however
- * far the position; sums in fp32, one rounding. T <= 2^30; T = 0 is a no-op. */
+ * the outputs). 1..1024 heads each. However far the position, an angle modulo
+ * one turn is off by less than 1.4 * 2^-32 turns (what 2^31 positions make of a
+ * frequency's rounding, and the lower 32 bits, which are dropped); from there on
+ * cosine and sine are formed in fp32 and err by at most 4 * 2^-24 more. Sums in
+ * fp32, one rounding. T <= 2^30; T = 0 is a no-op. */
 int moe_rope(const moe_rotary* rope, const void* q, int64_t ldq, void* q_out, int64_t ldqo,
              int32_t q_heads, const void* k, int64_t ldk, void* k_out, int64_t ldko,
              int32_t k_heads, const int32_t* positions, int32_t T, void* stream);

@@ -17,6 +17,28 @@ constexpr int32_t kMaxSeqs = 65536;
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxRopeDim = 1024;
 
+constexpr double kMaxRadians = 0x1p61;
+
+// r / (2 pi) modulo 1, in steps of 2^-64 to the nearest (but for the 2^-67 turns
+// that 128 bits of 1 / (2 pi) leave at the largest r): the whole number m of
+// r = m 2^e times those bits, of which the bits that weigh 2^-64 to 2^-1 remain.
+uint64_t turns_of(double r) {
+  constexpr uint64_t kHigh = 0x28be60db9391054a, kLow = 0x7f09d5f47d4d3770;  // 2^128 / (2 pi)
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(r), &e), 53);
+  const int drop = 64 - (e - 53);  // 55 or more, as r is at most 2^61
+  const unsigned __int128 low = (unsigned __int128)m * kLow, high = (unsigned __int128)m * kHigh + (uint64_t)(low >> 64);
+  const uint64_t bottom = (uint64_t)low;  // the product is high 2^64 + bottom
+  uint64_t u = 0;
+  if (drop < 64)
+    u = (uint64_t)(high << (64 - drop)) + (bottom >> drop) + (bottom >> (drop - 1) & 1);
+  else if (drop == 64)
+    u = (uint64_t)high + (bottom >> 63);
+  else if (drop < 192)
+    u = (uint64_t)(high >> (drop - 64)) + (uint64_t)(high >> (drop - 65) & 1);
+  return r < 0 ? 0 - u : u;
+}
+
 bool type_ok(int t) { return t >= MOE_BF16 && t <= MOE_F32; }
 int type_bytes(int t) { return t == MOE_F32 ? 4 : 2; }
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -156,12 +178,9 @@ int moe_rope_turns(const double* radians, int32_t n, uint64_t* turns) {
   if (!radians || !turns || n < 0) return MOE_EINVAL;
   for (int i = 0; i < n; ++i)
     if (!std::isfinite(radians[i])) return MOE_EINVAL;
-  for (int i = 0; i < n; ++i) {
-    long double f = radians[i] / 6.283185307179586476925286766559L;
-    f -= std::floor(f);
-    const long double u = std::nearbyint(f * 18446744073709551616.0L);
-    turns[i] = u >= 18446744073709551616.0L ? 0 : (uint64_t)u;
-  }
+  for (int i = 0; i < n; ++i)
+    if (std::fabs(radians[i]) > kMaxRadians) return MOE_EUNSUPPORTED;
+  for (int i = 0; i < n; ++i) turns[i] = turns_of(radians[i]);
   return MOE_OK;
 }
 
