@@ -431,8 +431,9 @@ int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64
  * row stride ldy (elements, from N to 2^20). K % 64 == 0, 64..65536; N
  * 1..2^18; T <= 2^30. Sums are exact (32-bit integers); the scales and the
  * bias are applied in fp32 and the result is rounded once. x and y must not
- * overlap. ws 16-byte aligned (null where moe_project_int8_workspace_bytes
- * gives 0); its contents do not matter. T = 0 is a no-op. */
+ * overlap. It needs no workspace: moe_project_int8_workspace_bytes gives 0 for
+ * every size, and ws (null or 16-byte aligned) and ws_bytes are reserved, never
+ * read or written. T = 0 is a no-op. */
 int moe_project_int8_workspace_bytes(int32_t N, int32_t K, int32_t T, size_t* bytes);
 int moe_project_int8(const int8_t* w, const float* w_scales, const float* bias, int32_t N, int32_t K,
                      const int8_t* x, int64_t ldx, const float* x_scales, void* y, int64_t ldy,

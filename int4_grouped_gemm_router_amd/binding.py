@@ -738,7 +738,7 @@ def moe_project(blob, N: int, K: int, x, y, T: int, adapters: Adapters | None = 
 # Checks and streams as above.
 
 def project_int8_workspace(N, K, T, device="cuda"):
-    """Workspace of moe_project_int8 for up to T tokens, or None where none is needed."""
+    """Workspace of moe_project_int8 for up to T tokens: None, as it needs none at any size."""
     import torch
     n = _sz(0)
     _check(lib().moe_project_int8_workspace_bytes(N, K, T, ctypes.byref(n)), "moe_project_int8_workspace_bytes")

@@ -116,22 +116,20 @@ extern "C" {
 int moe_project_int8_workspace_bytes(int32_t N, int32_t K, int32_t T, size_t* bytes) {
   if (!bytes) return MOE_EINVAL;
   const int rc = check_int8(N, K, T);
-  if (rc == MOE_OK) *bytes = int8_ws_bytes(N, K, std::max(T, 1));
+  if (rc == MOE_OK) *bytes = 0;  // (each of the kernels joins its parts within a block)
   return rc;
 }
 
 int moe_project_int8(const int8_t* w, const float* w_scales, const float* bias, int32_t N, int32_t K,
                      const int8_t* x, int64_t ldx, const float* x_scales, void* y, int64_t ldy,
-                     int32_t dtype, int32_t T, void* ws, size_t ws_bytes, void* stream) {
+                     int32_t dtype, int32_t T, void* ws, size_t /*ws_bytes*/, void* stream) {
   if (!type_ok(dtype)) return MOE_EINVAL;
   const int rc = check_int8(N, K, T);
   if (rc != MOE_OK || T == 0) return rc;
-  const size_t need = int8_ws_bytes(N, K, T);
   if (!w || !w_scales || !x || !x_scales || !y || !al16(w) || !al16(x) || !al4(w_scales) || !al4(x_scales) ||
       !al4(bias) || !aligned(y, type_bytes(dtype)) || ldx % 16 || !stride_ok(ldx, K) || !stride_ok(ldy, N) ||
-      (need && !ws) || !al16(ws))
+      !al16(ws))
     return MOE_EINVAL;
-  if (ws_bytes < need) return MOE_EWORKSPACE;
   Int8Args a{};
   a.w = w;
   a.x = x;
@@ -139,7 +137,6 @@ int moe_project_int8(const int8_t* w, const float* w_scales, const float* bias, 
   a.x_scales = x_scales;
   a.bias = bias;
   a.y = y;
-  a.ws = ws;
   a.ldx = ldx;
   a.ldy = ldy;
   a.N = N;

@@ -189,12 +189,10 @@ struct Int8Args {
   const int8_t *w, *x;       // [N][K], [T] with row stride ldx
   const float *w_scales, *x_scales, *bias;  // [N], [T], [N] or null
   void* y;                   // [T], row stride ldy
-  void* ws;                  // int8_ws_bytes
   int64_t ldx, ldy;
   int N, K, T, dtype;
   int wide;                  // rows of y are 16-byte aligned; set by the launcher
 };
-size_t int8_ws_bytes(int N, int K, int T);
 hipError_t launch_project_int8(const Int8Args& a, hipStream_t s);
 
 struct RopeArgs {

@@ -458,8 +458,6 @@ __global__ __launch_bounds__(kIThreads, 2) void int8_tile_kernel(Int8Args a) {
   }
 }
 
-size_t int8_ws_bytes(int /*N*/, int /*K*/, int /*T*/) { return 0; }
-
 namespace {
 
 constexpr int kVecTokens = 4;

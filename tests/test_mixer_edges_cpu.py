@@ -1,9 +1,25 @@
 """Host-side checks of the operators of a block's mixer half at the edges of what may be passed (no GPU needed)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from int4_grouped_gemm_router_amd import binding as B
+
+
+# ------------------------------------------------------------------ int8 projection
+
+def test_int8_needs_no_workspace():
+    """0 bytes at every size, from one token and one output to the largest; the binding has none to hand out."""
+    n = ctypes.c_size_t(7)
+    for N in (1, 64, 2000, 12288, 1 << 18):
+        for K in (64, 2048, 65536):
+            for T in (0, 1, 4, 5, 64, 500, 4096, 1 << 18, 1 << 30):
+                n.value = 7
+                assert B.lib().moe_project_int8_workspace_bytes(N, K, T, ctypes.byref(n)) == B.MOE_OK
+                assert n.value == 0, (N, K, T)
+    assert B.project_int8_workspace(12288, 2048, 4096, device="cpu") is None
 
 
 # ------------------------------------------------------------------ linear attention
