@@ -26,6 +26,13 @@ namespace {
 template <int TPR>
 constexpr int kGatedThreads = TPR > 256 ? TPR : 256;
 
+// Waves of a SIMD that the registers are for: eight (64 registers) for rows of 16
+// bits, but six with a second norm and an 8-bit output at once, which spill at
+// eight: 16384 x 512 70 against 19 us, 8192 x 4096 73, 69, 4096 x 8192 145, 92. At
+// 256 threads a row the spills stay out of the way (16384 x 2048 65.7 at either).
+template <class R, int TPR, int NV, int OUT8, bool NEXT>
+constexpr int kGatedWaves = NV > 1 || sizeof(typename R::type) == 4 ? 4 : NEXT && OUT8 != kOut8None && TPR != 256 ? 6 : 8;
+
 // e^z to about an ulp: the part of z log2(e) that its product loses is put
 // back as a factor. Below -110 the result is 0 in every use here (1 + e^z).
 __device__ inline float exp_full(float z) {
@@ -87,7 +94,7 @@ __device__ inline uint32_t row_all_once(uint32_t v, uint32_t* s, F f) {
 // (4.6 TB/s), with the 94 registers of a next row loaded ahead 73; 1500 x 4096
 // fp16, gated by heads of 128, 16 and 20.
 template <class R, int TPR, int NV, int OUT8, bool NEXT>
-__global__ __launch_bounds__(kGatedThreads<TPR>, NV == 1 && sizeof(typename R::type) == 2 ? 8 : 4) void gated_norm_kernel(GatedArgs a) {
+__global__ __launch_bounds__(kGatedThreads<TPR>, (kGatedWaves<R, TPR, NV, OUT8, NEXT>)) void gated_norm_kernel(GatedArgs a) {
   typedef typename R::type E;
   __shared__ uint32_t red[2][3][16];  // by turns: [turn % 2][which reduction][wave]
   constexpr int kRows = kGatedThreads<TPR> / TPR;
@@ -252,13 +259,21 @@ __global__ __launch_bounds__(kGatedThreads<TPR>, NV == 1 && sizeof(typename R::t
     }
     if constexpr (OUT8 != kOut8None) {
       // |v| as ordered bits: their integer maximum is the largest magnitude,
-      // with NaN above infinity (values past the row are 0, or NaN with its sum)
+      // with NaN above infinity (values past the row are left out: an infinite
+      // gate of the row makes NaN of their zeros)
       uint32_t m[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        const int c = (lt + TPR * j) * kVec;
         m[j] = 0;
+        if (c + kVec <= H) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) m[j] = max(m[j], __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+          for (int i = 0; i < kVec; ++i) m[j] = max(m[j], __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i)
+            if (c + i < H) m[j] = max(m[j], __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+        }
       }
       if (a.out8_group) {
 #pragma unroll

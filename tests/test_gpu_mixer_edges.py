@@ -1,6 +1,6 @@
 """GPU tests of the operators of a block's mixer half where the other ones do not go: linear attention's edge values in
 calls of several windows (states passed from one to the next), workspaces that captured graphs share, prompts followed by
-single tokens out of one pool of states.
+single tokens out of one pool of states, and infinite gates.
 
 Compared with the plain implementation in 64 bits (mixer_ref.py)."""
 import math
@@ -219,6 +219,24 @@ def test_linear_empty_sequences_copy_their_states(n):
     S, o = torch.full((n, H, D, D), 7.0, device="cuda"), torch.empty_like(q)
     B.moe_linear_attention(plan, q, q, q, torch.zeros((4, H), device="cuda"), o, cu, 4, state_in=pool.cuda(), state_out=S)
     assert torch.equal(S[1:].cpu().nan_to_num(nan=5.0), pool[1:].nan_to_num(nan=5.0)) and S[1, 0, 0, 5].isnan()
+
+
+# ------------------------------------------------------------------ the norm after a block
+
+@pytest.mark.parametrize("H", [128, 100, 500, 1000, 2048, 2500, 8192, 9000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_norm_infinite_gate_of_a_row(H, dtype):
+    """An infinite gate of a row makes it infinite, and so the scale of its 8-bit values, at every width."""
+    dt = M.DT[dtype]
+    x = (torch.rand((3, H), generator=torch.Generator().manual_seed(H)) + 0.5).to(dt)
+    z = torch.tensor([[1.0], [math.inf], [-2.0]]).to(dt)
+    for out8, kind in ((B.OUT8_INT8, torch.int8), (B.OUT8_E4M3, torch.float8_e4m3fn)):
+        n = B.gated_norm(H, dtype=dt, normalize=False, gate=B.GATE_SILU, gate_per_row=True, out8=out8)
+        h, q, s = torch.empty_like(x).cuda(), torch.empty((3, H), dtype=kind, device="cuda"), torch.empty((3, 1), device="cuda")
+        B.moe_gated_norm(n, x.cuda(), 3, gate=z.cuda(), h_out=h, q=q, scales=s)
+        assert (h[1] == math.inf).all() and h[[0, 2]].isfinite().all()
+        assert s[1, 0] == math.inf and s[[0, 2]].isfinite().all(), s
+        assert (q[1] == 0).all() if out8 == B.OUT8_INT8 else q[1].float().isnan().all()
 
 
 # ------------------------------------------------------------------ together
