@@ -424,7 +424,8 @@ int moe_project(const void* blob, int32_t N, int32_t K, const uint16_t* x, int64
 /* A projection by 8-bit integers with a scale for each token and each output:
  *   y[t][n] = x_scales[t] * w_scales[n] * sum_k x[t][k] w[n][k] + bias[n]
  * for x [T][K] with row stride ldx (bytes, a multiple of 16, from K to 2^20),
- * as moe_add_rmsnorm and moe_gated_norm leave int8 rows with one scale a row,
+ * as moe_add_rmsnorm and moe_gated_norm leave int8 rows with one scale a row
+ * (their e4m3 rows and rows with a scale for each group are not read here),
  * and w [N][K] row-major, contiguous; both 16-byte aligned, any value
  * -128..127. x_scales [T], w_scales [N] and bias [N] (or null) fp32. y [T][N]
  * of type dtype (MOE_BF16, MOE_F16 or MOE_F32), aligned to its element, with
@@ -439,7 +440,9 @@ int moe_project_int8(const int8_t* w, const float* w_scales, const float* bias, 
                      const int8_t* x, int64_t ldx, const float* x_scales, void* y, int64_t ldy,
                      int32_t dtype, int32_t T, void* ws, size_t ws_bytes, void* stream);
 
-/* Frequencies of rotary positions: pair i of a turned part of rot_dim values
+/* Frequencies of rotary positions (for any others, such as a YaRN whose ramp
+ * runs over the pairs' index between two rounded bounds, as many checkpoints
+ * have it, moe_rope_turns takes a model's own radians): pair i of a turned part of rot_dim values
  * turns by radians[i] = base^(-2i / rot_dim) per position, and for long
  * contexts by less (factor >= 1):
  *   MOE_ROPE_LINEAR  radians / factor
@@ -510,8 +513,9 @@ typedef struct {
  * heads contiguous within rows of strides ldq, ldk, ldv, ldo (elements,
  * multiples of 8, at most 2^20). g = log_decay, fp32: [T][v_heads] with row
  * stride ld_decay (v_heads..2^20), or [v_heads] for all tokens with ld_decay
- * 0. A g of -inf forgets everything before the token; where g is above 0, exp
- * of its sum over a sequence has to be finite.
+ * 0. A g of -inf forgets everything finite before the token (a NaN or infinity
+ * in a state stays, as its product with 0); where g is above 0, exp of its sum
+ * over a sequence has to be finite.
  * Sequence i holds the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
  * (device, int32 [n_seqs + 1], not decreasing, from 0; values are limited to
  * 0..T); rows of o behind the last are left as they were. Its state starts as
@@ -519,18 +523,22 @@ typedef struct {
  * [n][v_heads][qk_dim][v_dim], 16-byte aligned, n = n_in and n_out. Null
  * slots stand for i; a slot outside 0..n-1 (-1) starts from zeros or is not
  * kept, and so is every one of a null state. An empty sequence's state is
- * copied. state_in may be state_out; a slot that one sequence writes must not
- * be read or written by another (any number may read the same one).
+ * copied (a zero may lose its sign). state_in may be state_out; a slot that
+ * one sequence writes must not be read or written by another (any number may
+ * read the same one).
  * n_seqs <= 65536, T <= 2^30. States, sums and decays are fp32 or more; the
  * state's update keeps 24 significant bits of v's decayed rows, and for o the
  * state and the decayed products of q and k are rounded to bf16 as operands
- * of the matrix cores (o's own type). |v| is below 2^120. A NaN or infinity in
- * a token's row reaches that token's o and, from k, v or g, the later ones of
- * its sequence and its state (as NaN or infinity; from v in its own column
- * only), nothing else. ws 16-byte aligned, of
- * moe_linear_workspace_bytes (null where that is 0); its contents do not
- * matter, and a workspace for T tokens and n_seqs serves fewer. o must not
- * overlap any input. n_seqs = 0 is a no-op. */
+ * of the matrix cores (o's own type). How a sequence is cut, and so the last
+ * bits of its o and state, depends on the call: on T, and on whether a
+ * sequence of up to 8 tokens is one of 8 or more (then o's operands are not
+ * rounded, as in moe_linear_attention_step); one call gives the same bits
+ * each time. |v| is below 2^120. A NaN or infinity in a token's row reaches
+ * that token's o and, from k, v or g, the later ones of its sequence and its
+ * state (as NaN or infinity; from v in its own column only), nothing else. ws
+ * 16-byte aligned, of moe_linear_workspace_bytes (null where that is 0); its
+ * contents do not matter, and a workspace for T tokens and n_seqs serves fewer.
+ * o must not overlap any input. n_seqs = 0 is a no-op. */
 int moe_linear_workspace_bytes(const moe_linear* linear, int32_t n_seqs, int32_t T, size_t* bytes);
 int moe_linear_attention(const moe_linear* linear, const uint16_t* q, int64_t ldq, const uint16_t* k,
                          int64_t ldk, const uint16_t* v, int64_t ldv, const float* log_decay,

@@ -765,7 +765,9 @@ def moe_project_int8(w, w_scales, x, x_scales, y, T: int, bias=None, ws=None, st
 
 
 def rope_radians(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, context=0.0, slow=1.0, fast=32.0):
-    """(radians per position of each pair, float64; the factor on cosine and sine) of scaled rotary positions."""
+    """(radians per position of each pair, float64; the factor on cosine and sine) of scaled rotary positions. ROPE_YARN's
+    ramp is linear in a pair's turns over the context; models whose ramp runs over the pairs' index pass rope their own
+    `radians`."""
     out, m = np.empty(max(rot_dim, 0) // 2, np.float64), _f32(0)
     s = MoeRopeScaling(scaling, base, factor, context, slow, fast)
     _check(lib().moe_rope_radians(ctypes.byref(s), rot_dim, _ptr(out), ctypes.byref(m)), "moe_rope_radians")

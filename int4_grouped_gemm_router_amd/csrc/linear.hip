@@ -151,7 +151,9 @@ __device__ inline u32x2 column4(const void* p) {
 
 // Rows of R 16-byte pieces lie in LDS without gaps, piece c of row r at
 // c ^ swizzle(r): sixteen rows' same piece, and eight rows' same pair of
-// pieces, are then in different banks.
+// pieces, are then in different banks. (The output launch of 16384 tokens of 32
+// heads still counts 1.9 conflict cycles an LDS instruction; which of its
+// accesses has them is not known.)
 template <int R>
 __device__ inline int swizzle(int r) {
   return R >= 16 ? 2 * (r & 7) | (r >> 3 & 1) : 2 * (r >> 1 & 3) | (r >> 3 & 1);
@@ -331,11 +333,12 @@ __host__ __device__ inline Passed passed(const LinearArgs& a) {
 // 300 tokens 21.7, 15.8 us, 32 heads of 16384 tokens alike.) STATE: only S, from
 // zeros, of the sequence that goes on behind the window.
 //
-// Latency bounds it: 16384 tokens of 32 heads of 128 x 128 in 16 windows take 58
-// to 61, 13 and 125 to 138 us for the states, their passing and the outputs, which
-// move 0.18, 0.05 and 0.46 GB (3.0 to 3.8 TB/s); matrix cores are busy 0.31 (the
-// states) and 0.26 (the outputs) of the time, vector instructions issue in 0.37,
-// LDS is read in 0.17.
+// Latency bounds it: 16384 tokens of 32 heads of 128 x 128 in 16 windows take 59
+// to 64, 14 and 138 to 157 us for the states, their passing and the outputs where
+// each launch is waited for (the call, where they follow each other, takes 197);
+// they move 0.18, 0.05 and 0.46 GB (2.8 to 3.6 TB/s); matrix cores are busy 0.31
+// (the states) and 0.26 (the outputs) of the time, vector instructions issue in
+// 0.37, LDS is read in 0.17.
 template <int DK, int NT, int ST, bool STATE>
 __global__ __launch_bounds__(kChunkThreads, DK == 128 ? 3 : 2) void linear_chunk_kernel(LinearArgs a) {
   constexpr int RQ = DK / 8, RV = 8 * NT, kCols = 64 * NT;
@@ -864,6 +867,19 @@ __global__ __launch_bounds__(256) void linear_pass_kernel(LinearArgs a) {
 
 namespace {
 
+// In a call of kManySeqs sequences or more, those of up to kShortTokens tokens are
+// walked through by linear_walk_kernel, a block a sequence, head and 32 columns; in
+// chunks they follow each other within a window, at 2.5 us each with 4 heads of
+// 128 x 128 and 10 with 32. Chunks alone against the walk for short ones: 256
+// single tokens and a prompt of 2000, 32 heads, 1393 and 325 us, 4 heads 344 and
+// 69; 16 sequences of 4 tokens and two of 300, 4 heads, 52 and 29 (32 heads: 46
+// and 53); 64 of 8 tokens and one of 500, 32 heads, 127 and 117. Where all are
+// short enough for one window, chunks lose nothing: 8 sequences of a token, 32
+// heads, 11.5 and 12.6, 64 of 8 tokens 62 and 88; with 4 heads, in several
+// windows, 30 and 28. Limits of 1, 4, 8, 16 and 32 tokens: 64 of 8 and one of 500,
+// 32 heads, 133, 133, 117, 115, 116; 64 of 16 and one of 500, 111, 112, 111, 172,
+// 168 (a walk takes a token at a time). Below 8 sequences a launch more costs about
+// what it saves: 4 sequences of a token 7.4 and 8.0, of 8 tokens 7.4 and 13.4.
 constexpr int kManySeqs = 8, kShortTokens = 8;
 
 // Columns of a state a block holds. Half of them where that fills the chip
@@ -871,7 +887,10 @@ constexpr int kManySeqs = 8, kShortTokens = 8;
 // passing take less time. Heads of 128 x 128, 128 columns against 64: 16 heads of
 // 4096 tokens 58, 50 us, of 8192 82, 77; 32 heads of 1777 tokens 54, 47, of 4096
 // 81, 77, of 8192 120, 128; 64 heads of 1777 tokens 75.5, 73.4, of 2500 90.1,
-// 90.7, of 4096 124, 131.
+// 90.7, of 4096 124, 131. The rule is that of 128 x 128; 16 heads of other sizes,
+// 128 columns against 64: 96 x 80, 300 tokens 21.7, 16.0 us, 1777 34.2, 37.1, 4096
+// 49.4, 47.2, 8192 68.3, 70.5; 64 x 128, 300 tokens 16.3, 13.3, 4096 45.2, 37.7,
+// 8192 60.1, 56.2. (More than 128 rows leave no registers for 128 columns.)
 int chunk_cols(const LinearArgs& a, int64_t T) {
   return a.qk_dim > 128 || a.v_dim <= 64 || T * a.v_heads <= 144 * 1024 ? 64 : 128;
 }
@@ -882,7 +901,12 @@ int chunk_cols(const LinearArgs& a, int64_t T) {
 // windows: 4 heads of 384 tokens 17.8, 18.7 us, of 448 20.0, 19.4; 16 heads of
 // 512 tokens 22.6, 23.2, of 768 31.7, 29.2; 32 heads of 768 tokens 32.4, 34.8, of
 // 1024 41.3, 38.2; 64 heads of 1024 tokens 41.9, 54.5. Windows of at least 64
-// and 128 tokens: 12 heads of 1024 tokens 29.3, 25.3, of 1777 35.8, 34.4.
+// and 128 tokens: 12 heads of 1024 tokens 29.3, 25.3, of 1777 35.8, 34.4. Other
+// sizes, one window against windows: 16 heads of 64 x 64, 300 tokens 13.2, 17.8, 768
+// 25.9, 20.8; of 200 x 200, 512 tokens 34.2, 50.7, 1024 61.5, 57.4; of 256 x 256, 768
+// tokens 48.6, 58.8, 1024 62.0, 64.9, 1777 103, 78; 4 heads of 256 x 256, 300 tokens
+// 22.6, 26.0, 512 33.0, 30.2; 64 heads of 64 x 64, 768 tokens 26.8, 30.9, 1024 34.0,
+// 31.4.
 int most_windows(const LinearArgs& a, int64_t T) {
   const int per = a.v_heads * ((a.v_dim + chunk_cols(a, T) - 1) / chunk_cols(a, T));
   const int64_t least = T < 1024 ? 64 : 128;
@@ -933,8 +957,6 @@ size_t linear_ws_bytes(const LinearArgs& a) {
 
 hipError_t launch_linear_attention(const LinearArgs& in, hipStream_t s) {
   LinearArgs a = in;
-  // Many sequences: those of a few tokens are walked through, a block for each,
-  // since they would follow each other in a window, at about 4 us each.
   a.short_tokens = a.n_seqs >= kManySeqs ? kShortTokens : -1;
   if (a.short_tokens >= 0) {
     const hipError_t e = launch_walk(a, s);
