@@ -889,7 +889,8 @@ def _decay(g, T, heads, dev):
 def moe_linear_attention(l: MoeLinear, q, k, v, log_decay, o, cu_seqlens, T: int, state_in=None, slots_in=None,
                          state_out=None, slots_out=None, ws=None, stream=None):
     """o = linear attention of the sequences that cu_seqlens [n + 1] (int32) cuts T tokens into; log_decay
-    [T, v_heads] or [v_heads]. Their states start as state_in[slots_in] and end as state_out[slots_out]."""
+    [T, v_heads] or [v_heads]. Their states start as state_in[slots_in] and end as state_out[slots_out]; without slots
+    sequence i has state i."""
     import torch
     n = cu_seqlens.numel() - 1
     _need(n >= 0, "cu_seqlens: n + 1 values are needed")

@@ -207,6 +207,55 @@ def test_windows_offsets_out_of_order_stay_in_range():
         assert (o[T:] == 3.0).all() and (S[n] == 3.0).all() and (ws[size:] == GUARD).all()
 
 
+def test_as_many_windows_as_there_can_be(case):
+    """70000 tokens of one head: 512 windows, several of them within a sequence, others with many sequences."""
+    case([40000, 0, 3, 200] + [9] * 40 + [300] * 50 + [70000 - 40000 - 203 - 360 - 15000], Hk=1, Hv=1, dk=16, dv=8)
+
+
+def test_as_many_sequences_as_there_can_be():
+    """65536 sequences, single tokens but for three: by the step, and in one call with the others."""
+    n, H, D, scale = 65536, 1, 8, 0.5
+    g = torch.Generator().manual_seed(3)
+    lengths = torch.ones(n, dtype=torch.int64)
+    lengths[0], lengths[30000], lengths[n - 1] = 40, 600, 9
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lengths.cumsum(0)])
+    T = int(cu[-1])
+    q, k, v = ((torch.randn((T, H, D), generator=g) / 2).bfloat16() for _ in range(3))
+    decay = -torch.rand((T, H), generator=g) * 0.1
+    pool = torch.randn((n, H, D, D), generator=g)
+    plan = B.linear_attention(H, H, D, D, scale=scale)
+
+    def single(at, S, o):
+        """Those tokens as sequences of their own, whose states are those of `pool`."""
+        S0 = pool[S].double()
+        want = torch.exp(decay[at].double())[..., None, None] * S0 + k[at].double()[..., None] * v[at].double()[:, :, None, :]
+        size = torch.exp(decay[at].double())[..., None, None] * S0.abs() + (k[at].double()[..., None] * v[at].double()[:, :, None, :]).abs()
+        y = scale * (q[at].double()[..., None] * want).sum(2)
+        weight = scale * (q[at].double()[..., None].abs() * size).sum(2)
+        ro, rs = bound()(D, 1, False)
+        M._close(o, y, ro * weight, torch.bfloat16, "o")
+        return want, rs * size + 1e-37
+    o, S = torch.empty((n, H, D), dtype=torch.bfloat16, device="cuda"), torch.empty((n, H, D, D), device="cuda")
+    B.moe_linear_attention_step(plan, q[:n].cuda(), k[:n].cuda(), v[:n].cuda(), decay[:n].cuda(), o, n, state_in=pool.cuda(), state_out=S)
+    want, err = single(slice(0, n), slice(0, n), o)
+    assert ((S.cpu().double() - want).abs() <= err).all()
+
+    o, S = torch.empty((T, H, D), dtype=torch.bfloat16, device="cuda"), pool.cuda()
+    B.moe_linear_attention(plan, q.cuda(), k.cuda(), v.cuda(), decay.cuda(), o, cu.to(torch.int32).cuda(), T, state_in=S, state_out=S,
+                           ws=_windows(plan, n, T))
+    one = lengths == 1
+    at = cu[:-1][one]
+    want, err = single(at, one, o.cpu()[at])
+    assert ((S.cpu().double()[one] - want).abs() <= err).all()
+    for i in (0, 30000, n - 1):
+        part = slice(int(cu[i]), int(cu[i + 1]))
+        L = int(lengths[i])
+        y, weight, states, sums = linear_ref(q[part], k[part], v[part], decay[part], pool[i:i + 1], [0, L], scale)
+        ro, rs = bound()(D, L, True)
+        M._close(o[part], y, ro * weight, torch.bfloat16, f"o of sequence {i}")
+        assert ((S[i].cpu().double() - states[0]).abs() <= rs * sums[0] + 1e-37).all()
+
+
 @pytest.mark.parametrize("n", [2, 9])
 def test_linear_empty_sequences_copy_their_states(n):
     """The state of a sequence without tokens arrives as it is, large and small values, infinities and NaN among them."""
